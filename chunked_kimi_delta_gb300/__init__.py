@@ -1,4 +1,5 @@
-"""Chunked Kimi Delta Attention (KDA) forward for GB300 (sm_103a).
+"""Chunked Kimi Delta Attention (KDA) for GB300 (sm_103a), and the 8-bit
+projection path around it.
 
 A thin ctypes binding over the C ABI of ``include/kda.h`` (``libkda.so``,
 built in-tree by :mod:`chunked_kimi_delta_gb300.build`).  The Python
@@ -11,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libkda.so")
@@ -32,6 +33,9 @@ KDA_LAYOUT_HEAD_MAJOR = 1 << 11
 KDA_TEST_WAIT_TIMEOUT = 1 << 30   # test only: see include/kda.h
 KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGNMENT = 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_DEVICE_TIMEOUT = 4, 5, 6
+KDA_FP8_ROW, KDA_FP8_COL, KDA_FP8_TILE = 1, 2, 4
+KDA_FP8_NT, KDA_FP8_NN, KDA_FP8_TN = 0, 1, 2
+KDA_FP8_MATMUL_WORKSPACE_BYTES = 256
 CHUNK = 64
 
 
@@ -88,6 +92,49 @@ class kda_bwd_args(ctypes.Structure):
     ]
 
 
+class kda_rms_norm_args(ctypes.Structure):
+    """Mirror of ``kda_rms_norm_args`` in include/kda.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int),
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float), ("residual_out", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("fp8", ctypes.c_void_p), ("ld_fp8", ctypes.c_int64), ("fp8_scales", ctypes.c_void_p),
+    ]
+
+
+class kda_rms_norm_bwd_args(ctypes.Structure):
+    """Mirror of ``kda_rms_norm_bwd_args`` in include/kda.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int),
+        ("d_out", ctypes.c_void_p), ("h", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("d_residual", ctypes.c_void_p), ("eps", ctypes.c_float), ("dx", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class kda_fp8_quantize_args(ctypes.Structure):
+    """Mirror of ``kda_fp8_quantize_args`` in include/kda.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int),
+        ("x", ctypes.c_void_p), ("ld", ctypes.c_int64),
+        ("row", ctypes.c_void_p), ("col", ctypes.c_void_p), ("tile", ctypes.c_void_p),
+        ("row_scales", ctypes.c_void_p), ("col_scales", ctypes.c_void_p),
+        ("tile_scales", ctypes.c_void_p),
+    ]
+
+
+class kda_fp8_matmul_args(ctypes.Structure):
+    """Mirror of ``kda_fp8_matmul_args`` in include/kda.h."""
+    _fields_ = [
+        ("m", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("form", ctypes.c_int),
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("a_scales", ctypes.c_void_p),
+        ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("b_scales", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("out_dtype", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -125,6 +172,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kda_segment_bwd_summary_workspace_size": ([P, i32], ctypes.c_size_t),
         "kda_segment_bwd_summary": ([P, vp, vp, i32, vp, vp], ctypes.c_int),
         "kda_state_grad_scan": ([vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp], ctypes.c_int),
+        "kda_rms_norm": ([ctypes.POINTER(kda_rms_norm_args), vp], ctypes.c_int),
+        "kda_rms_norm_bwd_workspace_size": ([i64, i32], ctypes.c_size_t),
+        "kda_rms_norm_bwd": ([ctypes.POINTER(kda_rms_norm_bwd_args), vp], ctypes.c_int),
+        "kda_fp8_quantize": ([ctypes.POINTER(kda_fp8_quantize_args), vp], ctypes.c_int),
+        "kda_fp8_matmul": ([ctypes.POINTER(kda_fp8_matmul_args), vp], ctypes.c_int),
     }
     for name, (argt, rest) in sigs.items():
         f = getattr(lib, name)
@@ -752,3 +804,224 @@ def kda_state_grad_scan(M, E, dS_final=None, *, dS_out=None, dS_initial=None, st
 def kda_get_device_status(workspace, stream=None) -> int:
     """Reads and clears the device error word of a workspace; returns the status."""
     return load_library().kda_get_device_status(workspace.data_ptr(), _stream(stream))
+
+
+# ------------------------------------------------ 8-bit projection path
+
+class Fp8Matrix(NamedTuple):
+    """A scaled 8-bit matrix [R, C] (include/kda.h, "Scaled 8-bit matrices"):
+    ``data`` float8_e4m3fn [R, C] whose row pitch is a multiple of 16,
+    ``scales`` float8_e8m0fnu, ``kind`` "row" (scales [ceil(CB/4), R, 4]),
+    "col" ([ceil(RB/4), C, 4]) or "tile" ([RB, CB]), CB = ceil(C / 128)."""
+    data: object
+    scales: object
+    kind: str
+
+
+class RmsNorm(NamedTuple):
+    """Results of :func:`kda_rms_norm`; what was not asked for is None."""
+    out: object
+    residual_out: object
+    fp8: Optional[Fp8Matrix]
+
+
+def _scale_shape(rows, cols, kind):
+    rb, cb = -(-rows // 128), -(-cols // 128)
+    return {"row": (-(-cb // 4), rows, 4), "col": (-(-rb // 4), cols, 4), "tile": (rb, cb)}[kind]
+
+
+def _empty_fp8(rows, cols, kind, device) -> Fp8Matrix:
+    torch = _torch()
+    data = torch.empty(rows, -(-cols // 16) * 16, dtype=torch.float8_e4m3fn, device=device)
+    scales = torch.empty(_scale_shape(rows, cols, kind), dtype=torch.float8_e8m0fnu, device=device)
+    return Fp8Matrix(data[:, :cols], scales, kind)
+
+
+def _pitch(t) -> int:
+    """Row pitch in elements of a 2-D tensor with dense rows."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("a matrix with dense rows is needed")
+    if t.shape[0] > 1:
+        return t.stride(0)
+    return -(-max(t.stride(0), t.shape[1]) // 16) * 16  # one row: any pitch will do
+
+
+def _check_fp8(x: Fp8Matrix, kind: str):
+    torch = _torch()
+    if x.kind != kind:
+        raise ValueError(f"this operand needs {kind} scales, not {x.kind}")
+    if x.data.dtype != torch.float8_e4m3fn or x.scales.dtype != torch.float8_e8m0fnu:
+        raise TypeError("a scaled 8-bit matrix holds float8_e4m3fn values and float8_e8m0fnu scales")
+    if tuple(x.scales.shape) != _scale_shape(*x.data.shape, kind):
+        raise ValueError(f"{kind} scales of {tuple(x.data.shape)} values have shape "
+                         f"{_scale_shape(*x.data.shape, kind)}, not {tuple(x.scales.shape)}")
+    _contig(x.scales)
+
+
+def _check_weight(weight, cols):
+    if weight is not None and (tuple(weight.shape) != (cols,) or weight.dtype != _torch().float32):
+        raise ValueError("weight must be fp32 [cols]")
+
+
+def _like(t, x, what):
+    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        raise ValueError(f"{what} must have x's shape and dtype")
+
+
+def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None,
+                 residual_out=None, stream=None) -> RmsNorm:
+    """RMS norm of the last dimension of ``x + residual`` (``x`` without
+    one), times ``weight`` (fp32 [cols]; None: ones).  ``fp8=True`` also
+    returns the result as an :class:`Fp8Matrix` [rows, cols] with row scales;
+    ``out=False`` then leaves out the result in x's dtype.  ``residual_out``
+    (x + residual) may be given as ``x`` or ``residual`` to work in place.
+    See ``kda_rms_norm`` in include/kda.h."""
+    torch = _torch()
+    lib = load_library()
+    cols = x.shape[-1]
+    _check_weight(weight, cols)
+    _like(residual, x, "residual")
+    if out is False and not fp8:
+        raise ValueError("no result: out=False needs fp8=True")
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out is False:
+        out = None
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    elif residual_out is None:
+        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _like(out, x, "out")
+    _like(residual_out, x, "residual_out")
+    _contig(x, weight, residual, out, residual_out)
+    rows = x.numel() // cols if cols else 0
+    q = _empty_fp8(rows, cols, "row", x.device) if fp8 else None
+    _on_device(x, weight, residual, out, residual_out)
+    a = kda_rms_norm_args()
+    a.rows, a.cols, a.dtype = rows, cols, _dtype_code(x)
+    a.x, a.residual, a.weight, a.eps = _ptr(x), _ptr(residual), _ptr(weight), float(eps)
+    a.residual_out, a.out = _ptr(residual_out), _ptr(out)
+    if q is not None:
+        a.fp8, a.ld_fp8, a.fp8_scales = _ptr(q.data), _pitch(q.data), _ptr(q.scales)
+    _check(lib.kda_rms_norm(ctypes.byref(a), _stream(stream)), "kda_rms_norm")
+    return RmsNorm(out, residual_out, q)
+
+
+def kda_rms_norm_bwd(d_out, x, weight=None, d_residual=None, *, eps=1e-6, dx=None,
+                     want_dweight=True, workspace=None, stream=None):
+    """Backward of :func:`kda_rms_norm`: ``x`` is the tensor that was
+    normalised (``residual_out`` when there was a residual), ``d_residual``
+    the gradient that reaches it from elsewhere.  Returns ``(dx, dweight)``:
+    dx is the gradient of x and of the residual, dweight fp32 [cols] (None
+    without ``want_dweight``).  See ``kda_rms_norm_bwd`` in include/kda.h."""
+    torch = _torch()
+    lib = load_library()
+    cols = x.shape[-1]
+    _check_weight(weight, cols)
+    _like(d_out, x, "d_out")
+    _like(d_residual, x, "d_residual")
+    if dx is None:
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _like(dx, x, "dx")
+    dweight = torch.empty(cols, dtype=torch.float32, device=x.device) if want_dweight else None
+    _contig(d_out, x, weight, d_residual, dx)
+    _on_device(d_out, x, weight, d_residual, dx, workspace)
+    a = kda_rms_norm_bwd_args()
+    a.rows, a.cols, a.dtype = x.numel() // cols if cols else 0, cols, _dtype_code(x)
+    a.d_out, a.h, a.weight, a.d_residual = _ptr(d_out), _ptr(x), _ptr(weight), _ptr(d_residual)
+    a.eps, a.dx, a.dweight = float(eps), _ptr(dx), _ptr(dweight)
+    if want_dweight:
+        ws = _workspace(lib.kda_rms_norm_bwd_workspace_size(a.rows, cols), x.device, workspace)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _check(lib.kda_rms_norm_bwd(ctypes.byref(a), _stream(stream)), "kda_rms_norm_bwd")
+    return dx, dweight
+
+
+def kda_fp8_quantize(x, kinds=("row",), *, stream=None):
+    """Quantises ``x`` [rows, cols] (bf16 or fp32) to e4m3 with power-of-two
+    scales, once for each of ``kinds`` ("row", "col", "tile") from one read of
+    x.  Returns a tuple of :class:`Fp8Matrix` in the order of ``kinds``.  See
+    ``kda_fp8_quantize`` in include/kda.h."""
+    lib = load_library()
+    if isinstance(kinds, str):
+        kinds = (kinds,)
+    if not kinds or len(set(kinds)) != len(kinds) or set(kinds) - {"row", "col", "tile"}:
+        raise ValueError('kinds are "row", "col" and "tile", each once')
+    if x.dim() != 2:
+        raise ValueError("x is [rows, cols]")
+    _contig(x)
+    _on_device(x)
+    rows, cols = x.shape
+    parts = {k: _empty_fp8(rows, cols, k, x.device) for k in kinds}
+    a = kda_fp8_quantize_args()
+    a.rows, a.cols, a.dtype, a.x, a.ld = rows, cols, _dtype_code(x), _ptr(x), -(-cols // 16) * 16
+    for k, p in parts.items():
+        setattr(a, k, _ptr(p.data))
+        setattr(a, k + "_scales", _ptr(p.scales))
+    _check(lib.kda_fp8_quantize(ctypes.byref(a), _stream(stream)), "kda_fp8_quantize")
+    return tuple(parts.values())
+
+
+_FP8_FORMS = {"nt": (KDA_FP8_NT, "row", "tile"), "nn": (KDA_FP8_NN, "row", "tile"),
+              "tn": (KDA_FP8_TN, "col", "col")}
+_fp8_status_words = {}
+
+
+def _fp8_status_word(device):
+    """The zeroed error word shared by a device's matmul calls without a
+    ``workspace`` (made by the first of them: before any stream capture)."""
+    if device not in _fp8_status_words:
+        torch = _torch()
+        _fp8_status_words[device] = torch.zeros(KDA_FP8_MATMUL_WORKSPACE_BYTES, dtype=torch.uint8,
+                                                device=device)
+        torch.cuda.current_stream(device).synchronize()
+    return _fp8_status_words[device]
+
+
+def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out=None,
+                   workspace=None, stream=None):
+    """Product of two scaled 8-bit matrices, in the forms of a projection
+    y = x W^T with W [n_out, n_in]:
+      "nt"  a [m, k] row,  b [n, k] tile: the projection (a = x, b = W)
+      "nn"  a [m, k] row,  b [k, n] tile: the input's gradient (a = dy, b = W)
+      "tn"  a [k, m] col,  b [k, n] col:  the weight's gradient (a = dy, b = x)
+    Returns out [m, n] of ``out_dtype`` (bf16 by default, or fp32), or writes
+    ``out`` (rows dense, any pitch).  ``workspace`` (256 zeroed bytes) takes
+    the device error word; without it one per device is shared, read by
+    :func:`kda_fp8_matmul_status`.  See ``kda_fp8_matmul`` in include/kda.h."""
+    torch = _torch()
+    lib = load_library()
+    if form not in _FP8_FORMS:
+        raise ValueError('form is "nt", "nn" or "tn"')
+    code, ka, kb = _FP8_FORMS[form]
+    _check_fp8(a, ka)
+    _check_fp8(b, kb)
+    (k, m) = a.data.shape if form == "tn" else a.data.shape[::-1]
+    (n, k_b) = b.data.shape if form == "nt" else b.data.shape[::-1]
+    if k != k_b:
+        raise ValueError(f"the operands sum over {k} and {k_b}")
+    if out is None:
+        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.data.device)
+    elif tuple(out.shape) != (m, n) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be [{m}, {n}] of out_dtype")
+    p = kda_fp8_matmul_args()
+    p.m, p.n, p.k, p.form = m, n, k, code
+    p.a, p.lda, p.a_scales = _ptr(a.data), _pitch(a.data), _ptr(a.scales)
+    p.b, p.ldb, p.b_scales = _ptr(b.data), _pitch(b.data), _ptr(b.scales)
+    p.out, p.ldo, p.out_dtype = _ptr(out), _pitch(out), _dtype_code(out)
+    _on_device(a.data, a.scales, b.data, b.scales, out, workspace)
+    ws = _fp8_status_word(out.device) if workspace is None else workspace
+    p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _check(lib.kda_fp8_matmul(ctypes.byref(p), _stream(stream)), "kda_fp8_matmul")
+    return out
+
+
+def kda_fp8_matmul_status(stream=None) -> int:
+    """Device status of the matmul calls without a ``workspace`` on the
+    current device (synchronises ``stream``): KDA_OK, or
+    KDA_ERR_DEVICE_TIMEOUT when a bounded device wait gave up since the last
+    read."""
+    torch = _torch()
+    word = _fp8_status_word(torch.device("cuda", torch.cuda.current_device()))
+    return kda_get_device_status(word, stream)

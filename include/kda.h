@@ -476,6 +476,156 @@ kda_status kda_state_grad_scan(const float *M, const float *E, const float *dS_f
                                int32_t num_chains, int32_t num_segments, int32_t H, int32_t dk,
                                int32_t dv, float *dS_out, float *dS_initial, kda_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit projection path around a KDA layer: RMS norm with the residual's
+ * addition, quantiser, and the matrix product of 8-bit operands.
+ *
+ * Scaled 8-bit matrices.  A matrix [R, C] is held as e4m3 values with a row
+ * pitch ld >= C, ld a multiple of 16 (columns C .. ld - 1 are never read or
+ * written), and power-of-two scales, one byte each: byte b stands for
+ * 2^(b - 127), b = 255 for NaN.  The real value is value * scale.  Blocks are
+ * of 128; RB = ceil(R / 128), CB = ceil(C / 128):
+ *   KDA_FP8_ROW   one scale per row and 128 columns; bytes [ceil(CB/4), R, 4]:
+ *                 block j of row r at ((j / 4) * R + r) * 4 + j % 4
+ *   KDA_FP8_COL   one scale per column and 128 rows; bytes [ceil(RB/4), C, 4]
+ *   KDA_FP8_TILE  one scale per 128 x 128 block; bytes [RB, CB]
+ * Bytes of ROW and COL past the last block are written as 127 (1.0).
+ * Quantising takes the smallest e >= -127 with max|x| <= 448 * 2^e over the
+ * block's finite elements (e = 0 for a block of zeros) and rounds x * 2^-e to
+ * the nearest e4m3 value, ties to even; NaN and infinities become NaN (e4m3
+ * has no infinity) and leave their block's scale alone.
+ * ------------------------------------------------------------------------ */
+typedef enum { KDA_FP8_ROW = 1, KDA_FP8_COL = 2, KDA_FP8_TILE = 4 } kda_fp8_kind;
+
+/* Widest row kda_rms_norm and kda_rms_norm_bwd take. */
+#define KDA_RMS_NORM_MAX_COLS 32768
+
+/*
+ * RMS norm of each row, with the residual stream's addition before it and an
+ * 8-bit result after it:
+ *   h = x + residual  (fp32, rounded once to `dtype`: the residual stream as
+ *                      the next layer reads it, and what is normalised here)
+ *   y = h * (mean(h^2) + eps)^-1/2 * weight           (fp32)
+ *   out = y rounded to `dtype`;  fp8 = y quantised with ROW scales (from the
+ *   fp32 y, not from the rounded `out`)
+ * residual NULL: h = x and residual_out is ignored.  weight NULL: ones.
+ * out or fp8 may be NULL (not written), not both.  residual_out may be x or
+ * residual, and out may be x, residual or residual_out's input in place.
+ * rows == 0 launches nothing.  Errors: KDA_ERR_INVALID_ARG (rows < 0, cols <
+ * 1, null x, no output, residual without residual_out, fp8 without
+ * fp8_scales, ld_fp8 < cols), KDA_ERR_UNSUPPORTED (cols >
+ * KDA_RMS_NORM_MAX_COLS, rows > 2^31 - 1), KDA_ERR_ALIGNMENT (a pointer not
+ * 16-byte aligned, ld_fp8 not a multiple of 16), KDA_ERR_CUDA.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t cols;
+  kda_dtype dtype;          /* of x, residual, residual_out and out            */
+  const void *x;            /* [rows, cols]                                    */
+  const void *residual;     /* [rows, cols] or NULL                            */
+  const float *weight;      /* [cols] fp32 or NULL                             */
+  float eps;
+  void *residual_out;       /* [rows, cols], written when residual is given    */
+  void *out;                /* [rows, cols] or NULL                            */
+  void *fp8;                /* [rows, ld_fp8] e4m3 or NULL                     */
+  int64_t ld_fp8;
+  uint8_t *fp8_scales;      /* ROW scales of fp8                               */
+} kda_rms_norm_args;
+
+kda_status kda_rms_norm(const kda_rms_norm_args *args, kda_stream_t stream);
+
+/*
+ * Backward of kda_rms_norm (a quantised output counts as y: the rounding has
+ * gradient one).  h is the tensor that was normalised: residual_out, or x
+ * without a residual.  With n = h * rstd, rstd recomputed from h:
+ *   dx = rstd * (weight * d_out - n * mean(weight * d_out * n)) + d_residual
+ *   dweight = sum over rows of d_out * n
+ * dx is the gradient of x and, the same, of residual; d_residual is the
+ * gradient that reaches residual_out from elsewhere (NULL: zeros).  dx may be
+ * d_out, d_residual or h in place.  dweight NULL: not computed (no workspace
+ * needed).  Deterministic: sums run in a fixed order.  With rows == 0 dweight
+ * is zeros.  Errors as kda_rms_norm, plus KDA_ERR_WORKSPACE.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t cols;
+  kda_dtype dtype;          /* of d_out, h, d_residual and dx                  */
+  const void *d_out;        /* [rows, cols]                                    */
+  const void *h;            /* [rows, cols]                                    */
+  const float *weight;      /* [cols] fp32 or NULL                             */
+  const void *d_residual;   /* [rows, cols] or NULL                            */
+  float eps;
+  void *dx;                 /* [rows, cols]                                    */
+  float *dweight;           /* [cols] fp32 or NULL                             */
+  void *workspace;          /* kda_rms_norm_bwd_workspace_size bytes, 256-byte */
+  size_t workspace_bytes;   /* aligned                                         */
+} kda_rms_norm_bwd_args;
+
+size_t kda_rms_norm_bwd_workspace_size(int64_t rows, int32_t cols);
+kda_status kda_rms_norm_bwd(const kda_rms_norm_bwd_args *args, kda_stream_t stream);
+
+/*
+ * Quantises x [rows, cols] once for each kind given, reading it once: the
+ * values and scales of the kinds whose pointer is not NULL are written, each
+ * [rows, ld] in x's own orientation with its own scales.  rows == 0 or cols
+ * == 0 launches nothing.  Errors: KDA_ERR_INVALID_ARG (rows or cols < 0, no
+ * kind, values without scales, null x, ld < cols), KDA_ERR_UNSUPPORTED (more
+ * than 2^31 - 1 blocks), KDA_ERR_ALIGNMENT (pointers, ld % 16), KDA_ERR_CUDA.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t cols;
+  kda_dtype dtype;          /* of x                                            */
+  const void *x;            /* [rows, cols]                                    */
+  int64_t ld;               /* row pitch of the values, all kinds              */
+  void *row, *col, *tile;   /* [rows, ld] e4m3 or NULL                         */
+  uint8_t *row_scales, *col_scales, *tile_scales;
+} kda_fp8_quantize_args;
+
+kda_status kda_fp8_quantize(const kda_fp8_quantize_args *args, kda_stream_t stream);
+
+/*
+ * The matrix product of two scaled 8-bit matrices, in the three forms of a
+ * projection y = x W^T with W [n_out, n_in]:
+ *   KDA_FP8_NT  out[m, n] = sum_k a[m, k] b[n, k]   a ROW [m, k], b TILE [n, k]
+ *               the projection: a = x, b = W
+ *   KDA_FP8_NN  out[m, n] = sum_k a[m, k] b[k, n]   a ROW [m, k], b TILE [k, n]
+ *               the input's gradient: a = dy, b = W (as it is stored)
+ *   KDA_FP8_TN  out[m, n] = sum_k a[k, m] b[k, n]   a COL [k, m], b COL [k, n]
+ *               the weight's gradient: a = dy, b = x, k the tokens
+ * Products are exact, sums are held in fp32, out is rounded once to
+ * out_dtype.  Deterministic.  k == 0 writes zeros; m == 0 or n == 0 launches
+ * nothing.  The workspace holds only the device error word: it must be zero
+ * before the first call that uses it; a bounded device wait that gave up sets
+ * it (the call's output is then undefined) and kda_get_device_status reads
+ * and clears it.
+ * Errors: KDA_ERR_INVALID_ARG (sizes < 0, bad form or dtype, null pointers,
+ * a pitch smaller than its row), KDA_ERR_UNSUPPORTED (more than 2^31 - 1
+ * output tiles, a pitch of 2^31 bytes or more), KDA_ERR_ALIGNMENT (a, b or
+ * scales not 16-byte aligned, lda or ldb not a multiple of 16, out not
+ * aligned to its element), KDA_ERR_WORKSPACE, KDA_ERR_CUDA.
+ */
+typedef enum { KDA_FP8_NT = 0, KDA_FP8_NN = 1, KDA_FP8_TN = 2 } kda_fp8_form;
+
+typedef struct {
+  int32_t m, n, k;
+  kda_fp8_form form;
+  const void *a;            /* e4m3, pitch lda                                 */
+  int64_t lda;
+  const uint8_t *a_scales;
+  const void *b;            /* e4m3, pitch ldb                                 */
+  int64_t ldb;
+  const uint8_t *b_scales;
+  void *out;                /* [m, ldo] of out_dtype, columns 0 .. n-1 written */
+  int64_t ldo;
+  kda_dtype out_dtype;
+  void *workspace;          /* KDA_FP8_MATMUL_WORKSPACE_BYTES, 256-byte aligned */
+  size_t workspace_bytes;
+} kda_fp8_matmul_args;
+
+#define KDA_FP8_MATMUL_WORKSPACE_BYTES 256u
+kda_status kda_fp8_matmul(const kda_fp8_matmul_args *args, kda_stream_t stream);
+
 /* Reads and clears the device error word kept at the start of a forward or
  * summary workspace: synchronises the stream, returns KDA_OK or
  * KDA_ERR_DEVICE_TIMEOUT when a bounded device-side wait gave up.  Every
