@@ -132,6 +132,7 @@ class kda_fp8_matmul_args(ctypes.Structure):
         ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("b_scales", ctypes.c_void_p),
         ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("out_dtype", ctypes.c_int),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("flags", ctypes.c_uint32),
     ]
 
 
@@ -980,7 +981,7 @@ def _fp8_status_word(device):
 
 
 def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out=None,
-                   workspace=None, stream=None):
+                   workspace=None, extra_flags=0, stream=None):
     """Product of two scaled 8-bit matrices, in the forms of a projection
     y = x W^T with W [n_out, n_in]:
       "nt"  a [m, k] row,  b [n, k] tile: the projection (a = x, b = W)
@@ -1013,6 +1014,7 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
     _on_device(a.data, a.scales, b.data, b.scales, out, workspace)
     ws = _fp8_status_word(out.device) if workspace is None else workspace
     p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    p.flags = extra_flags
     _check(lib.kda_fp8_matmul(ctypes.byref(p), _stream(stream)), "kda_fp8_matmul")
     return out
 

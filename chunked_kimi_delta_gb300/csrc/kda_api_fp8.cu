@@ -68,6 +68,7 @@ kda_status kda_fp8_quantize(const kda_fp8_quantize_args *a, kda_stream_t stream)
 kda_status kda_fp8_matmul(const kda_fp8_matmul_args *a, kda_stream_t stream) {
   if (!a || a->m < 0 || a->n < 0 || a->k < 0 || bad_dtype(a->out_dtype)) return KDA_ERR_INVALID_ARG;
   if (a->form != KDA_FP8_NT && a->form != KDA_FP8_NN && a->form != KDA_FP8_TN) return KDA_ERR_INVALID_ARG;
+  if (a->flags & ~KDA_TEST_WAIT_TIMEOUT) return KDA_ERR_INVALID_ARG;
   if (a->m == 0 || a->n == 0) return KDA_OK;
   const int64_t es = a->out_dtype == KDA_F32 ? 4 : 2;
   if (!a->out || a->ldo < a->n) return KDA_ERR_INVALID_ARG;

@@ -599,8 +599,8 @@ kda_status kda_fp8_quantize(const kda_fp8_quantize_args *args, kda_stream_t stre
  * before the first call that uses it; a bounded device wait that gave up sets
  * it (the call's output is then undefined) and kda_get_device_status reads
  * and clears it.
- * Errors: KDA_ERR_INVALID_ARG (sizes < 0, bad form or dtype, null pointers,
- * a pitch smaller than its row), KDA_ERR_UNSUPPORTED (more than 2^31 - 1
+ * Errors: KDA_ERR_INVALID_ARG (sizes < 0, bad form or dtype, unknown flags,
+ * null pointers, a pitch smaller than its row), KDA_ERR_UNSUPPORTED (more than 2^31 - 1
  * output tiles, a pitch of 2^31 bytes or more), KDA_ERR_ALIGNMENT (a, b or
  * scales not 16-byte aligned, lda or ldb not a multiple of 16, out not
  * aligned to its element), KDA_ERR_WORKSPACE, KDA_ERR_CUDA.
@@ -621,6 +621,8 @@ typedef struct {
   kda_dtype out_dtype;
   void *workspace;          /* KDA_FP8_MATMUL_WORKSPACE_BYTES, 256-byte aligned */
   size_t workspace_bytes;
+  uint32_t flags;           /* 0; tests: KDA_TEST_WAIT_TIMEOUT (a bounded wait */
+                            /* in the kernel runs out, as in kda_chunk_fwd)    */
 } kda_fp8_matmul_args;
 
 #define KDA_FP8_MATMUL_WORKSPACE_BYTES 256u

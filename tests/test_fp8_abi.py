@@ -86,7 +86,7 @@ def test_quantize_refusals(lib, kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(m=-1), INVALID), (dict(n=-1), INVALID), (dict(k=-1), INVALID), (dict(form=3), INVALID),
-    (dict(out_dtype=5), INVALID), (dict(a=None), INVALID), (dict(b_scales=None), INVALID), (dict(out=None), INVALID),
+    (dict(out_dtype=5), INVALID), (dict(flags=1), INVALID), (dict(a=None), INVALID), (dict(b_scales=None), INVALID), (dict(out=None), INVALID),
     (dict(ldo=99), INVALID), (dict(lda=192), INVALID), (dict(form=kda.KDA_FP8_NN, ldb=96), INVALID),
     (dict(form=kda.KDA_FP8_TN, lda=0), INVALID), (dict(lda=201), ALIGNMENT), (dict(ldb=216), ALIGNMENT),
     (dict(a=BASE + 8), ALIGNMENT), (dict(out=BASE + 1), ALIGNMENT), (dict(out_dtype=kda.KDA_F32, out=BASE + 2), ALIGNMENT),

@@ -330,3 +330,17 @@ def test_matmul_in_a_graph(cuda_lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 512, 2048), (2500, 2600, 272)])
+def test_matmul_wait_that_runs_out_is_reported(cuda_lib, m, n, k):
+    """Both kernels (k split over a cluster; pairs of CTAs) end in bounded
+    time, report it, and the next call is right."""
+    a, b = _operands(cuda_lib, "nt", m, n, k, 90, lambda s, seed: _rand(s, torch.float32, seed))
+    want = cuda_lib.kda_fp8_matmul(a, b)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    cuda_lib.kda_fp8_matmul(a, b, workspace=ws, extra_flags=cuda_lib.KDA_TEST_WAIT_TIMEOUT)
+    assert cuda_lib.kda_get_device_status(ws) == cuda_lib.KDA_ERR_DEVICE_TIMEOUT
+    assert cuda_lib.kda_get_device_status(ws) == cuda_lib.KDA_OK
+    assert torch.equal(cuda_lib.kda_fp8_matmul(a, b, workspace=ws), want)
+    assert cuda_lib.kda_get_device_status(ws) == cuda_lib.KDA_OK
