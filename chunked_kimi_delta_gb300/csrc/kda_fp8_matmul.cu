@@ -15,11 +15,16 @@
 // of k: K-major where k is contiguous, MN-major where it is not, so no form
 // needs a transposed copy.  Edges are zeros from TMA.
 //
-// Scales.  Stored words (four blocks of k of one row) are what a column of
-// tensor memory holds: word of row r at lane r % 32, column r / 32, the same
-// in all four lane quarters.  Four warps load them from global memory and
-// store them to tensor memory (tcgen05.st), each its lane quarter, a ring of
-// words ahead of the MMAs.
+// Scales.  A stored word (four blocks of k of one row) is what a lane and
+// column of tensor memory hold: the word of row r at lane r % 32, column
+// r / 32, the same in all four lane quarters.  One warp brings the words into
+// a ring in shared memory as [32 lanes][4 columns] (cp.async, four bytes a
+// lane: rows need no alignment), and the thread that issues the MMAs copies
+// an entry to tensor memory ahead of them (tcgen05.cp, which orders itself
+// before the MMAs and repeats the entry for the four quarters).  Storing the
+// words to tensor memory from registers instead (tcgen05.st by four warps)
+// took 2,400 cycles a word against the 1,800 of its MMAs: 2.9 PFLOP/s at
+// 32768 x 4096 x 4096 where this reaches 3.5 PFLOP/s.
 #include <cuda_bf16.h>
 
 #include "kda_fp8.cuh"
@@ -32,6 +37,8 @@ using tcp::globaltimer;
 
 constexpr int SF_COLS = 16;       // tensor-memory columns of one ring entry: 4 lane side, 8 column side
 constexpr int SF_RING = 4;
+constexpr uint32_t SF_ENTRY = 1536;  // bytes of an entry in shared memory: 512 lane side, 2 x 512 column side
+constexpr uint32_t SF_BYTES = SF_RING * SF_ENTRY;
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t LANE_BYTES = 16384;  // lane-side box: 128 x 128 bytes
 
@@ -55,11 +62,32 @@ struct MmArgs {
 struct Bars {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t sf_full[SF_RING], sf_empty[SF_RING];
+  uint64_t sf_peer[SF_RING];  // pairs, first CTA: the entry is in the second CTA's shared memory too
   uint64_t acc_full[2], acc_empty[2];
   uint64_t never;
   uint32_t tmem;
   volatile uint32_t abort;
 };
+
+// Position in a ring of barriers, without divisions: the threads that feed the
+// tensor core go round it every few hundred cycles.
+struct Ring {
+  int size, s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int n) : size(n) {}
+  __device__ __forceinline__ void next() {
+    if (++s == size) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 
 // ---- cluster helpers
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -170,70 +198,77 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
-               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-               :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // ---- scales
-constexpr uint32_t WORD_ONE = FP8_SCALE_ONE * 0x01010101u;
-
-__device__ __forceinline__ uint32_t scale_word(const uint8_t *s, int64_t rows, int64_t row, int w) {
-  return row < rows ? __ldg(reinterpret_cast<const uint32_t *>(s) + w * rows + row) : WORD_ONE;
+// Rows past the edge take the last row's scale: it only reaches outputs that
+// are not stored.
+__device__ __forceinline__ void copy_word(uint32_t smem, const uint8_t *s, int rows, int row, int w) {
+  const uint32_t *p = reinterpret_cast<const uint32_t *>(s) + ((int64_t)w * rows + min(row, rows - 1));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem), "l"(p) : "memory");
 }
-// The four blocks of k of word w for the 128 lane-side rows from l0 on.
-__device__ __forceinline__ uint32_t tile_word(const MmArgs &a, int l0, int w) {
-  uint32_t word = WORD_ONE;
-  if (l0 < a.lanes) {
-    word = 0;
-    const uint8_t *p = a.lane_scales + (l0 / FP8_BLOCK) * a.tile_i;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int kb = 4 * w + j;
-      word |= (kb < a.kblocks ? (uint32_t)__ldg(p + kb * a.tile_k) : FP8_SCALE_ONE) << (8 * j);
-    }
-  }
-  return word;
+// TILE scales of the lane side, one byte for all 128 lanes: lane i holds the
+// byte of block 32 g + i, loaded one group of eight words ahead of its use.
+__device__ __forceinline__ uint32_t tile_bytes(const MmArgs &a, int l0, int g, int lane) {
+  return __ldg(a.lane_scales + (min(l0, a.lanes - 1) / FP8_BLOCK) * a.tile_i +
+               min(32 * g + lane, a.kblocks - 1) * a.tile_k);
 }
-// One ring entry into this warp's lane quarter.
-__device__ __forceinline__ void load_scales(const MmArgs &a, int l0, int c0, int w, int lane, uint32_t (&ls)[4],
-                                            uint32_t (&cs)[8]) {
+// One ring entry, by a full warp: word w of the tile at (l0, c0).  Its
+// barrier counts every lane twice: when its copies have landed, and when its
+// own stores are done.
+__device__ __forceinline__ void fill_scales(const MmArgs &a, uint8_t *entry, uint64_t *bar, int l0, int c0, int w,
+                                            uint32_t bytes, int lane) {
+  const uint32_t dst = tc::smem_u32(entry) + 16 * lane;
   if (a.tile_i) {
-    ls[0] = ls[1] = ls[2] = ls[3] = tile_word(a, l0, w);
+    uint32_t v = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v |= __shfl_sync(~0u, bytes, 4 * (w & 7) + j) << (8 * j);
+    *reinterpret_cast<uint4 *>(entry + 16 * lane) = make_uint4(v, v, v, v);
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) ls[c] = scale_word(a.lane_scales, a.lanes, (int64_t)l0 + 32 * c + lane, w);
+    for (int c = 0; c < 4; ++c) copy_word(dst + 4 * c, a.lane_scales, a.lanes, l0 + 32 * c + lane, w);
   }
 #pragma unroll
   for (int c = 0; c < 8; ++c)
-    cs[c] = 32 * c < a.width ? scale_word(a.col_scales, a.cols, (int64_t)c0 + 32 * c + lane, w) : WORD_ONE;
+    if (32 * c < a.width) copy_word(dst + 512 + 512 * (c >> 2) + 4 * (c & 3), a.col_scales, a.cols, c0 + 32 * c + lane, w);
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(tc::smem_u32(bar)) : "memory");
+  tc::mbar_arrive(bar);
 }
-__device__ __forceinline__ void store_scales(uint32_t tmem_sf, int quarter, const uint32_t (&ls)[4], const uint32_t (&cs)[8]) {
-  const uint32_t t = tmem_sf + ((uint32_t)(32 * quarter) << 16);
-  tmem_st4(t, ls);
-  tmem_st8(t + 4, cs);
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-  tc::tc_fence_before();
+// An entry from shared to tensor memory (in both CTAs of a pair, each from
+// its own), by the thread that issues the MMAs.  No swizzle, groups of eight
+// 16-byte rows 128 bytes apart.
+template <bool PAIR> __device__ __forceinline__ void copy_scales(uint32_t tmem_sf, uint32_t entry, int width) {
+  const uint64_t desc = (uint64_t)((entry & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (i == 2 && width <= 128) break;
+    if (PAIR)
+      asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem_sf + 4 * i), "l"(desc + 32 * i) : "memory");
+    else
+      asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem_sf + 4 * i), "l"(desc + 32 * i) : "memory");
+  }
 }
 
-// The four MMAs of one block of k.
-template <bool PAIR>
-__device__ __forceinline__ void mma_block(const MmArgs &a, uint32_t acc, uint32_t stage_addr, uint32_t sf, int kb,
-                                          bool first) {
-  const uint64_t ld = a.lane_mn ? tc::smem_desc_sw128(stage_addr, 16384, 1024) : tc::smem_desc_sw128(stage_addr, 16, 1024);
-  const uint64_t cd = a.col_mn ? tc::smem_desc_sw128(stage_addr + LANE_BYTES, 16384, 1024)
-                               : tc::smem_desc_sw128(stage_addr + LANE_BYTES, 16, 1024);
-  const uint32_t idesc = a.idesc | (uint32_t)(kb & 3) << 4 | (uint32_t)(kb & 3) << 29;  // byte of the scale words
+// The MMAs of a block of k: descriptors of stage 0, and what a stage and 32
+// of k add to them.
+struct MmaIssue {
+  uint64_t lane0, col0;
+  uint32_t lane_step, col_step, stage_step, idesc;
+  __device__ __forceinline__ MmaIssue(const MmArgs &a, const uint8_t *sm)
+      : lane_step(a.lane_step), col_step(a.col_step), stage_step(a.stage_bytes >> 4), idesc(a.idesc) {
+    const uint32_t s = tc::smem_u32(sm);
+    lane0 = tc::smem_desc_sw128(s, a.lane_mn ? 16384 : 16, 1024);
+    col0 = tc::smem_desc_sw128(s + LANE_BYTES, a.col_mn ? 16384 : 16, 1024);
+  }
+  // `byte`: the block's byte of the scale words; `first`: overwrites the accumulator
+  template <bool PAIR>
+  __device__ __forceinline__ void block(uint32_t acc, int stage, uint32_t sf, int byte, bool first) const {
+    const uint64_t l = lane0 + (uint64_t)(stage * stage_step), c = col0 + (uint64_t)(stage * stage_step);
+    const uint32_t id = idesc | (uint32_t)byte << 4 | (uint32_t)byte << 29;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    mma_scaled<PAIR>(acc, ld + (uint64_t)(j * a.lane_step), cd + (uint64_t)(j * a.col_step), idesc, sf, sf + 4,
-                     !(first && j == 0));
-}
+    for (int j = 0; j < 4; ++j)
+      mma_scaled<PAIR>(acc, l + (uint64_t)(j * lane_step), c + (uint64_t)(j * col_step), id, sf, sf + 4,
+                       j != 0 || !first);
+  }
+};
 
 // 32 accumulator columns (rows m from m0 on, below `end`) of this warp's lanes (columns n).
 template <typename T>
@@ -245,12 +280,12 @@ __device__ __forceinline__ void store_columns(const MmArgs &a, const uint32_t (&
     if (m0 + c < end) p[c * a.ldo] = from_f32<T>(__uint_as_float(r[c]));
 }
 
-// The last arrivals of MMA commits on a ring of `size` barriers used `count`
-// times: a CTA leaves only when none is still to come.
-__device__ __forceinline__ void ring_drain(uint64_t *ring, int size, int count, Bars *b, uint32_t *err,
-                                           uint32_t cluster_ctas) {
-  for (int i = count > size ? count - size : 0; i < count; ++i)
-    if (!mm_wait(ring + i % size, (i / size) & 1, b, err, cluster_ctas)) return;
+// The last arrivals of MMA commits on a ring: a CTA leaves only when none is
+// still to come.  Every slot's latest use, oldest first; a slot never used
+// (fewer uses than slots) answers at once, as in a producer's first round.
+__device__ __forceinline__ void ring_drain(uint64_t *bars, Ring r, Bars *b, uint32_t *err, uint32_t cluster_ctas) {
+  for (int i = 0; i < r.size; ++i, r.next())
+    if (!mm_wait(bars + r.s, r.phase ^ 1, b, err, cluster_ctas)) return;
 }
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -269,8 +304,8 @@ __device__ __forceinline__ void settle() {
 // Persistent CTA pairs: 256 columns n x width rows m per tile, one pair-wide
 // MMA (cta_group::2) on each CTA's 128 lanes and half of the column side.
 // Two accumulators: the epilogue of a tile runs under the next one's MMAs.
-// Warps 0-3 scales, 4-11 epilogue, 12 TMA, 13 MMA (first CTA of the pair).
-constexpr int PAIR_THREADS = 448;
+// Warps 0-7 epilogue, 8 scales, 9 TMA, 10 MMA (first CTA of the pair).
+constexpr int PAIR_THREADS = 352;
 constexpr int PAIR_MAX_WIDTH = 224;  // two accumulators and the scale ring fill the 512 columns
 constexpr uint32_t PAIR_SF = 2 * PAIR_MAX_WIDTH;
 
@@ -291,7 +326,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
       tc::mbar_init(b.empty + i, 1);
     }
     for (int i = 0; i < SF_RING; ++i) {
-      tc::mbar_init(b.sf_full + i, 8);   // four warps of each CTA
+      tc::mbar_init(b.sf_full + i, 64);
+      tc::mbar_init(b.sf_peer + i, 1);
       tc::mbar_init(b.sf_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -312,32 +348,38 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
   auto lane0_of = [&](int t) { return (t % a.lane_tiles) * 256 + (int)rank * 128; };  // this CTA's first n
   auto col0_of = [&](int t) { return (t / a.lane_tiles) * a.width; };                 // the tile's first m
 
-  if (warp < 4) {  // scales
-    int it = 0;
+  uint8_t *sf_ring = sm + a.stages * a.stage_bytes;
+  if (warp == 8) {  // scales
+    Ring f(SF_RING);
     bool ok = true;
+    const int words = (a.kblocks + 3) / 4;
+    uint32_t next = a.tile_i && pair < a.tiles ? tile_bytes(a, lane0_of(pair), 0, lane) : 0, bytes = 0;
     for (int t = pair; t < a.tiles && ok; t += pairs) {
-      for (int w = 0; w < (a.kblocks + 3) / 4; ++w, ++it) {
-        uint32_t ls[4], cs[8];
-        load_scales(a, lane0_of(t), col0_of(t), w, lane, ls, cs);
-        const int e = it % SF_RING;
-        ok = __all_sync(~0u, mm_wait(b.sf_empty + e, ((it / SF_RING) & 1) ^ 1, &b, a.err, 2));
+      const int l0 = lane0_of(t), c0 = col0_of(t);
+      for (int w = 0; w < words; ++w, f.next()) {
+        if (a.tile_i && (w & 7) == 0) {
+          bytes = next;
+          if (w + 8 < words) next = tile_bytes(a, l0, (w >> 3) + 1, lane);
+          else if (t + pairs < a.tiles) next = tile_bytes(a, lane0_of(t + pairs), 0, lane);
+        }
+        ok = __all_sync(~0u, mm_wait(b.sf_empty + f.s, f.phase ^ 1, &b, a.err, 2));
         if (!ok) break;
-        store_scales(tmem + PAIR_SF + e * SF_COLS, warp, ls, cs);
-        if (lane == 0) arrive_remote(peer_addr(b.sf_full + e, 0));
+        fill_scales(a, sf_ring + f.s * SF_ENTRY, b.sf_full + f.s, l0, c0, w, bytes, lane);
       }
     }
-    if (ok) ring_drain(b.sf_empty, SF_RING, it, &b, a.err, 2);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (ok) ring_drain(b.sf_empty, f, &b, a.err, 2);
     __syncwarp();
-  } else if (warp < 12) {  // epilogue
-    int it = 0;
-    for (int t = pair; t < a.tiles; t += pairs, ++it) {
-      const int buf = it & 1;
-      if (!__all_sync(~0u, mm_wait(b.acc_full + buf, (it >> 1) & 1, &b, a.err, 2))) break;
+  } else if (warp < 8) {  // epilogue
+    Ring full(2);
+    for (int t = pair; t < a.tiles; t += pairs, full.next()) {
+      const int buf = full.s;
+      if (!__all_sync(~0u, mm_wait(b.acc_full + buf, full.phase, &b, a.err, 2))) break;
       tc::tc_fence_after();
       const int n = lane0_of(t) + 32 * (warp & 3) + lane;
       const uint32_t acc = tmem + buf * PAIR_MAX_WIDTH + ((uint32_t)(32 * (warp & 3)) << 16);
       const int chunks = a.width / 32;
-      for (int ch = (warp - 4) >> 2; ch < chunks; ch += 2) {
+      for (int ch = warp >> 2; ch < chunks; ch += 2) {
         uint32_t r[32];
         tmem_ld32(acc + 32 * ch, r);
         tc::tmem_ld_wait();
@@ -347,55 +389,71 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
       if (lane == 0) arrive_remote(peer_addr(b.acc_empty + buf, 0));
       __syncwarp();
     }
-  } else if (warp == 12) {  // TMA
-    if (lane == 0) {
-      int it = 0;
+  } else if (warp == 9) {  // TMA
+    if (elect_one()) {
+      Ring r(a.stages);
       bool ok = true;
+      const uint32_t full0 = peer_addr(b.full, 0);
+      const uint32_t bytes = 2 * (LANE_BYTES + a.col_box_bytes);
       for (int t = pair; t < a.tiles && ok; t += pairs) {
         const int l0 = lane0_of(t), c0 = col0_of(t) + (int)rank * (a.width / 2);
-        for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-          const int s = it % a.stages;
-          ok = mm_wait(b.empty + s, ((it / a.stages) & 1) ^ 1, &b, a.err, 2);
+        for (int k0 = 0; k0 < a.kblocks * FP8_BLOCK; k0 += FP8_BLOCK) {
+          ok = mm_wait(b.empty + r.s, r.phase ^ 1, &b, a.err, 2);
           if (!ok) break;
-          if (rank == 0) tc::mbar_arrive_expect_tx(b.full + s, 2 * (LANE_BYTES + a.col_box_bytes));
-          const uint32_t bar = peer_addr(b.full + s, 0);
-          uint8_t *dst = sm + s * a.stage_bytes;
-          const int k0 = kb * FP8_BLOCK;
+          if (rank == 0) tc::mbar_arrive_expect_tx(b.full + r.s, bytes);
+          const uint32_t bar = full0 + 8 * r.s;
+          uint8_t *dst = sm + r.s * a.stage_bytes;
           tma_load_pair(dst, &lane_map, bar, a.lane_mn ? l0 : k0, a.lane_mn ? k0 : l0);
           tma_load_pair(dst + LANE_BYTES, &col_map, bar, a.col_mn ? c0 : k0, a.col_mn ? k0 : c0);
+          r.next();
         }
       }
-      if (ok) ring_drain(b.empty, a.stages, it, &b, a.err, 2);
+      if (ok) ring_drain(b.empty, r, &b, a.err, 2);
     }
     __syncwarp();
   } else if (rank == 0) {  // MMA
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = !a.test_wait || mm_wait_slow(&b.never, 0, &b, a.err, 2, 1000000ull);
-      int it = 0, is = 0, ia = 0;
-      for (int t = pair; t < a.tiles && ok; t += pairs, ++ia) {
-        const int buf = ia & 1;
-        ok = mm_wait(b.acc_empty + buf, ((ia >> 1) & 1) ^ 1, &b, a.err, 2);
+      const MmaIssue mma(a, sm);
+      Ring r(a.stages), f(SF_RING), acc(2);
+      for (int t = pair; t < a.tiles && ok; t += pairs, acc.next()) {
+        ok = mm_wait(b.acc_empty + acc.s, acc.phase ^ 1, &b, a.err, 2);
         if (!ok) break;
         tc::tc_fence_after();
-        for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-          const int e = is % SF_RING, s = it % a.stages;
-          if ((kb & 3) == 0) {
-            ok = mm_wait(b.sf_full + e, (is / SF_RING) & 1, &b, a.err, 2);
-            if (!ok) break;
-          }
-          ok = mm_wait(b.full + s, (it / a.stages) & 1, &b, a.err, 2);
+        for (int kb = 0; kb < a.kblocks; kb += 4) {
+          ok = mm_wait(b.sf_full + f.s, f.phase, &b, a.err, 2) && mm_wait(b.sf_peer + f.s, f.phase, &b, a.err, 2);
           if (!ok) break;
-          tc::tc_fence_after();
-          mma_block<true>(a, tmem + buf * PAIR_MAX_WIDTH, tc::smem_u32(sm + s * a.stage_bytes),
-                          tmem + PAIR_SF + e * SF_COLS, kb, kb == 0);
-          mm_commit<true>(b.empty + s);
-          if ((kb & 3) == 3 || kb == a.kblocks - 1) {
-            mm_commit<true>(b.sf_empty + e);
-            ++is;
+          tc::fence_proxy_async_smem();
+          copy_scales<true>(tmem + PAIR_SF + f.s * SF_COLS, tc::smem_u32(sf_ring) + f.s * SF_ENTRY, a.width);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (kb + i >= a.kblocks) break;
+            ok = mm_wait(b.full + r.s, r.phase, &b, a.err, 2);
+            if (!ok) break;
+            tc::tc_fence_after();
+            mma.block<true>(tmem + acc.s * PAIR_MAX_WIDTH, r.s, tmem + PAIR_SF + f.s * SF_COLS, i, kb + i == 0);
+            mm_commit<true>(b.empty + r.s);
+            r.next();
           }
+          if (!ok) break;
+          mm_commit<true>(b.sf_empty + f.s);
+          f.next();
         }
-        if (ok) mm_commit<true>(b.acc_full + buf);
+        if (ok) mm_commit<true>(b.acc_full + acc.s);
       }
+    }
+    __syncwarp();
+  } else {  // tells the first CTA which entries of scales have landed here
+    if (elect_one()) {
+      Ring f(SF_RING);
+      bool ok = true;
+      for (int t = pair; t < a.tiles && ok; t += pairs)
+        for (int w = 0; w < (a.kblocks + 3) / 4; ++w, f.next()) {
+          ok = mm_wait(b.sf_full + f.s, f.phase, &b, a.err, 2);
+          if (!ok) break;
+          tc::fence_proxy_async_smem();
+          arrive_remote(peer_addr(b.sf_peer + f.s, 0));
+        }
     }
     __syncwarp();
   }
@@ -411,8 +469,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
 // One tile of 128 columns n x width rows m for a cluster of `splits` CTAs,
 // each with its own range of k; the partial sums meet through distributed
 // shared memory and are added in the order of k.
-// Warps 0-3 scales, then epilogue; 4 TMA, 5 MMA.
-constexpr int SPLIT_THREADS = 192;
+// Warps 0-3 epilogue, 4 scales, 5 TMA, 6 MMA.
+constexpr int SPLIT_THREADS = 224;
 constexpr int SPLIT_MAX_WIDTH = 128;
 constexpr uint32_t SPLIT_TMEM = 256;  // two CTAs fit an SM
 
@@ -435,7 +493,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
       tc::mbar_init(b.empty + i, 1);
     }
     for (int i = 0; i < SF_RING; ++i) {
-      tc::mbar_init(b.sf_full + i, 4);
+      tc::mbar_init(b.sf_full + i, 64);
       tc::mbar_init(b.sf_empty + i, 1);
     }
     tc::mbar_init(b.acc_full, 1);
@@ -450,21 +508,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
   tc::tc_fence_after();
   const uint32_t tmem = b.tmem, tmem_sf = tmem + SPLIT_MAX_WIDTH;
 
+  uint8_t *sf_ring = sm + a.stages * a.stage_bytes;
   if (warp < 4) {
-    bool ok = true;
-    int it = 0;
-    for (int w = kb0 >> 2; 4 * w < kb1; ++w, ++it) {
-      uint32_t ls[4], cs[8];
-      load_scales(a, l0, c0, w, lane, ls, cs);
-      const int e = it % SF_RING;
-      ok = __all_sync(~0u, mm_wait(b.sf_empty + e, ((it / SF_RING) & 1) ^ 1, &b, a.err, splits));
-      if (!ok) break;
-      store_scales(tmem_sf + e * SF_COLS, warp, ls, cs);
-      if (lane == 0) tc::mbar_arrive(b.sf_full + e);
-    }
-    if (ok) ring_drain(b.sf_empty, SF_RING, it, &b, a.err, splits);
-    __syncwarp();
-    ok = ok && __all_sync(~0u, mm_wait(b.acc_full, 0, &b, a.err, splits));
+    const bool ok = __all_sync(~0u, mm_wait(b.acc_full, 0, &b, a.err, splits));
     tc::tc_fence_after();
     const int n = l0 + 32 * warp + lane;
     float *part = reinterpret_cast<float *>(sm);  // [columns][128]: the stages are free now
@@ -484,39 +530,54 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
       }
     tc::tc_fence_before();
   } else if (warp == 4) {
-    if (lane == 0) {
+    Ring f(SF_RING);
+    bool ok = true;
+    uint32_t bytes = 0;
+    for (int w = kb0 >> 2; 4 * w < kb1; ++w, f.next()) {
+      if (a.tile_i && ((w & 7) == 0 || w == kb0 >> 2)) bytes = tile_bytes(a, l0, w >> 3, lane);
+      ok = __all_sync(~0u, mm_wait(b.sf_empty + f.s, f.phase ^ 1, &b, a.err, splits));
+      if (!ok) break;
+      fill_scales(a, sf_ring + f.s * SF_ENTRY, b.sf_full + f.s, l0, c0, w, bytes, lane);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (ok) ring_drain(b.sf_empty, f, &b, a.err, splits);
+    __syncwarp();
+  } else if (warp == 5) {
+    if (elect_one()) {
+      Ring r(a.stages);
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int it = kb - kb0, s = it % a.stages;
-        ok = mm_wait(b.empty + s, ((it / a.stages) & 1) ^ 1, &b, a.err, splits);
+      for (int kb = kb0; kb < kb1; ++kb, r.next()) {
+        ok = mm_wait(b.empty + r.s, r.phase ^ 1, &b, a.err, splits);
         if (!ok) break;
-        tc::mbar_arrive_expect_tx(b.full + s, LANE_BYTES + a.col_box_bytes);
-        uint8_t *dst = sm + s * a.stage_bytes;
+        tc::mbar_arrive_expect_tx(b.full + r.s, LANE_BYTES + a.col_box_bytes);
+        uint8_t *dst = sm + r.s * a.stage_bytes;
         const int k0 = kb * FP8_BLOCK;
-        tc::tma_load_2d(dst, &lane_map, b.full + s, a.lane_mn ? l0 : k0, a.lane_mn ? k0 : l0);
-        tc::tma_load_2d(dst + LANE_BYTES, &col_map, b.full + s, a.col_mn ? c0 : k0, a.col_mn ? k0 : c0);
+        tc::tma_load_2d(dst, &lane_map, b.full + r.s, a.lane_mn ? l0 : k0, a.lane_mn ? k0 : l0);
+        tc::tma_load_2d(dst + LANE_BYTES, &col_map, b.full + r.s, a.col_mn ? c0 : k0, a.col_mn ? k0 : c0);
       }
-      if (ok) ring_drain(b.empty, a.stages, kb1 - kb0, &b, a.err, splits);
+      if (ok) ring_drain(b.empty, r, &b, a.err, splits);
     }
     __syncwarp();
   } else {
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = !a.test_wait || mm_wait_slow(&b.never, 0, &b, a.err, splits, 1000000ull);
-      int is = 0;
-      for (int kb = kb0; kb < kb1 && ok; ++kb) {
-        const int it = kb - kb0, s = it % a.stages, e = is % SF_RING;
+      const MmaIssue mma(a, sm);
+      Ring r(a.stages), f(SF_RING);
+      for (int kb = kb0; kb < kb1 && ok; ++kb, r.next()) {
         if (kb == kb0 || (kb & 3) == 0) {
-          ok = mm_wait(b.sf_full + e, (is / SF_RING) & 1, &b, a.err, splits);
+          ok = mm_wait(b.sf_full + f.s, f.phase, &b, a.err, splits);
           if (!ok) break;
+          tc::fence_proxy_async_smem();
+          copy_scales<false>(tmem_sf + f.s * SF_COLS, tc::smem_u32(sf_ring) + f.s * SF_ENTRY, a.width);
         }
-        ok = mm_wait(b.full + s, (it / a.stages) & 1, &b, a.err, splits);
+        ok = mm_wait(b.full + r.s, r.phase, &b, a.err, splits);
         if (!ok) break;
         tc::tc_fence_after();
-        mma_block<false>(a, tmem, tc::smem_u32(sm + s * a.stage_bytes), tmem_sf + e * SF_COLS, kb, kb == kb0);
-        mm_commit<false>(b.empty + s);
+        mma.block<false>(tmem, r.s, tmem_sf + f.s * SF_COLS, kb & 3, kb == kb0);
+        mm_commit<false>(b.empty + r.s);
         if ((kb & 3) == 3 || kb == kb1 - 1) {
-          mm_commit<false>(b.sf_empty + e);
-          ++is;
+          mm_commit<false>(b.sf_empty + f.s);
+          f.next();
         }
       }
       if (ok) mm_commit<false>(b.acc_full);
@@ -561,7 +622,7 @@ constexpr uint32_t SMEM_LIMIT = 227 * 1024 - 1024 - sizeof(Bars);  // dynamic, a
 template <typename T>
 cudaError_t launch_pair(const CUtensorMap &lm, const CUtensorMap &cm, const MmArgs &a, cudaStream_t st) {
   auto kern = fp8_matmul_pair_kernel<T>;
-  const int smem = (int)(a.stages * a.stage_bytes + 1024);
+  const int smem = (int)(a.stages * a.stage_bytes + SF_BYTES + 1024);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -581,7 +642,7 @@ cudaError_t launch_pair(const CUtensorMap &lm, const CUtensorMap &cm, const MmAr
 template <typename T>
 cudaError_t launch_split(const CUtensorMap &lm, const CUtensorMap &cm, const MmArgs &a, cudaStream_t st) {
   auto kern = fp8_matmul_split_kernel<T>;
-  int smem = (int)(a.stages * a.stage_bytes + 1024);
+  int smem = (int)(a.stages * a.stage_bytes + SF_BYTES + 1024);
   if (smem < 80 * 1024) smem = 80 * 1024;  // two CTAs an SM at most: that is what tensor memory holds
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -643,7 +704,7 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   }
   const int per_cta = ceil_div(a.kblocks, a.splits);
   // pairs have the SM to themselves; split CTAs share it two by two
-  const uint32_t budget = pair ? SMEM_LIMIT : (SMEM_LIMIT - 1024 - (uint32_t)sizeof(Bars)) / 2 - 1024;
+  const uint32_t budget = pair ? SMEM_LIMIT - SF_BYTES : (SMEM_LIMIT - 1024 - (uint32_t)sizeof(Bars)) / 2 - 1024 - SF_BYTES;
   a.stages = (int)(budget / a.stage_bytes);
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
   if (!pair && a.stages > per_cta) a.stages = per_cta;
