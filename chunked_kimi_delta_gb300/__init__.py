@@ -827,36 +827,61 @@ class RmsNorm(NamedTuple):
 
 
 def _scale_shape(rows, cols, kind):
-    rb, cb = -(-rows // 128), -(-cols // 128)
-    return {"row": (-(-cb // 4), rows, 4), "col": (-(-rb // 4), cols, 4), "tile": (rb, cb)}[kind]
+    if kind == "row":
+        return ((cols + 511) // 512, rows, 4)
+    if kind == "col":
+        return ((rows + 511) // 512, cols, 4)
+    return ((rows + 127) // 128, (cols + 127) // 128)
 
 
 def _empty_fp8(rows, cols, kind, device) -> Fp8Matrix:
     torch = _torch()
-    data = torch.empty(rows, -(-cols // 16) * 16, dtype=torch.float8_e4m3fn, device=device)
+    data = torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.float8_e4m3fn,
+                               device=device)
     scales = torch.empty(_scale_shape(rows, cols, kind), dtype=torch.float8_e8m0fnu, device=device)
-    return Fp8Matrix(data[:, :cols], scales, kind)
+    return Fp8Matrix(data, scales, kind)
 
 
 def _pitch(t) -> int:
     """Row pitch in elements of a 2-D tensor with dense rows."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    rows, cols = t.shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError("a matrix with dense rows is needed")
-    if t.shape[0] > 1:
-        return t.stride(0)
-    return -(-max(t.stride(0), t.shape[1]) // 16) * 16  # one row: any pitch will do
+    return pitch if rows > 1 else (max(pitch, cols) + 15) // 16 * 16  # one row: any pitch will do
+
+
+def _launch_device(lead, *ts) -> int:
+    """Index of the device of a call whose tensors are dense and all on the
+    current device (a handful of integer comparisons: these calls also run
+    for single tokens, where the host's time counts)."""
+    dev = lead.get_device()
+    fine = dev >= 0 and lead.is_contiguous() and dev == _torch().cuda.current_device()
+    for t in ts:
+        if t is not None:
+            fine = fine and t.get_device() == dev and t.is_contiguous()
+    if not fine:
+        _contig(lead, *ts)
+        _on_device(lead, *ts)
+    return dev
+
+
+def _raw_stream(stream, dev):
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _check_fp8(x: Fp8Matrix, kind: str):
     torch = _torch()
-    if x.kind != kind:
-        raise ValueError(f"this operand needs {kind} scales, not {x.kind}")
-    if x.data.dtype != torch.float8_e4m3fn or x.scales.dtype != torch.float8_e8m0fnu:
+    data, scales, have = x
+    if have != kind:
+        raise ValueError(f"this operand needs {kind} scales, not {have}")
+    if data.dtype != torch.float8_e4m3fn or scales.dtype != torch.float8_e8m0fnu:
         raise TypeError("a scaled 8-bit matrix holds float8_e4m3fn values and float8_e8m0fnu scales")
-    if tuple(x.scales.shape) != _scale_shape(*x.data.shape, kind):
-        raise ValueError(f"{kind} scales of {tuple(x.data.shape)} values have shape "
-                         f"{_scale_shape(*x.data.shape, kind)}, not {tuple(x.scales.shape)}")
-    _contig(x.scales)
+    if data.dim() != 2:
+        raise ValueError("a scaled 8-bit matrix is [rows, cols]")
+    if scales.shape != _scale_shape(*data.shape, kind):
+        raise ValueError(f"{kind} scales of {tuple(data.shape)} values have shape "
+                         f"{_scale_shape(*data.shape, kind)}, not {tuple(scales.shape)}")
 
 
 def _check_weight(weight, cols):
@@ -882,30 +907,29 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None
     cols = x.shape[-1]
     _check_weight(weight, cols)
     _like(residual, x, "residual")
-    if out is False and not fp8:
-        raise ValueError("no result: out=False needs fp8=True")
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    elif out is False:
+    if out is False:
+        if not fp8:
+            raise ValueError("no result: out=False needs fp8=True")
         out = None
+    elif out is None:
+        out = torch.empty_like(x)
+    else:
+        _like(out, x, "out")
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
     elif residual_out is None:
-        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    _like(out, x, "out")
-    _like(residual_out, x, "residual_out")
-    _contig(x, weight, residual, out, residual_out)
+        residual_out = torch.empty_like(x)
+    else:
+        _like(residual_out, x, "residual_out")
+    dev = _launch_device(x, weight, residual, out, residual_out)
     rows = x.numel() // cols if cols else 0
     q = _empty_fp8(rows, cols, "row", x.device) if fp8 else None
-    _on_device(x, weight, residual, out, residual_out)
-    a = kda_rms_norm_args()
-    a.rows, a.cols, a.dtype = rows, cols, _dtype_code(x)
-    a.x, a.residual, a.weight, a.eps = _ptr(x), _ptr(residual), _ptr(weight), float(eps)
-    a.residual_out, a.out = _ptr(residual_out), _ptr(out)
+    a = kda_rms_norm_args(rows, cols, _dtype_code(x), _ptr(x), _ptr(residual), _ptr(weight), eps,
+                          _ptr(residual_out), _ptr(out))
     if q is not None:
-        a.fp8, a.ld_fp8, a.fp8_scales = _ptr(q.data), _pitch(q.data), _ptr(q.scales)
-    _check(lib.kda_rms_norm(ctypes.byref(a), _stream(stream)), "kda_rms_norm")
+        a.fp8, a.ld_fp8, a.fp8_scales = q.data.data_ptr(), (cols + 15) // 16 * 16, q.scales.data_ptr()
+    _check(lib.kda_rms_norm(ctypes.byref(a), _raw_stream(stream, dev)), "kda_rms_norm")
     return RmsNorm(out, residual_out, q)
 
 
@@ -923,19 +947,20 @@ def kda_rms_norm_bwd(d_out, x, weight=None, d_residual=None, *, eps=1e-6, dx=Non
     _like(d_out, x, "d_out")
     _like(d_residual, x, "d_residual")
     if dx is None:
-        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-    _like(dx, x, "dx")
-    dweight = torch.empty(cols, dtype=torch.float32, device=x.device) if want_dweight else None
-    _contig(d_out, x, weight, d_residual, dx)
-    _on_device(d_out, x, weight, d_residual, dx, workspace)
-    a = kda_rms_norm_bwd_args()
-    a.rows, a.cols, a.dtype = x.numel() // cols if cols else 0, cols, _dtype_code(x)
-    a.d_out, a.h, a.weight, a.d_residual = _ptr(d_out), _ptr(x), _ptr(weight), _ptr(d_residual)
-    a.eps, a.dx, a.dweight = float(eps), _ptr(dx), _ptr(dweight)
+        dx = torch.empty_like(x)
+    else:
+        _like(dx, x, "dx")
+    dev = _launch_device(x, d_out, weight, d_residual, dx, workspace)
+    rows = x.numel() // cols if cols else 0
+    a = kda_rms_norm_bwd_args(rows, cols, _dtype_code(x), _ptr(d_out), _ptr(x), _ptr(weight),
+                              _ptr(d_residual), eps, _ptr(dx))
+    dweight = None
     if want_dweight:
-        ws = _workspace(lib.kda_rms_norm_bwd_workspace_size(a.rows, cols), x.device, workspace)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    _check(lib.kda_rms_norm_bwd(ctypes.byref(a), _stream(stream)), "kda_rms_norm_bwd")
+        dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
+        ws = _workspace(lib.kda_rms_norm_bwd_workspace_size(rows, cols), x.device, workspace)
+        a.dweight, a.workspace = dweight.data_ptr(), ws.data_ptr()
+        a.workspace_bytes = ws.numel() * ws.element_size()
+    _check(lib.kda_rms_norm_bwd(ctypes.byref(a), _raw_stream(stream, dev)), "kda_rms_norm_bwd")
     return dx, dweight
 
 
@@ -947,21 +972,19 @@ def kda_fp8_quantize(x, kinds=("row",), *, stream=None):
     lib = load_library()
     if isinstance(kinds, str):
         kinds = (kinds,)
-    if not kinds or len(set(kinds)) != len(kinds) or set(kinds) - {"row", "col", "tile"}:
+    if not kinds or len(set(kinds)) != len(kinds) or not {"row", "col", "tile"}.issuperset(kinds):
         raise ValueError('kinds are "row", "col" and "tile", each once')
     if x.dim() != 2:
         raise ValueError("x is [rows, cols]")
-    _contig(x)
-    _on_device(x)
+    dev = _launch_device(x)
     rows, cols = x.shape
-    parts = {k: _empty_fp8(rows, cols, k, x.device) for k in kinds}
-    a = kda_fp8_quantize_args()
-    a.rows, a.cols, a.dtype, a.x, a.ld = rows, cols, _dtype_code(x), _ptr(x), -(-cols // 16) * 16
-    for k, p in parts.items():
-        setattr(a, k, _ptr(p.data))
-        setattr(a, k + "_scales", _ptr(p.scales))
-    _check(lib.kda_fp8_quantize(ctypes.byref(a), _stream(stream)), "kda_fp8_quantize")
-    return tuple(parts.values())
+    parts = tuple(_empty_fp8(rows, cols, k, x.device) for k in kinds)
+    a = kda_fp8_quantize_args(rows, cols, _dtype_code(x), _ptr(x), (cols + 15) // 16 * 16)
+    for p in parts:
+        setattr(a, p.kind, p.data.data_ptr())
+        setattr(a, p.kind + "_scales", p.scales.data_ptr())
+    _check(lib.kda_fp8_quantize(ctypes.byref(a), _raw_stream(stream, dev)), "kda_fp8_quantize")
+    return parts
 
 
 _FP8_FORMS = {"nt": (KDA_FP8_NT, "row", "tile"), "nn": (KDA_FP8_NN, "row", "tile"),
@@ -969,15 +992,17 @@ _FP8_FORMS = {"nt": (KDA_FP8_NT, "row", "tile"), "nn": (KDA_FP8_NN, "row", "tile
 _fp8_status_words = {}
 
 
-def _fp8_status_word(device):
+def _fp8_status_word(dev: int):
     """The zeroed error word shared by a device's matmul calls without a
     ``workspace`` (made by the first of them: before any stream capture)."""
-    if device not in _fp8_status_words:
+    word = _fp8_status_words.get(dev)
+    if word is None:
         torch = _torch()
-        _fp8_status_words[device] = torch.zeros(KDA_FP8_MATMUL_WORKSPACE_BYTES, dtype=torch.uint8,
-                                                device=device)
-        torch.cuda.current_stream(device).synchronize()
-    return _fp8_status_words[device]
+        word = torch.zeros(KDA_FP8_MATMUL_WORKSPACE_BYTES, dtype=torch.uint8,
+                           device=torch.device("cuda", dev))
+        torch.cuda.current_stream(dev).synchronize()
+        _fp8_status_words[dev] = word
+    return word
 
 
 def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out=None,
@@ -998,24 +1023,27 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
     code, ka, kb = _FP8_FORMS[form]
     _check_fp8(a, ka)
     _check_fp8(b, kb)
-    (k, m) = a.data.shape if form == "tn" else a.data.shape[::-1]
-    (n, k_b) = b.data.shape if form == "nt" else b.data.shape[::-1]
+    ad, bd = a.data, b.data
+    (k, m) = ad.shape if form == "tn" else ad.shape[::-1]
+    (n, k_b) = bd.shape if form == "nt" else bd.shape[::-1]
     if k != k_b:
         raise ValueError(f"the operands sum over {k} and {k_b}")
     if out is None:
-        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.data.device)
-    elif tuple(out.shape) != (m, n) or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out must be [{m}, {n}] of out_dtype")
-    p = kda_fp8_matmul_args()
-    p.m, p.n, p.k, p.form = m, n, k, code
-    p.a, p.lda, p.a_scales = _ptr(a.data), _pitch(a.data), _ptr(a.scales)
-    p.b, p.ldb, p.b_scales = _ptr(b.data), _pitch(b.data), _ptr(b.scales)
-    p.out, p.ldo, p.out_dtype = _ptr(out), _pitch(out), _dtype_code(out)
-    _on_device(a.data, a.scales, b.data, b.scales, out, workspace)
-    ws = _fp8_status_word(out.device) if workspace is None else workspace
-    p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    p.flags = extra_flags
-    _check(lib.kda_fp8_matmul(ctypes.byref(p), _stream(stream)), "kda_fp8_matmul")
+        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=ad.device)
+        ldo = n
+    else:
+        if out.shape != (m, n) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be [{m}, {n}] of out_dtype")
+        ldo = _pitch(out)
+    lda, ldb, out_code = _pitch(ad), _pitch(bd), _dtype_code(out)
+    dev = _launch_device(a.scales, b.scales, workspace)
+    if ad.get_device() != dev or bd.get_device() != dev or out.get_device() != dev:
+        _on_device(a.scales, ad, bd, out)
+    ws = _fp8_status_word(dev) if workspace is None else workspace
+    p = kda_fp8_matmul_args(m, n, k, code, ad.data_ptr(), lda, a.scales.data_ptr(), bd.data_ptr(), ldb,
+                            b.scales.data_ptr(), out.data_ptr(), ldo, out_code, ws.data_ptr(),
+                            ws.numel() * ws.element_size(), extra_flags)
+    _check(lib.kda_fp8_matmul(ctypes.byref(p), _raw_stream(stream, dev)), "kda_fp8_matmul")
     return out
 
 
@@ -1024,6 +1052,4 @@ def kda_fp8_matmul_status(stream=None) -> int:
     current device (synchronises ``stream``): KDA_OK, or
     KDA_ERR_DEVICE_TIMEOUT when a bounded device wait gave up since the last
     read."""
-    torch = _torch()
-    word = _fp8_status_word(torch.device("cuda", torch.cuda.current_device()))
-    return kda_get_device_status(word, stream)
+    return kda_get_device_status(_fp8_status_word(_torch().cuda.current_device()), stream)

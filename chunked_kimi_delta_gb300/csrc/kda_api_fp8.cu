@@ -79,7 +79,10 @@ kda_status kda_fp8_matmul(const kda_fp8_matmul_args *a, kda_stream_t stream) {
   if (!a->a || !a->b || !a->a_scales || !a->b_scales) return KDA_ERR_INVALID_ARG;
   if (a->lda < (a->form == KDA_FP8_TN ? a->m : a->k) || a->ldb < (a->form == KDA_FP8_NT ? a->k : a->n))
     return KDA_ERR_INVALID_ARG;
-  if (a->lda > INT32_MAX || a->ldb > INT32_MAX || blocks(a->m) * blocks(a->n) > INT32_MAX)
+  // coordinates up to a tile past the edge stay 32-bit
+  const int32_t most = INT32_MAX - 1024;
+  if (a->m > most || a->n > most || a->k > most || a->lda > INT32_MAX || a->ldb > INT32_MAX ||
+      blocks(a->m) * blocks(a->n) > INT32_MAX / 64)
     return KDA_ERR_UNSUPPORTED;
   if (mis16(a->a) || mis16(a->b) || mis16(a->a_scales) || mis16(a->b_scales) || a->lda % 16 != 0 ||
       a->ldb % 16 != 0)

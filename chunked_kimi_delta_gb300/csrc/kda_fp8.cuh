@@ -25,21 +25,25 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(float amax) {
 // 2^-e of a scale byte below 248 (which fp8_scale_byte never exceeds).
 __device__ __forceinline__ float fp8_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// Four scaled values as e4m3 bytes, lowest first.  x * 0 + x keeps finite
-// values and turns an infinity into NaN, which the saturating conversion
-// would otherwise clamp to 448.
+// Four scaled values as e4m3 bytes, lowest first.  None is infinite
+// (drop_infinities): the conversion would clamp it to 448.
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float inv) {
-  a *= inv; b *= inv; c *= inv; d *= inv;
-  a = __fmaf_rn(a, 0.f, a); b = __fmaf_rn(b, 0.f, b); c = __fmaf_rn(c, 0.f, c); d = __fmaf_rn(d, 0.f, d);
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
 
-// |x| of finite elements, 0 of others.
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a < __int_as_float(0x7f800000) ? a : 0.f;
+// Largest magnitude, NaN left out (fmaxf returns the other operand).
+__device__ __forceinline__ float block_amax(const float (&y)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+  return m;
+}
+// e4m3 has no infinity: they become NaN, and so leave block_amax alone.
+__device__ __forceinline__ void drop_infinities(float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i], 0.f, y[i]);
 }
 
 // Eight consecutive elements of a row, zeros from element `n` on (n <= 0:

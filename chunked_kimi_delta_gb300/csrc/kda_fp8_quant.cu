@@ -7,12 +7,63 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Eight elements as loaded: fp32, or bf16 pairs (four registers).
+template <typename T> struct Vec8;
+template <> struct Vec8<float> {
+  float f[8];
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = f[j];
+  }
+  __device__ __forceinline__ void set(const float (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = o[j];
+  }
+};
+template <> struct Vec8<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[2 * j] = __uint_as_float(w[j] << 16);
+      o[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&o)[8]) {  // exact: the values are bf16 (or NaN)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(o[2 * j]) >> 16 | (__float_as_uint(o[2 * j + 1]) & 0xFFFF0000u);
+  }
+};
+
+// The magnitudes' maxima: of one vector, and column by column.  bf16 works on
+// pairs: a maximum is one of its operands, so nothing is rounded.
+__device__ __forceinline__ float row_amax(const Vec8<float> &v) { return block_amax(v.f); }
+__device__ __forceinline__ float row_amax(const Vec8<__nv_bfloat16> &v) {
+  const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(v.w);
+  const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])), __hmax2(__habs2(p[2]), __habs2(p[3])));
+  const float2 f = __bfloat1622float2(m);
+  return fmaxf(fmaxf(f.x, f.y), 0.f);  // 0 when both are NaN
+}
+__device__ __forceinline__ void col_amax(Vec8<float> &m, const Vec8<float> &v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m.f[j] = fmaxf(m.f[j], fabsf(v.f[j]));
+}
+__device__ __forceinline__ void col_amax(Vec8<__nv_bfloat16> &m, const Vec8<__nv_bfloat16> &v) {
+  __nv_bfloat162 *a = reinterpret_cast<__nv_bfloat162 *>(m.w);
+  const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(v.w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[j] = __hmax2(a[j], __habs2(b[j]));
+}
+
 // One CTA per 128 x 128 block: thread t holds columns 8 (t % 16) .. + 7 of
 // the rows t / 16 + 16 i, i < 8.  A row's maximum is that of 16 neighbouring
 // lanes; a column's is over i, the two half-warps and the eight warps; the
-// block's is that of its columns.
+// block's is that of its columns.  Memory bounds it: every element is read
+// once and written once for each kind.  The block stays in registers as it
+// was loaded (32 of them for bf16), so that three CTAs share an SM and one
+// loads while another converts.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(kda_fp8_quantize_args a, int cblocks) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) fp8_quantize_kernel(kda_fp8_quantize_args a, int cblocks) {
   __shared__ float colmax[8][FP8_BLOCK];
   __shared__ float warpmax[8];
   const int rb = blockIdx.x / cblocks, cb = blockIdx.x % cblocks;
@@ -20,26 +71,53 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(kda_fp8_quantize
   const int c = cb * FP8_BLOCK + 8 * lane16;      // first column of this thread
   const int n = a.cols - c;                       // columns it holds, at most 8
   const int64_t r0 = (int64_t)rb * FP8_BLOCK + threadIdx.x / 16;
-  float v[8][8];
+  const T *x = static_cast<const T *>(a.x) + r0 * a.cols + c;
+  Vec8<T> v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 16 * i;
-    load8<T, VEC>(static_cast<const T *>(a.x) + r * a.cols + c, r < a.rows ? n : 0, v[i]);
+    float f[8];
+    load8<T, VEC>(x + (int64_t)(16 * i) * a.cols, r0 + 16 * i < a.rows ? n : 0, f);
+    v[i].set(f);
+  }
+  Vec8<T> cmax = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) col_amax(cmax, v[i]);
+  float cm[8];
+  cmax.get(cm);
+  bool inf = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cm[j] = fmaxf(cm[j], 0.f);
+    inf |= isinf(cm[j]);
+  }
+  if (inf) {  // infinities count as NaN
+    cmax = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[8];
+      v[i].get(f);
+      drop_infinities(f);
+      v[i].set(f);
+      col_amax(cmax, v[i]);
+    }
+    cmax.get(cm);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], 0.f);
   }
   if (a.row) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float m = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[i][j]));
+      float m = row_amax(v[i]);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
       const uint32_t sb = fp8_scale_byte(m);
       const float inv = fp8_inv_scale(sb);
       const int64_t r = r0 + 16 * i;
       if (r >= a.rows) continue;
-      store8_fp8(static_cast<uint8_t *>(a.row) + r * a.ld + c, n, fp8_pack4(v[i][0], v[i][1], v[i][2], v[i][3], inv),
-                 fp8_pack4(v[i][4], v[i][5], v[i][6], v[i][7], inv));
+      float f[8];
+      v[i].get(f);
+      store8_fp8(static_cast<uint8_t *>(a.row) + r * a.ld + c, n, fp8_pack4(f[0], f[1], f[2], f[3], inv),
+                 fp8_pack4(f[4], f[5], f[6], f[7], inv));
       if (lane16 == 0) {
         uint8_t *s = a.row_scales + ((int64_t)(cb >> 2) * a.rows + r) * 4;
         s[cb & 3] = (uint8_t)sb;
@@ -49,14 +127,8 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(kda_fp8_quantize
     }
   }
   if (!a.col && !a.tile) return;
-  float cm[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i][j]));
-    cm[j] = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-  }
+  for (int j = 0; j < 8; ++j) cm[j] = fmaxf(cm[j], __shfl_xor_sync(~0u, cm[j], 16));
   if ((threadIdx.x & 16) == 0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) colmax[warp][8 * lane16 + j] = cm[j];
@@ -78,8 +150,9 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(kda_fp8_quantize
       const int64_t r = r0 + 16 * i;
       if (r >= a.rows) continue;
       float s[8];
+      v[i].get(s);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = v[i][j] * inv[j];
+      for (int j = 0; j < 8; ++j) s[j] *= inv[j];
       store8_fp8(static_cast<uint8_t *>(a.col) + r * a.ld + c, n, fp8_pack4(s[0], s[1], s[2], s[3], 1.f),
                  fp8_pack4(s[4], s[5], s[6], s[7], 1.f));
     }
@@ -111,8 +184,10 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(kda_fp8_quantize
     for (int i = 0; i < 8; ++i) {
       const int64_t r = r0 + 16 * i;
       if (r >= a.rows) continue;
-      store8_fp8(static_cast<uint8_t *>(a.tile) + r * a.ld + c, n, fp8_pack4(v[i][0], v[i][1], v[i][2], v[i][3], inv),
-                 fp8_pack4(v[i][4], v[i][5], v[i][6], v[i][7], inv));
+      float f[8];
+      v[i].get(f);
+      store8_fp8(static_cast<uint8_t *>(a.tile) + r * a.ld + c, n, fp8_pack4(f[0], f[1], f[2], f[3], inv),
+                 fp8_pack4(f[4], f[5], f[6], f[7], inv));
     }
     if (threadIdx.x == 0) a.tile_scales[(int64_t)rb * cblocks + cb] = (uint8_t)sb;
   }

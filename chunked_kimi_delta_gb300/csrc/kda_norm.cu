@@ -1,211 +1,411 @@
 // kda_norm.cu - RMS norm with the residual's addition and an 8-bit result, and
 // its backward.
+//
+//   h = x + r,  y = h rstd w,  rstd = (mean h^2 + eps)^-1/2
+//   dx = rstd (w g - n mean(w g n)) + d,  dw = sum over rows of g n,  n = h rstd
+//
+// Both read every element once and write it once, so memory bounds them; what
+// costs is the wait for a row's sum between its loads and its stores.  CTAs
+// are persistent and walk the rows with a stride of the grid; each thread
+// copies its own columns of the rows to come into shared memory (cp.async,
+// kDepth rows ahead) and no thread reads another's copies, so the copies need
+// no barrier and stay in flight while a row's sum is formed.
 #include "kda_fp8.cuh"
 
 namespace kda {
 namespace {
 
-// Sum over the CTA's threads, the same value in all of them: shuffles inside
-// a warp, then the warps' sums in order.  `red`: one float per warp.
-__device__ __forceinline__ float cta_sum(float v, float *red) {
+constexpr int kDepth = 3;  // rows in flight per CTA
+
+// How a row's columns are read and which thread holds them.
+//   RING    cp.async into shared memory, kDepth rows ahead; thread t holds
+//           columns 8 (t + i threads) .. + 7
+//   DIRECT  16-byte loads straight to registers: rows too wide for the ring
+//   ODD     rows that do not start on 16 bytes (cols % 8 != 0): one element at
+//           a time, column 16 j + t % 16 of the group, so that 16 lanes read
+//           neighbouring elements
+// In all three, 16 neighbouring lanes hold the 128 columns of one scale.
+enum Mode { RING, DIRECT, ODD };
+
+template <typename T> struct Raw;  // eight elements as stored
+template <> struct Raw<float> { uint4 v[2]; };
+template <> struct Raw<__nv_bfloat16> { uint4 v[1]; };
+
+__device__ __forceinline__ void unpack(const Raw<float> &r, float (&f)[8]) {
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16> &r, float (&f)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // bf16 is the upper half of an fp32
+    f[2 * j] = __uint_as_float(w[j] << 16);
+    f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+// Eight elements of a row of `cols` for this thread's i-th place.
+template <Mode M> __device__ __forceinline__ int first_col(int i) {
+  const int t = threadIdx.x + i * blockDim.x;
+  return M == ODD ? (t >> 4) * FP8_BLOCK + (t & 15) : 8 * t;
+}
+constexpr int kOddStep = 16;
+
+template <typename T, Mode M> __device__ __forceinline__ void load(const T *row, int c, int cols, float (&f)[8]) {
+  if (M == ODD) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = c + kOddStep * j < cols ? to_f32<T>(row[c + kOddStep * j]) : 0.f;
+  } else {
+    load8<T, true>(row + c, cols - c, f);
+  }
+}
+template <typename T, Mode M> __device__ __forceinline__ void store(T *row, int c, int cols, const float (&f)[8]) {
+  if (M == ODD) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + kOddStep * j < cols) row[c + kOddStep * j] = from_f32<T>(f[j]);
+  } else {
+    store8<T, true>(row + c, cols - c, f);
+  }
+}
+
+// The ring of one tensor: thread-private slots of eight elements.
+template <typename T> __device__ __forceinline__ void copy_ahead(Raw<T> *slot, const T *src) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(slot);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Raw<T>) / 16); ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"(d + 16 * i), "l"(reinterpret_cast<const uint4 *>(src) + i) : "memory");
+}
+__device__ __forceinline__ void commit_ahead() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_oldest() { asm volatile("cp.async.wait_group %0;" :: "n"(kDepth - 1) : "memory"); }
+
+// Sums over the CTA's threads, the same values in all of them: shuffles
+// inside a warp, then the warps' sums in order.  `red` alternates between two
+// buffers from call to call, so one barrier is enough.
+template <int N> __device__ __forceinline__ void cta_sums(float (&v)[N], float (*red)[32]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(~0u, v[n], o);
   const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int n = 0; n < N; ++n) red[n][threadIdx.x >> 5] = v[n];
   __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < warps; ++i) s += red[i];
-  __syncthreads();
-  return s;
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = 0.f;
+  for (int i = 0; i < warps; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += red[n][i];
 }
 
-// Largest finite magnitude of the 128 columns that 16 neighbouring lanes hold.
-__device__ __forceinline__ float half_warp_amax(const float (&y)[8]) {
-  float m = 0.f;
+template <typename T, Mode M, int VPT>
+__global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_kernel(kda_rms_norm_args a) {
+  extern __shared__ uint4 smem_raw[];
+  __shared__ float red[2][1][32];
+  const int cols = a.cols, blocks = (cols + FP8_BLOCK - 1) / FP8_BLOCK;
+  const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
+  const int tensors = res ? 2 : 1;  // in the ring, as the launch sized it
+  Raw<T> *ring = reinterpret_cast<Raw<T> *>(smem_raw) + threadIdx.x;
+  auto slot = [&](int stage, int tensor, int i) { return ring + ((stage * tensors + tensor) * VPT + i) * blockDim.x; };
+  auto fetch = [&](int64_t row, int stage) {
+    if (M != RING) return;
+    if (row < a.rows) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(y[i]));
+      for (int i = 0; i < VPT; ++i) {
+        const int c = first_col<M>(i);
+        if (c >= cols) continue;
+        copy_ahead(slot(stage, 0, i), x + row * cols + c);
+        if (res) copy_ahead(slot(stage, 1, i), res + row * cols + c);
+      }
+    }
+    commit_ahead();
+  };
+  for (int s = 0; s < kDepth; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0, parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    float h[VPT][8], sums[1] = {0.f};
+    if (M == RING) wait_oldest();
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  return m;
-}
-
-// One CTA per row; the row stays in registers between the sum of squares and
-// the result: thread t holds columns 8 (t + i blockDim) .. + 7 for i < VPT, so
-// 16 neighbouring lanes hold the 128 columns of one scale.
-template <typename T, bool VEC, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 512 : 1024) rms_norm_kernel(kda_rms_norm_args a) {
-  __shared__ float red[32];
-  const int64_t row = blockIdx.x;
-  const int cols = a.cols;
-  const T *x = static_cast<const T *>(a.x) + row * cols;
-  const T *res = a.residual ? static_cast<const T *>(a.residual) + row * cols : nullptr;
-  float h[VPT][8];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = 8 * (threadIdx.x + i * blockDim.x);
-    load8<T, VEC>(x + c, cols - c, h[i]);
-    if (res) {
+    for (int i = 0; i < VPT; ++i) {
+      const int c = first_col<M>(i);
       float r[8];
-      load8<T, VEC>(res + c, cols - c, r);
+      if (M == RING) {
+        if (c < cols) {
+          unpack(*slot(stage, 0, i), h[i]);
+          if (res) unpack(*slot(stage, 1, i), r);
+        } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = to_f32<T>(from_f32<T>(h[i][j] + r[j]));
-      store8<T, VEC>(static_cast<T *>(a.residual_out) + row * cols + c, cols - c, h[i]);
+          for (int j = 0; j < 8; ++j) h[i][j] = r[j] = 0.f;
+        }
+      } else {
+        load<T, M>(x + row * cols, c, cols, h[i]);
+        if (res) load<T, M>(res + row * cols, c, cols, r);
+      }
+      if (res) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = to_f32<T>(from_f32<T>(h[i][j] + r[j]));
+        store<T, M>(static_cast<T *>(a.residual_out) + row * cols, c, cols, h[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[0] = fmaf(h[i][j], h[i][j], sums[0]);
     }
+    cta_sums(sums, red[parity]);
+    parity ^= 1;
+    // every thread has used its slots: the sum needed them
+    fetch(row + (int64_t)kDepth * gridDim.x, stage);
+    stage = stage == kDepth - 1 ? 0 : stage + 1;
+    const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+    for (int i = 0; i < VPT; ++i) {
+      const int c = first_col<M>(i);
+      float y[8];
+      if (a.weight) {
+        load<float, M>(a.weight, c, cols, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= h[i][j] * rstd;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd;
+      }
+      if (a.out) store<T, M>(static_cast<T *>(a.out) + row * cols, c, cols, y);
+      if (a.fp8) {
+        float m = block_amax(y);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if (__any_sync(~0u, isinf(m))) {  // infinities count as NaN
+          drop_infinities(y);
+          m = block_amax(y);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        }
+        const uint32_t sb = fp8_scale_byte(m);
+        const float inv = fp8_inv_scale(sb);
+        const uint32_t lo = fp8_pack4(y[0], y[1], y[2], y[3], inv), hi = fp8_pack4(y[4], y[5], y[6], y[7], inv);
+        uint8_t *q = static_cast<uint8_t *>(a.fp8) + row * a.ld_fp8;
+        if (M == ODD) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c + kOddStep * j < cols) q[c + kOddStep * j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+        } else if (c < cols) {
+          *reinterpret_cast<uint2 *>(q + c) = make_uint2(lo, hi);
+        }
+        const int b = c / FP8_BLOCK;
+        if ((threadIdx.x & 15) == 0 && b < ((blocks + 3) & ~3))
+          a.fp8_scales[((b >> 2) * a.rows + row) * 4 + (b & 3)] = (uint8_t)sb;  // 1.0 past the last block
+      }
+    }
   }
-  const float rstd = 1.f / sqrtf(cta_sum(ss, red) / (float)cols + a.eps);
-  const int cb = (cols + FP8_BLOCK - 1) / FP8_BLOCK;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = 8 * (threadIdx.x + i * blockDim.x);
-    float w[8], y[8];
-    if (a.weight) {
-      load8<float, VEC>(a.weight + c, cols - c, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * w[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd;
-    }
-    if (a.out) store8<T, VEC>(static_cast<T *>(a.out) + row * cols + c, cols - c, y);
-    if (a.fp8) {
-      const uint32_t sb = fp8_scale_byte(half_warp_amax(y));
-      const float inv = fp8_inv_scale(sb);
-      store8_fp8(static_cast<uint8_t *>(a.fp8) + row * a.ld_fp8 + c, cols - c,
-                 fp8_pack4(y[0], y[1], y[2], y[3], inv), fp8_pack4(y[4], y[5], y[6], y[7], inv));
-      const int b = c / FP8_BLOCK;
-      if ((threadIdx.x & 15) == 0 && b < ((cb + 3) & ~3))
-        a.fp8_scales[((b >> 2) * a.rows + row) * 4 + (b & 3)] = (uint8_t)sb;  // 1.0 past the last block
-    }
-  }
-}
-
-template <typename T, bool VEC>
-cudaError_t norm_typed(const kda_rms_norm_args &a, cudaStream_t st) {
-  // whole groups of four blocks, so that the scales past the last block get written
-  const int vecs = (a.cols + 511) / 512 * 64;
-  const int vpt = vecs <= 512 ? 1 : vecs <= 2048 ? 2 : 4;
-  const int threads = (vecs / vpt + 31) / 32 * 32;
-  const dim3 grid((unsigned)a.rows);
-  if (vpt == 1) rms_norm_kernel<T, VEC, 1><<<grid, threads, 0, st>>>(a);
-  else if (vpt == 2) rms_norm_kernel<T, VEC, 2><<<grid, threads, 0, st>>>(a);
-  else rms_norm_kernel<T, VEC, 4><<<grid, threads, 0, st>>>(a);
-  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ backward
 
-constexpr int kBwdParts = 608;  // partial dweight rows: 4 CTAs on each of 152 SMs
+constexpr int kMaxParts = 608;  // partial dweight rows at most: 4 CTAs on each of 152 SMs
 
-// CTAs walk the rows with a stride of the grid; dweight of a CTA's rows is
-// summed in its registers and left as one row of partial sums.
-template <typename T, bool VEC, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 512 : 1024) rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
-  __shared__ float red[32];
+// dweight of a CTA's rows is summed in its registers and left as one row of
+// partial sums.
+template <typename T, Mode M, int VPT>
+__global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
+  extern __shared__ uint4 smem_raw[];
+  __shared__ float red[2][2][32];
   const int cols = a.cols;
+  const T *hp = static_cast<const T *>(a.h), *gp = static_cast<const T *>(a.d_out);
+  const T *dp = static_cast<const T *>(a.d_residual);
+  const int tensors = dp ? 3 : 2;  // in the ring, as the launch sized it
+  Raw<T> *ring = reinterpret_cast<Raw<T> *>(smem_raw) + threadIdx.x;
+  auto slot = [&](int stage, int tensor, int i) { return ring + ((stage * tensors + tensor) * VPT + i) * blockDim.x; };
+  auto fetch = [&](int64_t row, int stage) {
+    if (M != RING) return;
+    if (row < a.rows) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = first_col<M>(i);
+        if (c >= cols) continue;
+        copy_ahead(slot(stage, 0, i), hp + row * cols + c);
+        copy_ahead(slot(stage, 1, i), gp + row * cols + c);
+        if (dp) copy_ahead(slot(stage, 2, i), dp + row * cols + c);
+      }
+    }
+    commit_ahead();
+  };
   float dw[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  for (int s = 0; s < kDepth; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0, parity = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float h[VPT][8], g[VPT][8];
-    float ss = 0.f, sg = 0.f;
+    float sums[2] = {0.f, 0.f};
+    if (M == RING) wait_oldest();
+    // h and g are read again after the sum, from the ring or the caches: kept
+    // in registers they would leave room for half the threads.
+    auto get = [&](int tensor, const T *p, int i, int c, float (&f)[8]) {
+      if (M != RING) {
+        load<T, M>(p + row * cols, c, cols, f);
+      } else if (c < cols) {
+        unpack(*slot(stage, tensor, i), f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      }
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = 8 * (threadIdx.x + i * blockDim.x);
-      load8<T, VEC>(static_cast<const T *>(a.h) + row * cols + c, cols - c, h[i]);
-      load8<T, VEC>(static_cast<const T *>(a.d_out) + row * cols + c, cols - c, g[i]);
-      float w[8];
-      if (a.weight) load8<float, VEC>(a.weight + c, cols - c, w);
+      const int c = first_col<M>(i);
+      float h[8], g[8], w[8];
+      get(0, hp, i, c, h);
+      get(1, gp, i, c, g);
+      if (a.weight) load<float, M>(a.weight, c, cols, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        ss = fmaf(h[i][j], h[i][j], ss);
-        sg = fmaf(a.weight ? g[i][j] * w[j] : g[i][j], h[i][j], sg);
+        sums[0] = fmaf(h[j], h[j], sums[0]);
+        sums[1] = fmaf(a.weight ? g[j] * w[j] : g[j], h[j], sums[1]);
       }
     }
-    ss = cta_sum(ss, red);
-    sg = cta_sum(sg, red);
-    const float rstd = 1.f / sqrtf(ss / (float)cols + a.eps);
-    const float mean = sg * rstd / (float)cols;  // mean of weight * d_out * n
+    cta_sums(sums, red[parity]);
+    parity ^= 1;
+    const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
+    const float mean = sums[1] * rstd / (float)cols;  // mean of weight * d_out * n
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = 8 * (threadIdx.x + i * blockDim.x);
-      float w[8], r[8], dx[8];
-      if (a.weight) load8<float, VEC>(a.weight + c, cols - c, w);
-      if (a.d_residual) load8<T, VEC>(static_cast<const T *>(a.d_residual) + row * cols + c, cols - c, r);
+      const int c = first_col<M>(i);
+      float h[8], g[8], w[8], d[8], dx[8];
+      get(0, hp, i, c, h);
+      get(1, gp, i, c, g);
+      if (a.weight) load<float, M>(a.weight, c, cols, w);
+      if (dp) get(2, dp, i, c, d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float n = h[i][j] * rstd;
-        dw[i][j] = fmaf(g[i][j], n, dw[i][j]);
-        dx[j] = rstd * ((a.weight ? g[i][j] * w[j] : g[i][j]) - n * mean);
-        if (a.d_residual) dx[j] += r[j];
+        const float n = h[j] * rstd;
+        dw[i][j] = fmaf(g[j], n, dw[i][j]);
+        dx[j] = rstd * ((a.weight ? g[j] * w[j] : g[j]) - n * mean);
+        if (dp) dx[j] += d[j];
       }
-      store8<T, VEC>(static_cast<T *>(a.dx) + row * cols + c, cols - c, dx);
+      store<T, M>(static_cast<T *>(a.dx) + row * cols, c, cols, dx);
     }
+    // this thread has used its slots: its stores needed them
+    fetch(row + (int64_t)kDepth * gridDim.x, stage);
+    stage = stage == kDepth - 1 ? 0 : stage + 1;
   }
   if (a.dweight) {
     float *part = static_cast<float *>(a.workspace) + (int64_t)blockIdx.x * cols;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = 8 * (threadIdx.x + i * blockDim.x);
-      store8<float, VEC>(part + c, cols - c, dw[i]);
-    }
+    for (int i = 0; i < VPT; ++i) store<float, M>(part, first_col<M>(i), cols, dw[i]);
   }
 }
 
-// dweight[c] = the sum of the partial rows: 32 columns x 8 row lanes per CTA,
+// dweight[c] = the sum of the partial rows: 32 columns x 32 row lanes per CTA,
 // each lane in row order, then the lanes in order.
-__global__ void __launch_bounds__(256) dweight_kernel(const float *__restrict__ part, int parts, int cols,
-                                                      float *__restrict__ dw) {
-  __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) dweight_kernel(const float *__restrict__ part, int parts, int cols,
+                                                       float *__restrict__ dw) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < cols)
-    for (int p = r; p < parts; p += 8) v += part[(int64_t)p * cols + c];
+  if (c < cols) {
+#pragma unroll 4
+    for (int p = r; p < parts; p += 32) v += part[(int64_t)p * cols + c];
+  }
   s[r][lane] = v;
   __syncthreads();
   if (r == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][lane];
+    for (int i = 1; i < 32; ++i) v += s[i][lane];
     dw[c] = v;
   }
 }
 
-template <typename T, bool VEC>
-cudaError_t bwd_typed(const kda_rms_norm_bwd_args &a, cudaStream_t st) {
-  const int vecs = (a.cols + 7) / 8;
-  const int vpt = vecs <= 512 ? 1 : vecs <= 2048 ? 2 : 4;
-  const int threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
-  const int parts = (int)(a.rows < kBwdParts ? a.rows : kBwdParts);
-  if (vpt == 1) rms_norm_bwd_kernel<T, VEC, 1><<<parts, threads, 0, st>>>(a);
-  else if (vpt == 2) rms_norm_bwd_kernel<T, VEC, 2><<<parts, threads, 0, st>>>(a);
-  else rms_norm_bwd_kernel<T, VEC, 4><<<parts, threads, 0, st>>>(a);
-  if (a.dweight)
-    dweight_kernel<<<(a.cols + 31) / 32, 256, 0, st>>>(static_cast<const float *>(a.workspace), parts, a.cols,
-                                                       a.dweight);
+// ------------------------------------------------------------------ launch
+
+// Threads for `vecs` groups of eight columns at vpt of them a thread.
+int threads_for(int vecs, int vpt) { return ((vecs + vpt - 1) / vpt + 31) / 32 * 32; }
+
+struct Shape {
+  Mode mode;
+  int vpt, threads, grid;
+  size_t smem;
+};
+
+// `tensors` of `esize` bytes an element travel through the ring.  Rows fit it
+// while kDepth of them leave room for two CTAs' worth of threads at vpt 2;
+// then as many CTAs as shared memory and 1,024 threads an SM hold (96 KB of
+// rows in flight an SM cover the latency of memory at full bandwidth).
+Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize) {
+  Shape s{};
+  s.vpt = vecs <= 64 ? 1 : 2;
+  s.threads = threads_for(vecs, s.vpt);
+  s.smem = (size_t)kDepth * tensors * s.vpt * s.threads * 8 * esize;
+  if (cols % 8 != 0) s.mode = ODD;
+  else if (s.threads <= 512 && s.smem <= 200 * 1024) s.mode = RING;
+  else s.mode = DIRECT;
+  int per_sm;
+  if (s.mode == RING) {
+    per_sm = (int)(227 * 1024 / (s.smem + 2048));
+    if (per_sm > 1024 / s.threads) per_sm = 1024 / s.threads;
+  } else {
+    s.vpt = vecs <= 1024 ? 1 : 4;
+    s.threads = threads_for(vecs, s.vpt);
+    s.smem = 0;
+    per_sm = 2048 / s.threads;
+  }
+  if (per_sm < 1) per_sm = 1;
+  if (per_sm > 8) per_sm = 8;
+  const int64_t most = 152 * (int64_t)per_sm;
+  s.grid = (int)(rows < most ? rows : most);
+  return s;
+}
+
+template <typename K, typename A>
+cudaError_t launch_rows(K kern, const Shape &s, const A &a, cudaStream_t st) {
+  if (s.smem > 40 * 1024) {  // with the static part, past the 48 KB that need no leave
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<s.grid, s.threads, s.smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T> cudaError_t norm_typed(const kda_rms_norm_args &a, cudaStream_t st) {
+  // whole groups of four blocks, so that the scales past the last block get written
+  const Shape s = shape_for(a.rows, a.cols, (a.cols + 511) / 512 * 64, a.residual ? 2 : 1, sizeof(T));
+  if (s.mode == RING)
+    return s.vpt == 1 ? launch_rows(rms_norm_kernel<T, RING, 1>, s, a, st) : launch_rows(rms_norm_kernel<T, RING, 2>, s, a, st);
+  if (s.mode == DIRECT)
+    return s.vpt == 1 ? launch_rows(rms_norm_kernel<T, DIRECT, 1>, s, a, st) : launch_rows(rms_norm_kernel<T, DIRECT, 4>, s, a, st);
+  return s.vpt == 1 ? launch_rows(rms_norm_kernel<T, ODD, 1>, s, a, st) : launch_rows(rms_norm_kernel<T, ODD, 4>, s, a, st);
+}
+
+template <typename T> cudaError_t bwd_typed(const kda_rms_norm_bwd_args &a, cudaStream_t st) {
+  // whole groups of 16 threads: the odd layout spreads a block over them
+  Shape s = shape_for(a.rows, a.cols, (a.cols + 127) / 128 * 16, a.d_residual ? 3 : 2, sizeof(T));
+  if (s.grid > kMaxParts) s.grid = kMaxParts;
+  cudaError_t e;
+  if (s.mode == RING)
+    e = s.vpt == 1 ? launch_rows(rms_norm_bwd_kernel<T, RING, 1>, s, a, st) : launch_rows(rms_norm_bwd_kernel<T, RING, 2>, s, a, st);
+  else if (s.mode == DIRECT)
+    e = s.vpt == 1 ? launch_rows(rms_norm_bwd_kernel<T, DIRECT, 1>, s, a, st) : launch_rows(rms_norm_bwd_kernel<T, DIRECT, 4>, s, a, st);
+  else
+    e = s.vpt == 1 ? launch_rows(rms_norm_bwd_kernel<T, ODD, 1>, s, a, st) : launch_rows(rms_norm_bwd_kernel<T, ODD, 4>, s, a, st);
+  if (e != cudaSuccess || !a.dweight) return e;
+  dweight_kernel<<<(a.cols + 31) / 32, 1024, 0, st>>>(static_cast<const float *>(a.workspace), s.grid, a.cols, a.dweight);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const kda_rms_norm_args &a, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0;  // rows then start on 16-byte boundaries
-  if (a.dtype == KDA_F32) return vec ? norm_typed<float, true>(a, st) : norm_typed<float, false>(a, st);
-  return vec ? norm_typed<__nv_bfloat16, true>(a, st) : norm_typed<__nv_bfloat16, false>(a, st);
+  return a.dtype == KDA_F32 ? norm_typed<float>(a, st) : norm_typed<__nv_bfloat16>(a, st);
 }
 
 size_t rms_norm_bwd_workspace(int64_t rows, int32_t cols) {
-  return align256(sizeof(float) * (size_t)(rows < kBwdParts ? rows : kBwdParts) * (size_t)cols);
+  return align256(sizeof(float) * (size_t)(rows < kMaxParts ? rows : kMaxParts) * (size_t)cols);
 }
 
 cudaError_t launch_rms_norm_bwd(const kda_rms_norm_bwd_args &a, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0;
-  if (a.dtype == KDA_F32) return vec ? bwd_typed<float, true>(a, st) : bwd_typed<float, false>(a, st);
-  return vec ? bwd_typed<__nv_bfloat16, true>(a, st) : bwd_typed<__nv_bfloat16, false>(a, st);
+  return a.dtype == KDA_F32 ? bwd_typed<float>(a, st) : bwd_typed<__nv_bfloat16>(a, st);
 }
 
 }  // namespace kda

@@ -46,7 +46,7 @@ def _check_fp8(m, y, rel):
 
 
 NORM_SHAPES = [(1, 1), (3, 7), (2, 128), (5, 130), (1, 4096), (33, 512), (17, 1111), (4, 2048),
-               (7, 4100), (2, 5000), (3, 16392), (2, 32768), (2, 32767)]
+               (7, 4100), (2, 5000), (3, 16392), (2, 32768), (2, 32767), (8001, 264), (4003, 1023)]
 
 
 @pytest.mark.parametrize("rows,cols", NORM_SHAPES)
