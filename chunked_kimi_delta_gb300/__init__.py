@@ -198,9 +198,15 @@ def _check(status: int, what: str):
 
 # ---------------------------------------------------------------- marshalling
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -885,7 +891,7 @@ def _check_fp8(x: Fp8Matrix, kind: str):
 
 
 def _check_weight(weight, cols):
-    if weight is not None and (tuple(weight.shape) != (cols,) or weight.dtype != _torch().float32):
+    if weight is not None and (weight.shape != (cols,) or weight.dtype != _torch().float32):
         raise ValueError("weight must be fp32 [cols]")
 
 

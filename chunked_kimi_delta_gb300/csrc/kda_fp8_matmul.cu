@@ -39,6 +39,13 @@ constexpr int SF_COLS = 16;       // tensor-memory columns of one ring entry: 4 
 constexpr int SF_RING = 4;
 constexpr uint32_t SF_ENTRY = 1536;  // bytes of an entry in shared memory: 512 lane side, 2 x 512 column side
 constexpr uint32_t SF_BYTES = SF_RING * SF_ENTRY;
+static_assert(SF_BYTES % 1024 == 0, "what follows the ring is aligned like a tile");
+// Blocks of k that tensor memory sums before an fp32 result takes the sum into
+// registers.  A step of the MMA (32 of k) rounds the running sum by about
+// 2^-24 of it; their number, not the size of k, then bounds the error
+// (relative 8e-7 at k = 8200 in one sum, 4e-7 in spans).  bf16 results
+// round at 2^-9 and take k in one span.
+constexpr int SPAN = 32;
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t LANE_BYTES = 16384;  // lane-side box: 128 x 128 bytes
 
@@ -53,8 +60,10 @@ struct MmArgs {
   uint32_t lane_step, col_step;  // descriptor units per 32 of k
   bool lane_mn, col_mn;          // MN-major operands
   int lane_tiles, tiles, splits;
+  int span;                  // blocks of k that one accumulator sums
   void *out;
   int64_t ldo;
+  bool out_tma;              // the output takes TMA stores (bf16, 16-byte rows)
   uint32_t *err;
   bool test_wait;
 };
@@ -114,6 +123,13 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
   return ok != 0;
+}
+
+__device__ __forceinline__ float4 load_peer(const float *p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(peer_addr(p, rank)));
+  return v;
 }
 
 // Bounded wait.  The first wait of a cluster that runs out records the
@@ -187,17 +203,6 @@ __device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map,
       :: "r"(tc::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
 // ---- scales
 // Rows past the edge take the last row's scale: it only reaches outputs that
 // are not stored.
@@ -270,14 +275,70 @@ struct MmaIssue {
   }
 };
 
-// 32 accumulator columns (rows m from m0 on, below `end`) of this warp's lanes (columns n).
+// 16 accumulator columns (rows m from m0 on, below `end`) of this warp's lanes (columns n).
 template <typename T>
-__device__ __forceinline__ void store_columns(const MmArgs &a, const uint32_t (&r)[32], int n, int m0, int end) {
+__device__ __forceinline__ void store_columns(const MmArgs &a, const float (&v)[16], int n, int m0, int end) {
   if (n >= a.lanes) return;
   T *p = static_cast<T *>(a.out) + (int64_t)m0 * a.ldo + n;
 #pragma unroll
-  for (int c = 0; c < 32; ++c)
-    if (m0 + c < end) p[c * a.ldo] = from_f32<T>(__uint_as_float(r[c]));
+  for (int c = 0; c < 16; ++c)
+    if (m0 + c < end) p[c * a.ldo] = from_f32<T>(v[c]);
+}
+// The same columns of one span of k: added to `sum`, which ends up in v.
+__device__ __forceinline__ void add_span(float (&sum)[16], float (&v)[16], bool first) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] = sum[c] = (first ? 0.f : sum[c]) + v[c];
+}
+
+// ---- bf16 results of a pair's tile through shared memory
+// 16 lanes x 32 columns of tensor memory as matrix fragments: register
+// 4 c + 2 h + i is lane 8 h + t / 4, column 8 c + 2 (t % 4) + i of thread t.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+constexpr uint32_t OUT_PANEL = 4096;               // 32 rows m x 64 columns n of bf16
+constexpr uint32_t OUT_BUF = 2 * OUT_PANEL;        // the 128 lanes
+constexpr uint32_t OUT_BYTES = 4 * OUT_BUF;        // two buffers for each half of the epilogue's warps
+// One warp's 32 lanes of a 32-row chunk into the staging tile: fragments are
+// stored transposed, so that a row m of shared memory holds neighbouring n.
+__device__ __forceinline__ void stage_chunk(uint32_t acc, uint8_t *buf, int quarter, int lane) {
+  uint32_t f[2][16];
+  tmem_ld_frag(acc, f[0]);
+  tmem_ld_frag(acc + (16u << 16), f[1]);
+  tc::tmem_ld_wait();
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n8 = 0; n8 < 2; ++n8) {
+      uint32_t v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(f[h][4 * c + 2 * n8]), __uint_as_float(f[h][4 * c + 2 * n8 + 1]));
+        v[c] = *reinterpret_cast<const uint32_t *>(&p);
+      }
+      // lane t gives the address of row m = t: 16 bytes of n, swizzled as the TMA store reads them
+      const uint32_t chunk = (uint32_t)(4 * quarter + 2 * h + n8);  // of eight columns n
+      const uint32_t addr = tc::smem_u32(buf) + (chunk >> 3) * OUT_PANEL + lane * 128 + (((chunk & 7) ^ (lane & 7)) << 4);
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                   :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    }
+}
+// Barrier of 128 threads, the AND of their flags returned to each.
+__device__ __forceinline__ bool half_and(bool v, int bar) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+               "selp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((uint32_t)v), "r"(bar) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               :: "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(src)) : "memory");
 }
 
 // The last arrivals of MMA commits on a ring: a CTA leaves only when none is
@@ -312,6 +373,7 @@ constexpr uint32_t PAIR_SF = 2 * PAIR_MAX_WIDTH;
 template <typename T>
 __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap lane_map,
                                                                           const __grid_constant__ CUtensorMap col_map,
+                                                                          const __grid_constant__ CUtensorMap out_map,
                                                                           const __grid_constant__ MmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars b;
@@ -371,24 +433,60 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
     if (ok) ring_drain(b.sf_empty, f, &b, a.err, 2);
     __syncwarp();
   } else if (warp < 8) {  // epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    const bool staged = a.out_tma && sizeof(T) == 2, issuer = (threadIdx.x & 127) == 0;
+    uint8_t *out_buf = sm + a.stages * a.stage_bytes + SF_BYTES + half * 2 * OUT_BUF;
+    auto half_sync = [&]() { asm volatile("bar.sync %0, 128;" :: "r"(1 + half) : "memory"); };
     Ring full(2);
-    for (int t = pair; t < a.tiles; t += pairs, full.next()) {
-      const int buf = full.s;
-      if (!__all_sync(~0u, mm_wait(b.acc_full + buf, full.phase, &b, a.err, 2))) break;
+    int buf = 0;
+    float sum[8][16];  // this thread's outputs over the spans of k, when there is more than one
+    for (int t = pair, kb = 0; t < a.tiles; full.next()) {
+      // one answer for the four warps that meet at a barrier
+      if (!half_and(mm_wait(b.acc_full + full.s, full.phase, &b, a.err, 2), 1 + half)) break;
       tc::tc_fence_after();
-      const int n = lane0_of(t) + 32 * (warp & 3) + lane;
-      const uint32_t acc = tmem + buf * PAIR_MAX_WIDTH + ((uint32_t)(32 * (warp & 3)) << 16);
-      const int chunks = a.width / 32;
-      for (int ch = warp >> 2; ch < chunks; ch += 2) {
-        uint32_t r[32];
-        tmem_ld32(acc + 32 * ch, r);
-        tc::tmem_ld_wait();
-        store_columns<T>(a, r, n, col0_of(t) + 32 * ch, min(a.cols, col0_of(t) + a.width));
+      const int l0 = lane0_of(t), c0 = col0_of(t);
+      const uint32_t acc = tmem + full.s * PAIR_MAX_WIDTH + ((uint32_t)(32 * quarter) << 16);
+      const int end = min(a.width, a.cols - c0);
+      const bool first = kb == 0, last = kb + a.span >= a.kblocks;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 32 * half + 64 * i;
+        if (c >= a.width) break;
+        if (staged) {
+          if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          half_sync();  // the buffer's last store has been read
+          stage_chunk(acc + c, out_buf + buf * OUT_BUF, quarter, lane);
+          tc::fence_proxy_async_smem();
+          half_sync();
+          if (issuer) {
+            if (c < end)
+              for (int p = 0; p < 2 && l0 + 64 * p < a.lanes; ++p)
+                tma_store_2d(&out_map, out_buf + buf * OUT_BUF + p * OUT_PANEL, l0 + 64 * p, c0 + c);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          buf ^= 1;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float v[16];
+            tc::tmem_ld16(acc + c + 16 * u, v);
+            tc::tmem_ld_wait();
+            if (sizeof(T) == 4 && !(first && last)) add_span(sum[2 * i + u], v, first);
+            if (last) store_columns<T>(a, v, l0 + 32 * quarter + lane, c0 + c + 16 * u, c0 + end);
+          }
+        }
       }
       tc::tc_fence_before();
-      if (lane == 0) arrive_remote(peer_addr(b.acc_empty + buf, 0));
+      if (lane == 0) arrive_remote(peer_addr(b.acc_empty + full.s, 0));
       __syncwarp();
+      kb += a.span;
+      if (last) {
+        kb = 0;
+        t += pairs;
+      }
     }
+    if (staged && issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   } else if (warp == 9) {  // TMA
     if (elect_one()) {
       Ring r(a.stages);
@@ -416,22 +514,24 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
       bool ok = !a.test_wait || mm_wait_slow(&b.never, 0, &b, a.err, 2, 1000000ull);
       const MmaIssue mma(a, sm);
       Ring r(a.stages), f(SF_RING), acc(2);
-      for (int t = pair; t < a.tiles && ok; t += pairs, acc.next()) {
+      int kb = 0;  // a tile is one span of k after another, an accumulator each
+      for (int t = pair; t < a.tiles && ok; kb = kb < a.kblocks ? kb : (t += pairs, 0), acc.next()) {
         ok = mm_wait(b.acc_empty + acc.s, acc.phase ^ 1, &b, a.err, 2);
         if (!ok) break;
         tc::tc_fence_after();
-        for (int kb = 0; kb < a.kblocks; kb += 4) {
+        const int span0 = kb, span1 = min(kb + a.span, a.kblocks);
+        for (; kb < span1; kb += 4) {
           ok = mm_wait(b.sf_full + f.s, f.phase, &b, a.err, 2) && mm_wait(b.sf_peer + f.s, f.phase, &b, a.err, 2);
           if (!ok) break;
           tc::fence_proxy_async_smem();
           copy_scales<true>(tmem + PAIR_SF + f.s * SF_COLS, tc::smem_u32(sf_ring) + f.s * SF_ENTRY, a.width);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (kb + i >= a.kblocks) break;
+            if (kb + i >= span1) break;
             ok = mm_wait(b.full + r.s, r.phase, &b, a.err, 2);
             if (!ok) break;
             tc::tc_fence_after();
-            mma.block<true>(tmem + acc.s * PAIR_MAX_WIDTH, r.s, tmem + PAIR_SF + f.s * SF_COLS, i, kb + i == 0);
+            mma.block<true>(tmem + acc.s * PAIR_MAX_WIDTH, r.s, tmem + PAIR_SF + f.s * SF_COLS, i, kb + i == span0);
             mm_commit<true>(b.empty + r.s);
             r.next();
           }
@@ -471,7 +571,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
 // shared memory and are added in the order of k.
 // Warps 0-3 epilogue, 4 scales, 5 TMA, 6 MMA.
 constexpr int SPLIT_THREADS = 224;
-constexpr int SPLIT_MAX_WIDTH = 128;
+constexpr int SPLIT_MAX_WIDTH = 64;
 constexpr uint32_t SPLIT_TMEM = 256;  // two CTAs fit an SM
 
 template <typename T>
@@ -487,7 +587,18 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
   const int l0 = (tile % a.lane_tiles) * 128, c0 = (tile / a.lane_tiles) * a.width;
   const int kb0 = (int)((int64_t)a.kblocks * rank / splits), kb1 = (int)((int64_t)a.kblocks * (rank + 1) / splits);
 
-  if (threadIdx.x == 0) {
+  // The CTAs of a cluster work by themselves until their sums meet: a wait
+  // that runs out ends this CTA's waits only.
+  auto issue_load = [&](int kb, int s) {
+    tc::mbar_arrive_expect_tx(b.full + s, LANE_BYTES + a.col_box_bytes);
+    uint8_t *dst = sm + s * a.stage_bytes;
+    const int k0 = kb * FP8_BLOCK;
+    tc::tma_load_2d(dst, &lane_map, b.full + s, a.lane_mn ? l0 : k0, a.lane_mn ? k0 : l0);
+    tc::tma_load_2d(dst + LANE_BYTES, &col_map, b.full + s, a.col_mn ? c0 : k0, a.col_mn ? k0 : c0);
+  };
+  if (threadIdx.x == 160) {  // the TMA warp fills the stages while the others set up
+    tc::tma_prefetch_desc(&lane_map);
+    tc::tma_prefetch_desc(&col_map);
     for (int i = 0; i < a.stages; ++i) {
       tc::mbar_init(b.full + i, 1);
       tc::mbar_init(b.empty + i, 1);
@@ -496,91 +607,110 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
       tc::mbar_init(b.sf_full + i, 64);
       tc::mbar_init(b.sf_empty + i, 1);
     }
-    tc::mbar_init(b.acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(b.acc_full + i, 1);
+      tc::mbar_init(b.acc_empty + i, 4);  // the four epilogue warps
+    }
     tc::mbar_init(&b.never, 1);
     b.abort = 0;
     tc::mbar_fence_init();
+    for (int kb = kb0; kb < kb1 && kb - kb0 < a.stages; ++kb) issue_load(kb, kb - kb0);
   }
   if (warp == 0) mm_alloc<false>(&b.tmem, SPLIT_TMEM);
   tc::tc_fence_before();
   __syncthreads();
-  if (splits > 1) cluster_sync();  // `abort` of every CTA is set before a peer may write it
   tc::tc_fence_after();
-  const uint32_t tmem = b.tmem, tmem_sf = tmem + SPLIT_MAX_WIDTH;
+  const uint32_t tmem = b.tmem, tmem_sf = tmem + 2 * SPLIT_MAX_WIDTH;
 
   uint8_t *sf_ring = sm + a.stages * a.stage_bytes;
   if (warp < 4) {
-    const bool ok = __all_sync(~0u, mm_wait(b.acc_full, 0, &b, a.err, splits));
-    tc::tc_fence_after();
     const int n = l0 + 32 * warp + lane;
-    float *part = reinterpret_cast<float *>(sm);  // [columns][128]: the stages are free now
+    float *part = reinterpret_cast<float *>(sm);  // [columns][128]: the stages are free after the last MMA
     const int valid = min(a.width, a.cols - c0);
-    if (ok)
-      for (int ch = 0; 32 * ch < valid; ++ch) {
-        uint32_t r[32];
-        tmem_ld32(tmem + 32 * ch + ((uint32_t)(32 * warp) << 16), r);
+    float sum[SPLIT_MAX_WIDTH / 16][16];  // this thread's sums over the spans of k, when there is more than one
+    Ring full(2);
+    for (int kb = kb0; kb < kb1; kb += a.span, full.next()) {
+      if (!__all_sync(~0u, mm_wait(b.acc_full + full.s, full.phase, &b, a.err, 1))) break;
+      tc::tc_fence_after();
+      const bool first = kb == kb0, last = kb + a.span >= kb1;
+#pragma unroll
+      for (int i = 0; i < SPLIT_MAX_WIDTH / 16; ++i) {
+        if (16 * i >= valid) break;
+        float v[16];
+        tc::tmem_ld16(tmem + full.s * SPLIT_MAX_WIDTH + 16 * i + ((uint32_t)(32 * warp) << 16), v);
         tc::tmem_ld_wait();
+        if (sizeof(T) == 4 && !(first && last)) add_span(sum[i], v, first);
+        if (!last) continue;
         if (splits == 1) {
-          store_columns<T>(a, r, n, c0 + 32 * ch, c0 + valid);
+          store_columns<T>(a, v, n, c0 + 16 * i, c0 + valid);
         } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (32 * ch + c < valid) part[(32 * ch + c) * 128 + 32 * warp + lane] = __uint_as_float(r[c]);
+          for (int c = 0; c < 16; ++c)
+            if (16 * i + c < valid) part[(16 * i + c) * 128 + 32 * warp + lane] = v[c];
         }
       }
-    tc::tc_fence_before();
+      tc::tc_fence_before();
+      if (lane == 0) tc::mbar_arrive(b.acc_empty + full.s);
+      __syncwarp();
+    }
   } else if (warp == 4) {
     Ring f(SF_RING);
     bool ok = true;
     uint32_t bytes = 0;
     for (int w = kb0 >> 2; 4 * w < kb1; ++w, f.next()) {
       if (a.tile_i && ((w & 7) == 0 || w == kb0 >> 2)) bytes = tile_bytes(a, l0, w >> 3, lane);
-      ok = __all_sync(~0u, mm_wait(b.sf_empty + f.s, f.phase ^ 1, &b, a.err, splits));
+      ok = __all_sync(~0u, mm_wait(b.sf_empty + f.s, f.phase ^ 1, &b, a.err, 1));
       if (!ok) break;
       fill_scales(a, sf_ring + f.s * SF_ENTRY, b.sf_full + f.s, l0, c0, w, bytes, lane);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (ok) ring_drain(b.sf_empty, f, &b, a.err, splits);
+    if (ok) ring_drain(b.sf_empty, f, &b, a.err, 1);
     __syncwarp();
   } else if (warp == 5) {
     if (elect_one()) {
       Ring r(a.stages);
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb, r.next()) {
-        ok = mm_wait(b.empty + r.s, r.phase ^ 1, &b, a.err, splits);
+        if (kb - kb0 < a.stages) continue;  // on its way
+        ok = mm_wait(b.empty + r.s, r.phase ^ 1, &b, a.err, 1);
         if (!ok) break;
-        tc::mbar_arrive_expect_tx(b.full + r.s, LANE_BYTES + a.col_box_bytes);
-        uint8_t *dst = sm + r.s * a.stage_bytes;
-        const int k0 = kb * FP8_BLOCK;
-        tc::tma_load_2d(dst, &lane_map, b.full + r.s, a.lane_mn ? l0 : k0, a.lane_mn ? k0 : l0);
-        tc::tma_load_2d(dst + LANE_BYTES, &col_map, b.full + r.s, a.col_mn ? c0 : k0, a.col_mn ? k0 : c0);
+        issue_load(kb, r.s);
       }
-      if (ok) ring_drain(b.empty, r, &b, a.err, splits);
+      if (ok) ring_drain(b.empty, r, &b, a.err, 1);
     }
     __syncwarp();
   } else {
     if (elect_one()) {
-      bool ok = !a.test_wait || mm_wait_slow(&b.never, 0, &b, a.err, splits, 1000000ull);
+      bool ok = !a.test_wait || mm_wait_slow(&b.never, 0, &b, a.err, 1, 1000000ull);
       const MmaIssue mma(a, sm);
-      Ring r(a.stages), f(SF_RING);
+      Ring r(a.stages), f(SF_RING), acc(2);
+      int in_span = 0;
       for (int kb = kb0; kb < kb1 && ok; ++kb, r.next()) {
+        if (in_span == 0) {
+          ok = mm_wait(b.acc_empty + acc.s, acc.phase ^ 1, &b, a.err, 1);
+          if (!ok) break;
+        }
         if (kb == kb0 || (kb & 3) == 0) {
-          ok = mm_wait(b.sf_full + f.s, f.phase, &b, a.err, splits);
+          ok = mm_wait(b.sf_full + f.s, f.phase, &b, a.err, 1);
           if (!ok) break;
           tc::fence_proxy_async_smem();
           copy_scales<false>(tmem_sf + f.s * SF_COLS, tc::smem_u32(sf_ring) + f.s * SF_ENTRY, a.width);
         }
-        ok = mm_wait(b.full + r.s, r.phase, &b, a.err, splits);
+        ok = mm_wait(b.full + r.s, r.phase, &b, a.err, 1);
         if (!ok) break;
         tc::tc_fence_after();
-        mma.block<false>(tmem, r.s, tmem_sf + f.s * SF_COLS, kb & 3, kb == kb0);
+        mma.block<false>(tmem + acc.s * SPLIT_MAX_WIDTH, r.s, tmem_sf + f.s * SF_COLS, kb & 3, in_span == 0);
         mm_commit<false>(b.empty + r.s);
         if ((kb & 3) == 3 || kb == kb1 - 1) {
           mm_commit<false>(b.sf_empty + f.s);
           f.next();
         }
+        if (++in_span == a.span || kb == kb1 - 1) {
+          mm_commit<false>(b.acc_full + acc.s);
+          acc.next();
+          in_span = 0;
+        }
       }
-      if (ok) mm_commit<false>(b.acc_full);
     }
     __syncwarp();
   }
@@ -590,19 +720,34 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
   if (splits == 1) return;
   cluster_sync();
   if (warp < 4 && !b.abort) {
-    // element e of the tile (column e / 128, lane e % 128): CTA (e / 128) % splits
-    const int n = l0 + (int)threadIdx.x;
-    const int valid = min(a.width, a.cols - c0);
-    for (int c = rank; c < valid; c += splits) {
-      const float *p = reinterpret_cast<const float *>(sm) + c * 128 + threadIdx.x;
-      float v[8], s = 0.f;
+    // Four columns at a time per CTA, a warp each, four lanes of the tile per
+    // thread; two of these in flight, since a load from a peer takes long.
+    const int valid = min(a.width, a.cols - c0), step = 4 * (int)splits;
+    const float *part = reinterpret_cast<const float *>(sm) + 4 * lane;
+    for (int c = 4 * (int)rank + warp; c < valid; c += 2 * step) {
+      float4 v[2][8];
 #pragma unroll
-      for (uint32_t r = 0; r < 8; ++r)
-        if (r < splits) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(peer_addr(p, r)));
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (uint32_t r = 0; r < 8; ++r)
-        if (r < splits) s += v[r];
-      if (n < a.lanes) static_cast<T *>(a.out)[(int64_t)(c0 + c) * a.ldo + n] = from_f32<T>(s);
+        for (uint32_t r = 0; r < 8; ++r)
+          if (r < splits && c + u * step < valid) v[u][r] = load_peer(part + (c + u * step) * 128, r);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (c + u * step >= valid) break;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r)
+          if (r < splits) {
+            s[0] += v[u][r].x;
+            s[1] += v[u][r].y;
+            s[2] += v[u][r].z;
+            s[3] += v[u][r].w;
+          }
+        T *p = static_cast<T *>(a.out) + (int64_t)(c0 + c + u * step) * a.ldo + l0 + 4 * lane;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (l0 + 4 * lane + q < a.lanes) p[q] = from_f32<T>(s[q]);
+      }
     }
   }
   __syncwarp();
@@ -620,9 +765,10 @@ uint32_t idesc_scaled(int M, int N, bool lane_mn, bool col_mn) {
 constexpr uint32_t SMEM_LIMIT = 227 * 1024 - 1024 - sizeof(Bars);  // dynamic, after alignment
 
 template <typename T>
-cudaError_t launch_pair(const CUtensorMap &lm, const CUtensorMap &cm, const MmArgs &a, cudaStream_t st) {
+cudaError_t launch_pair(const CUtensorMap &lm, const CUtensorMap &cm, const CUtensorMap &om, const MmArgs &a,
+                        cudaStream_t st) {
   auto kern = fp8_matmul_pair_kernel<T>;
-  const int smem = (int)(a.stages * a.stage_bytes + SF_BYTES + 1024);
+  const int smem = (int)(a.stages * a.stage_bytes + SF_BYTES + (a.out_tma ? OUT_BYTES : 0) + 1024);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -636,7 +782,7 @@ cudaError_t launch_pair(const CUtensorMap &lm, const CUtensorMap &cm, const MmAr
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, lm, cm, a);
+  return cudaLaunchKernelEx(&cfg, kern, lm, cm, om, a);
 }
 
 template <typename T>
@@ -662,6 +808,27 @@ cudaError_t launch_split(const CUtensorMap &lm, const CUtensorMap &cm, const MmA
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+struct Plan {
+  bool pair;
+  int width, splits;
+};
+
+// Pairs of CTAs take 256 x 224 tiles when there is one for each of the 76
+// pairs.  Fewer tiles leave pairs idle, and 128 x 64 ones for single CTAs,
+// two to an SM, are then as fast or faster (us, pairs at their best width
+// against single CTAs: 777 x 1111 x 2064 10.8 / 9.8, 512 x 4096 x 4096 13.9 /
+// 14.8, 300 x 1024 x 1024 7.5 / 6.8).  Where those do not fill the SMs, k is
+// split while a part keeps at least four blocks: a smaller part costs more in
+// the meeting of the sums than it saves (1 x 4096 x 4096: 8.5 us in 2 parts,
+// 7.1 in 4, 6.9 in 8).
+Plan choose_plan(int m, int n, int kblocks) {
+  if ((int64_t)ceil_div(n, 256) * ceil_div(m, PAIR_MAX_WIDTH) >= 76) return {true, PAIR_MAX_WIDTH, 1};
+  Plan p{false, m <= 16 ? 16 : m <= 32 ? 32 : SPLIT_MAX_WIDTH, 1};
+  const int64_t tiles = (int64_t)ceil_div(n, 128) * ceil_div(m, p.width);
+  while (p.splits < 8 && 8 * p.splits <= kblocks && tiles * p.splits * 2 <= 152) p.splits *= 2;
+  return p;
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
@@ -683,42 +850,41 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   a.err = static_cast<uint32_t *>(p.workspace);
   a.test_wait = (p.flags & KDA_TEST_WAIT_TIMEOUT) != 0;
 
-  // Pairs when they have tiles for half of the GPU's 76 pairs, clusters that split k otherwise.
-  const int64_t pair_tiles = (int64_t)ceil_div(p.n, 256) * ceil_div(p.m, PAIR_MAX_WIDTH);
-  const bool pair = pair_tiles >= 38;
-  if (pair) {
-    a.width = PAIR_MAX_WIDTH;
-    a.lane_tiles = ceil_div(p.n, 256);
-    a.splits = 1;
-  } else {
-    a.width = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : SPLIT_MAX_WIDTH;
-    a.lane_tiles = ceil_div(p.n, 128);
-  }
-  const int box_rows = pair ? a.width / 2 : a.width;  // column-side rows of one CTA
+  const Plan plan = choose_plan(p.m, p.n, a.kblocks);
+  const bool pair = plan.pair;
+  a.width = plan.width;
+  a.splits = plan.splits;
+  a.span = p.out_dtype == KDA_F32 ? SPAN : a.kblocks;
+  a.lane_tiles = ceil_div(p.n, pair ? 256 : 128);
   a.tiles = a.lane_tiles * ceil_div(p.m, a.width);
+  const int box_rows = pair ? a.width / 2 : a.width;  // column-side rows of one CTA
   a.col_box_bytes = a.col_mn ? 16384 : (uint32_t)box_rows * 128;
   a.stage_bytes = LANE_BYTES + ((a.col_box_bytes + 1023) & ~1023u);
-  if (!pair) {
-    a.splits = 1;
-    while (a.splits < 8 && a.splits * 2 <= a.kblocks && (int64_t)a.tiles * a.splits * 2 <= 304) a.splits *= 2;
-  }
-  const int per_cta = ceil_div(a.kblocks, a.splits);
-  // pairs have the SM to themselves; split CTAs share it two by two
-  const uint32_t budget = pair ? SMEM_LIMIT - SF_BYTES : (SMEM_LIMIT - 1024 - (uint32_t)sizeof(Bars)) / 2 - 1024 - SF_BYTES;
+  const int64_t row_bytes = p.ldo * 2;
+  a.out_tma = pair && p.out_dtype == KDA_BF16 && row_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
+              p.ldo <= INT32_MAX;
+  // a pair has its SMs to itself, and so do split CTAs when there is one for each; else two share
+  const bool alone = pair || (int64_t)a.tiles * a.splits <= 152;
+  uint32_t budget = SMEM_LIMIT - SF_BYTES - (a.out_tma ? OUT_BYTES : 0);
+  if (!alone) budget = (SMEM_LIMIT - 1024 - (uint32_t)sizeof(Bars)) / 2 - 1024 - SF_BYTES;
   a.stages = (int)(budget / a.stage_bytes);
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
-  if (!pair && a.stages > per_cta) a.stages = per_cta;
-  if (!pair && a.stages * a.stage_bytes < (uint32_t)a.width * 512) a.stages = ceil_div(a.width * 512, a.stage_bytes);
+  if (!pair) {
+    const int per_cta = ceil_div(a.kblocks, a.splits);
+    if (a.stages > per_cta) a.stages = per_cta;
+    if (a.stages * a.stage_bytes < (uint32_t)a.width * 512) a.stages = ceil_div(a.width * 512, a.stage_bytes);
+  }
   a.idesc = idesc_scaled(pair ? 256 : 128, a.width, a.lane_mn, a.col_mn);
 
-  CUtensorMap lm, cm;
+  CUtensorMap lm, cm, om{};
   const bool ok = (a.lane_mn ? tcp::make_byte_map(p.b, p.n, p.k, p.ldb, 128, lm)
                              : tcp::make_byte_map(p.b, p.k, p.n, p.ldb, 128, lm)) &&
                   (a.col_mn ? tcp::make_byte_map(p.a, p.m, p.k, p.lda, 128, cm)
-                            : tcp::make_byte_map(p.a, p.k, p.m, p.lda, (uint32_t)box_rows, cm));
+                            : tcp::make_byte_map(p.a, p.k, p.m, p.lda, (uint32_t)box_rows, cm)) &&
+                  (!a.out_tma || tcp::make_bf16_map(p.out, p.n, p.m, p.ldo, 32, om));
   if (!ok) return cudaErrorInvalidValue;
   if (pair)
-    return p.out_dtype == KDA_F32 ? launch_pair<float>(lm, cm, a, st) : launch_pair<__nv_bfloat16>(lm, cm, a, st);
+    return p.out_dtype == KDA_F32 ? launch_pair<float>(lm, cm, om, a, st) : launch_pair<__nv_bfloat16>(lm, cm, om, a, st);
   return p.out_dtype == KDA_F32 ? launch_split<float>(lm, cm, a, st) : launch_split<__nv_bfloat16>(lm, cm, a, st);
 }
 

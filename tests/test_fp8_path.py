@@ -235,7 +235,9 @@ def _product(form, a, b):
 # scale word or not, long sums over few outputs, and one with several tiles in flight per SM
 MM_SHAPES = [(1, 1, 1), (1, 256, 512), (2, 130, 100), (16, 128, 128), (17, 129, 129), (64, 384, 640),
              (100, 200, 300), (128, 128, 1024), (255, 257, 520), (300, 1111, 2064), (5, 4100, 384),
-             (1000, 136, 1288), (9, 100, 8200), (2500, 2600, 272)]
+             (1000, 136, 1288), (9, 100, 8200), (2500, 2600, 272),
+             # sums long enough to be taken out of tensor memory in between: k split or not, and pairs
+             (3, 130, 34000), (640, 1300, 4200), (2500, 2600, 8400)]
 
 
 @pytest.mark.parametrize("m,n,k", MM_SHAPES)
