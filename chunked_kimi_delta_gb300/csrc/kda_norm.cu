@@ -5,21 +5,22 @@
 //   dx = rstd (w g - n mean(w g n)) + d,  dw = sum over rows of g n,  n = h rstd
 //
 // Both read every element once and write it once, so memory bounds them; what
-// costs is the wait for a row's sum between its loads and its stores.  CTAs
-// are persistent and walk the rows with a stride of the grid; each thread
-// copies its own columns of the rows to come into shared memory (cp.async,
-// kDepth rows ahead) and no thread reads another's copies, so the copies need
-// no barrier and stay in flight while a row's sum is formed.
+// costs is the wait for a row's sum between its loads and its stores.  Teams
+// of threads (a CTA, or a warp for rows of up to 1,024 columns) are
+// persistent and walk the rows; each thread copies its own columns of the rows
+// to come into shared memory (cp.async, kDepth rows ahead) and no thread reads
+// another's copies, so the copies need no barrier and stay in flight while a
+// row's sum is formed.
 #include "kda_fp8.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kDepth = 3;  // rows in flight per CTA
+constexpr int kDepth = 2;  // rows in flight per team
 
 // How a row's columns are read and which thread holds them.
-//   RING    cp.async into shared memory, kDepth rows ahead; thread t holds
-//           columns 8 (t + i threads) .. + 7
+//   RING    cp.async into shared memory, kDepth rows ahead; thread t of a team
+//           holds columns 8 (t + i team) .. + 7
 //   DIRECT  16-byte loads straight to registers: rows too wide for the ring
 //   ODD     rows that do not start on 16 bytes (cols % 8 != 0): one element at
 //           a time, column 16 j + t % 16 of the group, so that 16 lanes read
@@ -46,8 +47,8 @@ __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16> &r, float (&f)[8
 }
 
 // Eight elements of a row of `cols` for this thread's i-th place.
-template <Mode M> __device__ __forceinline__ int first_col(int i) {
-  const int t = threadIdx.x + i * blockDim.x;
+template <Mode M, bool WARP> __device__ __forceinline__ int first_col(int i) {
+  const int t = WARP ? (threadIdx.x & 31) + i * 32 : threadIdx.x + i * blockDim.x;
   return M == ODD ? (t >> 4) * FP8_BLOCK + (t & 15) : 8 * t;
 }
 constexpr int kOddStep = 16;
@@ -70,6 +71,15 @@ template <typename T, Mode M> __device__ __forceinline__ void store(T *row, int 
   }
 }
 
+template <Mode M> __device__ __forceinline__ void load_weight(const float *w, int c, int cols, float (&f)[8]) {
+  if (w) {
+    load<float, M>(w, c, cols, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 1.f;
+  }
+}
+
 // The ring of one tensor: thread-private slots of eight elements.
 template <typename T> __device__ __forceinline__ void copy_ahead(Raw<T> *slot, const T *src) {
   const uint32_t d = (uint32_t)__cvta_generic_to_shared(slot);
@@ -81,14 +91,15 @@ template <typename T> __device__ __forceinline__ void copy_ahead(Raw<T> *slot, c
 __device__ __forceinline__ void commit_ahead() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_oldest() { asm volatile("cp.async.wait_group %0;" :: "n"(kDepth - 1) : "memory"); }
 
-// Sums over the CTA's threads, the same values in all of them: shuffles
+// Sums over the team's threads, the same values in all of them: shuffles
 // inside a warp, then the warps' sums in order.  `red` alternates between two
 // buffers from call to call, so one barrier is enough.
-template <int N> __device__ __forceinline__ void cta_sums(float (&v)[N], float (*red)[32]) {
+template <bool WARP, int N> __device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[32]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(~0u, v[n], o);
+  if (WARP) return;
   const int warps = blockDim.x >> 5;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -101,8 +112,8 @@ template <int N> __device__ __forceinline__ void cta_sums(float (&v)[N], float (
     for (int n = 0; n < N; ++n) v[n] += red[n][i];
 }
 
-template <typename T, Mode M, int VPT>
-__global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_kernel(kda_rms_norm_args a) {
+template <typename T, Mode M, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : M == RING ? 512 : 1024) rms_norm_kernel(kda_rms_norm_args a) {
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][1][32];
   const int cols = a.cols, blocks = (cols + FP8_BLOCK - 1) / FP8_BLOCK;
@@ -115,7 +126,7 @@ __global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_kernel(kda_rm
     if (row < a.rows) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = first_col<M>(i);
+        const int c = first_col<M, WARP>(i);
         if (c >= cols) continue;
         copy_ahead(slot(stage, 0, i), x + row * cols + c);
         if (res) copy_ahead(slot(stage, 1, i), res + row * cols + c);
@@ -123,14 +134,22 @@ __global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_kernel(kda_rm
     }
     commit_ahead();
   };
-  for (int s = 0; s < kDepth; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  const int teams = WARP ? blockDim.x >> 5 : 1;
+  const int64_t row0 = WARP ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = (int64_t)gridDim.x * teams;
+  for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
+  float w[M == RING ? VPT : 1][8];  // the ring's threads keep their columns' weights
+  if (M == RING) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) load_weight<M>(a.weight, first_col<M, WARP>(i), cols, w[i]);
+  }
   int stage = 0, parity = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  for (int64_t row = row0; row < a.rows; row += step) {
     float h[VPT][8], sums[1] = {0.f};
     if (M == RING) wait_oldest();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = first_col<M>(i);
+      const int c = first_col<M, WARP>(i);
       float r[8];
       if (M == RING) {
         if (c < cols) {
@@ -152,24 +171,19 @@ __global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_kernel(kda_rm
 #pragma unroll
       for (int j = 0; j < 8; ++j) sums[0] = fmaf(h[i][j], h[i][j], sums[0]);
     }
-    cta_sums(sums, red[parity]);
+    team_sums<WARP>(sums, red[parity]);
     parity ^= 1;
     // every thread has used its slots: the sum needed them
-    fetch(row + (int64_t)kDepth * gridDim.x, stage);
+    fetch(row + kDepth * step, stage);
     stage = stage == kDepth - 1 ? 0 : stage + 1;
     const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = first_col<M>(i);
+      const int c = first_col<M, WARP>(i);
       float y[8];
-      if (a.weight) {
-        load<float, M>(a.weight, c, cols, y);
+      if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= h[i][j] * rstd;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd;
-      }
+      for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * w[M == RING ? i : 0][j];
       if (a.out) store<T, M>(static_cast<T *>(a.out) + row * cols, c, cols, y);
       if (a.fp8) {
         float m = block_amax(y);
@@ -202,12 +216,12 @@ __global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_kernel(kda_rm
 
 // ------------------------------------------------------------------ backward
 
-constexpr int kMaxParts = 608;  // partial dweight rows at most: 4 CTAs on each of 152 SMs
+constexpr int kMaxParts = 1216;  // partial dweight rows at most: 8 CTAs on each of 152 SMs
 
-// dweight of a CTA's rows is summed in its registers and left as one row of
+// dweight of a team's rows is summed in its registers; a CTA leaves one row of
 // partial sums.
-template <typename T, Mode M, int VPT>
-__global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
+template <typename T, Mode M, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : M == RING ? 512 : 1024) rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][2][32];
   const int cols = a.cols;
@@ -221,7 +235,7 @@ __global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_bwd_kernel(kd
     if (row < a.rows) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = first_col<M>(i);
+        const int c = first_col<M, WARP>(i);
         if (c >= cols) continue;
         copy_ahead(slot(stage, 0, i), hp + row * cols + c);
         copy_ahead(slot(stage, 1, i), gp + row * cols + c);
@@ -235,9 +249,17 @@ __global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_bwd_kernel(kd
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-  for (int s = 0; s < kDepth; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  const int teams = WARP ? blockDim.x >> 5 : 1;
+  const int64_t row0 = WARP ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = (int64_t)gridDim.x * teams;
+  for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
+  float w[M == RING ? VPT : 1][8];
+  if (M == RING) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) load_weight<M>(a.weight, first_col<M, WARP>(i), cols, w[i]);
+  }
   int stage = 0, parity = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  for (int64_t row = row0; row < a.rows; row += step) {
     float sums[2] = {0.f, 0.f};
     if (M == RING) wait_oldest();
     // h and g are read again after the sum, from the ring or the caches: kept
@@ -254,107 +276,141 @@ __global__ void __launch_bounds__(M == RING ? 512 : 1024) rms_norm_bwd_kernel(kd
     };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = first_col<M>(i);
-      float h[8], g[8], w[8];
+      const int c = first_col<M, WARP>(i);
+      float h[8], g[8];
       get(0, hp, i, c, h);
       get(1, gp, i, c, g);
-      if (a.weight) load<float, M>(a.weight, c, cols, w);
+      if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sums[0] = fmaf(h[j], h[j], sums[0]);
-        sums[1] = fmaf(a.weight ? g[j] * w[j] : g[j], h[j], sums[1]);
+        sums[1] = fmaf(g[j] * w[M == RING ? i : 0][j], h[j], sums[1]);
       }
     }
-    cta_sums(sums, red[parity]);
+    team_sums<WARP>(sums, red[parity]);
     parity ^= 1;
     const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
     const float mean = sums[1] * rstd / (float)cols;  // mean of weight * d_out * n
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = first_col<M>(i);
-      float h[8], g[8], w[8], d[8], dx[8];
+      const int c = first_col<M, WARP>(i);
+      float h[8], g[8], d[8], dx[8];
       get(0, hp, i, c, h);
       get(1, gp, i, c, g);
-      if (a.weight) load<float, M>(a.weight, c, cols, w);
+      if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
       if (dp) get(2, dp, i, c, d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float n = h[j] * rstd;
         dw[i][j] = fmaf(g[j], n, dw[i][j]);
-        dx[j] = rstd * ((a.weight ? g[j] * w[j] : g[j]) - n * mean);
+        dx[j] = rstd * (g[j] * w[M == RING ? i : 0][j] - n * mean);
         if (dp) dx[j] += d[j];
       }
       store<T, M>(static_cast<T *>(a.dx) + row * cols, c, cols, dx);
     }
     // this thread has used its slots: its stores needed them
-    fetch(row + (int64_t)kDepth * gridDim.x, stage);
+    fetch(row + kDepth * step, stage);
     stage = stage == kDepth - 1 ? 0 : stage + 1;
   }
-  if (a.dweight) {
-    float *part = static_cast<float *>(a.workspace) + (int64_t)blockIdx.x * cols;
+  if (!a.dweight) return;
+  float *part = static_cast<float *>(a.workspace) + (int64_t)blockIdx.x * cols;
+  if (!WARP) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) store<float, M>(part, first_col<M>(i), cols, dw[i]);
+    for (int i = 0; i < VPT; ++i) store<float, M>(part, first_col<M, WARP>(i), cols, dw[i]);
+    return;
   }
+  // the warps' sums, in their order, through shared memory
+  float *sum = reinterpret_cast<float *>(smem_raw);
+  for (int v = 0; v < teams; ++v) {
+    __syncthreads();
+    if ((int)(threadIdx.x >> 5) != v) continue;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = first_col<M, WARP>(i);
+      float f[8];
+      load<float, M>(sum, c, cols, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = v ? f[j] + dw[i][j] : dw[i][j];
+      store<float, M>(sum, c, cols, f);
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < cols; c += blockDim.x) part[c] = sum[c];
 }
 
-// dweight[c] = the sum of the partial rows: 32 columns x 32 row lanes per CTA,
-// each lane in row order, then the lanes in order.
-__global__ void __launch_bounds__(1024) dweight_kernel(const float *__restrict__ part, int parts, int cols,
-                                                       float *__restrict__ dw) {
-  __shared__ float s[32][33];
-  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+// dweight[c] = the sum of the partial rows: 8 columns x 64 row lanes per CTA
+// (a CTA of 32 columns leaves too few of them), each lane in row order, then
+// the lanes of a warp pairwise, then the warps in order.
+constexpr int kSumThreads = 512;
+__global__ void __launch_bounds__(kSumThreads) dweight_kernel(const float *__restrict__ part, int parts, int cols,
+                                                              float *__restrict__ dw) {
+  __shared__ float s[kSumThreads / 32][8];
+  const int col = threadIdx.x & 7, c = blockIdx.x * 8 + col;
   float v = 0.f;
   if (c < cols) {
 #pragma unroll 4
-    for (int p = r; p < parts; p += 32) v += part[(int64_t)p * cols + c];
+    for (int p = threadIdx.x >> 3; p < parts; p += kSumThreads / 8) v += part[(int64_t)p * cols + c];
   }
-  s[r][lane] = v;
+  v += __shfl_xor_sync(~0u, v, 8);
+  v += __shfl_xor_sync(~0u, v, 16);
+  if ((threadIdx.x & 31) < 8) s[threadIdx.x >> 5][col] = v;
   __syncthreads();
-  if (r == 0 && c < cols) {
+  if (threadIdx.x < 8 && c < cols) {
+    v = 0.f;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) v += s[i][lane];
+    for (int i = 0; i < kSumThreads / 32; ++i) v += s[i][col];
     dw[c] = v;
   }
 }
 
 // ------------------------------------------------------------------ launch
 
-// Threads for `vecs` groups of eight columns at vpt of them a thread.
-int threads_for(int vecs, int vpt) { return ((vecs + vpt - 1) / vpt + 31) / 32 * 32; }
-
 struct Shape {
   Mode mode;
+  bool warp;
   int vpt, threads, grid;
   size_t smem;
 };
 
-// `tensors` of `esize` bytes an element travel through the ring.  Rows fit it
-// while kDepth of them leave room for two CTAs' worth of threads at vpt 2;
-// then as many CTAs as shared memory and 1,024 threads an SM hold (96 KB of
-// rows in flight an SM cover the latency of memory at full bandwidth).
-Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize) {
+// `vecs` groups of eight columns a row, of which `tensors` x `esize` bytes an
+// element travel through the ring; a CTA's threads take two each from `wide`
+// of them on, else one; `per_sm_threads`: the threads an SM's registers hold.
+//
+// Warps take a row each up to 512 columns, and up to 1,024 in the ring
+// (32768 rows of bf16, forward / backward: 512 columns 21.6 / 28.5 us with a
+// warp a row, 24.1 / 35.1 with a CTA; 1,024 columns 38 / 50 and 42 / 59;
+// odd rows of 903 columns 52 / 90 and 43 / 60).
+Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wide, int per_sm_threads) {
   Shape s{};
-  s.vpt = vecs <= 64 ? 1 : 2;
-  s.threads = threads_for(vecs, s.vpt);
-  s.smem = (size_t)kDepth * tensors * s.vpt * s.threads * 8 * esize;
-  if (cols % 8 != 0) s.mode = ODD;
-  else if (s.threads <= 512 && s.smem <= 200 * 1024) s.mode = RING;
-  else s.mode = DIRECT;
-  int per_sm;
-  if (s.mode == RING) {
-    per_sm = (int)(227 * 1024 / (s.smem + 2048));
-    if (per_sm > 1024 / s.threads) per_sm = 1024 / s.threads;
+  s.mode = cols % 8 != 0 ? ODD : RING;
+  s.warp = vecs <= (s.mode == ODD ? 64 : 128);
+  auto cta = [&](int vpt) {
+    s.vpt = vpt;
+    s.threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
+  };
+  if (s.warp) {
+    s.vpt = vecs <= 64 ? 2 : 4;
+    s.threads = 256;
+    if (s.vpt == 4) per_sm_threads = 512;
   } else {
-    s.vpt = vecs <= 1024 ? 1 : 4;
-    s.threads = threads_for(vecs, s.vpt);
-    s.smem = 0;
+    cta(vecs < wide ? 1 : 2);
+  }
+  s.smem = (size_t)kDepth * tensors * s.vpt * s.threads * 8 * esize;
+  // rows too wide for two of them in shared memory, or for 512 threads: straight from memory
+  if (s.mode == RING && (s.threads > 512 || s.smem > 200 * 1024)) s.mode = DIRECT;
+  int per_sm = per_sm_threads / s.threads;
+  if (s.mode == RING) {
+    const int fit = (int)(227 * 1024 / (s.smem + 2048));
+    per_sm = fit < per_sm ? fit : per_sm;
+  } else {
+    s.smem = s.warp ? 4096 : 0;  // the backward's sums over warps
+    if (!s.warp) cta(vecs <= 1024 ? 1 : 4);
     per_sm = 2048 / s.threads;
   }
   if (per_sm < 1) per_sm = 1;
-  if (per_sm > 8) per_sm = 8;
-  const int64_t most = 152 * (int64_t)per_sm;
-  s.grid = (int)(rows < most ? rows : most);
+  const int64_t teams = s.warp ? s.threads / 32 : 1, most = 152 * (int64_t)per_sm;
+  const int64_t need = (rows + teams - 1) / teams;
+  s.grid = (int)(need < most ? need : most);
   return s;
 }
 
@@ -370,27 +426,35 @@ cudaError_t launch_rows(K kern, const Shape &s, const A &a, cudaStream_t st) {
 
 template <typename T> cudaError_t norm_typed(const kda_rms_norm_args &a, cudaStream_t st) {
   // whole groups of four blocks, so that the scales past the last block get written
-  const Shape s = shape_for(a.rows, a.cols, (a.cols + 511) / 512 * 64, a.residual ? 2 : 1, sizeof(T));
-  if (s.mode == RING)
-    return s.vpt == 1 ? launch_rows(rms_norm_kernel<T, RING, 1>, s, a, st) : launch_rows(rms_norm_kernel<T, RING, 2>, s, a, st);
-  if (s.mode == DIRECT)
-    return s.vpt == 1 ? launch_rows(rms_norm_kernel<T, DIRECT, 1>, s, a, st) : launch_rows(rms_norm_kernel<T, DIRECT, 4>, s, a, st);
-  return s.vpt == 1 ? launch_rows(rms_norm_kernel<T, ODD, 1>, s, a, st) : launch_rows(rms_norm_kernel<T, ODD, 4>, s, a, st);
+  const Shape s = shape_for(a.rows, a.cols, (a.cols + 511) / 512 * 64, a.residual ? 2 : 1, sizeof(T), 0, 1024);
+#define KDA_NORM(M_, V_, W_) return launch_rows(rms_norm_kernel<T, M_, V_, W_>, s, a, st)
+  if (s.warp) {
+    if (s.mode == RING) { if (s.vpt == 2) KDA_NORM(RING, 2, true); else KDA_NORM(RING, 4, true); }
+    KDA_NORM(ODD, 2, true);
+  }
+  if (s.mode == RING) KDA_NORM(RING, 2, false);
+  if (s.mode == DIRECT) { if (s.vpt == 1) KDA_NORM(DIRECT, 1, false); else KDA_NORM(DIRECT, 4, false); }
+  if (s.vpt == 1) KDA_NORM(ODD, 1, false); else KDA_NORM(ODD, 4, false);
+#undef KDA_NORM
 }
 
 template <typename T> cudaError_t bwd_typed(const kda_rms_norm_bwd_args &a, cudaStream_t st) {
   // whole groups of 16 threads: the odd layout spreads a block over them
-  Shape s = shape_for(a.rows, a.cols, (a.cols + 127) / 128 * 16, a.d_residual ? 3 : 2, sizeof(T));
+  Shape s = shape_for(a.rows, a.cols, (a.cols + 127) / 128 * 16, a.d_residual ? 3 : 2, sizeof(T), 257, 768);
   if (s.grid > kMaxParts) s.grid = kMaxParts;
   cudaError_t e;
-  if (s.mode == RING)
-    e = s.vpt == 1 ? launch_rows(rms_norm_bwd_kernel<T, RING, 1>, s, a, st) : launch_rows(rms_norm_bwd_kernel<T, RING, 2>, s, a, st);
-  else if (s.mode == DIRECT)
-    e = s.vpt == 1 ? launch_rows(rms_norm_bwd_kernel<T, DIRECT, 1>, s, a, st) : launch_rows(rms_norm_bwd_kernel<T, DIRECT, 4>, s, a, st);
-  else
-    e = s.vpt == 1 ? launch_rows(rms_norm_bwd_kernel<T, ODD, 1>, s, a, st) : launch_rows(rms_norm_bwd_kernel<T, ODD, 4>, s, a, st);
+#define KDA_BWD(M_, V_, W_) e = launch_rows(rms_norm_bwd_kernel<T, M_, V_, W_>, s, a, st)
+  if (s.warp) {
+    if (s.mode == RING) { if (s.vpt == 2) KDA_BWD(RING, 2, true); else KDA_BWD(RING, 4, true); }
+    else KDA_BWD(ODD, 2, true);
+  }
+  else if (s.mode == RING) { if (s.vpt == 1) KDA_BWD(RING, 1, false); else KDA_BWD(RING, 2, false); }
+  else if (s.mode == DIRECT) { if (s.vpt == 1) KDA_BWD(DIRECT, 1, false); else KDA_BWD(DIRECT, 4, false); }
+  else if (s.vpt == 1) KDA_BWD(ODD, 1, false);
+  else KDA_BWD(ODD, 4, false);
+#undef KDA_BWD
   if (e != cudaSuccess || !a.dweight) return e;
-  dweight_kernel<<<(a.cols + 31) / 32, 1024, 0, st>>>(static_cast<const float *>(a.workspace), s.grid, a.cols, a.dweight);
+  dweight_kernel<<<(a.cols + 7) / 8, kSumThreads, 0, st>>>(static_cast<const float *>(a.workspace), s.grid, a.cols, a.dweight);
   return cudaGetLastError();
 }
 

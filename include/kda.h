@@ -570,7 +570,7 @@ kda_status kda_rms_norm_bwd(const kda_rms_norm_bwd_args *args, kda_stream_t stre
  * [rows, ld] in x's own orientation with its own scales.  rows == 0 or cols
  * == 0 launches nothing.  Errors: KDA_ERR_INVALID_ARG (rows or cols < 0, no
  * kind, values without scales, null x, ld < cols), KDA_ERR_UNSUPPORTED (more
- * than 2^31 - 1 blocks), KDA_ERR_ALIGNMENT (pointers, ld % 16), KDA_ERR_CUDA.
+ * than 2^30 - 1 blocks), KDA_ERR_ALIGNMENT (pointers, ld % 16), KDA_ERR_CUDA.
  */
 typedef struct {
   int64_t rows;
