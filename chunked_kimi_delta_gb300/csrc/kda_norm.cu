@@ -28,24 +28,6 @@ constexpr int kDepth = 2;  // rows in flight per team
 // In all three, 16 neighbouring lanes hold the 128 columns of one scale.
 enum Mode { RING, DIRECT, ODD };
 
-template <typename T> struct Raw;  // eight elements as stored
-template <> struct Raw<float> { uint4 v[2]; };
-template <> struct Raw<__nv_bfloat16> { uint4 v[1]; };
-
-__device__ __forceinline__ void unpack(const Raw<float> &r, float (&f)[8]) {
-  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
-}
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16> &r, float (&f)[8]) {
-  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {  // bf16 is the upper half of an fp32
-    f[2 * j] = __uint_as_float(w[j] << 16);
-    f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
-}
-
 // Eight elements of a row of `cols` for this thread's i-th place.
 template <Mode M, bool WARP> __device__ __forceinline__ int first_col(int i) {
   const int t = WARP ? (threadIdx.x & 31) + i * 32 : threadIdx.x + i * blockDim.x;
@@ -53,38 +35,33 @@ template <Mode M, bool WARP> __device__ __forceinline__ int first_col(int i) {
 }
 constexpr int kOddStep = 16;
 
-template <typename T, Mode M> __device__ __forceinline__ void load(const T *row, int c, int cols, float (&f)[8]) {
-  if (M == ODD) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c + kOddStep * j < cols ? to_f32<T>(row[c + kOddStep * j]) : 0.f;
-  } else {
-    load8<T, true>(row + c, cols - c, f);
-  }
+template <typename T, Mode M> __device__ __forceinline__ Raw8<T> load(const T *row, int c, int cols) {
+  if (M == ODD) return raw_gather<T>(row + c, kOddStep, cols - c);
+  return c < cols ? raw_load<T>(row + c) : raw_zero<T>();
 }
-template <typename T, Mode M> __device__ __forceinline__ void store(T *row, int c, int cols, const float (&f)[8]) {
-  if (M == ODD) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + kOddStep * j < cols) row[c + kOddStep * j] = from_f32<T>(f[j]);
-  } else {
-    store8<T, true>(row + c, cols - c, f);
-  }
+template <typename T, Mode M> __device__ __forceinline__ void store(T *row, int c, int cols, const Raw8<T> &r) {
+  if (M == ODD) raw_scatter<T>(row + c, kOddStep, cols - c, r);
+  else if (c < cols) raw_store<T>(row + c, r);
 }
-
-template <Mode M> __device__ __forceinline__ void load_weight(const float *w, int c, int cols, float (&f)[8]) {
+template <typename T, Mode M> __device__ __forceinline__ void store(T *row, int c, int cols, const float2 (&f)[4]) {
+  Raw8<T> r;
+  r.put(f);
+  store<T, M>(row, c, cols, r);
+}
+template <Mode M> __device__ __forceinline__ void load_weight(const float *w, int c, int cols, float2 (&f)[4]) {
   if (w) {
-    load<float, M>(w, c, cols, f);
+    load<float, M>(w, c, cols).get(f);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 1.f;
+    for (int j = 0; j < 4; ++j) f[j] = f2_splat(1.f);
   }
 }
 
 // The ring of one tensor: thread-private slots of eight elements.
-template <typename T> __device__ __forceinline__ void copy_ahead(Raw<T> *slot, const T *src) {
+template <typename T> __device__ __forceinline__ void copy_ahead(Raw8<T> *slot, const T *src) {
   const uint32_t d = (uint32_t)__cvta_generic_to_shared(slot);
 #pragma unroll
-  for (int i = 0; i < (int)(sizeof(Raw<T>) / 16); ++i)
+  for (int i = 0; i < (int)(sizeof(Raw8<T>) / 16); ++i)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
                  :: "r"(d + 16 * i), "l"(reinterpret_cast<const uint4 *>(src) + i) : "memory");
 }
@@ -113,13 +90,13 @@ template <bool WARP, int N> __device__ __forceinline__ void team_sums(float (&v)
 }
 
 template <typename T, Mode M, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : M == RING ? 512 : 1024) rms_norm_kernel(kda_rms_norm_args a) {
+__global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 1024) rms_norm_kernel(kda_rms_norm_args a) {
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][1][32];
   const int cols = a.cols, blocks = (cols + FP8_BLOCK - 1) / FP8_BLOCK;
   const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
   const int tensors = res ? 2 : 1;  // in the ring, as the launch sized it
-  Raw<T> *ring = reinterpret_cast<Raw<T> *>(smem_raw) + threadIdx.x;
+  Raw8<T> *ring = reinterpret_cast<Raw8<T> *>(smem_raw) + threadIdx.x;
   auto slot = [&](int stage, int tensor, int i) { return ring + ((stage * tensors + tensor) * VPT + i) * blockDim.x; };
   auto fetch = [&](int64_t row, int stage) {
     if (M != RING) return;
@@ -138,78 +115,78 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING ? 512 : 1024) rms_norm_
   const int64_t row0 = WARP ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = (int64_t)gridDim.x * teams;
   for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
-  float w[M == RING ? VPT : 1][8];  // the ring's threads keep their columns' weights
+  float2 w[M == RING ? VPT : 1][4];  // the ring's threads keep their columns' weights
   if (M == RING) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) load_weight<M>(a.weight, first_col<M, WARP>(i), cols, w[i]);
   }
   int stage = 0, parity = 0;
   for (int64_t row = row0; row < a.rows; row += step) {
-    float h[VPT][8], sums[1] = {0.f};
+    Raw8<T> h[VPT];
+    float2 ss = f2_splat(0.f);
     if (M == RING) wait_oldest();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
-      float r[8];
       if (M == RING) {
-        if (c < cols) {
-          unpack(*slot(stage, 0, i), h[i]);
-          if (res) unpack(*slot(stage, 1, i), r);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] = r[j] = 0.f;
-        }
+        h[i] = c < cols ? *slot(stage, 0, i) : raw_zero<T>();
+        if (res && c < cols) h[i] = raw_add(h[i], *slot(stage, 1, i));
       } else {
-        load<T, M>(x + row * cols, c, cols, h[i]);
-        if (res) load<T, M>(res + row * cols, c, cols, r);
+        h[i] = load<T, M>(x + row * cols, c, cols);
+        if (res) h[i] = raw_add(h[i], load<T, M>(res + row * cols, c, cols));
       }
-      if (res) {
+      if (res) store<T, M>(static_cast<T *>(a.residual_out) + row * cols, c, cols, h[i]);
+      float2 f[4];
+      h[i].get(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = to_f32<T>(from_f32<T>(h[i][j] + r[j]));
-        store<T, M>(static_cast<T *>(a.residual_out) + row * cols, c, cols, h[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sums[0] = fmaf(h[i][j], h[i][j], sums[0]);
+      for (int j = 0; j < 4; ++j) ss = f2_fma(f[j], f[j], ss);
     }
+    float sums[1] = {ss.x + ss.y};
     team_sums<WARP>(sums, red[parity]);
     parity ^= 1;
-    // every thread has used its slots: the sum needed them
+    // every thread of the team has used its slots: the sum needed them
     fetch(row + kDepth * step, stage);
     stage = stage == kDepth - 1 ? 0 : stage + 1;
     const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
-      float y[8];
+      float2 p[4];  // h w; y = h w rstd
+      h[i].get(p);
       if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * w[M == RING ? i : 0][j];
-      if (a.out) store<T, M>(static_cast<T *>(a.out) + row * cols, c, cols, y);
-      if (a.fp8) {
-        float m = block_amax(y);
+      for (int j = 0; j < 4; ++j) p[j] = f2_mul(p[j], w[M == RING ? i : 0][j]);
+      if (a.out) {
+        float2 y[4];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        if (__any_sync(~0u, isinf(m))) {  // infinities count as NaN
-          drop_infinities(y);
-          m = block_amax(y);
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        }
-        const uint32_t sb = fp8_scale_byte(m);
-        const float inv = fp8_inv_scale(sb);
-        const uint32_t lo = fp8_pack4(y[0], y[1], y[2], y[3], inv), hi = fp8_pack4(y[4], y[5], y[6], y[7], inv);
-        uint8_t *q = static_cast<uint8_t *>(a.fp8) + row * a.ld_fp8;
-        if (M == ODD) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (c + kOddStep * j < cols) q[c + kOddStep * j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
-        } else if (c < cols) {
-          *reinterpret_cast<uint2 *>(q + c) = make_uint2(lo, hi);
-        }
-        const int b = c / FP8_BLOCK;
-        if ((threadIdx.x & 15) == 0 && b < ((blocks + 3) & ~3))
-          a.fp8_scales[((b >> 2) * a.rows + row) * 4 + (b & 3)] = (uint8_t)sb;  // 1.0 past the last block
+        for (int j = 0; j < 4; ++j) y[j] = f2_mul(p[j], f2_splat(rstd));
+        store<T, M>(static_cast<T *>(a.out) + row * cols, c, cols, y);
       }
+      if (!a.fp8) continue;
+      // rounding is monotone: the largest |y| is the largest |h w| times rstd,
+      // and a power of two changes no rounding: y 2^-e = h w (rstd 2^-e)
+      float m = fmaxf(half_warp_max(block_amax(p)) * rstd, 0.f), factor = rstd;
+      if (__any_sync(~0u, isinf(m))) {  // infinities count as NaN
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = f2_mul(p[j], f2_splat(rstd));
+        drop_infinities(p);
+        m = half_warp_max(block_amax(p));
+        factor = 1.f;
+      }
+      const uint32_t sb = fp8_scale_byte(m);
+      const float2 inv = f2_splat(factor * fp8_inv_scale(sb));
+      const uint32_t lo = fp8_pack4(p[0], p[1], inv), hi = fp8_pack4(p[2], p[3], inv);
+      uint8_t *q = static_cast<uint8_t *>(a.fp8) + row * a.ld_fp8;
+      if (M == ODD) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + kOddStep * j < cols) q[c + kOddStep * j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+      } else if (c < cols) {
+        *reinterpret_cast<uint2 *>(q + c) = make_uint2(lo, hi);
+      }
+      const int b = c / FP8_BLOCK;
+      if ((threadIdx.x & 15) == 0 && b < ((blocks + 3) & ~3))
+        a.fp8_scales[((b >> 2) * a.rows + row) * 4 + (b & 3)] = (uint8_t)sb;  // 1.0 past the last block
     }
   }
 }
@@ -221,14 +198,15 @@ constexpr int kMaxParts = 1216;  // partial dweight rows at most: 8 CTAs on each
 // dweight of a team's rows is summed in its registers; a CTA leaves one row of
 // partial sums.
 template <typename T, Mode M, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : M == RING ? 512 : 1024) rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
+__global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 1024, WARP && VPT == 2 ? 3 : M != RING && VPT == 1 ? 2 : 1)
+rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][2][32];
   const int cols = a.cols;
   const T *hp = static_cast<const T *>(a.h), *gp = static_cast<const T *>(a.d_out);
   const T *dp = static_cast<const T *>(a.d_residual);
   const int tensors = dp ? 3 : 2;  // in the ring, as the launch sized it
-  Raw<T> *ring = reinterpret_cast<Raw<T> *>(smem_raw) + threadIdx.x;
+  Raw8<T> *ring = reinterpret_cast<Raw8<T> *>(smem_raw) + threadIdx.x;
   auto slot = [&](int stage, int tensor, int i) { return ring + ((stage * tensors + tensor) * VPT + i) * blockDim.x; };
   auto fetch = [&](int64_t row, int stage) {
     if (M != RING) return;
@@ -244,67 +222,63 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING ? 512 : 1024) rms_norm_
     }
     commit_ahead();
   };
-  float dw[VPT][8];
+  float2 dw[VPT][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) dw[i][j] = f2_splat(0.f);
   const int teams = WARP ? blockDim.x >> 5 : 1;
   const int64_t row0 = WARP ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = (int64_t)gridDim.x * teams;
   for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
-  float w[M == RING ? VPT : 1][8];
+  float2 w[M == RING ? VPT : 1][4];
   if (M == RING) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) load_weight<M>(a.weight, first_col<M, WARP>(i), cols, w[i]);
   }
   int stage = 0, parity = 0;
   for (int64_t row = row0; row < a.rows; row += step) {
-    float sums[2] = {0.f, 0.f};
     if (M == RING) wait_oldest();
     // h and g are read again after the sum, from the ring or the caches: kept
-    // in registers they would leave room for half the threads.
-    auto get = [&](int tensor, const T *p, int i, int c, float (&f)[8]) {
-      if (M != RING) {
-        load<T, M>(p + row * cols, c, cols, f);
-      } else if (c < cols) {
-        unpack(*slot(stage, tensor, i), f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 0.f;
-      }
+    // in registers they would leave room for fewer threads.
+    auto get = [&](int tensor, const T *p, int i, int c) {
+      if (M != RING) return load<T, M>(p + row * cols, c, cols);
+      return c < cols ? *slot(stage, tensor, i) : raw_zero<T>();
     };
+    float2 ss = f2_splat(0.f), sg = f2_splat(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
-      float h[8], g[8];
-      get(0, hp, i, c, h);
-      get(1, gp, i, c, g);
+      float2 h[4], g[4];
+      get(0, hp, i, c).get(h);
+      get(1, gp, i, c).get(g);
       if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sums[0] = fmaf(h[j], h[j], sums[0]);
-        sums[1] = fmaf(g[j] * w[M == RING ? i : 0][j], h[j], sums[1]);
+      for (int j = 0; j < 4; ++j) {
+        ss = f2_fma(h[j], h[j], ss);
+        sg = f2_fma(f2_mul(g[j], w[M == RING ? i : 0][j]), h[j], sg);
       }
     }
+    float sums[2] = {ss.x + ss.y, sg.x + sg.y};
     team_sums<WARP>(sums, red[parity]);
     parity ^= 1;
     const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
     const float mean = sums[1] * rstd / (float)cols;  // mean of weight * d_out * n
+    const float2 r2 = f2_splat(rstd), nm = f2_splat(-mean * rstd * rstd);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
-      float h[8], g[8], d[8], dx[8];
-      get(0, hp, i, c, h);
-      get(1, gp, i, c, g);
+      float2 h[4], g[4], d[4], dx[4];
+      get(0, hp, i, c).get(h);
+      get(1, gp, i, c).get(g);
       if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
-      if (dp) get(2, dp, i, c, d);
+      if (dp) get(2, dp, i, c).get(d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = h[j] * rstd;
-        dw[i][j] = fmaf(g[j], n, dw[i][j]);
-        dx[j] = rstd * (g[j] * w[M == RING ? i : 0][j] - n * mean);
-        if (dp) dx[j] += d[j];
+      for (int j = 0; j < 4; ++j) {
+        dw[i][j] = f2_fma(g[j], f2_mul(h[j], r2), dw[i][j]);
+        // rstd (w g - n mean) + d
+        const float2 t = dp ? f2_fma(h[j], nm, d[j]) : f2_mul(h[j], nm);
+        dx[j] = f2_fma(f2_mul(g[j], w[M == RING ? i : 0][j]), r2, t);
       }
       store<T, M>(static_cast<T *>(a.dx) + row * cols, c, cols, dx);
     }
@@ -327,10 +301,10 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING ? 512 : 1024) rms_norm_
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
-      float f[8];
-      load<float, M>(sum, c, cols, f);
+      float2 f[4];
+      load<float, M>(sum, c, cols).get(f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = v ? f[j] + dw[i][j] : dw[i][j];
+      for (int j = 0; j < 4; ++j) f[j] = v ? f2_add(f[j], dw[i][j]) : dw[i][j];
       store<float, M>(sum, c, cols, f);
     }
   }
@@ -380,7 +354,7 @@ struct Shape {
 // (32768 rows of bf16, forward / backward: 512 columns 21.6 / 28.5 us with a
 // warp a row, 24.1 / 35.1 with a CTA; 1,024 columns 38 / 50 and 42 / 59;
 // odd rows of 903 columns 52 / 90 and 43 / 60).
-Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wide, int per_sm_threads) {
+Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wide, int per_sm_threads, int rounds) {
   Shape s{};
   s.mode = cols % 8 != 0 ? ODD : RING;
   s.warp = vecs <= (s.mode == ODD ? 64 : 128);
@@ -394,6 +368,7 @@ Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wi
     if (s.vpt == 4) per_sm_threads = 512;
   } else {
     cta(vecs < wide ? 1 : 2);
+    if (s.vpt == 2 && tensors > 2) per_sm_threads = 512;  // the backward's: 88 registers
   }
   s.smem = (size_t)kDepth * tensors * s.vpt * s.threads * 8 * esize;
   // rows too wide for two of them in shared memory, or for 512 threads: straight from memory
@@ -404,12 +379,17 @@ Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wi
     per_sm = fit < per_sm ? fit : per_sm;
   } else {
     s.smem = s.warp ? 4096 : 0;  // the backward's sums over warps
-    if (!s.warp) cta(vecs <= 1024 ? 1 : 4);
+    if (!s.warp) cta(vecs <= 512 ? 1 : 4);
     per_sm = 2048 / s.threads;
   }
   if (per_sm < 1) per_sm = 1;
-  const int64_t teams = s.warp ? s.threads / 32 : 1, most = 152 * (int64_t)per_sm;
+  const int64_t teams = s.warp ? s.threads / 32 : 1, resident = 152 * (int64_t)per_sm;
   const int64_t need = (rows + teams - 1) / teams;
+  // Up to `rounds` CTAs in turn on each place, of at least 8 rows: SMs are not
+  // equally fast (32768 x 4096: 168 us in one round, 155 in two, 140 in six).
+  // A CTA alone on its SM has no neighbour to cover its start: one round.
+  int64_t most = per_sm > 1 ? need / (8 * resident) : 1;
+  most = resident * (most < 1 ? 1 : most > rounds ? rounds : most);
   s.grid = (int)(need < most ? need : most);
   return s;
 }
@@ -426,7 +406,7 @@ cudaError_t launch_rows(K kern, const Shape &s, const A &a, cudaStream_t st) {
 
 template <typename T> cudaError_t norm_typed(const kda_rms_norm_args &a, cudaStream_t st) {
   // whole groups of four blocks, so that the scales past the last block get written
-  const Shape s = shape_for(a.rows, a.cols, (a.cols + 511) / 512 * 64, a.residual ? 2 : 1, sizeof(T), 0, 1024);
+  const Shape s = shape_for(a.rows, a.cols, (a.cols + 511) / 512 * 64, a.residual ? 2 : 1, sizeof(T), 0, 1024, 6);
 #define KDA_NORM(M_, V_, W_) return launch_rows(rms_norm_kernel<T, M_, V_, W_>, s, a, st)
   if (s.warp) {
     if (s.mode == RING) { if (s.vpt == 2) KDA_NORM(RING, 2, true); else KDA_NORM(RING, 4, true); }
@@ -440,7 +420,7 @@ template <typename T> cudaError_t norm_typed(const kda_rms_norm_args &a, cudaStr
 
 template <typename T> cudaError_t bwd_typed(const kda_rms_norm_bwd_args &a, cudaStream_t st) {
   // whole groups of 16 threads: the odd layout spreads a block over them
-  Shape s = shape_for(a.rows, a.cols, (a.cols + 127) / 128 * 16, a.d_residual ? 3 : 2, sizeof(T), 257, 768);
+  Shape s = shape_for(a.rows, a.cols, (a.cols + 127) / 128 * 16, a.d_residual ? 3 : 2, sizeof(T), 257, 768, 1);
   if (s.grid > kMaxParts) s.grid = kMaxParts;
   cudaError_t e;
 #define KDA_BWD(M_, V_, W_) e = launch_rows(rms_norm_bwd_kernel<T, M_, V_, W_>, s, a, st)
