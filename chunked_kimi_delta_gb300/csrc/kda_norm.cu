@@ -48,6 +48,14 @@ template <typename T, Mode M> __device__ __forceinline__ void store(T *row, int 
   r.put(f);
   store<T, M>(row, c, cols, r);
 }
+// Products on pairs; the odd layout's scattered loads do not end up in
+// register pairs, and moving them there costs more than it saves.
+template <Mode M> __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  return M == ODD ? make_float2(a.x * b.x, a.y * b.y) : f2_mul(a, b);
+}
+template <Mode M> __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  return M == ODD ? make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)) : f2_fma(a, b, c);
+}
 template <Mode M> __device__ __forceinline__ void load_weight(const float *w, int c, int cols, float2 (&f)[4]) {
   if (w) {
     load<float, M>(w, c, cols).get(f);
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
       float2 f[4];
       h[i].get(f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ss = f2_fma(f[j], f[j], ss);
+      for (int j = 0; j < 4; ++j) ss = fma2<M>(f[j], f[j], ss);
     }
     float sums[1] = {ss.x + ss.y};
     team_sums<WARP>(sums, red[parity]);
@@ -155,11 +163,11 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
       h[i].get(p);
       if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = f2_mul(p[j], w[M == RING ? i : 0][j]);
+      for (int j = 0; j < 4; ++j) p[j] = mul2<M>(p[j], w[M == RING ? i : 0][j]);
       if (a.out) {
         float2 y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = f2_mul(p[j], f2_splat(rstd));
+        for (int j = 0; j < 4; ++j) y[j] = mul2<M>(p[j], f2_splat(rstd));
         store<T, M>(static_cast<T *>(a.out) + row * cols, c, cols, y);
       }
       if (!a.fp8) continue;
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
       float m = fmaxf(half_warp_max(block_amax(p)) * rstd, 0.f), factor = rstd;
       if (__any_sync(~0u, isinf(m))) {  // infinities count as NaN
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = f2_mul(p[j], f2_splat(rstd));
+        for (int j = 0; j < 4; ++j) p[j] = mul2<M>(p[j], f2_splat(rstd));
         drop_infinities(p);
         m = half_warp_max(block_amax(p));
         factor = 1.f;
@@ -198,7 +206,7 @@ constexpr int kMaxParts = 1216;  // partial dweight rows at most: 8 CTAs on each
 // dweight of a team's rows is summed in its registers; a CTA leaves one row of
 // partial sums.
 template <typename T, Mode M, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 1024, WARP && VPT == 2 ? 3 : M != RING && VPT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT < 4 ? 512 : 1024, WARP && VPT == 2 ? 4 : M != RING && VPT == 1 ? 2 : 1)
 rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][2][32];
@@ -255,8 +263,8 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
       if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        ss = f2_fma(h[j], h[j], ss);
-        sg = f2_fma(f2_mul(g[j], w[M == RING ? i : 0][j]), h[j], sg);
+        ss = fma2<M>(h[j], h[j], ss);
+        sg = fma2<M>(mul2<M>(g[j], w[M == RING ? i : 0][j]), h[j], sg);
       }
     }
     float sums[2] = {ss.x + ss.y, sg.x + sg.y};
@@ -275,10 +283,10 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
       if (dp) get(2, dp, i, c).get(d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        dw[i][j] = f2_fma(g[j], f2_mul(h[j], r2), dw[i][j]);
+        dw[i][j] = fma2<M>(g[j], mul2<M>(h[j], r2), dw[i][j]);
         // rstd (w g - n mean) + d
-        const float2 t = dp ? f2_fma(h[j], nm, d[j]) : f2_mul(h[j], nm);
-        dx[j] = f2_fma(f2_mul(g[j], w[M == RING ? i : 0][j]), r2, t);
+        const float2 t = dp ? fma2<M>(h[j], nm, d[j]) : mul2<M>(h[j], nm);
+        dx[j] = fma2<M>(mul2<M>(g[j], w[M == RING ? i : 0][j]), r2, t);
       }
       store<T, M>(static_cast<T *>(a.dx) + row * cols, c, cols, dx);
     }
@@ -348,7 +356,7 @@ struct Shape {
 
 // `vecs` groups of eight columns a row, of which `tensors` x `esize` bytes an
 // element travel through the ring; a CTA's threads take two each from `wide`
-// of them on, else one; `per_sm_threads`: the threads an SM's registers hold.
+// of them on (four from 1,025), else one; `per_sm_threads`: the threads an SM's registers hold.
 //
 // Warps take a row each up to 512 columns, and up to 1,024 in the ring
 // (32768 rows of bf16, forward / backward: 512 columns 21.6 / 28.5 us with a
@@ -367,11 +375,11 @@ Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wi
     s.threads = 256;
     if (s.vpt == 4) per_sm_threads = 512;
   } else {
-    cta(vecs < wide ? 1 : 2);
+    cta(vecs < wide ? 1 : vecs <= 1024 ? 2 : 4);
     if (s.vpt == 2 && tensors > 2) per_sm_threads = 512;  // the backward's: 88 registers
   }
   s.smem = (size_t)kDepth * tensors * s.vpt * s.threads * 8 * esize;
-  // rows too wide for two of them in shared memory, or for 512 threads: straight from memory
+  // rows too wide for two of them in shared memory, or for 512 threads of four: straight from memory
   if (s.mode == RING && (s.threads > 512 || s.smem > 200 * 1024)) s.mode = DIRECT;
   int per_sm = per_sm_threads / s.threads;
   if (s.mode == RING) {
@@ -379,7 +387,7 @@ Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wi
     per_sm = fit < per_sm ? fit : per_sm;
   } else {
     s.smem = s.warp ? 4096 : 0;  // the backward's sums over warps
-    if (!s.warp) cta(vecs <= 512 ? 1 : 4);
+    if (!s.warp) cta(vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4);
     per_sm = 2048 / s.threads;
   }
   if (per_sm < 1) per_sm = 1;
@@ -412,9 +420,9 @@ template <typename T> cudaError_t norm_typed(const kda_rms_norm_args &a, cudaStr
     if (s.mode == RING) { if (s.vpt == 2) KDA_NORM(RING, 2, true); else KDA_NORM(RING, 4, true); }
     KDA_NORM(ODD, 2, true);
   }
-  if (s.mode == RING) KDA_NORM(RING, 2, false);
-  if (s.mode == DIRECT) { if (s.vpt == 1) KDA_NORM(DIRECT, 1, false); else KDA_NORM(DIRECT, 4, false); }
-  if (s.vpt == 1) KDA_NORM(ODD, 1, false); else KDA_NORM(ODD, 4, false);
+  if (s.mode == RING) { if (s.vpt == 2) KDA_NORM(RING, 2, false); else KDA_NORM(RING, 4, false); }
+  if (s.mode == DIRECT) KDA_NORM(DIRECT, 4, false);
+  if (s.vpt == 1) KDA_NORM(ODD, 1, false); else if (s.vpt == 2) KDA_NORM(ODD, 2, false); else KDA_NORM(ODD, 4, false);
 #undef KDA_NORM
 }
 
@@ -428,9 +436,14 @@ template <typename T> cudaError_t bwd_typed(const kda_rms_norm_bwd_args &a, cuda
     if (s.mode == RING) { if (s.vpt == 2) KDA_BWD(RING, 2, true); else KDA_BWD(RING, 4, true); }
     else KDA_BWD(ODD, 2, true);
   }
-  else if (s.mode == RING) { if (s.vpt == 1) KDA_BWD(RING, 1, false); else KDA_BWD(RING, 2, false); }
-  else if (s.mode == DIRECT) { if (s.vpt == 1) KDA_BWD(DIRECT, 1, false); else KDA_BWD(DIRECT, 4, false); }
+  else if (s.mode == RING) {
+    if (s.vpt == 1) KDA_BWD(RING, 1, false);
+    else if (s.vpt == 2) KDA_BWD(RING, 2, false);
+    else KDA_BWD(RING, 4, false);
+  }
+  else if (s.mode == DIRECT) KDA_BWD(DIRECT, 4, false);
   else if (s.vpt == 1) KDA_BWD(ODD, 1, false);
+  else if (s.vpt == 2) KDA_BWD(ODD, 2, false);
   else KDA_BWD(ODD, 4, false);
 #undef KDA_BWD
   if (e != cudaSuccess || !a.dweight) return e;
