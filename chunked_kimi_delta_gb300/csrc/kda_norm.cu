@@ -76,8 +76,8 @@ template <typename T> __device__ __forceinline__ void copy_ahead(Raw8<T> *slot, 
 __device__ __forceinline__ void commit_ahead() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_oldest() { asm volatile("cp.async.wait_group %0;" :: "n"(kDepth - 1) : "memory"); }
 
-// Sums over the team's threads, the same values in all of them: shuffles
-// inside a warp, then the warps' sums in order.  `red` alternates between two
+// Sums over the team's threads, the same values in all of them, pairwise: the
+// lanes of a warp, then the warps.  `red` alternates between two
 // buffers from call to call, so one barrier is enough.
 template <bool WARP, int N> __device__ __forceinline__ void team_sums(float (&v)[N], float (*red)[32]) {
 #pragma unroll
@@ -90,11 +90,13 @@ template <bool WARP, int N> __device__ __forceinline__ void team_sums(float (&v)
 #pragma unroll
     for (int n = 0; n < N; ++n) red[n][threadIdx.x >> 5] = v[n];
   __syncthreads();
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = 0.f;
-  for (int i = 0; i < warps; ++i)
+  for (int n = 0; n < N; ++n) v[n] = lane < warps ? red[n][lane] : 0.f;
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += red[n][i];
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(~0u, v[n], o);
 }
 
 template <typename T, Mode M, int VPT, bool WARP>
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][1][32];
   const int cols = a.cols, blocks = (cols + FP8_BLOCK - 1) / FP8_BLOCK;
+  const float inv_cols = 1.f / (float)cols;
   const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
   const int tensors = res ? 2 : 1;  // in the ring, as the launch sized it
   Raw8<T> *ring = reinterpret_cast<Raw8<T> *>(smem_raw) + threadIdx.x;
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
     // every thread of the team has used its slots: the sum needed them
     fetch(row + kDepth * step, stage);
     stage = stage == kDepth - 1 ? 0 : stage + 1;
-    const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
+    const float rstd = 1.f / sqrtf(fmaf(sums[0], inv_cols, a.eps));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
@@ -211,6 +214,7 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][2][32];
   const int cols = a.cols;
+  const float inv_cols = 1.f / (float)cols;
   const T *hp = static_cast<const T *>(a.h), *gp = static_cast<const T *>(a.d_out);
   const T *dp = static_cast<const T *>(a.d_residual);
   const int tensors = dp ? 3 : 2;  // in the ring, as the launch sized it
@@ -270,8 +274,8 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
     float sums[2] = {ss.x + ss.y, sg.x + sg.y};
     team_sums<WARP>(sums, red[parity]);
     parity ^= 1;
-    const float rstd = 1.f / sqrtf(sums[0] / (float)cols + a.eps);
-    const float mean = sums[1] * rstd / (float)cols;  // mean of weight * d_out * n
+    const float rstd = 1.f / sqrtf(fmaf(sums[0], inv_cols, a.eps));
+    const float mean = sums[1] * rstd * inv_cols;  // mean of weight * d_out * n
     const float2 r2 = f2_splat(rstd), nm = f2_splat(-mean * rstd * rstd);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
