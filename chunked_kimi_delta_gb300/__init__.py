@@ -832,6 +832,22 @@ class RmsNorm(NamedTuple):
     fp8: Optional[Fp8Matrix]
 
 
+# These calls also run for single tokens, where the host's time counts: each
+# tensor's properties are read once, and the general checks above are only
+# called to name what is wrong.
+_F8 = _E8 = _BF16 = _F32 = None
+
+
+def _ready():
+    """(torch, lib), with the dtypes above in place."""
+    global _F8, _E8, _BF16, _F32
+    if _F8 is None:
+        torch = _torch()
+        _E8, _BF16, _F32 = torch.float8_e8m0fnu, torch.bfloat16, torch.float32
+        _F8 = torch.float8_e4m3fn
+    return _torch_module or _torch(), _lib or load_library()
+
+
 def _scale_shape(rows, cols, kind):
     if kind == "row":
         return ((cols + 511) // 512, rows, 4)
@@ -841,11 +857,10 @@ def _scale_shape(rows, cols, kind):
 
 
 def _empty_fp8(rows, cols, kind, device) -> Fp8Matrix:
-    torch = _torch()
-    data = torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.float8_e4m3fn,
-                               device=device)
-    scales = torch.empty(_scale_shape(rows, cols, kind), dtype=torch.float8_e8m0fnu, device=device)
-    return Fp8Matrix(data, scales, kind)
+    torch, _ = _ready()
+    return Fp8Matrix(
+        torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=_F8, device=device),
+        torch.empty(_scale_shape(rows, cols, kind), dtype=_E8, device=device), kind)
 
 
 def _pitch(t) -> int:
@@ -859,10 +874,9 @@ def _pitch(t) -> int:
 
 def _launch_device(lead, *ts) -> int:
     """Index of the device of a call whose tensors are dense and all on the
-    current device (a handful of integer comparisons: these calls also run
-    for single tokens, where the host's time counts)."""
+    current device."""
     dev = lead.get_device()
-    fine = dev >= 0 and lead.is_contiguous() and dev == _torch().cuda.current_device()
+    fine = dev >= 0 and lead.is_contiguous() and dev == _torch_module.cuda.current_device()
     for t in ts:
         if t is not None:
             fine = fine and t.get_device() == dev and t.is_contiguous()
@@ -873,31 +887,25 @@ def _launch_device(lead, *ts) -> int:
 
 
 def _raw_stream(stream, dev):
-    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-def _check_fp8(x: Fp8Matrix, kind: str):
-    torch = _torch()
-    data, scales, have = x
-    if have != kind:
-        raise ValueError(f"this operand needs {kind} scales, not {have}")
-    if data.dtype != torch.float8_e4m3fn or scales.dtype != torch.float8_e8m0fnu:
-        raise TypeError("a scaled 8-bit matrix holds float8_e4m3fn values and float8_e8m0fnu scales")
-    if data.dim() != 2:
-        raise ValueError("a scaled 8-bit matrix is [rows, cols]")
-    if scales.shape != _scale_shape(*data.shape, kind):
-        raise ValueError(f"{kind} scales of {tuple(data.shape)} values have shape "
-                         f"{_scale_shape(*data.shape, kind)}, not {tuple(scales.shape)}")
+    return _torch_module._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _check_weight(weight, cols):
-    if weight is not None and (weight.shape != (cols,) or weight.dtype != _torch().float32):
+    if weight.shape != (cols,) or weight.dtype is not _F32:
         raise ValueError("weight must be fp32 [cols]")
 
 
-def _like(t, x, what):
-    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+def _like(t, shape, dtype, what):
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{what} must have x's shape and dtype")
+
+
+def _in_code(dtype) -> int:
+    if dtype is _BF16:
+        return KDA_BF16
+    if dtype is _F32:
+        return KDA_F32
+    raise TypeError(f"unsupported dtype {dtype}")
 
 
 def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None,
@@ -908,11 +916,11 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None
     ``out=False`` then leaves out the result in x's dtype.  ``residual_out``
     (x + residual) may be given as ``x`` or ``residual`` to work in place.
     See ``kda_rms_norm`` in include/kda.h."""
-    torch = _torch()
-    lib = load_library()
-    cols = x.shape[-1]
-    _check_weight(weight, cols)
-    _like(residual, x, "residual")
+    torch, lib = _ready()
+    shape, dtype = x.shape, x.dtype
+    code, cols = _in_code(dtype), shape[-1]
+    if weight is not None:
+        _check_weight(weight, cols)
     if out is False:
         if not fp8:
             raise ValueError("no result: out=False needs fp8=True")
@@ -920,22 +928,26 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None
     elif out is None:
         out = torch.empty_like(x)
     else:
-        _like(out, x, "out")
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-    elif residual_out is None:
-        residual_out = torch.empty_like(x)
-    else:
-        _like(residual_out, x, "residual_out")
+        _like(out, shape, dtype, "out")
+    if residual is not None:
+        _like(residual, shape, dtype, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        else:
+            _like(residual_out, shape, dtype, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
     dev = _launch_device(x, weight, residual, out, residual_out)
     rows = x.numel() // cols if cols else 0
-    q = _empty_fp8(rows, cols, "row", x.device) if fp8 else None
-    a = kda_rms_norm_args(rows, cols, _dtype_code(x), _ptr(x), _ptr(residual), _ptr(weight), eps,
-                          _ptr(residual_out), _ptr(out))
-    if q is not None:
-        a.fp8, a.ld_fp8, a.fp8_scales = q.data.data_ptr(), (cols + 15) // 16 * 16, q.scales.data_ptr()
-    _check(lib.kda_rms_norm(ctypes.byref(a), _raw_stream(stream, dev)), "kda_rms_norm")
+    q, q_ptr, ld, scales_ptr = None, None, 0, None
+    if fp8:
+        q = _empty_fp8(rows, cols, "row", x.device)
+        q_ptr, ld, scales_ptr = q.data.data_ptr(), (cols + 15) // 16 * 16, q.scales.data_ptr()
+    a = kda_rms_norm_args(rows, cols, code, x.data_ptr(), _ptr(residual), _ptr(weight), eps,
+                          _ptr(residual_out), _ptr(out), q_ptr, ld, scales_ptr)
+    status = lib.kda_rms_norm(ctypes.byref(a), _raw_stream(stream, dev))
+    if status:
+        raise KdaError(status, "kda_rms_norm")
     return RmsNorm(out, residual_out, q)
 
 
@@ -946,27 +958,31 @@ def kda_rms_norm_bwd(d_out, x, weight=None, d_residual=None, *, eps=1e-6, dx=Non
     the gradient that reaches it from elsewhere.  Returns ``(dx, dweight)``:
     dx is the gradient of x and of the residual, dweight fp32 [cols] (None
     without ``want_dweight``).  See ``kda_rms_norm_bwd`` in include/kda.h."""
-    torch = _torch()
-    lib = load_library()
-    cols = x.shape[-1]
-    _check_weight(weight, cols)
-    _like(d_out, x, "d_out")
-    _like(d_residual, x, "d_residual")
+    torch, lib = _ready()
+    shape, dtype = x.shape, x.dtype
+    code, cols = _in_code(dtype), shape[-1]
+    if weight is not None:
+        _check_weight(weight, cols)
+    _like(d_out, shape, dtype, "d_out")
+    if d_residual is not None:
+        _like(d_residual, shape, dtype, "d_residual")
     if dx is None:
         dx = torch.empty_like(x)
     else:
-        _like(dx, x, "dx")
+        _like(dx, shape, dtype, "dx")
     dev = _launch_device(x, d_out, weight, d_residual, dx, workspace)
     rows = x.numel() // cols if cols else 0
-    a = kda_rms_norm_bwd_args(rows, cols, _dtype_code(x), _ptr(d_out), _ptr(x), _ptr(weight),
-                              _ptr(d_residual), eps, _ptr(dx))
+    a = kda_rms_norm_bwd_args(rows, cols, code, d_out.data_ptr(), x.data_ptr(), _ptr(weight),
+                              _ptr(d_residual), eps, dx.data_ptr())
     dweight = None
     if want_dweight:
-        dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
+        dweight = torch.empty(cols, dtype=_F32, device=x.device)
         ws = _workspace(lib.kda_rms_norm_bwd_workspace_size(rows, cols), x.device, workspace)
         a.dweight, a.workspace = dweight.data_ptr(), ws.data_ptr()
         a.workspace_bytes = ws.numel() * ws.element_size()
-    _check(lib.kda_rms_norm_bwd(ctypes.byref(a), _raw_stream(stream, dev)), "kda_rms_norm_bwd")
+    status = lib.kda_rms_norm_bwd(ctypes.byref(a), _raw_stream(stream, dev))
+    if status:
+        raise KdaError(status, "kda_rms_norm_bwd")
     return dx, dweight
 
 
@@ -975,21 +991,24 @@ def kda_fp8_quantize(x, kinds=("row",), *, stream=None):
     scales, once for each of ``kinds`` ("row", "col", "tile") from one read of
     x.  Returns a tuple of :class:`Fp8Matrix` in the order of ``kinds``.  See
     ``kda_fp8_quantize`` in include/kda.h."""
-    lib = load_library()
+    _, lib = _ready()
     if isinstance(kinds, str):
         kinds = (kinds,)
     if not kinds or len(set(kinds)) != len(kinds) or not {"row", "col", "tile"}.issuperset(kinds):
         raise ValueError('kinds are "row", "col" and "tile", each once')
     if x.dim() != 2:
         raise ValueError("x is [rows, cols]")
-    dev = _launch_device(x)
+    code, dev = _in_code(x.dtype), _launch_device(x)
     rows, cols = x.shape
-    parts = tuple(_empty_fp8(rows, cols, k, x.device) for k in kinds)
-    a = kda_fp8_quantize_args(rows, cols, _dtype_code(x), _ptr(x), (cols + 15) // 16 * 16)
+    device = x.device
+    parts = tuple([_empty_fp8(rows, cols, k, device) for k in kinds])
+    a = kda_fp8_quantize_args(rows, cols, code, x.data_ptr(), (cols + 15) // 16 * 16)
     for p in parts:
         setattr(a, p.kind, p.data.data_ptr())
         setattr(a, p.kind + "_scales", p.scales.data_ptr())
-    _check(lib.kda_fp8_quantize(ctypes.byref(a), _raw_stream(stream, dev)), "kda_fp8_quantize")
+    status = lib.kda_fp8_quantize(ctypes.byref(a), _raw_stream(stream, dev))
+    if status:
+        raise KdaError(status, "kda_fp8_quantize")
     return parts
 
 
@@ -998,9 +1017,10 @@ _FP8_FORMS = {"nt": (KDA_FP8_NT, "row", "tile"), "nn": (KDA_FP8_NN, "row", "tile
 _fp8_status_words = {}
 
 
-def _fp8_status_word(dev: int):
-    """The zeroed error word shared by a device's matmul calls without a
-    ``workspace`` (made by the first of them: before any stream capture)."""
+def _fp8_status_word(dev: int) -> int:
+    """Address of the zeroed error word shared by a device's matmul calls
+    without a ``workspace`` (made by the first of them: before any stream
+    capture)."""
     word = _fp8_status_words.get(dev)
     if word is None:
         torch = _torch()
@@ -1008,7 +1028,23 @@ def _fp8_status_word(dev: int):
                            device=torch.device("cuda", dev))
         torch.cuda.current_stream(dev).synchronize()
         _fp8_status_words[dev] = word
-    return word
+    return word.data_ptr()
+
+
+def _check_fp8(x: Fp8Matrix, kind: str):
+    """(rows, cols, pitch) of an operand of this kind."""
+    data, scales, have = x
+    if have != kind:
+        raise ValueError(f"this operand needs {kind} scales, not {have}")
+    if data.dtype is not _F8 or scales.dtype is not _E8:
+        raise TypeError("a scaled 8-bit matrix holds float8_e4m3fn values and float8_e8m0fnu scales")
+    if data.dim() != 2:
+        raise ValueError("a scaled 8-bit matrix is [rows, cols]")
+    rows, cols = data.shape
+    if scales.shape != _scale_shape(rows, cols, kind):
+        raise ValueError(f"{kind} scales of {(rows, cols)} values have shape "
+                         f"{_scale_shape(rows, cols, kind)}, not {tuple(scales.shape)}")
+    return rows, cols, _pitch(data)
 
 
 def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out=None,
@@ -1022,34 +1058,40 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
     ``out`` (rows dense, any pitch).  ``workspace`` (256 zeroed bytes) takes
     the device error word; without it one per device is shared, read by
     :func:`kda_fp8_matmul_status`.  See ``kda_fp8_matmul`` in include/kda.h."""
-    torch = _torch()
-    lib = load_library()
+    torch, lib = _ready()
     if form not in _FP8_FORMS:
         raise ValueError('form is "nt", "nn" or "tn"')
     code, ka, kb = _FP8_FORMS[form]
-    _check_fp8(a, ka)
-    _check_fp8(b, kb)
-    ad, bd = a.data, b.data
-    (k, m) = ad.shape if form == "tn" else ad.shape[::-1]
-    (n, k_b) = bd.shape if form == "nt" else bd.shape[::-1]
+    m, k, lda = _check_fp8(a, ka)
+    n, k_b, ldb = _check_fp8(b, kb)
+    if form != "nt":
+        n, k_b = k_b, n
+        if form == "tn":
+            m, k = k, m
     if k != k_b:
         raise ValueError(f"the operands sum over {k} and {k_b}")
+    ad, bd, a_scales, b_scales = a.data, b.data, a.scales, b.scales
     if out is None:
-        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=ad.device)
+        out = torch.empty((m, n), dtype=out_dtype or _BF16, device=ad.device)
         ldo = n
     else:
-        if out.shape != (m, n) or (out_dtype is not None and out.dtype != out_dtype):
+        if out.shape != (m, n) or (out_dtype is not None and out.dtype is not out_dtype):
             raise ValueError(f"out must be [{m}, {n}] of out_dtype")
         ldo = _pitch(out)
-    lda, ldb, out_code = _pitch(ad), _pitch(bd), _dtype_code(out)
-    dev = _launch_device(a.scales, b.scales, workspace)
+    out_code = _in_code(out.dtype)
+    dev = _launch_device(a_scales, b_scales)
     if ad.get_device() != dev or bd.get_device() != dev or out.get_device() != dev:
-        _on_device(a.scales, ad, bd, out)
-    ws = _fp8_status_word(dev) if workspace is None else workspace
-    p = kda_fp8_matmul_args(m, n, k, code, ad.data_ptr(), lda, a.scales.data_ptr(), bd.data_ptr(), ldb,
-                            b.scales.data_ptr(), out.data_ptr(), ldo, out_code, ws.data_ptr(),
-                            ws.numel() * ws.element_size(), extra_flags)
-    _check(lib.kda_fp8_matmul(ctypes.byref(p), _raw_stream(stream, dev)), "kda_fp8_matmul")
+        _on_device(a_scales, ad, bd, out)
+    if workspace is None:
+        ws, ws_bytes = _fp8_status_word(dev), KDA_FP8_MATMUL_WORKSPACE_BYTES
+    else:
+        _on_device(a_scales, workspace)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    p = kda_fp8_matmul_args(m, n, k, code, ad.data_ptr(), lda, a_scales.data_ptr(), bd.data_ptr(), ldb,
+                            b_scales.data_ptr(), out.data_ptr(), ldo, out_code, ws, ws_bytes, extra_flags)
+    status = lib.kda_fp8_matmul(ctypes.byref(p), _raw_stream(stream, dev))
+    if status:
+        raise KdaError(status, "kda_fp8_matmul")
     return out
 
 
@@ -1058,4 +1100,6 @@ def kda_fp8_matmul_status(stream=None) -> int:
     current device (synchronises ``stream``): KDA_OK, or
     KDA_ERR_DEVICE_TIMEOUT when a bounded device wait gave up since the last
     read."""
-    return kda_get_device_status(_fp8_status_word(_torch().cuda.current_device()), stream)
+    dev = _torch().cuda.current_device()
+    _fp8_status_word(dev)
+    return kda_get_device_status(_fp8_status_words[dev], stream)
