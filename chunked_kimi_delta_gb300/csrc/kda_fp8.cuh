@@ -179,6 +179,40 @@ __device__ __forceinline__ void store8_fp8(uint8_t *p, int n, uint32_t lo, uint3
   }
 }
 
+// The kernels of this path follow one another, most of them for tens of
+// microseconds: each may be set up while the one before it in the stream
+// ends.  grid_start() lets the next one come and then waits for the end of
+// the one before (its writes are visible after it); no thread touches global
+// memory ahead of it.
+__device__ __forceinline__ void grid_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Host: launches a kernel that calls grid_start(), in clusters of `cluster`.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                              cudaStream_t st, A... args) {
+  if (smem > 40 * 1024) {  // with the static part, past the 48 KB that need no leave
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Host: launchers.
 cudaError_t launch_rms_norm(const kda_rms_norm_args &a, cudaStream_t st);
 cudaError_t launch_rms_norm_bwd(const kda_rms_norm_bwd_args &a, cudaStream_t st);

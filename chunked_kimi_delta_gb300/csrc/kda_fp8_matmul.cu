@@ -213,7 +213,7 @@ __device__ __forceinline__ void copy_word(uint32_t smem, const uint8_t *s, int r
 // TILE scales of the lane side, one byte for all 128 lanes: lane i holds the
 // byte of block 32 g + i, loaded one group of eight words ahead of its use.
 __device__ __forceinline__ uint32_t tile_bytes(const MmArgs &a, int l0, int g, int lane) {
-  return __ldg(a.lane_scales + (min(l0, a.lanes - 1) / FP8_BLOCK) * a.tile_i +
+  return *(a.lane_scales + (min(l0, a.lanes - 1) / FP8_BLOCK) * a.tile_i +
                min(32 * g + lane, a.kblocks - 1) * a.tile_k);
 }
 // One ring entry, by a full warp: word w of the tile at (l0, c0).  Its
@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
   tc::tc_fence_before();
   cluster_sync();
   tc::tc_fence_after();
+  grid_start();
   const uint32_t tmem = b.tmem;
 
   auto lane0_of = [&](int t) { return (t % a.lane_tiles) * 256 + (int)rank * 128; };  // this CTA's first n
@@ -614,12 +615,14 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
     tc::mbar_init(&b.never, 1);
     b.abort = 0;
     tc::mbar_fence_init();
+    grid_start();
     for (int kb = kb0; kb < kb1 && kb - kb0 < a.stages; ++kb) issue_load(kb, kb - kb0);
   }
   if (warp == 0) mm_alloc<false>(&b.tmem, SPLIT_TMEM);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  grid_start();
   const uint32_t tmem = b.tmem, tmem_sf = tmem + 2 * SPLIT_MAX_WIDTH;
 
   uint8_t *sf_ring = sm + a.stages * a.stage_bytes;
@@ -764,48 +767,6 @@ uint32_t idesc_scaled(int M, int N, bool lane_mn, bool col_mn) {
 
 constexpr uint32_t SMEM_LIMIT = 227 * 1024 - 1024 - sizeof(Bars);  // dynamic, after alignment
 
-template <typename T>
-cudaError_t launch_pair(const CUtensorMap &lm, const CUtensorMap &cm, const CUtensorMap &om, const MmArgs &a,
-                        cudaStream_t st) {
-  auto kern = fp8_matmul_pair_kernel<T>;
-  const int smem = (int)(a.stages * a.stage_bytes + SF_BYTES + (a.out_tma ? OUT_BYTES : 0) + 1024);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(2 * (a.tiles < 76 ? a.tiles : 76)));
-  cfg.blockDim = dim3(PAIR_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, lm, cm, om, a);
-}
-
-template <typename T>
-cudaError_t launch_split(const CUtensorMap &lm, const CUtensorMap &cm, const MmArgs &a, cudaStream_t st) {
-  auto kern = fp8_matmul_split_kernel<T>;
-  int smem = (int)(a.stages * a.stage_bytes + SF_BYTES + 1024);
-  if (smem < 80 * 1024) smem = 80 * 1024;  // two CTAs an SM at most: that is what tensor memory holds
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.tiles * a.splits));
-  cfg.blockDim = dim3(SPLIT_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = (unsigned)a.splits;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, lm, cm, a);
-}
-
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 struct Plan {
@@ -883,9 +844,19 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
                             : tcp::make_byte_map(p.a, p.k, p.m, p.lda, (uint32_t)box_rows, cm)) &&
                   (!a.out_tma || tcp::make_bf16_map(p.out, p.n, p.m, p.ldo, 32, om));
   if (!ok) return cudaErrorInvalidValue;
-  if (pair)
-    return p.out_dtype == KDA_F32 ? launch_pair<float>(lm, cm, om, a, st) : launch_pair<__nv_bfloat16>(lm, cm, om, a, st);
-  return p.out_dtype == KDA_F32 ? launch_split<float>(lm, cm, a, st) : launch_split<__nv_bfloat16>(lm, cm, a, st);
+  uint32_t smem = a.stages * a.stage_bytes + SF_BYTES + 1024;
+  if (pair) {
+    smem += a.out_tma ? OUT_BYTES : 0;
+    const unsigned grid = 2u * (unsigned)(a.tiles < 76 ? a.tiles : 76);
+    return p.out_dtype == KDA_F32
+               ? launch_overlapped(fp8_matmul_pair_kernel<float>, grid, PAIR_THREADS, smem, 2, st, lm, cm, om, a)
+               : launch_overlapped(fp8_matmul_pair_kernel<__nv_bfloat16>, grid, PAIR_THREADS, smem, 2, st, lm, cm, om, a);
+  }
+  if (smem < 80 * 1024) smem = 80 * 1024;  // two CTAs an SM at most: that is what tensor memory holds
+  const unsigned grid = (unsigned)(a.tiles * a.splits), cluster = (unsigned)a.splits;
+  return p.out_dtype == KDA_F32
+             ? launch_overlapped(fp8_matmul_split_kernel<float>, grid, SPLIT_THREADS, smem, cluster, st, lm, cm, a)
+             : launch_overlapped(fp8_matmul_split_kernel<__nv_bfloat16>, grid, SPLIT_THREADS, smem, cluster, st, lm, cm, a);
 }
 
 }  // namespace kda

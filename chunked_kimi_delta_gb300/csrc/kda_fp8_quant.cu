@@ -99,6 +99,7 @@ fp8_quantize_kernel(kda_fp8_quantize_args a, int cblocks, int tiles) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  grid_start();
   fetch(blockIdx.x, 0);
   fetch(blockIdx.x + gridDim.x, 1);
   int buf = 0;
@@ -227,14 +228,9 @@ fp8_quantize_kernel(kda_fp8_quantize_args a, int cblocks, int tiles) {
 }
 
 template <typename T, Mode M> cudaError_t launch(const kda_fp8_quantize_args &a, int cblocks, int tiles, cudaStream_t st) {
-  auto kern = fp8_quantize_kernel<T, M>;
-  const int smem = M == RING ? 2 * 8 * kThreads * 16 : 0, most = 152 * (sizeof(T) == 2 && M != ODD ? 3 : 2);
-  if (M == RING) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<tiles < most ? tiles : most, kThreads, smem, st>>>(a, cblocks, tiles);
-  return cudaGetLastError();
+  const int most = 152 * (sizeof(T) == 2 && M != ODD ? 3 : 2);
+  return launch_overlapped(fp8_quantize_kernel<T, M>, (unsigned)(tiles < most ? tiles : most), kThreads,
+                           M == RING ? 2 * 8 * kThreads * 16 : 0, 1, st, a, cblocks, tiles);
 }
 
 }  // namespace

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
   const int teams = WARP ? blockDim.x >> 5 : 1;
   const int64_t row0 = WARP ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = (int64_t)gridDim.x * teams;
+  grid_start();
   for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
   float2 w[M == RING ? VPT : 1][4];  // the ring's threads keep their columns' weights
   if (M == RING) {
@@ -242,6 +243,7 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
   const int teams = WARP ? blockDim.x >> 5 : 1;
   const int64_t row0 = WARP ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = (int64_t)gridDim.x * teams;
+  grid_start();
   for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
   float2 w[M == RING ? VPT : 1][4];
   if (M == RING) {
@@ -328,11 +330,11 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
 // (a CTA of 32 columns leaves too few of them), each lane in row order, then
 // the lanes of a warp pairwise, then the warps in order.
 constexpr int kSumThreads = 512;
-__global__ void __launch_bounds__(kSumThreads) dweight_kernel(const float *__restrict__ part, int parts, int cols,
-                                                              float *__restrict__ dw) {
+__global__ void __launch_bounds__(kSumThreads) dweight_kernel(const float *part, int parts, int cols, float *dw) {
   __shared__ float s[kSumThreads / 32][8];
   const int col = threadIdx.x & 7, c = blockIdx.x * 8 + col;
   float v = 0.f;
+  grid_start();
   if (c < cols) {
 #pragma unroll 4
     for (int p = threadIdx.x >> 3; p < parts; p += kSumThreads / 8) v += part[(int64_t)p * cols + c];
@@ -406,14 +408,8 @@ Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wi
   return s;
 }
 
-template <typename K, typename A>
-cudaError_t launch_rows(K kern, const Shape &s, const A &a, cudaStream_t st) {
-  if (s.smem > 40 * 1024) {  // with the static part, past the 48 KB that need no leave
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<s.grid, s.threads, s.smem, st>>>(a);
-  return cudaGetLastError();
+template <typename A> cudaError_t launch_rows(void (*kern)(A), const Shape &s, const A &a, cudaStream_t st) {
+  return launch_overlapped(kern, (unsigned)s.grid, (unsigned)s.threads, s.smem, 1, st, a);
 }
 
 template <typename T> cudaError_t norm_typed(const kda_rms_norm_args &a, cudaStream_t st) {
@@ -451,8 +447,8 @@ template <typename T> cudaError_t bwd_typed(const kda_rms_norm_bwd_args &a, cuda
   else KDA_BWD(ODD, 4, false);
 #undef KDA_BWD
   if (e != cudaSuccess || !a.dweight) return e;
-  dweight_kernel<<<(a.cols + 7) / 8, kSumThreads, 0, st>>>(static_cast<const float *>(a.workspace), s.grid, a.cols, a.dweight);
-  return cudaGetLastError();
+  return launch_overlapped(dweight_kernel, (unsigned)((a.cols + 7) / 8), kSumThreads, 0, 1, st,
+                           static_cast<const float *>(a.workspace), s.grid, a.cols, a.dweight);
 }
 
 }  // namespace
