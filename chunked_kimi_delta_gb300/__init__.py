@@ -835,17 +835,22 @@ class RmsNorm(NamedTuple):
 # These calls also run for single tokens, where the host's time counts: each
 # tensor's properties are read once, and the general checks above are only
 # called to name what is wrong.
-_F8 = _E8 = _BF16 = _F32 = None
+_F8 = _E8 = _BF16 = _F32 = _alloc = None
 
 
 def _ready():
-    """(torch, lib), with the dtypes above in place."""
-    global _F8, _E8, _BF16, _F32
+    """The library, with the names above in place."""
+    global _F8, _E8, _BF16, _F32, _alloc
     if _F8 is None:
         torch = _torch()
         _E8, _BF16, _F32 = torch.float8_e8m0fnu, torch.bfloat16, torch.float32
+        # (size, stride, dtype) on the current device; the general function takes
+        # several times as long as the rest of a small call
+        _alloc = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+        _alloc = getattr(_alloc, "_empty_strided_cuda", None) or (
+            lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda"))
         _F8 = torch.float8_e4m3fn
-    return _torch_module or _torch(), _lib or load_library()
+    return _lib or load_library()
 
 
 def _scale_shape(rows, cols, kind):
@@ -856,11 +861,11 @@ def _scale_shape(rows, cols, kind):
     return ((rows + 127) // 128, (cols + 127) // 128)
 
 
-def _empty_fp8(rows, cols, kind, device) -> Fp8Matrix:
-    torch, _ = _ready()
-    return Fp8Matrix(
-        torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=_F8, device=device),
-        torch.empty(_scale_shape(rows, cols, kind), dtype=_E8, device=device), kind)
+def _empty_fp8(rows, cols, kind) -> Fp8Matrix:
+    """Uninitialised, on the current device."""
+    shape = _scale_shape(rows, cols, kind)
+    stride = (shape[1], 1) if kind == "tile" else (4 * shape[1], 4, 1)
+    return Fp8Matrix(_alloc((rows, cols), ((cols + 15) // 16 * 16, 1), _F8), _alloc(shape, stride, _E8), kind)
 
 
 def _pitch(t) -> int:
@@ -916,32 +921,33 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None
     ``out=False`` then leaves out the result in x's dtype.  ``residual_out``
     (x + residual) may be given as ``x`` or ``residual`` to work in place.
     See ``kda_rms_norm`` in include/kda.h."""
-    torch, lib = _ready()
+    lib = _ready()
     shape, dtype = x.shape, x.dtype
     code, cols = _in_code(dtype), shape[-1]
     if weight is not None:
         _check_weight(weight, cols)
-    if out is False:
+    want_out = out is not False
+    if not want_out:
         if not fp8:
             raise ValueError("no result: out=False needs fp8=True")
         out = None
-    elif out is None:
-        out = torch.empty_like(x)
-    else:
+    elif out is not None:
         _like(out, shape, dtype, "out")
     if residual is not None:
         _like(residual, shape, dtype, "residual")
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
-        else:
+        if residual_out is not None:
             _like(residual_out, shape, dtype, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     dev = _launch_device(x, weight, residual, out, residual_out)
+    if want_out and out is None:
+        out = _alloc(tuple(shape), x.stride(), dtype)
+    if residual is not None and residual_out is None:
+        residual_out = _alloc(tuple(shape), x.stride(), dtype)
     rows = x.numel() // cols if cols else 0
     q, q_ptr, ld, scales_ptr = None, None, 0, None
     if fp8:
-        q = _empty_fp8(rows, cols, "row", x.device)
+        q = _empty_fp8(rows, cols, "row")
         q_ptr, ld, scales_ptr = q.data.data_ptr(), (cols + 15) // 16 * 16, q.scales.data_ptr()
     a = kda_rms_norm_args(rows, cols, code, x.data_ptr(), _ptr(residual), _ptr(weight), eps,
                           _ptr(residual_out), _ptr(out), q_ptr, ld, scales_ptr)
@@ -958,7 +964,7 @@ def kda_rms_norm_bwd(d_out, x, weight=None, d_residual=None, *, eps=1e-6, dx=Non
     the gradient that reaches it from elsewhere.  Returns ``(dx, dweight)``:
     dx is the gradient of x and of the residual, dweight fp32 [cols] (None
     without ``want_dweight``).  See ``kda_rms_norm_bwd`` in include/kda.h."""
-    torch, lib = _ready()
+    lib = _ready()
     shape, dtype = x.shape, x.dtype
     code, cols = _in_code(dtype), shape[-1]
     if weight is not None:
@@ -966,18 +972,19 @@ def kda_rms_norm_bwd(d_out, x, weight=None, d_residual=None, *, eps=1e-6, dx=Non
     _like(d_out, shape, dtype, "d_out")
     if d_residual is not None:
         _like(d_residual, shape, dtype, "d_residual")
-    if dx is None:
-        dx = torch.empty_like(x)
-    else:
+    if dx is not None:
         _like(dx, shape, dtype, "dx")
     dev = _launch_device(x, d_out, weight, d_residual, dx, workspace)
+    if dx is None:
+        dx = _alloc(tuple(shape), x.stride(), dtype)
     rows = x.numel() // cols if cols else 0
     a = kda_rms_norm_bwd_args(rows, cols, code, d_out.data_ptr(), x.data_ptr(), _ptr(weight),
                               _ptr(d_residual), eps, dx.data_ptr())
     dweight = None
     if want_dweight:
-        dweight = torch.empty(cols, dtype=_F32, device=x.device)
-        ws = _workspace(lib.kda_rms_norm_bwd_workspace_size(rows, cols), x.device, workspace)
+        dweight = _alloc((cols,), (1,), _F32)
+        need = lib.kda_rms_norm_bwd_workspace_size(rows, cols)
+        ws = _alloc((need // 4,), (1,), _F32) if workspace is None else _workspace(need, x.device, workspace)
         a.dweight, a.workspace = dweight.data_ptr(), ws.data_ptr()
         a.workspace_bytes = ws.numel() * ws.element_size()
     status = lib.kda_rms_norm_bwd(ctypes.byref(a), _raw_stream(stream, dev))
@@ -991,7 +998,7 @@ def kda_fp8_quantize(x, kinds=("row",), *, stream=None):
     scales, once for each of ``kinds`` ("row", "col", "tile") from one read of
     x.  Returns a tuple of :class:`Fp8Matrix` in the order of ``kinds``.  See
     ``kda_fp8_quantize`` in include/kda.h."""
-    _, lib = _ready()
+    lib = _ready()
     if isinstance(kinds, str):
         kinds = (kinds,)
     if not kinds or len(set(kinds)) != len(kinds) or not {"row", "col", "tile"}.issuperset(kinds):
@@ -1000,8 +1007,7 @@ def kda_fp8_quantize(x, kinds=("row",), *, stream=None):
         raise ValueError("x is [rows, cols]")
     code, dev = _in_code(x.dtype), _launch_device(x)
     rows, cols = x.shape
-    device = x.device
-    parts = tuple([_empty_fp8(rows, cols, k, device) for k in kinds])
+    parts = tuple([_empty_fp8(rows, cols, k) for k in kinds])
     a = kda_fp8_quantize_args(rows, cols, code, x.data_ptr(), (cols + 15) // 16 * 16)
     for p in parts:
         setattr(a, p.kind, p.data.data_ptr())
@@ -1058,7 +1064,7 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
     ``out`` (rows dense, any pitch).  ``workspace`` (256 zeroed bytes) takes
     the device error word; without it one per device is shared, read by
     :func:`kda_fp8_matmul_status`.  See ``kda_fp8_matmul`` in include/kda.h."""
-    torch, lib = _ready()
+    lib = _ready()
     if form not in _FP8_FORMS:
         raise ValueError('form is "nt", "nn" or "tn"')
     code, ka, kb = _FP8_FORMS[form]
@@ -1071,17 +1077,21 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
     if k != k_b:
         raise ValueError(f"the operands sum over {k} and {k_b}")
     ad, bd, a_scales, b_scales = a.data, b.data, a.scales, b.scales
-    if out is None:
-        out = torch.empty((m, n), dtype=out_dtype or _BF16, device=ad.device)
-        ldo = n
-    else:
+    ldo = n
+    if out is not None:
         if out.shape != (m, n) or (out_dtype is not None and out.dtype is not out_dtype):
             raise ValueError(f"out must be [{m}, {n}] of out_dtype")
-        ldo = _pitch(out)
-    out_code = _in_code(out.dtype)
+        out_dtype, ldo = out.dtype, _pitch(out)
+    elif out_dtype is None:
+        out_dtype = _BF16
+    out_code = _in_code(out_dtype)
     dev = _launch_device(a_scales, b_scales)
-    if ad.get_device() != dev or bd.get_device() != dev or out.get_device() != dev:
-        _on_device(a_scales, ad, bd, out)
+    if ad.get_device() != dev or bd.get_device() != dev:
+        _on_device(a_scales, ad, bd)
+    if out is None:
+        out = _alloc((m, n), (n, 1), out_dtype)
+    elif out.get_device() != dev:
+        _on_device(a_scales, out)
     if workspace is None:
         ws, ws_bytes = _fp8_status_word(dev), KDA_FP8_MATMUL_WORKSPACE_BYTES
     else:

@@ -128,7 +128,8 @@ def test_binding_refusals(lib):
 
 
 def _matrix(rows, cols, kind):
-    return kda._empty_fp8(rows, cols, kind, "cpu")
+    data = torch.zeros(rows, -(-cols // 16) * 16, dtype=torch.uint8).view(torch.float8_e4m3fn)[:, :cols]
+    return kda.Fp8Matrix(data, torch.zeros(kda._scale_shape(rows, cols, kind), dtype=torch.uint8).view(torch.float8_e8m0fnu), kind)
 
 
 def test_binding_matmul_refusals(lib):
