@@ -18,7 +18,7 @@ extern "C" {
 kda_status kda_rms_norm(const kda_rms_norm_args *a, kda_stream_t stream) {
   if (!a || a->rows < 0 || a->cols < 1 || bad_dtype(a->dtype)) return KDA_ERR_INVALID_ARG;
   if (a->rows > 0 && (!a->x || (!a->out && !a->fp8))) return KDA_ERR_INVALID_ARG;
-  if (a->residual && !a->residual_out) return KDA_ERR_INVALID_ARG;
+  if (a->residual && (!a->residual_out || a->residual_out == a->out)) return KDA_ERR_INVALID_ARG;
   if (a->fp8 && (!a->fp8_scales || a->ld_fp8 < a->cols)) return KDA_ERR_INVALID_ARG;
   if (a->cols > KDA_RMS_NORM_MAX_COLS || a->rows > INT32_MAX) return KDA_ERR_UNSUPPORTED;
   if (mis16(a->x) || mis16(a->residual) || mis16(a->weight) || mis16(a->residual_out) || mis16(a->out) ||

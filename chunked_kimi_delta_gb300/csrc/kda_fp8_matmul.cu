@@ -138,7 +138,7 @@ __device__ bool mm_wait_slow(uint64_t *bar, uint32_t parity, Bars *b, uint32_t *
                              unsigned long long limit_ns) {
   const unsigned long long t0 = globaltimer();
   while (true) {
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < 8; ++i)  // a try may be held by the hardware for milliseconds
       if (try_wait_cluster(bar, parity)) return true;
     if (b->abort) return false;
     if (globaltimer() - t0 > limit_ns) {

@@ -8,7 +8,8 @@
  * in chunks of 64 tokens, together with the segment affine summary (M, S~)
  * of a token range, the ordered prefix scan S <- M_j S + S~_j that composes
  * summaries, and the gather/scatter of per-request states between a cache
- * pool and packed rows.
+ * pool and packed rows; and, around such a layer, the 8-bit projection path
+ * (RMS norm, quantiser, matrix product).
  *
  * Conventions shared by every call
  *  - All tensor pointers are DEVICE pointers unless a comment says "host".
@@ -509,11 +510,11 @@ typedef enum { KDA_FP8_ROW = 1, KDA_FP8_COL = 2, KDA_FP8_TILE = 4 } kda_fp8_kind
  *   out = y rounded to `dtype`;  fp8 = y quantised with ROW scales (from the
  *   fp32 y, not from the rounded `out`)
  * residual NULL: h = x and residual_out is ignored.  weight NULL: ones.
- * out or fp8 may be NULL (not written), not both.  residual_out may be x or
- * residual, and out may be x, residual or residual_out's input in place.
+ * out or fp8 may be NULL (not written), not both.  In place: each of
+ * residual_out and out may be x or residual, but not both the same.
  * rows == 0 launches nothing.  Errors: KDA_ERR_INVALID_ARG (rows < 0, cols <
- * 1, null x, no output, residual without residual_out, fp8 without
- * fp8_scales, ld_fp8 < cols), KDA_ERR_UNSUPPORTED (cols >
+ * 1, null x, no output, residual without residual_out, out the same as
+ * residual_out, fp8 without fp8_scales, ld_fp8 < cols), KDA_ERR_UNSUPPORTED (cols >
  * KDA_RMS_NORM_MAX_COLS, rows > 2^31 - 1), KDA_ERR_ALIGNMENT (a pointer not
  * 16-byte aligned, ld_fp8 not a multiple of 16), KDA_ERR_CUDA.
  */

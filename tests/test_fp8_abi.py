@@ -51,7 +51,8 @@ INVALID, UNSUPPORTED, ALIGNMENT, WORKSPACE = 1, 2, 3, 4
 
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(x=None), INVALID), (dict(dtype=7), INVALID),
-    (dict(out=None, fp8=None), INVALID), (dict(residual_out=None), INVALID), (dict(fp8_scales=None), INVALID),
+    (dict(out=None, fp8=None), INVALID), (dict(residual_out=None), INVALID),
+    (dict(residual_out=5 * BASE), INVALID), (dict(fp8_scales=None), INVALID),
     (dict(ld_fp8=240), INVALID), (dict(cols=32769, ld_fp8=32784), UNSUPPORTED), (dict(rows=1 << 31), UNSUPPORTED),
     (dict(x=BASE + 2), ALIGNMENT), (dict(weight=BASE + 4), ALIGNMENT), (dict(ld_fp8=264), ALIGNMENT),
     (dict(fp8_scales=BASE + 8), ALIGNMENT), (dict(rows=0), 0)])
@@ -78,7 +79,7 @@ def test_norm_bwd_refusals(lib, kw, want):
     (dict(row=None, col=None, tile=None), INVALID), (dict(row_scales=None), INVALID),
     (dict(col_scales=None), INVALID), (dict(tile_scales=None), INVALID), (dict(ld=240), INVALID),
     (dict(ld=260), ALIGNMENT), (dict(x=BASE + 4), ALIGNMENT), (dict(col=BASE + 8), ALIGNMENT),
-    (dict(rows=1 << 40, cols=1 << 20, ld=1 << 20), UNSUPPORTED), (dict(rows=0), 0), (dict(cols=0), 0)])
+    (dict(rows=1 << 40, cols=1 << 20, ld=1 << 20), UNSUPPORTED), (dict(rows=1 << 37), UNSUPPORTED), (dict(rows=0), 0), (dict(cols=0), 0)])
 def test_quantize_refusals(lib, kw, want):
     assert lib.kda_fp8_quantize(ctypes.byref(_quant(**kw)), None) == want
     assert lib.kda_fp8_quantize(None, None) == INVALID
@@ -90,7 +91,8 @@ def test_quantize_refusals(lib, kw, want):
     (dict(ldo=99), INVALID), (dict(lda=192), INVALID), (dict(form=kda.KDA_FP8_NN, ldb=96), INVALID),
     (dict(form=kda.KDA_FP8_TN, lda=0), INVALID), (dict(lda=201), ALIGNMENT), (dict(ldb=216), ALIGNMENT),
     (dict(a=BASE + 8), ALIGNMENT), (dict(out=BASE + 1), ALIGNMENT), (dict(out_dtype=kda.KDA_F32, out=BASE + 2), ALIGNMENT),
-    (dict(lda=1 << 31), UNSUPPORTED), (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=255), WORKSPACE),
+    (dict(lda=1 << 31), UNSUPPORTED),
+    (dict(m=(1 << 31) - 1), UNSUPPORTED), (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=255), WORKSPACE),
     (dict(workspace=BASE + 128), ALIGNMENT), (dict(m=0), 0), (dict(n=0), 0)])
 def test_matmul_refusals(lib, kw, want):
     assert lib.kda_fp8_matmul(ctypes.byref(_mm(**kw)), None) == want

@@ -346,3 +346,32 @@ def test_matmul_wait_that_runs_out_is_reported(cuda_lib, m, n, k):
     assert cuda_lib.kda_get_device_status(ws) == cuda_lib.KDA_OK
     assert torch.equal(cuda_lib.kda_fp8_matmul(a, b, workspace=ws), want)
     assert cuda_lib.kda_get_device_status(ws) == cuda_lib.KDA_OK
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """Rows whose elements and bytes lie past 2^31 and 2^32: the last ones
+    equal the same rows worked alone."""
+    rows, cols = 1_050_000, 2056   # 2.2e9 elements
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-300:] = _rand((300, cols), torch.bfloat16, 100)
+    x[:300] = x[-300:]
+    got = cuda_lib.kda_rms_norm(x, None, fp8=True)
+    alone = cuda_lib.kda_rms_norm(x[-300:].clone(), None, fp8=True)
+    for part in (got.out[-300:], got.out[:300]):
+        assert torch.equal(part, alone.out)
+    assert torch.equal(got.fp8.data[-300:].view(torch.uint8), alone.fp8.data.view(torch.uint8))
+    assert torch.equal(got.fp8.scales[:, -300:].view(torch.uint8), alone.fp8.scales.view(torch.uint8))
+    dx, _ = cuda_lib.kda_rms_norm_bwd(got.out, x)
+    dx_alone, _ = cuda_lib.kda_rms_norm_bwd(alone.out, x[-300:].clone())
+    assert torch.equal(dx[-300:], dx_alone)
+    del dx, got
+    row, = cuda_lib.kda_fp8_quantize(x)
+    row_alone, = cuda_lib.kda_fp8_quantize(x[-300:].clone())
+    assert torch.equal(row.data[-300:].view(torch.uint8), row_alone.data.view(torch.uint8))
+    w, = cuda_lib.kda_fp8_quantize(_rand((2304, cols), torch.float32, 101), kinds="tile")
+    y = cuda_lib.kda_fp8_matmul(row, w)   # 2.4e9 outputs
+    y_alone = cuda_lib.kda_fp8_matmul(row_alone, w, out_dtype=torch.float32)
+    # the two kernels may sum in another order
+    d = (y[-300:].float() - y_alone).abs().max()
+    assert float(d) <= float(y_alone.abs().max()) * 2 * U16
+    assert torch.equal(y[-300:], y[:300])
