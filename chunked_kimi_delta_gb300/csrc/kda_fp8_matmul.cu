@@ -132,8 +132,9 @@ __device__ __forceinline__ float4 load_peer(const float *p, uint32_t rank) {
   return v;
 }
 
-// Bounded wait.  The first wait of a cluster that runs out records the
-// timeout and tells every CTA of the cluster, whose waits then end too.
+// Bounded wait.  The first wait that runs out records the timeout and tells
+// the CTA, and with pairs (cluster_ctas 2) the other one: their waits then
+// end too.
 __device__ bool mm_wait_slow(uint64_t *bar, uint32_t parity, Bars *b, uint32_t *err, uint32_t cluster_ctas,
                              unsigned long long limit_ns) {
   const unsigned long long t0 = globaltimer();
@@ -143,7 +144,8 @@ __device__ bool mm_wait_slow(uint64_t *bar, uint32_t parity, Bars *b, uint32_t *
     if (b->abort) return false;
     if (globaltimer() - t0 > limit_ns) {
       atomicOr(err, DEV_ERR_TIMEOUT);
-      for (uint32_t r = 0; r < cluster_ctas; ++r)
+      b->abort = 1;
+      for (uint32_t r = 0; cluster_ctas > 1 && r < cluster_ctas; ++r)
         asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(peer_addr(&b->abort, r)), "r"(1u) : "memory");
       return false;
     }
@@ -365,6 +367,13 @@ __device__ __forceinline__ void settle() {
 // Persistent CTA pairs: 256 columns n x width rows m per tile, one pair-wide
 // MMA (cta_group::2) on each CTA's 128 lanes and half of the column side.
 // Two accumulators: the epilogue of a tile runs under the next one's MMAs.
+// What bounds it is the way of the operands: a block of k brings 30.7 KB to
+// an SM, 480 cycles at 64 bytes a cycle from L2 (and again 480 for shared
+// memory to take them in and give them to the MMAs at 128), against 448
+// cycles of MMAs; measured 565 at 32768 x 4096 x 4096 (311 us, 3.5 PFLOP/s
+// from rest, 363 us back to back under the power cap; tensor pipe 78% busy).
+// Half of the MMAs left out changed little (300 us), 26% less read from L2 by
+// multicast of the lane side to a second pair nothing at all.
 // Warps 0-7 epilogue, 8 scales, 9 TMA, 10 MMA (first CTA of the pair).
 constexpr int PAIR_THREADS = 352;
 constexpr int PAIR_MAX_WIDTH = 224;  // two accumulators and the scale ring fill the 512 columns
