@@ -127,8 +127,9 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
   const int64_t step = (int64_t)gridDim.x * teams;
   grid_start();
   for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
-  float2 w[M == RING ? VPT : 1][4];  // the ring's threads keep their columns' weights
-  if (M == RING) {
+  constexpr bool KEEP = VPT < 4 || M == RING;  // threads of few columns keep their weights
+  float2 w[KEEP ? VPT : 1][4];
+  if (KEEP) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) load_weight<M>(a.weight, first_col<M, WARP>(i), cols, w[i]);
   }
@@ -165,9 +166,9 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
       const int c = first_col<M, WARP>(i);
       float2 p[4];  // h w; y = h w rstd
       h[i].get(p);
-      if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
+      if (!KEEP) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = mul2<M>(p[j], w[M == RING ? i : 0][j]);
+      for (int j = 0; j < 4; ++j) p[j] = mul2<M>(p[j], w[KEEP ? i : 0][j]);
       if (a.out) {
         float2 y[4];
 #pragma unroll
@@ -210,7 +211,7 @@ constexpr int kMaxParts = 1216;  // partial dweight rows at most: 8 CTAs on each
 // dweight of a team's rows is summed in its registers; a CTA leaves one row of
 // partial sums.
 template <typename T, Mode M, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT < 4 ? 512 : 1024, WARP && VPT == 2 ? 4 : M != RING && VPT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT < 4 ? 512 : 1024, WARP && VPT == 2 ? (M == ODD ? 2 : 4) : M != RING && VPT == 1 ? 2 : 1)
 rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
   extern __shared__ uint4 smem_raw[];
   __shared__ float red[2][2][32];
@@ -245,17 +246,29 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
   const int64_t step = (int64_t)gridDim.x * teams;
   grid_start();
   for (int s = 0; s < kDepth; ++s) fetch(row0 + s * step, s);
-  float2 w[M == RING ? VPT : 1][4];
-  if (M == RING) {
+  constexpr bool KEEP = VPT < 4 || M == RING;  // as above; outside the ring, the row's values too
+  float2 w[KEEP ? VPT : 1][4];
+  if (KEEP) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) load_weight<M>(a.weight, first_col<M, WARP>(i), cols, w[i]);
   }
   int stage = 0, parity = 0;
   for (int64_t row = row0; row < a.rows; row += step) {
     if (M == RING) wait_oldest();
-    // h and g are read again after the sum, from the ring or the caches: kept
-    // in registers they would leave room for fewer threads.
+    // In the ring, h and g are read again after the sum: kept in registers they
+    // would leave room for fewer threads.
+    Raw8<T> kept[KEEP && M != RING ? VPT : 1][3];
+    if (KEEP && M != RING) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = first_col<M, WARP>(i);
+        kept[i][0] = load<T, M>(hp + row * cols, c, cols);
+        kept[i][1] = load<T, M>(gp + row * cols, c, cols);
+        if (dp) kept[i][2] = load<T, M>(dp + row * cols, c, cols);
+      }
+    }
     auto get = [&](int tensor, const T *p, int i, int c) {
+      if (KEEP && M != RING) return kept[i][tensor];
       if (M != RING) return load<T, M>(p + row * cols, c, cols);
       return c < cols ? *slot(stage, tensor, i) : raw_zero<T>();
     };
@@ -266,11 +279,11 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
       float2 h[4], g[4];
       get(0, hp, i, c).get(h);
       get(1, gp, i, c).get(g);
-      if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
+      if (!KEEP) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         ss = fma2<M>(h[j], h[j], ss);
-        sg = fma2<M>(mul2<M>(g[j], w[M == RING ? i : 0][j]), h[j], sg);
+        sg = fma2<M>(mul2<M>(g[j], w[KEEP ? i : 0][j]), h[j], sg);
       }
     }
     float sums[2] = {ss.x + ss.y, sg.x + sg.y};
@@ -285,14 +298,14 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
       float2 h[4], g[4], d[4], dx[4];
       get(0, hp, i, c).get(h);
       get(1, gp, i, c).get(g);
-      if (M != RING) load_weight<M>(a.weight, c, cols, w[0]);
+      if (!KEEP) load_weight<M>(a.weight, c, cols, w[0]);
       if (dp) get(2, dp, i, c).get(d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         dw[i][j] = fma2<M>(g[j], mul2<M>(h[j], r2), dw[i][j]);
         // rstd (w g - n mean) + d
         const float2 t = dp ? fma2<M>(h[j], nm, d[j]) : mul2<M>(h[j], nm);
-        dx[j] = fma2<M>(mul2<M>(g[j], w[M == RING ? i : 0][j]), r2, t);
+        dx[j] = fma2<M>(mul2<M>(g[j], w[KEEP ? i : 0][j]), r2, t);
       }
       store<T, M>(static_cast<T *>(a.dx) + row * cols, c, cols, dx);
     }
