@@ -63,7 +63,7 @@ struct MmArgs {
   int span;                  // blocks of k that one accumulator sums
   void *out;
   int64_t ldo;
-  bool out_tma;              // the output takes TMA stores (bf16, 16-byte rows)
+  bool out_tma;              // the output takes TMA stores (rows on 16 bytes)
   uint32_t *err;
   bool test_wait;
 };
@@ -305,7 +305,7 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
 }
 constexpr uint32_t OUT_PANEL = 4096;               // 32 rows m x 64 columns n of bf16
 constexpr uint32_t OUT_BUF = 2 * OUT_PANEL;        // the 128 lanes
-constexpr uint32_t OUT_BYTES = 4 * OUT_BUF;        // two buffers for each half of the epilogue's warps
+constexpr uint32_t OUT_BYTES = 4 * OUT_BUF;        // two buffers for each half of the epilogue's warps (fp32: for each warp)
 // One warp's 32 lanes of a 32-row chunk into the staging tile: fragments are
 // stored transposed, so that a row m of shared memory holds neighbouring n.
 __device__ __forceinline__ void stage_chunk(uint32_t acc, uint8_t *buf, int quarter, int lane) {
@@ -482,7 +482,25 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
             tc::tmem_ld16(acc + c + 16 * u, v);
             tc::tmem_ld_wait();
             if (sizeof(T) == 4 && !(first && last)) add_span(sum[2 * i + u], v, first);
-            if (last) store_columns<T>(a, v, l0 + 32 * quarter + lane, c0 + c + 16 * u, c0 + end);
+            if (!last) continue;
+            if (sizeof(T) == 4 && a.out_tma) {
+              // this warp's own 16 rows m x 32 columns n, 128 bytes a row
+              float *stage = reinterpret_cast<float *>(sm + a.stages * a.stage_bytes + SF_BYTES) + (2 * warp + u) * 512;
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+              __syncwarp();  // the buffer's last store has been read
+#pragma unroll
+              for (int j = 0; j < 16; ++j) stage[32 * j + lane] = v[j];
+              tc::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (16 * u + c < end && l0 + 32 * quarter < a.lanes)
+                  tma_store_2d(&out_map, stage, l0 + 32 * quarter, c0 + c + 16 * u);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              }
+              __syncwarp();
+            } else {
+              store_columns<T>(a, v, l0 + 32 * quarter + lane, c0 + c + 16 * u, c0 + end);
+            }
           }
         }
       }
@@ -495,7 +513,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
         t += pairs;
       }
     }
-    if (staged && issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (a.out_tma && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   } else if (warp == 9) {  // TMA
     if (elect_one()) {
@@ -830,9 +848,8 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   const int box_rows = pair ? a.width / 2 : a.width;  // column-side rows of one CTA
   a.col_box_bytes = a.col_mn ? 16384 : (uint32_t)box_rows * 128;
   a.stage_bytes = LANE_BYTES + ((a.col_box_bytes + 1023) & ~1023u);
-  const int64_t row_bytes = p.ldo * 2;
-  a.out_tma = pair && p.out_dtype == KDA_BF16 && row_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
-              p.ldo <= INT32_MAX;
+  const bool f32 = p.out_dtype == KDA_F32;
+  a.out_tma = pair && p.ldo * (f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo <= INT32_MAX;
   // a pair has its SMs to itself, and so do split CTAs when there is one for each; else two share
   const bool alone = pair || (int64_t)a.tiles * a.splits <= 152;
   uint32_t budget = SMEM_LIMIT - SF_BYTES - (a.out_tma ? OUT_BYTES : 0);
@@ -851,19 +868,19 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
                              : tcp::make_byte_map(p.b, p.k, p.n, p.ldb, 128, lm)) &&
                   (a.col_mn ? tcp::make_byte_map(p.a, p.m, p.k, p.lda, 128, cm)
                             : tcp::make_byte_map(p.a, p.k, p.m, p.lda, (uint32_t)box_rows, cm)) &&
-                  (!a.out_tma || tcp::make_bf16_map(p.out, p.n, p.m, p.ldo, 32, om));
+                  (!a.out_tma || tcp::make_out_tile_map(p.out, f32, p.n, p.m, p.ldo, f32 ? 32 : 64, f32 ? 16 : 32, om));
   if (!ok) return cudaErrorInvalidValue;
   uint32_t smem = a.stages * a.stage_bytes + SF_BYTES + 1024;
   if (pair) {
     smem += a.out_tma ? OUT_BYTES : 0;
     const unsigned grid = 2u * (unsigned)(a.tiles < 76 ? a.tiles : 76);
-    return p.out_dtype == KDA_F32
+    return f32
                ? launch_overlapped(fp8_matmul_pair_kernel<float>, grid, PAIR_THREADS, smem, 2, st, lm, cm, om, a)
                : launch_overlapped(fp8_matmul_pair_kernel<__nv_bfloat16>, grid, PAIR_THREADS, smem, 2, st, lm, cm, om, a);
   }
   if (smem < 80 * 1024) smem = 80 * 1024;  // two CTAs an SM at most: that is what tensor memory holds
   const unsigned grid = (unsigned)(a.tiles * a.splits), cluster = (unsigned)a.splits;
-  return p.out_dtype == KDA_F32
+  return f32
              ? launch_overlapped(fp8_matmul_split_kernel<float>, grid, SPLIT_THREADS, smem, cluster, st, lm, cm, a)
              : launch_overlapped(fp8_matmul_split_kernel<__nv_bfloat16>, grid, SPLIT_THREADS, smem, cluster, st, lm, cm, a);
 }

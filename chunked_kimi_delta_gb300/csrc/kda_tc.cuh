@@ -265,9 +265,10 @@ bool make_value_map(const void *x, int64_t T_tot, int H, CUtensorMap &map);
 // bytes x box_outer rows, swizzled, zeros outside.
 bool make_byte_map(const void *p, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_outer,
                    CUtensorMap &map);
-// The same for bf16 (pitch in elements): boxes of 64 elements x box_outer rows.
-bool make_bf16_map(const void *p, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_outer,
-                   CUtensorMap &map);
+// A result [outer, pitch] of fp32 or bf16 (pitch in elements) for TMA stores
+// of tiles whose rows are 128 bytes: plain (fp32) or swizzled (bf16).
+bool make_out_tile_map(const void *p, bool f32, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_inner,
+                       uint32_t box_outer, CUtensorMap &map);
 bool make_out_map(const void *o, int64_t T_tot, int H, int dv, CUtensorMap &map);
 
 // Segment summary (kda_tc_summary.cu): M [.., dk, dk] and S~ [.., dk, dv] of
