@@ -801,8 +801,11 @@ struct Plan {
   int width, splits;
 };
 
-// Pairs of CTAs take 256 x 224 tiles when there is one for each of the 76
-// pairs.  Fewer tiles leave pairs idle, and 128 x 64 ones for single CTAs,
+// Pairs of CTAs take the work when there is a 256 x 224 tile for each of the
+// 76 pairs, in tiles as wide as makes their turns shortest: a turn costs about
+// its width and 120 columns more (3000 x 2048 x 2048, two turns at any width
+// from 160 to 224: 14.3, 14.5, 14.9 us; 2000 x 8192 x 2048, four turns of 224
+// or five of 192: 24.8 and 27.6).  Fewer tiles leave pairs idle, and 128 x 64 ones for single CTAs,
 // two to an SM, are then as fast or faster (us, pairs at their best width
 // against single CTAs: 777 x 1111 x 2064 10.8 / 9.8, 512 x 4096 x 4096 13.9 /
 // 14.8, 300 x 1024 x 1024 7.5 / 6.8).  Where those do not fill the SMs, k is
@@ -810,7 +813,19 @@ struct Plan {
 // the meeting of the sums than it saves (1 x 4096 x 4096: 8.5 us in 2 parts,
 // 7.1 in 4, 6.9 in 8).
 Plan choose_plan(int m, int n, int kblocks) {
-  if ((int64_t)ceil_div(n, 256) * ceil_div(m, PAIR_MAX_WIDTH) >= 76) return {true, PAIR_MAX_WIDTH, 1};
+  const int64_t lane_tiles = ceil_div(n, 256);
+  if (lane_tiles * ceil_div(m, PAIR_MAX_WIDTH) >= 76) {
+    Plan best{true, PAIR_MAX_WIDTH, 1};
+    int64_t least = INT64_MAX;
+    for (int width = PAIR_MAX_WIDTH; width >= 128; width -= 32) {
+      const int64_t cost = (int64_t)ceil_div(lane_tiles * ceil_div(m, width), 76) * (width + 120);
+      if (cost < least) {
+        least = cost;
+        best.width = width;
+      }
+    }
+    return best;
+  }
   Plan p{false, m <= 16 ? 16 : m <= 32 ? 32 : SPLIT_MAX_WIDTH, 1};
   const int64_t tiles = (int64_t)ceil_div(n, 128) * ceil_div(m, p.width);
   while (p.splits < 8 && 8 * p.splits <= kblocks && tiles * p.splits * 2 <= 152) p.splits *= 2;
