@@ -303,12 +303,11 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) 
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-constexpr uint32_t OUT_PANEL = 4096;               // 32 rows m x 64 columns n of bf16
-constexpr uint32_t OUT_BUF = 2 * OUT_PANEL;        // the 128 lanes
-constexpr uint32_t OUT_BYTES = 4 * OUT_BUF;        // two buffers for each half of the epilogue's warps (fp32: for each warp)
-// One warp's 32 lanes of a 32-row chunk into the staging tile: fragments are
-// stored transposed, so that a row m of shared memory holds neighbouring n.
-__device__ __forceinline__ void stage_chunk(uint32_t acc, uint8_t *buf, int quarter, int lane) {
+constexpr uint32_t OUT_BUF = 2048;                // a warp's 32 rows m x 32 columns n of bf16, or 16 of fp32
+constexpr uint32_t OUT_BYTES = 8 * 2 * OUT_BUF;   // two for each warp of the epilogue
+// A warp's 32 lanes of 32 rows m into its staging tile: fragments are stored
+// transposed, so that a row m of shared memory holds neighbouring n.
+__device__ __forceinline__ void stage_chunk(uint32_t acc, uint8_t *buf, int lane) {
   uint32_t f[2][16];
   tmem_ld_frag(acc, f[0]);
   tmem_ld_frag(acc + (16u << 16), f[1]);
@@ -323,20 +322,11 @@ __device__ __forceinline__ void stage_chunk(uint32_t acc, uint8_t *buf, int quar
         const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(f[h][4 * c + 2 * n8]), __uint_as_float(f[h][4 * c + 2 * n8 + 1]));
         v[c] = *reinterpret_cast<const uint32_t *>(&p);
       }
-      // lane t gives the address of row m = t: 16 bytes of n, swizzled as the TMA store reads them
-      const uint32_t chunk = (uint32_t)(4 * quarter + 2 * h + n8);  // of eight columns n
-      const uint32_t addr = tc::smem_u32(buf) + (chunk >> 3) * OUT_PANEL + lane * 128 + (((chunk & 7) ^ (lane & 7)) << 4);
+      // lane t gives the address of row m = t: 16 bytes of n, in the 64-byte swizzle that the TMA store reads
+      const uint32_t addr = tc::smem_u32(buf) + lane * 64 + (((2 * h + n8) ^ ((lane >> 1) & 3)) << 4);
       asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
                    :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
     }
-}
-// Barrier of 128 threads, the AND of their flags returned to each.
-__device__ __forceinline__ bool half_and(bool v, int bar) {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
-               "selp.u32 %0, 1, 0, q;\n\t}"
-               : "=r"(r) : "r"((uint32_t)v), "r"(bar) : "memory");
-  return r != 0;
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
@@ -444,17 +434,30 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
     __syncwarp();
   } else if (warp < 8) {  // epilogue
     const int quarter = warp & 3, half = warp >> 2;
-    const bool staged = a.out_tma && sizeof(T) == 2, issuer = (threadIdx.x & 127) == 0;
-    uint8_t *out_buf = sm + a.stages * a.stage_bytes + SF_BYTES + half * 2 * OUT_BUF;
-    auto half_sync = [&]() { asm volatile("bar.sync %0, 128;" :: "r"(1 + half) : "memory"); };
-    Ring full(2);
+    // Full columns leave through this warp's two staging tiles and TMA stores:
+    // whole sectors whatever the order of the lanes, and nothing to wait for.
+    uint8_t *stage = sm + a.stages * a.stage_bytes + SF_BYTES + warp * 2 * OUT_BUF;
     int buf = 0;
+    auto stage_begin = [&]() {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();  // the tile's last store has been read
+      return stage + buf * OUT_BUF;
+    };
+    auto stage_end = [&](int n0, int m0, bool any) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (any) tma_store_2d(&out_map, stage + buf * OUT_BUF, n0, m0);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      buf ^= 1;
+    };
+    Ring full(2);
     float sum[8][16];  // this thread's outputs over the spans of k, when there is more than one
     for (int t = pair, kb = 0; t < a.tiles; full.next()) {
-      // one answer for the four warps that meet at a barrier
-      if (!half_and(mm_wait(b.acc_full + full.s, full.phase, &b, a.err, 2), 1 + half)) break;
+      if (!__all_sync(~0u, mm_wait(b.acc_full + full.s, full.phase, &b, a.err, 2))) break;
       tc::tc_fence_after();
-      const int l0 = lane0_of(t), c0 = col0_of(t);
+      const int n0 = lane0_of(t) + 32 * quarter, c0 = col0_of(t);
       const uint32_t acc = tmem + full.s * PAIR_MAX_WIDTH + ((uint32_t)(32 * quarter) << 16);
       const int end = min(a.width, a.cols - c0);
       const bool first = kb == 0, last = kb + a.span >= a.kblocks;
@@ -462,45 +465,25 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
       for (int i = 0; i < 4; ++i) {
         const int c = 32 * half + 64 * i;
         if (c >= a.width) break;
-        if (staged) {
-          if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          half_sync();  // the buffer's last store has been read
-          stage_chunk(acc + c, out_buf + buf * OUT_BUF, quarter, lane);
-          tc::fence_proxy_async_smem();
-          half_sync();
-          if (issuer) {
-            if (c < end)
-              for (int p = 0; p < 2 && l0 + 64 * p < a.lanes; ++p)
-                tma_store_2d(&out_map, out_buf + buf * OUT_BUF + p * OUT_PANEL, l0 + 64 * p, c0 + c);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
-          buf ^= 1;
-        } else {
+        if (sizeof(T) == 2 && a.out_tma) {
+          stage_chunk(acc + c, stage_begin(), lane);
+          stage_end(n0, c0 + c, c < end && n0 < a.lanes);
+          continue;
+        }
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float v[16];
-            tc::tmem_ld16(acc + c + 16 * u, v);
-            tc::tmem_ld_wait();
-            if (sizeof(T) == 4 && !(first && last)) add_span(sum[2 * i + u], v, first);
-            if (!last) continue;
-            if (sizeof(T) == 4 && a.out_tma) {
-              // this warp's own 16 rows m x 32 columns n, 128 bytes a row
-              float *stage = reinterpret_cast<float *>(sm + a.stages * a.stage_bytes + SF_BYTES) + (2 * warp + u) * 512;
-              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-              __syncwarp();  // the buffer's last store has been read
+        for (int u = 0; u < 2; ++u) {
+          float v[16];
+          tc::tmem_ld16(acc + c + 16 * u, v);
+          tc::tmem_ld_wait();
+          if (sizeof(T) == 4 && !(first && last)) add_span(sum[2 * i + u], v, first);
+          if (!last) continue;
+          if (sizeof(T) == 4 && a.out_tma) {  // 128 bytes a row, as they are
+            float *dst = reinterpret_cast<float *>(stage_begin());
 #pragma unroll
-              for (int j = 0; j < 16; ++j) stage[32 * j + lane] = v[j];
-              tc::fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (16 * u + c < end && l0 + 32 * quarter < a.lanes)
-                  tma_store_2d(&out_map, stage, l0 + 32 * quarter, c0 + c + 16 * u);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-              }
-              __syncwarp();
-            } else {
-              store_columns<T>(a, v, l0 + 32 * quarter + lane, c0 + c + 16 * u, c0 + end);
-            }
+            for (int j = 0; j < 16; ++j) dst[32 * j + lane] = v[j];
+            stage_end(n0, c0 + c + 16 * u, c + 16 * u < end && n0 < a.lanes);
+          } else {
+            store_columns<T>(a, v, n0 + lane, c0 + c + 16 * u, c0 + end);
           }
         }
       }
@@ -883,7 +866,7 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
                              : tcp::make_byte_map(p.b, p.k, p.n, p.ldb, 128, lm)) &&
                   (a.col_mn ? tcp::make_byte_map(p.a, p.m, p.k, p.lda, 128, cm)
                             : tcp::make_byte_map(p.a, p.k, p.m, p.lda, (uint32_t)box_rows, cm)) &&
-                  (!a.out_tma || tcp::make_out_tile_map(p.out, f32, p.n, p.m, p.ldo, f32 ? 32 : 64, f32 ? 16 : 32, om));
+                  (!a.out_tma || tcp::make_out_tile_map(p.out, f32, p.n, p.m, p.ldo, 32, f32 ? 16 : 32, om));
   if (!ok) return cudaErrorInvalidValue;
   uint32_t smem = a.stages * a.stage_bytes + SF_BYTES + 1024;
   if (pair) {

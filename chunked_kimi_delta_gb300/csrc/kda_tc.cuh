@@ -266,7 +266,7 @@ bool make_value_map(const void *x, int64_t T_tot, int H, CUtensorMap &map);
 bool make_byte_map(const void *p, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_outer,
                    CUtensorMap &map);
 // A result [outer, pitch] of fp32 or bf16 (pitch in elements) for TMA stores
-// of tiles whose rows are 128 bytes: plain (fp32) or swizzled (bf16).
+// of tiles 32 elements wide: plain (fp32) or in the 64-byte swizzle (bf16).
 bool make_out_tile_map(const void *p, bool f32, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_inner,
                        uint32_t box_outer, CUtensorMap &map);
 bool make_out_map(const void *o, int64_t T_tot, int H, int dv, CUtensorMap &map);
