@@ -881,7 +881,7 @@ def _launch_device(lead, *ts) -> int:
     """Index of the device of a call whose tensors are dense and all on the
     current device."""
     dev = lead.get_device()
-    fine = dev >= 0 and lead.is_contiguous() and dev == _torch_module.cuda.current_device()
+    fine = dev >= 0 and lead.is_contiguous() and dev == _torch_module._C._cuda_getDevice()
     for t in ts:
         if t is not None:
             fine = fine and t.get_device() == dev and t.is_contiguous()
@@ -1033,8 +1033,8 @@ def _fp8_status_word(dev: int) -> int:
         word = torch.zeros(KDA_FP8_MATMUL_WORKSPACE_BYTES, dtype=torch.uint8,
                            device=torch.device("cuda", dev))
         torch.cuda.current_stream(dev).synchronize()
-        _fp8_status_words[dev] = word
-    return word.data_ptr()
+        word = _fp8_status_words[dev] = (word.data_ptr(), word)
+    return word[0]
 
 
 def _check_fp8(x: Fp8Matrix, kind: str):
@@ -1044,12 +1044,16 @@ def _check_fp8(x: Fp8Matrix, kind: str):
         raise ValueError(f"this operand needs {kind} scales, not {have}")
     if data.dtype is not _F8 or scales.dtype is not _E8:
         raise TypeError("a scaled 8-bit matrix holds float8_e4m3fn values and float8_e8m0fnu scales")
-    if data.dim() != 2:
+    shape = data.shape
+    if len(shape) != 2:
         raise ValueError("a scaled 8-bit matrix is [rows, cols]")
-    rows, cols = data.shape
+    rows, cols = shape
     if scales.shape != _scale_shape(rows, cols, kind):
         raise ValueError(f"{kind} scales of {(rows, cols)} values have shape "
                          f"{_scale_shape(rows, cols, kind)}, not {tuple(scales.shape)}")
+    pitch, step = data.stride()
+    if rows > 1 and step == 1:
+        return rows, cols, pitch
     return rows, cols, _pitch(data)
 
 
@@ -1070,13 +1074,14 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
     code, ka, kb = _FP8_FORMS[form]
     m, k, lda = _check_fp8(a, ka)
     n, k_b, ldb = _check_fp8(b, kb)
-    if form != "nt":
+    if code != KDA_FP8_NT:
         n, k_b = k_b, n
-        if form == "tn":
+        if code == KDA_FP8_TN:
             m, k = k, m
     if k != k_b:
         raise ValueError(f"the operands sum over {k} and {k_b}")
-    ad, bd, a_scales, b_scales = a.data, b.data, a.scales, b.scales
+    ad, a_scales, _ = a
+    bd, b_scales, _ = b
     ldo = n
     if out is not None:
         if out.shape != (m, n) or (out_dtype is not None and out.dtype is not out_dtype):
@@ -1112,4 +1117,4 @@ def kda_fp8_matmul_status(stream=None) -> int:
     read."""
     dev = _torch().cuda.current_device()
     _fp8_status_word(dev)
-    return kda_get_device_status(_fp8_status_words[dev], stream)
+    return kda_get_device_status(_fp8_status_words[dev][1], stream)

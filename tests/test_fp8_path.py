@@ -375,3 +375,36 @@ def test_offsets_beyond_32_bits(cuda_lib):
     d = (y[-300:].float() - y_alone).abs().max()
     assert float(d) <= float(y_alone.abs().max()) * 2 * U16
     assert torch.equal(y[-300:], y[:300])
+
+
+def test_calls_in_a_row_keep_their_order(cuda_lib):
+    """Each kernel is set up while the one before it ends: a chain of calls,
+    each on the last one's results and some in place, gives bit for bit what
+    it gives with a synchronisation after every call; torch's own kernels in
+    between."""
+    w, = cuda_lib.kda_fp8_quantize(_rand((1024, 1024), torch.float32, 110) / 32, kinds="tile")
+    x0, r0 = _rand((700, 1024), torch.bfloat16, 111), _rand((700, 1024), torch.bfloat16, 112)
+
+    def chain(wait):
+        x, r, total = x0.clone(), r0.clone(), torch.zeros(1024, 1024, device="cuda")
+        for i in range(12):
+            n = cuda_lib.kda_rms_norm(x, None, r, fp8=True, residual_out=r)
+            wait()
+            x = cuda_lib.kda_fp8_matmul(n.fp8, w)
+            wait()
+            row, col = cuda_lib.kda_fp8_quantize(x, ("row", "col"))
+            wait()
+            g = cuda_lib.kda_fp8_matmul(row, w, "nn")
+            wait()
+            g, dw = cuda_lib.kda_rms_norm_bwd(g, r, None, x, dx=g)
+            wait()
+            n_col, = cuda_lib.kda_fp8_quantize(n.out, "col")
+            total += cuda_lib.kda_fp8_matmul(col, n_col, "tn", out_dtype=torch.float32)
+            wait()
+            x = (x.float() * 0.5 + g.float() + dw * 1e-3).bfloat16()
+        return x, r, total
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(chain(lambda: None), want):
+            assert torch.equal(a, b)
