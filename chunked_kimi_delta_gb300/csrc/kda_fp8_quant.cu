@@ -8,8 +8,8 @@
 // instructions (24 an element for rows and columns together as first written,
 // 17 now), so maxima are taken on bf16 pairs, products on fp32 pairs, and a
 // column's scale is worked out by one thread and not by the sixteen that hold
-// its rows.  32768 x 4096 bf16: row 64.6 us, col 63.5 us (93% of the copy
-// rate), both at once 92 us (86%).
+// its rows.  32768 x 4096 bf16: row 64.5 us, col 61.2 us (97% of the copy
+// rate), both at once 90.7 us (87%).
 #include "kda_fp8.cuh"
 
 namespace kda {
@@ -229,7 +229,8 @@ fp8_quantize_kernel(kda_fp8_quantize_args a, int cblocks, int tiles) {
 }
 
 template <typename T, Mode M> cudaError_t launch(const kda_fp8_quantize_args &a, int cblocks, int tiles, cudaStream_t st) {
-  const int most = 152 * (sizeof(T) == 2 && M != ODD ? 3 : 2);
+  // three CTAs in turn on each place: SMs are not equally fast (one: 92.1 us, three: 90.7, one per block: 101)
+  const int most = 3 * 152 * (sizeof(T) == 2 && M != ODD ? 3 : 2);
   return launch_overlapped(fp8_quantize_kernel<T, M>, (unsigned)(tiles < most ? tiles : most), kThreads,
                            M == RING ? 8 * kThreads * 16 : 0, 1, st, a, cblocks, tiles);
 }
