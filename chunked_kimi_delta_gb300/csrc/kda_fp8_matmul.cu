@@ -360,10 +360,10 @@ __device__ __forceinline__ void settle() {
 // What bounds it is the way of the operands: a block of k brings 30.7 KB to
 // an SM, 480 cycles at 64 bytes a cycle from L2 (and again 480 for shared
 // memory to take them in and give them to the MMAs at 128), against 448
-// cycles of MMAs; measured 565 at 32768 x 4096 x 4096 (311 us, 3.5 PFLOP/s
-// from rest, 363 us back to back under the power cap; tensor pipe 78% busy).
-// Half of the MMAs left out changed little (300 us), 26% less read from L2 by
-// multicast of the lane side to a second pair nothing at all.
+// cycles of MMAs; measured about 560 at 32768 x 4096 x 4096 (306 us, 3.6
+// PFLOP/s from rest, 363 us back to back under the power cap; tensor pipe 78%
+// busy).  Half of the MMAs left out changed little (314 to 300 us), 26% less
+// read from L2 by multicast of the lane side to a second pair nothing at all.
 // Warps 0-7 epilogue, 8 scales, 9 TMA, 10 MMA (first CTA of the pair).
 constexpr int PAIR_THREADS = 352;
 constexpr int PAIR_MAX_WIDTH = 224;  // two accumulators and the scale ring fill the 512 columns
@@ -580,6 +580,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
 // One tile of 128 columns n x width rows m for a cluster of `splits` CTAs,
 // each with its own range of k; the partial sums meet through distributed
 // shared memory and are added in the order of k.
+// What bounds it is latency, from the launch over one pass of loads and MMAs
+// to the meeting of the sums: 1 x 4096 x 4096 takes 6.5 us where the weight's
+// bytes take 2.5.
 // Warps 0-3 epilogue, 4 scales, 5 TMA, 6 MMA.
 constexpr int SPLIT_THREADS = 224;
 constexpr int SPLIT_MAX_WIDTH = 64;
