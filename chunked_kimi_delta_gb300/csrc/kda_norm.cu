@@ -181,16 +181,19 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
       if (!a.fp8) continue;
       // rounding is monotone: the largest |y| is the largest |h w| times rstd,
       // and a power of two changes no rounding: y 2^-e = h w (rstd 2^-e)
-      float m = fmaxf(half_warp_max(block_amax(p)) * rstd, 0.f), factor = rstd;
-      if (__any_sync(~0u, isinf(m))) {  // infinities count as NaN
+      const float m = fmaxf(half_warp_max(block_amax(p)) * rstd, 0.f);
+      uint32_t sb = fp8_scale_byte(m);
+      float factor = rstd * fp8_inv_scale(sb);
+      // by way of y: infinities, which count as NaN, and a block of |h w| below
+      // 2^-118, whose factor may leave the range of fp32
+      if (__any_sync(~0u, isinf(m) || isinf(factor))) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[j] = mul2<M>(p[j], f2_splat(rstd));
         drop_infinities(p);
-        m = half_warp_max(block_amax(p));
-        factor = 1.f;
+        sb = fp8_scale_byte(half_warp_max(block_amax(p)));
+        factor = fp8_inv_scale(sb);
       }
-      const uint32_t sb = fp8_scale_byte(m);
-      const float2 inv = f2_splat(factor * fp8_inv_scale(sb));
+      const float2 inv = f2_splat(factor);
       const uint32_t lo = fp8_pack4(p[0], p[1], inv), hi = fp8_pack4(p[2], p[3], inv);
       uint8_t *q = static_cast<uint8_t *>(a.fp8) + row * a.ld_fp8;
       if (M == ODD) {

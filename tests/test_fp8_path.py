@@ -103,6 +103,25 @@ def test_norm_nan_and_inf_stay_in_their_row(cuda_lib):
     assert float(torch.nan_to_num(got.out[2]).abs().max()) == 0
 
 
+@pytest.mark.parametrize("cols", [256, 200, 4096, 1111])
+@pytest.mark.parametrize("size", [1e-34, 1e-37, 1e-39])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_of_tiny_values(cuda_lib, cols, size, dtype):
+    """Values near the lower end of fp32, with zeros among them: y * 2^-e is
+    of ordinary size, the factors that lead there are not."""
+    x = (_rand((5, cols), torch.float32, 31) * size).to(dtype)
+    x[1, ::3] = 0
+    x[2, :128] = 0
+    got = cuda_lib.kda_rms_norm(x, fp8=True)
+    y = x.double().cpu().numpy() / np.sqrt(1e-6)
+    # e4m3 keeps 4 bits (half a step: 2^-4 of the value) and, below its normal
+    # range, steps of 2^-9 of the scale (448 * 2^e < 2 max |y|, e >= -127);
+    # fp32 adds 2^-20 and its own smallest step
+    amax = np.abs(y).max()
+    tol = np.abs(y) * (2.0**-4 + 2.0**-20) + max(2 * amax / 448, 2.0**-127) * 2.0**-10 + 2.0**-147
+    assert np.all(np.abs(ref.values(got.fp8) - y) <= tol)
+
+
 def test_norm_leading_dims_and_another_stream(cuda_lib):
     x = _rand((6 * 5, 640), torch.bfloat16, 6).view(6, 5, 640)
     want = cuda_lib.kda_rms_norm(x.view(30, 640), fp8=True)
