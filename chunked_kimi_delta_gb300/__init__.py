@@ -891,8 +891,16 @@ def _launch_device(lead, *ts) -> int:
     return dev
 
 
-def _raw_stream(stream, dev):
-    return _torch_module._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+def _raw_stream(dev):
+    return _torch_module._C._cuda_getCurrentRawStream(dev)
+
+
+def _under(stream):
+    """Context of the calls given a ``stream``: what they allocate, results
+    and scratch, is that stream's own, so that none of it is handed out again
+    by another stream while the call runs."""
+    cuda = _torch().cuda
+    return cuda.stream(stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(_stream(stream)))
 
 
 def _check_weight(weight, cols):
@@ -921,6 +929,9 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None
     ``out=False`` then leaves out the result in x's dtype.  ``residual_out``
     (x + residual) may be given as ``x`` or ``residual`` to work in place.
     See ``kda_rms_norm`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_rms_norm(x, weight, residual, eps=eps, fp8=fp8, out=out, residual_out=residual_out)
     lib = _ready()
     shape, dtype = x.shape, x.dtype
     code, cols = _in_code(dtype), shape[-1]
@@ -951,7 +962,7 @@ def kda_rms_norm(x, weight=None, residual=None, *, eps=1e-6, fp8=False, out=None
         q_ptr, ld, scales_ptr = q.data.data_ptr(), (cols + 15) // 16 * 16, q.scales.data_ptr()
     a = kda_rms_norm_args(rows, cols, code, x.data_ptr(), _ptr(residual), _ptr(weight), eps,
                           _ptr(residual_out), _ptr(out), q_ptr, ld, scales_ptr)
-    status = lib.kda_rms_norm(ctypes.byref(a), _raw_stream(stream, dev))
+    status = lib.kda_rms_norm(ctypes.byref(a), _raw_stream(dev))
     if status:
         raise KdaError(status, "kda_rms_norm")
     return RmsNorm(out, residual_out, q)
@@ -964,6 +975,10 @@ def kda_rms_norm_bwd(d_out, x, weight=None, d_residual=None, *, eps=1e-6, dx=Non
     the gradient that reaches it from elsewhere.  Returns ``(dx, dweight)``:
     dx is the gradient of x and of the residual, dweight fp32 [cols] (None
     without ``want_dweight``).  See ``kda_rms_norm_bwd`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_rms_norm_bwd(d_out, x, weight, d_residual, eps=eps, dx=dx, want_dweight=want_dweight,
+                                    workspace=workspace)
     lib = _ready()
     shape, dtype = x.shape, x.dtype
     code, cols = _in_code(dtype), shape[-1]
@@ -987,7 +1002,7 @@ def kda_rms_norm_bwd(d_out, x, weight=None, d_residual=None, *, eps=1e-6, dx=Non
         ws = _alloc((need // 4,), (1,), _F32) if workspace is None else _workspace(need, x.device, workspace)
         a.dweight, a.workspace = dweight.data_ptr(), ws.data_ptr()
         a.workspace_bytes = ws.numel() * ws.element_size()
-    status = lib.kda_rms_norm_bwd(ctypes.byref(a), _raw_stream(stream, dev))
+    status = lib.kda_rms_norm_bwd(ctypes.byref(a), _raw_stream(dev))
     if status:
         raise KdaError(status, "kda_rms_norm_bwd")
     return dx, dweight
@@ -998,6 +1013,9 @@ def kda_fp8_quantize(x, kinds=("row",), *, stream=None):
     scales, once for each of ``kinds`` ("row", "col", "tile") from one read of
     x.  Returns a tuple of :class:`Fp8Matrix` in the order of ``kinds``.  See
     ``kda_fp8_quantize`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_fp8_quantize(x, kinds)
     lib = _ready()
     if isinstance(kinds, str):
         kinds = (kinds,)
@@ -1012,7 +1030,7 @@ def kda_fp8_quantize(x, kinds=("row",), *, stream=None):
     for p in parts:
         setattr(a, p.kind, p.data.data_ptr())
         setattr(a, p.kind + "_scales", p.scales.data_ptr())
-    status = lib.kda_fp8_quantize(ctypes.byref(a), _raw_stream(stream, dev))
+    status = lib.kda_fp8_quantize(ctypes.byref(a), _raw_stream(dev))
     if status:
         raise KdaError(status, "kda_fp8_quantize")
     return parts
@@ -1068,6 +1086,10 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
     ``out`` (rows dense, any pitch).  ``workspace`` (256 zeroed bytes) takes
     the device error word; without it one per device is shared, read by
     :func:`kda_fp8_matmul_status`.  See ``kda_fp8_matmul`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_fp8_matmul(a, b, form, out_dtype=out_dtype, out=out, workspace=workspace,
+                                  extra_flags=extra_flags)
     lib = _ready()
     if form not in _FP8_FORMS:
         raise ValueError('form is "nt", "nn" or "tn"')
@@ -1104,7 +1126,7 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     p = kda_fp8_matmul_args(m, n, k, code, ad.data_ptr(), lda, a_scales.data_ptr(), bd.data_ptr(), ldb,
                             b_scales.data_ptr(), out.data_ptr(), ldo, out_code, ws, ws_bytes, extra_flags)
-    status = lib.kda_fp8_matmul(ctypes.byref(p), _raw_stream(stream, dev))
+    status = lib.kda_fp8_matmul(ctypes.byref(p), _raw_stream(dev))
     if status:
         raise KdaError(status, "kda_fp8_matmul")
     return out

@@ -133,6 +133,33 @@ def test_norm_leading_dims_and_another_stream(cuda_lib):
     assert torch.equal(got.fp8.data.view(torch.uint8), want.fp8.data.view(torch.uint8))
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_results_and_scratch_belong_to_the_stream_of_the_call(cuda_lib, handle):
+    """Memory of a call on another stream is not handed out again by the
+    current one: the scratch of the backward is let go of before the call runs."""
+    k = cuda_lib
+    x = _rand((300, 1000), torch.bfloat16, 8)
+    want_dx, want_dw = k.kda_rms_norm_bwd(x, x)
+    aq, wq = k.kda_fp8_quantize(x, ("row", "tile"))
+    want_y = k.kda_fp8_matmul(aq, wq, "nt")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    stream = side.cuda_stream if handle else side
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms: what follows on `side` has not run yet
+    y = k.kda_fp8_matmul(aq, wq, "nt", stream=stream)
+    q, = k.kda_fp8_quantize(x, "row", stream=stream)
+    dx, dw = k.kda_rms_norm_bwd(x, x, stream=stream)
+    parts = k._ready().kda_rms_norm_bwd_workspace_size(300, 1000)
+    scribble = [torch.full((parts // 4,), 7.0, device="cuda") for _ in range(4)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(bool((s == 7.0).all()) for s in scribble)
+    assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw) and torch.equal(y, want_y)
+    assert torch.equal(q.data.view(torch.uint8), aq.data.view(torch.uint8))
+
+
 def _bwd_ref(g, h, w, d, eps):
     """dx, dweight and, for the tolerances, the same sums over magnitudes."""
     rstd = 1 / np.sqrt((h * h).mean(-1, keepdims=True) + eps)
