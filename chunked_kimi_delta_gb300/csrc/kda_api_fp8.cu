@@ -58,7 +58,9 @@ kda_status kda_fp8_quantize(const kda_fp8_quantize_args *a, kda_stream_t stream)
   if ((a->row && !a->row_scales) || (a->col && !a->col_scales) || (a->tile && !a->tile_scales))
     return KDA_ERR_INVALID_ARG;
   if (a->ld < a->cols) return KDA_ERR_INVALID_ARG;
-  if (blocks(a->rows) * blocks(a->cols) > INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;
+  // rows first: the product of any two 64-bit counts could wrap
+  if (a->rows / FP8_BLOCK >= INT32_MAX / 2 || blocks(a->rows) * blocks(a->cols) > INT32_MAX / 2)
+    return KDA_ERR_UNSUPPORTED;
   if (mis16(a->x) || mis16(a->row) || mis16(a->col) || mis16(a->tile) || mis16(a->row_scales) ||
       mis16(a->col_scales) || mis16(a->tile_scales) || a->ld % 16 != 0)
     return KDA_ERR_ALIGNMENT;

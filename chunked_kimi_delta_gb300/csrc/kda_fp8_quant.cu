@@ -238,7 +238,7 @@ template <typename T, Mode M> cudaError_t launch(const kda_fp8_quantize_args &a,
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const kda_fp8_quantize_args &a, cudaStream_t st) {
-  const int cblocks = (a.cols + FP8_BLOCK - 1) / FP8_BLOCK;
+  const int cblocks = (int)(((int64_t)a.cols + FP8_BLOCK - 1) / FP8_BLOCK);
   const int tiles = (int)((a.rows + FP8_BLOCK - 1) / FP8_BLOCK * cblocks);
   const bool vec = a.cols % 8 == 0;
   if (a.dtype == KDA_F32) return vec ? launch<float, DIRECT>(a, cblocks, tiles, st) : launch<float, ODD>(a, cblocks, tiles, st);

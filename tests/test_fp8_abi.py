@@ -85,6 +85,13 @@ def test_quantize_refusals(lib, kw, want):
     assert lib.kda_fp8_quantize(None, None) == INVALID
 
 
+@pytest.mark.parametrize("rows", [1 << 38, 1 << 46, 1 << 62, (1 << 63) - 1])
+def test_quantize_refuses_any_number_of_blocks_past_its_limit(lib, rows):
+    cols = (1 << 31) - 16
+    assert lib.kda_fp8_quantize(ctypes.byref(_quant(rows=rows)), None) == UNSUPPORTED
+    assert lib.kda_fp8_quantize(ctypes.byref(_quant(rows=rows, cols=cols, ld=cols)), None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("kw,want", [
     (dict(m=-1), INVALID), (dict(n=-1), INVALID), (dict(k=-1), INVALID), (dict(form=3), INVALID),
     (dict(out_dtype=5), INVALID), (dict(flags=1), INVALID), (dict(a=None), INVALID), (dict(b_scales=None), INVALID), (dict(out=None), INVALID),
