@@ -791,16 +791,20 @@ struct Plan {
 // 76 pairs, in tiles as wide as makes their turns shortest: a turn costs about
 // its width and 120 columns more (3000 x 2048 x 2048, two turns at any width
 // from 160 to 224: 14.3, 14.5, 14.9 us; 2000 x 8192 x 2048, four turns of 224
-// or five of 192: 24.8 and 27.6).  Fewer tiles leave pairs idle, and 128 x 64 ones for single CTAs,
-// two to an SM, are then as fast or faster (us, pairs at their best width
-// against single CTAs: 777 x 1111 x 2064 10.8 / 9.8, 512 x 4096 x 4096 13.9 /
-// 14.8, 300 x 1024 x 1024 7.5 / 6.8).  Where those do not fill the SMs, k is
-// split while a part keeps at least four blocks: a smaller part costs more in
-// the meeting of the sums than it saves (1 x 4096 x 4096: 8.5 us in 2 parts,
-// 7.1 in 4, 6.9 in 8).
+// or five of 192: 24.8 and 27.6).  Fewer tiles leave pairs idle, and 128 x 64
+// ones for single CTAs, two to an SM, are then as fast or faster (us, pairs at
+// their best width against single CTAs: 777 x 1111 x 2064 10.8 / 9.8, 512 x
+// 4096 x 4096 13.9 / 14.8, 300 x 1024 x 1024 7.5 / 6.8).  So they are up to 64
+// rows: a lane-side box then serves one tile whichever kernel reads it, and
+// two CTAs an SM keep more of them in flight (1 x 32768 x 4096 37.6 / 23.3,
+// 64 x 32768 x 4096 31.4 / 24.5, 64 x 100000 x 2048 42.0 / 38.3; but 100 x
+// 32768 x 4096, each box read twice, 32.0 / 42.1).  Where single CTAs do not
+// fill the SMs, k is split while a part keeps at least four blocks: a smaller
+// part costs more in the meeting of the sums than it saves (1 x 4096 x 4096:
+// 8.5 us in 2 parts, 7.1 in 4, 6.9 in 8).
 Plan choose_plan(int m, int n, int kblocks) {
   const int64_t lane_tiles = ceil_div(n, 256);
-  if (lane_tiles * ceil_div(m, PAIR_MAX_WIDTH) >= 76) {
+  if (m > SPLIT_MAX_WIDTH && lane_tiles * ceil_div(m, PAIR_MAX_WIDTH) >= 76) {
     Plan best{true, PAIR_MAX_WIDTH, 1};
     int64_t least = INT64_MAX;
     for (int width = PAIR_MAX_WIDTH; width >= 128; width -= 32) {

@@ -323,6 +323,13 @@ def test_matmul_of_small_integers_is_exact(cuda_lib, form, m, n, k):
     assert np.array_equal(_np(got), want)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 20000, 200), (33, 19500, 136), (64, 39000, 264), (65, 19500, 136), (7, 40001, 4200)])
+@pytest.mark.parametrize("form", ["nt", "nn"])
+def test_matmul_of_few_rows_and_many_columns(cuda_lib, form, m, n, k):
+    """A few tokens through a wide projection."""
+    test_matmul(cuda_lib, form, m, n, k)
+
+
 def test_matmul_pitches_streams_and_canaries(cuda_lib):
     """Operands and result inside wider buffers; nothing outside is touched;
     another stream; a caller's workspace."""
