@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
 // each with its own range of k; the partial sums meet through distributed
 // shared memory and are added in the order of k.
 // What bounds it is latency, from the launch over one pass of loads and MMAs
-// to the meeting of the sums: 1 x 4096 x 4096 takes 6.5 us where the weight's
+// to the meeting of the sums: 1 x 4096 x 4096 takes 6.3 us where the weight's
 // bytes take 2.5.
 // Warps 0-3 epilogue, 4 scales, 5 TMA, 6 MMA.
 constexpr int SPLIT_THREADS = 224;
@@ -800,8 +800,10 @@ struct Plan {
 // 64 x 32768 x 4096 31.4 / 24.5, 64 x 100000 x 2048 42.0 / 38.3; but 100 x
 // 32768 x 4096, each box read twice, 32.0 / 42.1).  Where single CTAs do not
 // fill the SMs, k is split while a part keeps at least four blocks: a smaller
-// part costs more in the meeting of the sums than it saves (1 x 4096 x 4096:
-// 8.5 us in 2 parts, 7.1 in 4, 6.9 in 8).
+// part costs more in the meeting of the sums than it saves.  Up to one CTA an
+// SM; up to two where few rows make the sums short (with one / two: 1 x 4096 x
+// 4096 7.4 / 6.3 us, 1 x 8192 x 4096 9.4 / 8.4, 1 x 4096 x 16384 15.0 / 13.6,
+// but 777 x 1111 x 2064 8.3 / 10.5).
 Plan choose_plan(int m, int n, int kblocks) {
   const int64_t lane_tiles = ceil_div(n, 256);
   if (m > SPLIT_MAX_WIDTH && lane_tiles * ceil_div(m, PAIR_MAX_WIDTH) >= 76) {
@@ -818,7 +820,7 @@ Plan choose_plan(int m, int n, int kblocks) {
   }
   Plan p{false, m <= 16 ? 16 : m <= 32 ? 32 : SPLIT_MAX_WIDTH, 1};
   const int64_t tiles = (int64_t)ceil_div(n, 128) * ceil_div(m, p.width);
-  while (p.splits < 8 && 8 * p.splits <= kblocks && tiles * p.splits * 2 <= 152) p.splits *= 2;
+  while (p.splits < 8 && 8 * p.splits <= kblocks && tiles * p.splits * 2 <= (p.width <= 32 ? 304 : 152)) p.splits *= 2;
   return p;
 }
 
@@ -855,8 +857,12 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   a.stage_bytes = LANE_BYTES + ((a.col_box_bytes + 1023) & ~1023u);
   const bool f32 = p.out_dtype == KDA_F32;
   a.out_tma = pair && p.ldo * (f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo <= INT32_MAX;
-  // a pair has its SMs to itself, and so do split CTAs when there is one for each; else two share
-  const bool alone = pair || (int64_t)a.tiles * a.splits <= 152;
+  // A pair has its SMs to itself, and so do split CTAs when all of them fit that
+  // way; else two share one.  A cluster stays within a group of SMs, whose number
+  // is no multiple of it: fours fill 144 SMs, eights surely 64 (1 x 2048 x 8192,
+  // 16 clusters of eight: 12.5 us alone, in two turns, 6.8 sharing).
+  const int64_t fit = a.splits == 8 ? 64 : a.splits == 4 ? 144 : 152;
+  const bool alone = pair || (int64_t)a.tiles * a.splits <= fit;
   uint32_t budget = SMEM_LIMIT - SF_BYTES - (a.out_tma ? OUT_BYTES : 0);
   if (!alone) budget = (SMEM_LIMIT - 1024 - (uint32_t)sizeof(Bars)) / 2 - 1024 - SF_BYTES;
   a.stages = (int)(budget / a.stage_bytes);
