@@ -361,7 +361,7 @@ __device__ __forceinline__ void settle() {
 // an SM, 480 cycles at 64 bytes a cycle from L2 (and again 480 for shared
 // memory to take them in and give them to the MMAs at 128), against 448
 // cycles of MMAs; measured about 560 at 32768 x 4096 x 4096 (306 us, 3.6
-// PFLOP/s from rest, 363 us back to back under the power cap; tensor pipe 78%
+// PFLOP/s from rest, 363 to 368 us back to back under the power cap; tensor pipe 78%
 // busy).  Half of the MMAs left out changed little (314 to 300 us), 26% less
 // read from L2 by multicast of the lane side to a second pair nothing at all.
 // Warps 0-7 epilogue, 8 scales, 9 TMA, 10 MMA (first CTA of the pair).

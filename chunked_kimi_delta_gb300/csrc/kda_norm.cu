@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
 constexpr int kMaxParts = 1216;  // partial dweight rows at most: 8 CTAs on each of 152 SMs
 
 // dweight of a team's rows is summed in its registers; a CTA leaves one row of
-// partial sums.  32768 x 4096 bf16 with the residual's gradient: 161 us for
+// partial sums.  32768 x 4096 bf16 with the residual's gradient: 162 us for
 // this and the sum of the parts, 6.7 TB/s, 98% of the copy rate.
 template <typename T, Mode M, int VPT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT < 4 ? 512 : 1024, WARP && VPT == 2 ? (M == ODD ? 2 : 4) : M != RING && VPT == 1 ? 2 : 1)
