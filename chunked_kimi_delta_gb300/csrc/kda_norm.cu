@@ -167,34 +167,22 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
-      float2 p[4];  // h w; y = h w rstd
-      h[i].get(p);
+      // (h rstd) w: h w may leave the range of fp32 where y does not
+      float2 y[4];
+      h[i].get(y);
       if (!KEEP) load_weight<M>(a.weight, c, cols, w[0]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = mul2<M>(p[j], w[KEEP ? i : 0][j]);
-      if (a.out) {
-        float2 y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = mul2<M>(p[j], f2_splat(rstd));
-        store<T, M>(static_cast<T *>(a.out) + row * cols, c, cols, y);
-      }
+      for (int j = 0; j < 4; ++j) y[j] = mul2<M>(mul2<M>(y[j], f2_splat(rstd)), w[KEEP ? i : 0][j]);
+      if (a.out) store<T, M>(static_cast<T *>(a.out) + row * cols, c, cols, y);
       if (!a.fp8) continue;
-      // rounding is monotone: the largest |y| is the largest |h w| times rstd,
-      // and a power of two changes no rounding: y 2^-e = h w (rstd 2^-e)
-      const float m = fmaxf(half_warp_max(block_amax(p)) * rstd, 0.f);
-      uint32_t sb = fp8_scale_byte(m);
-      float factor = rstd * fp8_inv_scale(sb);
-      // by way of y: infinities, which count as NaN, and a block of |h w| below
-      // 2^-118, whose factor may leave the range of fp32
-      if (__any_sync(~0u, isinf(m) || isinf(factor))) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = mul2<M>(p[j], f2_splat(rstd));
-        drop_infinities(p);
-        sb = fp8_scale_byte(half_warp_max(block_amax(p)));
-        factor = fp8_inv_scale(sb);
+      float m = half_warp_max(block_amax(y));
+      if (__any_sync(~0u, isinf(m))) {  // infinities count as NaN
+        drop_infinities(y);
+        m = half_warp_max(block_amax(y));
       }
-      const float2 inv = f2_splat(factor);
-      const uint32_t lo = fp8_pack4(p[0], p[1], inv), hi = fp8_pack4(p[2], p[3], inv);
+      const uint32_t sb = fp8_scale_byte(m);
+      const float2 inv = f2_splat(fp8_inv_scale(sb));
+      const uint32_t lo = fp8_pack4(y[0], y[1], inv), hi = fp8_pack4(y[2], y[3], inv);
       uint8_t *q = static_cast<uint8_t *>(a.fp8) + row * a.ld_fp8;
       if (M == ODD) {
 #pragma unroll

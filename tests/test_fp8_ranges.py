@@ -1,0 +1,27 @@
+"""The 8-bit projection path at the ends of fp32's range and over long sums,
+on the GPU against 64-bit references."""
+import numpy as np
+import pytest
+import torch
+
+from test_fp8_path import U16, U32, Y_REL, _bwd_ref, _check_fp8, _norm_ref, _np, _rand
+
+pytestmark = pytest.mark.gpu
+
+# a warp a row, a CTA a row, straight from memory, and the same with rows that start anywhere
+WIDTHS = [264, 4096, 16392, 903, 1111, 20001]
+
+
+@pytest.mark.parametrize("cols", WIDTHS)
+@pytest.mark.parametrize("size,weight", [(1e15, 1e25), (1e-17, 1e-25)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_whose_products_leave_the_range(cuda_lib, cols, size, weight, dtype):
+    """h * weight lies outside of fp32's normal numbers, y = h rstd weight
+    well inside."""
+    x = (_rand((7, cols), torch.float32, 1) * size).to(dtype)
+    w = (1 + 0.1 * torch.randn(cols, device="cuda")) * weight
+    got = cuda_lib.kda_rms_norm(x, w, eps=0.0, fp8=True)
+    y = _norm_ref(_np(x), _np(w), 0.0)
+    u = U16 if dtype == torch.bfloat16 else U32
+    assert np.all(np.abs(_np(got.out) - y) <= np.abs(y) * (Y_REL + u * (1 + Y_REL)))
+    _check_fp8(got.fp8, y, Y_REL)
