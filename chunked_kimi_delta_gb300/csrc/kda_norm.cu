@@ -286,7 +286,7 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
     parity ^= 1;
     const float rstd = 1.f / sqrtf(fmaf(sums[0], inv_cols, a.eps));
     const float mean = sums[1] * rstd * inv_cols;  // mean of weight * d_out * n
-    const float2 r2 = f2_splat(rstd), nm = f2_splat(-mean * rstd * rstd);
+    const float2 r2 = f2_splat(rstd), nm = f2_splat(-mean);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = first_col<M, WARP>(i);
@@ -297,10 +297,11 @@ rms_norm_bwd_kernel(kda_rms_norm_bwd_args a) {
       if (dp) get(2, dp, i, c).get(d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        dw[i][j] = fma2<M>(g[j], mul2<M>(h[j], r2), dw[i][j]);
+        const float2 n = mul2<M>(h[j], r2);  // rstd squared may leave the range of fp32
+        dw[i][j] = fma2<M>(g[j], n, dw[i][j]);
         // rstd (w g - n mean) + d
-        const float2 t = dp ? fma2<M>(h[j], nm, d[j]) : mul2<M>(h[j], nm);
-        dx[j] = fma2<M>(mul2<M>(g[j], w[KEEP ? i : 0][j]), r2, t);
+        const float2 t = fma2<M>(n, nm, mul2<M>(g[j], w[KEEP ? i : 0][j]));
+        dx[j] = dp ? fma2<M>(t, r2, d[j]) : mul2<M>(t, r2);
       }
       store<T, M>(static_cast<T *>(a.dx) + row * cols, c, cols, dx);
     }
