@@ -40,12 +40,15 @@ constexpr int SF_RING = 4;
 constexpr uint32_t SF_ENTRY = 1536;  // bytes of an entry in shared memory: 512 lane side, 2 x 512 column side
 constexpr uint32_t SF_BYTES = SF_RING * SF_ENTRY;
 static_assert(SF_BYTES % 1024 == 0, "what follows the ring is aligned like a tile");
-// Blocks of k that tensor memory sums before an fp32 result takes the sum into
-// registers.  A step of the MMA (32 of k) rounds the running sum by about
-// 2^-24 of it; their number, not the size of k, then bounds the error
-// (relative 8e-7 at k = 8200 in one sum, 4e-7 in spans).  bf16 results
-// round at 2^-9 and take k in one span.
-constexpr int SPAN = 32;
+// Blocks of k that tensor memory sums before the epilogue takes the sum into
+// registers.  A step of the MMA (32 of k) drops up to 2^-23 of the running sum,
+// always towards zero (measured on positive terms: 1.1e-8 a step); their
+// number in a span, not the size of k, then bounds the error.  fp32 results:
+// relative 8e-7 at k = 8200 in one sum, 4e-7 in spans.  bf16 results round by
+// up to 2^-8; 4,096 steps, 5e-5 on positive terms, stay an eightieth of that,
+// and what fits one span (k up to 131,072) has a kernel without the sums in
+// registers (777 x 1111 x 2064: 8.6 us, with them 9.5).
+constexpr int SPAN_F32 = 32, SPAN_BF16 = 1024;
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t LANE_BYTES = 16384;  // lane-side box: 128 x 128 bytes
 
@@ -369,7 +372,8 @@ constexpr int PAIR_THREADS = 352;
 constexpr int PAIR_MAX_WIDTH = 224;  // two accumulators and the scale ring fill the 512 columns
 constexpr uint32_t PAIR_SF = 2 * PAIR_MAX_WIDTH;
 
-template <typename T>
+// SPANS: a tile's sum may take more than one span of k.
+template <typename T, bool SPANS>
 __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap lane_map,
                                                                           const __grid_constant__ CUtensorMap col_map,
                                                                           const __grid_constant__ CUtensorMap out_map,
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
       for (int i = 0; i < 4; ++i) {
         const int c = 32 * half + 64 * i;
         if (c >= a.width) break;
-        if (sizeof(T) == 2 && a.out_tma) {
+        if (sizeof(T) == 2 && !SPANS && a.out_tma) {
           stage_chunk(acc + c, stage_begin(), lane);
           stage_end(n0, c0 + c, c < end && n0 < a.lanes);
           continue;
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
           float v[16];
           tc::tmem_ld16(acc + c + 16 * u, v);
           tc::tmem_ld_wait();
-          if (sizeof(T) == 4 && !(first && last)) add_span(sum[2 * i + u], v, first);
+          if (SPANS && !(first && last)) add_span(sum[2 * i + u], v, first);
           if (!last) continue;
           if (sizeof(T) == 4 && a.out_tma) {  // 128 bytes a row, as they are
             float *dst = reinterpret_cast<float *>(stage_begin());
@@ -588,7 +592,7 @@ constexpr int SPLIT_THREADS = 224;
 constexpr int SPLIT_MAX_WIDTH = 64;
 constexpr uint32_t SPLIT_TMEM = 256;  // two CTAs fit an SM
 
-template <typename T>
+template <typename T, bool SPANS>
 __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(const __grid_constant__ CUtensorMap lane_map,
                                                                             const __grid_constant__ CUtensorMap col_map,
                                                                             const __grid_constant__ MmArgs a) {
@@ -655,7 +659,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 2) fp8_matmul_split_kernel(cons
         float v[16];
         tc::tmem_ld16(tmem + full.s * SPLIT_MAX_WIDTH + 16 * i + ((uint32_t)(32 * warp) << 16), v);
         tc::tmem_ld_wait();
-        if (sizeof(T) == 4 && !(first && last)) add_span(sum[i], v, first);
+        if (SPANS && !(first && last)) add_span(sum[i], v, first);
         if (!last) continue;
         if (splits == 1) {
           store_columns<T>(a, v, n, c0 + 16 * i, c0 + valid);
@@ -849,14 +853,17 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   const bool pair = plan.pair;
   a.width = plan.width;
   a.splits = plan.splits;
-  a.span = p.out_dtype == KDA_F32 ? SPAN : a.kblocks;
+  a.span = p.out_dtype == KDA_F32 ? SPAN_F32 : SPAN_BF16;
   a.lane_tiles = ceil_div(p.n, pair ? 256 : 128);
   a.tiles = a.lane_tiles * ceil_div(p.m, a.width);
   const int box_rows = pair ? a.width / 2 : a.width;  // column-side rows of one CTA
   a.col_box_bytes = a.col_mn ? 16384 : (uint32_t)box_rows * 128;
   a.stage_bytes = LANE_BYTES + ((a.col_box_bytes + 1023) & ~1023u);
   const bool f32 = p.out_dtype == KDA_F32;
-  a.out_tma = pair && p.ldo * (f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo <= INT32_MAX;
+  const bool spans = f32 || a.kblocks > a.span;  // kernels that add up spans of k
+  // sums of spans in bf16 leave by plain stores: over so long a k that costs nothing
+  a.out_tma = pair && f32 == spans && p.ldo * (f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
+              p.ldo <= INT32_MAX;
   // A pair has its SMs to itself, and so do split CTAs when all of them fit that
   // way; else two share one.  A cluster stays within a group of SMs, whose number
   // is no multiple of it: fours fill 144 SMs, eights surely 64 (1 x 2048 x 8192,
@@ -885,15 +892,17 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   if (pair) {
     smem += a.out_tma ? OUT_BYTES : 0;
     const unsigned grid = 2u * (unsigned)(a.tiles < 76 ? a.tiles : 76);
-    return f32
-               ? launch_overlapped(fp8_matmul_pair_kernel<float>, grid, PAIR_THREADS, smem, 2, st, lm, cm, om, a)
-               : launch_overlapped(fp8_matmul_pair_kernel<__nv_bfloat16>, grid, PAIR_THREADS, smem, 2, st, lm, cm, om, a);
+    return launch_overlapped(f32     ? fp8_matmul_pair_kernel<float, true>
+                             : spans ? fp8_matmul_pair_kernel<__nv_bfloat16, true>
+                                     : fp8_matmul_pair_kernel<__nv_bfloat16, false>,
+                             grid, PAIR_THREADS, smem, 2, st, lm, cm, om, a);
   }
   if (smem < 80 * 1024) smem = 80 * 1024;  // two CTAs an SM at most: that is what tensor memory holds
   const unsigned grid = (unsigned)(a.tiles * a.splits), cluster = (unsigned)a.splits;
-  return f32
-             ? launch_overlapped(fp8_matmul_split_kernel<float>, grid, SPLIT_THREADS, smem, cluster, st, lm, cm, a)
-             : launch_overlapped(fp8_matmul_split_kernel<__nv_bfloat16>, grid, SPLIT_THREADS, smem, cluster, st, lm, cm, a);
+  return launch_overlapped(f32     ? fp8_matmul_split_kernel<float, true>
+                           : spans ? fp8_matmul_split_kernel<__nv_bfloat16, true>
+                                   : fp8_matmul_split_kernel<__nv_bfloat16, false>,
+                           grid, SPLIT_THREADS, smem, cluster, st, lm, cm, a);
 }
 
 }  // namespace kda
