@@ -23,19 +23,36 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
+// One map.  The encoder is a driver call and wants a current context, which a
+// host thread has only after a call of the runtime that needs one: a thread
+// that has made none is given its device's context first.
+bool encode(CUtensorMap *m, CUtensorMapDataType dt, cuuint32_t rank, const void *ptr, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle sw, CUtensorMapL2promotion l2) {
+  auto fn = encoder();
+  if (!fn) return false;
+  memset(m, 0, sizeof(*m));
+  const cuuint32_t es[3] = {1, 1, 1};
+  auto once = [&]() {
+    return fn(m, dt, rank, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, l2,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = once();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+    r = once();
+  }
+  return r == CUDA_SUCCESS;
+}
+
 // Token-major [T_tot, H, D] tensor seen as 3-D (D, H, T_tot); a box covers
 // `box0` channels of one head over 64 tokens.
 bool encode3(CUtensorMap *m, CUtensorMapDataType dt, uint32_t esize, const void *ptr, int D, int H,
              int64_t T, uint32_t box0, CUtensorMapSwizzle sw) {
-  auto fn = encoder();
-  if (!fn) return false;
-  memset(m, 0, sizeof(*m));
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
   cuuint64_t strides[2] = {(cuuint64_t)D * esize, (cuuint64_t)H * D * esize};
   cuuint32_t box[3] = {box0, 1, (cuuint32_t)BT};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, dt, 3, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(m, dt, 3, ptr, dims, strides, box, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace
@@ -66,31 +83,22 @@ bool make_value_map(const void *x, int64_t T_tot, int H, CUtensorMap &map) {
 
 bool make_byte_map(const void *p, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_outer,
                    CUtensorMap &map) {
-  auto fn = encoder();
-  if (!fn || inner <= 0 || outer <= 0) return false;
-  memset(&map, 0, sizeof(map));
+  if (inner <= 0 || outer <= 0) return false;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   cuuint64_t strides[1] = {(cuuint64_t)pitch};
   cuuint32_t box[2] = {128, box_outer};
-  cuuint32_t es[2] = {1, 1};
-  return fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool make_out_tile_map(const void *p, bool f32, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_inner,
                        uint32_t box_outer, CUtensorMap &map) {
-  auto fn = encoder();
-  if (!fn || inner <= 0 || outer <= 0) return false;
-  memset(&map, 0, sizeof(map));
+  if (inner <= 0 || outer <= 0) return false;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   cuuint64_t strides[1] = {(cuuint64_t)pitch * (f32 ? 4 : 2)};
   cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t es[2] = {1, 1};
-  return fn(&map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p),
-            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(&map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box,
+                f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 }  // namespace tcp
