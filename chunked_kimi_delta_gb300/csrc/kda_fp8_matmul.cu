@@ -44,11 +44,15 @@ static_assert(SF_BYTES % 1024 == 0, "what follows the ring is aligned like a til
 // registers.  A step of the MMA (32 of k) drops up to 2^-23 of the running sum,
 // always towards zero (measured on positive terms: 1.1e-8 a step); their
 // number in a span, not the size of k, then bounds the error.  fp32 results:
-// relative 8e-7 at k = 8200 in one sum, 4e-7 in spans.  bf16 results round by
-// up to 2^-8; 4,096 steps, 5e-5 on positive terms, stay an eightieth of that,
-// and what fits one span (k up to 131,072) has a kernel without the sums in
-// registers (777 x 1111 x 2064: 8.6 us, with them 9.5).
-constexpr int SPAN_F32 = 32, SPAN_BF16 = 1024;
+// relative 3.7e-7 at k = 8200 in spans of 32 blocks, 1.7e-7 in 16, 1.3e-7 in
+// 12, where one fp32 sum on the CUDA cores has 1.6e-7.  Shorter ones hold the
+// MMAs up (32768 x 4096 x 4096 "nt": 328 us in spans of 32 blocks,
+// 335 in 16, 350 in 12, 380 in 8; "tn" 4096 x 2048 x 8200: 59, 60, 59, 63).
+// bf16 results round by up to 2^-8; 4,096 steps, 5e-5 on positive terms, stay
+// an eightieth of that, and what fits one span (k up to 131,072) has a kernel
+// without the sums in registers (777 x 1111 x 2064: 8.6 us, with them 9.5).
+constexpr int SPAN_F32 = 12, SPAN_BF16 = 1024;
+static_assert(SPAN_F32 % 4 == 0 && SPAN_BF16 % 4 == 0, "a span starts with a word of scales");
 constexpr int MAX_STAGES = 8;
 constexpr uint32_t LANE_BYTES = 16384;  // lane-side box: 128 x 128 bytes
 
@@ -465,10 +469,29 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
       const uint32_t acc = tmem + full.s * PAIR_MAX_WIDTH + ((uint32_t)(32 * quarter) << 16);
       const int end = min(a.width, a.cols - c0);
       const bool first = kb == 0, last = kb + a.span >= a.kblocks;
+      auto free_accumulator = [&]() {
+        tc::tc_fence_before();
+        if (lane == 0) arrive_remote(peer_addr(b.acc_empty + full.s, 0));
+        __syncwarp();
+      };
+      if (SPANS) {  // into registers, and the accumulator is free before the stores
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 32 * half + 64 * i;
+          if (c >= a.width) break;
+          float v[2][16];
+          tc::tmem_ld16(acc + c, v[0]);
+          tc::tmem_ld16(acc + c + 16, v[1]);
+          tc::tmem_ld_wait();
+          add_span(sum[2 * i], v[0], first);
+          add_span(sum[2 * i + 1], v[1], first);
+        }
+        free_accumulator();
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = 32 * half + 64 * i;
-        if (c >= a.width) break;
+        if (c >= a.width || (SPANS && !last)) break;
         if (sizeof(T) == 2 && !SPANS && a.out_tma) {
           stage_chunk(acc + c, stage_begin(), lane);
           stage_end(n0, c0 + c, c < end && n0 < a.lanes);
@@ -477,10 +500,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           float v[16];
-          tc::tmem_ld16(acc + c + 16 * u, v);
-          tc::tmem_ld_wait();
-          if (SPANS && !(first && last)) add_span(sum[2 * i + u], v, first);
-          if (!last) continue;
+          if (!SPANS) {
+            tc::tmem_ld16(acc + c + 16 * u, v);
+            tc::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = sum[2 * i + u][j];
+          }
           if (sizeof(T) == 4 && a.out_tma) {  // 128 bytes a row, as they are
             float *dst = reinterpret_cast<float *>(stage_begin());
 #pragma unroll
@@ -491,9 +517,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
           }
         }
       }
-      tc::tc_fence_before();
-      if (lane == 0) arrive_remote(peer_addr(b.acc_empty + full.s, 0));
-      __syncwarp();
+      if (!SPANS) free_accumulator();
       kb += a.span;
       if (last) {
         kb = 0;

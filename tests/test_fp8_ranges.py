@@ -98,3 +98,23 @@ def test_bf16_products_in_several_spans_are_exact(cuda_lib, form, m, n):
         want += A.double() @ B.double()
     assert torch.equal(got, want.bfloat16())
     assert torch.equal(cuda_lib.kda_fp8_matmul(a, b, form, out_dtype=torch.float32).double(), want)
+
+
+@pytest.mark.parametrize("m,n", [(3, 130), (640, 1300), (4096, 2048)])
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+def test_fp32_products_lose_little_beside_a_large_term(cuda_lib, form, m, n):
+    """One term of 2^26, then 32 terms at a time that add up to 1.5: beside
+    the large one a step may lose its 1.5, but not beyond the span of k that
+    the large one is in, 48 steps at most.  The sums of the six spans round to
+    multiples of 8."""
+    k = 8192
+    a, b = torch.ones(m, k, device="cuda"), torch.full((k, n), 1.5 / 32, device="cuda")
+    a[:, :128], b[:128] = 0, 0
+    a[:, 5], b[5] = 2.0 ** 13, 2.0 ** 13
+    want = 2.0 ** 26 + 1.5 * (k - 128) / 32
+    x = a.t().contiguous() if form == "tn" else a
+    y = b.t().contiguous() if form == "nt" else b
+    x8, = cuda_lib.kda_fp8_quantize(x, "col" if form == "tn" else "row")
+    y8, = cuda_lib.kda_fp8_quantize(y, "col" if form == "tn" else "tile")
+    got = cuda_lib.kda_fp8_matmul(x8, y8, form, out_dtype=torch.float32).double()
+    assert float((got - want).abs().max()) <= 48 * 1.5 + 6 * 4
