@@ -189,12 +189,19 @@ __device__ __forceinline__ void grid_start() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Dynamic shared memory that a kernel of this path may ask for: of a CTA's
+// 227 KB, 1 KB is left to its static variables.
+constexpr size_t MAX_DYNAMIC_SMEM = 226 * 1024;
+
 // Host: launches a kernel that calls grid_start(), in clusters of `cluster`.
+// The limit of a kernel is one value for all host threads: it is always set to
+// the same, never to what this call needs, which another thread's call of
+// another size could lower between the setting and the launch.
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
                               cudaStream_t st, A... args) {
   if (smem > 40 * 1024) {  // with the static part, past the 48 KB that need no leave
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MAX_DYNAMIC_SMEM);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute at[2]{};

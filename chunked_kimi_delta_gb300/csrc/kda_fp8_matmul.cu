@@ -806,7 +806,8 @@ uint32_t idesc_scaled(int M, int N, bool lane_mn, bool col_mn) {
          (uint32_t)(M >> 4) << 24;
 }
 
-constexpr uint32_t SMEM_LIMIT = 227 * 1024 - 1024 - sizeof(Bars);  // dynamic, after alignment
+constexpr uint32_t SMEM_LIMIT = MAX_DYNAMIC_SMEM - 1024;  // after alignment
+static_assert(sizeof(Bars) <= 227 * 1024 - MAX_DYNAMIC_SMEM, "static shared memory");
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
