@@ -178,6 +178,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kda_rms_norm_bwd": ([ctypes.POINTER(kda_rms_norm_bwd_args), vp], ctypes.c_int),
         "kda_fp8_quantize": ([ctypes.POINTER(kda_fp8_quantize_args), vp], ctypes.c_int),
         "kda_fp8_matmul": ([ctypes.POINTER(kda_fp8_matmul_args), vp], ctypes.c_int),
+        "kda_fp8_matmul_shared_workspace": ([ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
     }
     for name, (argt, rest) in sigs.items():
         f = getattr(lib, name)
@@ -1042,17 +1043,15 @@ _fp8_status_words = {}
 
 
 def _fp8_status_word(dev: int) -> int:
-    """Address of the zeroed error word shared by a device's matmul calls
-    without a ``workspace`` (made by the first of them: before any stream
-    capture)."""
+    """Address of the library's own error word on the current device ``dev``,
+    shared by the matmul calls without a ``workspace``: the same for every
+    thread, and there before a stream capture as during one."""
     word = _fp8_status_words.get(dev)
     if word is None:
-        torch = _torch()
-        word = torch.zeros(KDA_FP8_MATMUL_WORKSPACE_BYTES, dtype=torch.uint8,
-                           device=torch.device("cuda", dev))
-        torch.cuda.current_stream(dev).synchronize()
-        word = _fp8_status_words[dev] = (word.data_ptr(), word)
-    return word[0]
+        p = ctypes.c_void_p()
+        _check(load_library().kda_fp8_matmul_shared_workspace(ctypes.byref(p)), "kda_fp8_matmul_shared_workspace")
+        word = _fp8_status_words[dev] = p.value
+    return word
 
 
 def _check_fp8(x: Fp8Matrix, kind: str):
@@ -1084,8 +1083,8 @@ def kda_fp8_matmul(a: Fp8Matrix, b: Fp8Matrix, form="nt", *, out_dtype=None, out
       "tn"  a [k, m] col,  b [k, n] col:  the weight's gradient (a = dy, b = x)
     Returns out [m, n] of ``out_dtype`` (bf16 by default, or fp32), or writes
     ``out`` (rows dense, any pitch).  ``workspace`` (256 zeroed bytes) takes
-    the device error word; without it one per device is shared, read by
-    :func:`kda_fp8_matmul_status`.  See ``kda_fp8_matmul`` in include/kda.h."""
+    the device error word; without it the library's own is shared by all
+    calls on the device, read by :func:`kda_fp8_matmul_status`.  See ``kda_fp8_matmul`` in include/kda.h."""
     if stream is not None:
         with _under(stream):
             return kda_fp8_matmul(a, b, form, out_dtype=out_dtype, out=out, workspace=workspace,
@@ -1137,6 +1136,5 @@ def kda_fp8_matmul_status(stream=None) -> int:
     current device (synchronises ``stream``): KDA_OK, or
     KDA_ERR_DEVICE_TIMEOUT when a bounded device wait gave up since the last
     read."""
-    dev = _torch().cuda.current_device()
-    _fp8_status_word(dev)
-    return kda_get_device_status(_fp8_status_words[dev][1], stream)
+    word = _fp8_status_word(_torch().cuda.current_device())
+    return load_library().kda_get_device_status(word, _stream(stream))

@@ -11,6 +11,8 @@ inline kda_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK 
 inline bool bad_dtype(kda_dtype d) { return d != KDA_F32 && d != KDA_BF16; }
 inline int64_t blocks(int64_t n) { return (n + FP8_BLOCK - 1) / FP8_BLOCK; }
 
+__device__ __align__(256) unsigned char g_matmul_workspace[KDA_FP8_MATMUL_WORKSPACE_BYTES];
+
 }  // namespace
 
 extern "C" {
@@ -92,6 +94,19 @@ kda_status kda_fp8_matmul(const kda_fp8_matmul_args *a, kda_stream_t stream) {
   if (!a->workspace || a->workspace_bytes < KDA_FP8_MATMUL_WORKSPACE_BYTES) return KDA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return KDA_ERR_ALIGNMENT;
   return cuda_status(launch_fp8_matmul(*a, st));
+}
+
+kda_status kda_fp8_matmul_shared_workspace(void **workspace) {
+  if (!workspace) return KDA_ERR_INVALID_ARG;
+  // The first question on a device loads the array: not an operation that a
+  // capture of this thread's would record, so it need not refuse it.
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return KDA_ERR_CUDA;
+  void *p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_matmul_workspace);
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess || e != cudaSuccess || !p) return KDA_ERR_CUDA;
+  *workspace = p;
+  return KDA_OK;
 }
 
 }  // extern "C"

@@ -629,6 +629,13 @@ typedef struct {
 #define KDA_FP8_MATMUL_WORKSPACE_BYTES 256u
 kda_status kda_fp8_matmul(const kda_fp8_matmul_args *args, kda_stream_t stream);
 
+/* A workspace for kda_fp8_matmul in the library's own memory on the current
+ * device: zero when the library is loaded, the same for every caller and
+ * thread, so that one kda_get_device_status call answers for all calls made
+ * with it.  Nothing is allocated or launched: it may be asked for during a
+ * stream capture.  Errors: KDA_ERR_INVALID_ARG (null), KDA_ERR_CUDA. */
+kda_status kda_fp8_matmul_shared_workspace(void **workspace);
+
 /* Reads and clears the device error word kept at the start of a forward or
  * summary workspace: synchronises the stream, returns KDA_OK or
  * KDA_ERR_DEVICE_TIMEOUT when a bounded device-side wait gave up.  Every

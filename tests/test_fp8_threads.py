@@ -1,5 +1,9 @@
-"""The 8-bit projection path called by several host threads at once."""
+"""The 8-bit projection path called by several host threads at once, and
+for the first time during a stream capture."""
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -69,3 +73,56 @@ def test_sizes_that_need_different_shared_memory(cuda_lib):
     torch.cuda.synchronize()
     assert counts == [0] * len(counts), "refused calls"
     assert all(torch.equal(o, w) for o, w in checks)
+
+
+def test_threads_share_one_error_word(cuda_lib):
+    """Threads that make a device's first products together use the same
+    error word: a report in it is not lost, and none of them holds memory that
+    was let go of."""
+    dev = torch.cuda.current_device()
+    for _ in range(20):
+        cuda_lib._fp8_status_words.clear()
+        got = []
+        _run([lambda: got.append(cuda_lib._fp8_status_word(dev))] * 6)
+        assert len(set(got)) == 1
+    assert cuda_lib.kda_fp8_matmul_status() == cuda_lib.KDA_OK
+
+
+_FIRST_CALLS_IN_A_CAPTURE = """
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import chunked_kimi_delta_gb300 as kda
+x = torch.randn(300, 1024, device="cuda").bfloat16()
+w = torch.randn(1024, 1024, device="cuda")
+
+def layer():
+    n = kda.kda_rms_norm(x, None, x, fp8=True)
+    w8, = kda.kda_fp8_quantize(w, "tile")
+    y = kda.kda_fp8_matmul(n.fp8, w8)
+    d_row, d_col = kda.kda_fp8_quantize(y, ("row", "col"))
+    n_col, = kda.kda_fp8_quantize(n.out, "col")
+    dw = kda.kda_fp8_matmul(d_col, n_col, "tn", out_dtype=torch.float32)
+    dx, dweight = kda.kda_rms_norm_bwd(kda.kda_fp8_matmul(d_row, w8, "nn"), n.residual_out)
+    return n.out, n.residual_out, y, dw, dx, dweight
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = layer()
+for seed in (1, 2):
+    x.copy_(torch.randn(x.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, layer()))
+assert kda.kda_fp8_matmul_status() == kda.KDA_OK
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture(cuda_lib):
+    """Norm, quantiser and products whose first call is recorded into a graph:
+    replayed on other inputs they give what calls outside give, bit for bit."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(cuda_lib.__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS_IN_A_CAPTURE, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr
