@@ -220,6 +220,15 @@ cudaError_t launch_overlapped(void (*kern)(P...), unsigned grid, unsigned thread
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
+// Host: SMs of the current device (152 on a whole GB300, fewer where a process
+// is given a part of one).
+inline int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 152;  // no device: the launch will say so
+  return sms < 2 ? 2 : sms;
+}
+
 // Host: launchers.
 cudaError_t launch_rms_norm(const kda_rms_norm_args &a, cudaStream_t st);
 cudaError_t launch_rms_norm_bwd(const kda_rms_norm_bwd_args &a, cudaStream_t st);

@@ -816,30 +816,30 @@ struct Plan {
   int width, splits;
 };
 
-// Pairs of CTAs take the work when there is a 256 x 224 tile for each of the
-// 76 pairs, in tiles as wide as makes their turns shortest: a turn costs about
-// its width and 120 columns more (3000 x 2048 x 2048, two turns at any width
-// from 160 to 224: 14.3, 14.5, 14.9 us; 2000 x 8192 x 2048, four turns of 224
-// or five of 192: 24.8 and 27.6).  Fewer tiles leave pairs idle, and 128 x 64
-// ones for single CTAs, two to an SM, are then as fast or faster (us, pairs at
-// their best width against single CTAs: 777 x 1111 x 2064 10.8 / 9.8, 512 x
-// 4096 x 4096 13.9 / 14.8, 300 x 1024 x 1024 7.5 / 6.8).  So they are up to 64
-// rows: a lane-side box then serves one tile whichever kernel reads it, and
-// two CTAs an SM keep more of them in flight (1 x 32768 x 4096 37.6 / 23.3,
-// 64 x 32768 x 4096 31.4 / 24.5, 64 x 100000 x 2048 42.0 / 38.3; but 100 x
-// 32768 x 4096, each box read twice, 32.0 / 42.1).  Where single CTAs do not
-// fill the SMs, k is split while a part keeps at least four blocks: a smaller
-// part costs more in the meeting of the sums than it saves.  Up to one CTA an
-// SM; up to two where few rows make the sums short (with one / two: 1 x 4096 x
-// 4096 7.4 / 6.3 us, 1 x 8192 x 4096 9.4 / 8.4, 1 x 4096 x 16384 15.0 / 13.6,
-// but 777 x 1111 x 2064 8.3 / 10.5).
-Plan choose_plan(int m, int n, int kblocks) {
-  const int64_t lane_tiles = ceil_div(n, 256);
-  if (m > SPLIT_MAX_WIDTH && lane_tiles * ceil_div(m, PAIR_MAX_WIDTH) >= 76) {
+// Pairs of CTAs take the work when there is a 256 x 224 tile for each pair of
+// the `sms` SMs (all figures here: 152 of them), in tiles as wide as makes
+// their turns shortest: a turn costs about its width and 120 columns more (3000
+// x 2048 x 2048, two turns at any width from 160 to 224: 14.3, 14.5, 14.9 us;
+// 2000 x 8192 x 2048, four turns of 224 or five of 192: 24.8 and 27.6).  Fewer
+// tiles leave pairs idle, and 128 x 64 ones for single CTAs, two to an SM, are
+// then as fast or faster (us, pairs at their best width against single CTAs:
+// 777 x 1111 x 2064 10.8 / 9.8, 512 x 4096 x 4096 13.9 / 14.8, 300 x 1024 x
+// 1024 7.5 / 6.8).  So they are up to 64 rows: a lane-side box then serves one
+// tile whichever kernel reads it, and two CTAs an SM keep more of them in
+// flight (1 x 32768 x 4096 37.6 / 23.3, 64 x 32768 x 4096 31.4 / 24.5, 64 x
+// 100000 x 2048 42.0 / 38.3; but 100 x 32768 x 4096, each box read twice, 32.0
+// / 42.1).  Where single CTAs do not fill the SMs, k is split while a part
+// keeps at least four blocks: a smaller part costs more in the meeting of the
+// sums than it saves.  Up to one CTA an SM; up to two where few rows make the
+// sums short (with one / two: 1 x 4096 x 4096 7.4 / 6.3 us, 1 x 8192 x 4096 9.4
+// / 8.4, 1 x 4096 x 16384 15.0 / 13.6, but 777 x 1111 x 2064 8.3 / 10.5).
+Plan choose_plan(int m, int n, int kblocks, int sms) {
+  const int64_t lane_tiles = ceil_div(n, 256), pairs = sms / 2;
+  if (m > SPLIT_MAX_WIDTH && lane_tiles * ceil_div(m, PAIR_MAX_WIDTH) >= pairs) {
     Plan best{true, PAIR_MAX_WIDTH, 1};
     int64_t least = INT64_MAX;
     for (int width = PAIR_MAX_WIDTH; width >= 128; width -= 32) {
-      const int64_t cost = (int64_t)ceil_div(lane_tiles * ceil_div(m, width), 76) * (width + 120);
+      const int64_t cost = (int64_t)ceil_div(lane_tiles * ceil_div(m, width), pairs) * (width + 120);
       if (cost < least) {
         least = cost;
         best.width = width;
@@ -849,7 +849,7 @@ Plan choose_plan(int m, int n, int kblocks) {
   }
   Plan p{false, m <= 16 ? 16 : m <= 32 ? 32 : SPLIT_MAX_WIDTH, 1};
   const int64_t tiles = (int64_t)ceil_div(n, 128) * ceil_div(m, p.width);
-  while (p.splits < 8 && 8 * p.splits <= kblocks && tiles * p.splits * 2 <= (p.width <= 32 ? 304 : 152)) p.splits *= 2;
+  while (p.splits < 8 && 8 * p.splits <= kblocks && tiles * p.splits * 2 <= (p.width <= 32 ? 2 * sms : sms)) p.splits *= 2;
   return p;
 }
 
@@ -874,7 +874,8 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   a.err = static_cast<uint32_t *>(p.workspace);
   a.test_wait = (p.flags & KDA_TEST_WAIT_TIMEOUT) != 0;
 
-  const Plan plan = choose_plan(p.m, p.n, a.kblocks);
+  const int sms = sm_count();
+  const Plan plan = choose_plan(p.m, p.n, a.kblocks, sms);
   const bool pair = plan.pair;
   a.width = plan.width;
   a.splits = plan.splits;
@@ -891,9 +892,9 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
               p.ldo <= INT32_MAX;
   // A pair has its SMs to itself, and so do split CTAs when all of them fit that
   // way; else two share one.  A cluster stays within a group of SMs, whose number
-  // is no multiple of it: fours fill 144 SMs, eights surely 64 (1 x 2048 x 8192,
-  // 16 clusters of eight: 12.5 us alone, in two turns, 6.8 sharing).
-  const int64_t fit = a.splits == 8 ? 64 : a.splits == 4 ? 144 : 152;
+  // is no multiple of it: of 152 SMs fours fill 144, eights surely 64 (1 x 2048 x
+  // 8192, 16 clusters of eight: 12.5 us alone, in two turns, 6.8 sharing).
+  const int64_t fit = a.splits == 8 ? sms * 64 / 152 : a.splits == 4 ? sms * 144 / 152 : sms;
   const bool alone = pair || (int64_t)a.tiles * a.splits <= fit;
   uint32_t budget = SMEM_LIMIT - SF_BYTES - (a.out_tma ? OUT_BYTES : 0);
   if (!alone) budget = (SMEM_LIMIT - 1024 - (uint32_t)sizeof(Bars)) / 2 - 1024 - SF_BYTES;
@@ -916,7 +917,7 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   uint32_t smem = a.stages * a.stage_bytes + SF_BYTES + 1024;
   if (pair) {
     smem += a.out_tma ? OUT_BYTES : 0;
-    const unsigned grid = 2u * (unsigned)(a.tiles < 76 ? a.tiles : 76);
+    const unsigned grid = 2u * (unsigned)(a.tiles < sms / 2 ? a.tiles : sms / 2);
     return launch_overlapped(f32     ? fp8_matmul_pair_kernel<float, true>
                              : spans ? fp8_matmul_pair_kernel<__nv_bfloat16, true>
                                      : fp8_matmul_pair_kernel<__nv_bfloat16, false>,

@@ -230,7 +230,7 @@ fp8_quantize_kernel(kda_fp8_quantize_args a, int cblocks, int tiles) {
 
 template <typename T, Mode M> cudaError_t launch(const kda_fp8_quantize_args &a, int cblocks, int tiles, cudaStream_t st) {
   // three CTAs in turn on each place: SMs are not equally fast (one: 92.1 us, three: 90.7, one per block: 101)
-  const int most = 3 * 152 * (sizeof(T) == 2 && M != ODD ? 3 : 2);
+  const int most = 3 * sm_count() * (sizeof(T) == 2 && M != ODD ? 3 : 2);
   return launch_overlapped(fp8_quantize_kernel<T, M>, (unsigned)(tiles < most ? tiles : most), kThreads,
                            M == RING ? 8 * kThreads * 16 : 0, 1, st, a, cblocks, tiles);
 }

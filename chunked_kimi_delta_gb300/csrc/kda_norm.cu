@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(WARP ? 256 : M == RING || VPT == 1 ? 512 : 102
 
 // ------------------------------------------------------------------ backward
 
-constexpr int kMaxParts = 1216;  // partial dweight rows at most: 8 CTAs on each of 152 SMs
+constexpr int kMaxParts = 1216;  // partial dweight rows, and CTAs, at most: eight on each of 152 SMs
 
 // dweight of a team's rows is summed in its registers; a CTA leaves one row of
 // partial sums.  32768 x 4096 bf16 with the residual's gradient: 162 us for
@@ -406,7 +406,7 @@ Shape shape_for(int64_t rows, int cols, int vecs, int tensors, int esize, int wi
     per_sm = 2048 / s.threads;
   }
   if (per_sm < 1) per_sm = 1;
-  const int64_t teams = s.warp ? s.threads / 32 : 1, resident = 152 * (int64_t)per_sm;
+  const int64_t teams = s.warp ? s.threads / 32 : 1, resident = sm_count() * (int64_t)per_sm;
   const int64_t need = (rows + teams - 1) / teams;
   // Up to `rounds` CTAs in turn on each place, of at least 8 rows: SMs are not
   // equally fast (32768 x 4096: 168 us in one round, 155 in two, 140 in six).
