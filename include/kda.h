@@ -601,8 +601,9 @@ kda_status kda_fp8_quantize(const kda_fp8_quantize_args *args, kda_stream_t stre
  * it (the call's output is then undefined) and kda_get_device_status reads
  * and clears it.
  * Errors: KDA_ERR_INVALID_ARG (sizes < 0, bad form or dtype, unknown flags,
- * null pointers, a pitch smaller than its row), KDA_ERR_UNSUPPORTED (more than 2^31 - 1
- * output tiles, a pitch of 2^31 bytes or more), KDA_ERR_ALIGNMENT (a, b or
+ * null pointers, a pitch smaller than its row), KDA_ERR_UNSUPPORTED (m, n or k
+ * above 2^31 - 1025, more than 2^25 - 1 blocks of 128 x 128 in out, lda or ldb
+ * of 2^31 or more), KDA_ERR_ALIGNMENT (a, b or
  * scales not 16-byte aligned, lda or ldb not a multiple of 16, out not
  * aligned to its element), KDA_ERR_WORKSPACE, KDA_ERR_CUDA.
  */
