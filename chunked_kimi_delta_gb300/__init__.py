@@ -33,7 +33,6 @@ KDA_LAYOUT_HEAD_MAJOR = 1 << 11
 KDA_TEST_WAIT_TIMEOUT = 1 << 30   # test only: see include/kda.h
 KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGNMENT = 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_DEVICE_TIMEOUT = 4, 5, 6
-KDA_FP8_ROW, KDA_FP8_COL, KDA_FP8_TILE = 1, 2, 4
 KDA_FP8_NT, KDA_FP8_NN, KDA_FP8_TN = 0, 1, 2
 KDA_FP8_MATMUL_WORKSPACE_BYTES = 256
 CHUNK = 64

@@ -486,18 +486,16 @@ kda_status kda_state_grad_scan(const float *M, const float *E, const float *dS_f
  * written), and power-of-two scales, one byte each: byte b stands for
  * 2^(b - 127), b = 255 for NaN.  The real value is value * scale.  Blocks are
  * of 128; RB = ceil(R / 128), CB = ceil(C / 128):
- *   KDA_FP8_ROW   one scale per row and 128 columns; bytes [ceil(CB/4), R, 4]:
- *                 block j of row r at ((j / 4) * R + r) * 4 + j % 4
- *   KDA_FP8_COL   one scale per column and 128 rows; bytes [ceil(RB/4), C, 4]
- *   KDA_FP8_TILE  one scale per 128 x 128 block; bytes [RB, CB]
+ *   ROW   one scale per row and 128 columns; bytes [ceil(CB/4), R, 4]:
+ *         block j of row r at ((j / 4) * R + r) * 4 + j % 4
+ *   COL   one scale per column and 128 rows; bytes [ceil(RB/4), C, 4]
+ *   TILE  one scale per 128 x 128 block; bytes [RB, CB]
  * Bytes of ROW and COL past the last block are written as 127 (1.0).
  * Quantising takes the smallest e >= -127 with max|x| <= 448 * 2^e over the
  * block's finite elements (e = 0 for a block of zeros) and rounds x * 2^-e to
  * the nearest e4m3 value, ties to even; NaN and infinities become NaN (e4m3
  * has no infinity) and leave their block's scale alone.
  * ------------------------------------------------------------------------ */
-typedef enum { KDA_FP8_ROW = 1, KDA_FP8_COL = 2, KDA_FP8_TILE = 4 } kda_fp8_kind;
-
 /* Widest row kda_rms_norm and kda_rms_norm_bwd take. */
 #define KDA_RMS_NORM_MAX_COLS 32768
 
