@@ -259,8 +259,6 @@ cudaError_t launch_tc_bwd_dh(const BwdChainArgs &a, const SeqInfo &s, int H, int
 
 // TMA map of a bf16 [T_tot, H, 128] tensor in the forward's v-tile layout.
 bool make_value_map(const void *x, int64_t T_tot, int H, CUtensorMap &map);
-// The chain's output o, bf16 [T_tot, H, dv]: boxes of 64 channels x 64 tokens
-// of one head, 128-byte swizzle (the layout of the chain's staging tile).
 // A matrix of bytes [outer, pitch], `inner` of them in a row: boxes of 128
 // bytes x box_outer rows, swizzled, zeros outside.
 bool make_byte_map(const void *p, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_outer,
@@ -269,6 +267,8 @@ bool make_byte_map(const void *p, int64_t inner, int64_t outer, int64_t pitch, u
 // of tiles 32 elements wide: plain (fp32) or in the 64-byte swizzle (bf16).
 bool make_out_tile_map(const void *p, bool f32, int64_t inner, int64_t outer, int64_t pitch, uint32_t box_inner,
                        uint32_t box_outer, CUtensorMap &map);
+// The chain's output o, bf16 [T_tot, H, dv]: boxes of 64 channels x 64 tokens
+// of one head, 128-byte swizzle (the layout of the chain's staging tile).
 bool make_out_map(const void *o, int64_t T_tot, int H, int dv, CUtensorMap &map);
 
 // Segment summary (kda_tc_summary.cu): M [.., dk, dk] and S~ [.., dk, dv] of
