@@ -70,7 +70,7 @@ struct MmArgs {
   int span;                  // blocks of k that one accumulator sums
   void *out;
   int64_t ldo;
-  bool out_tma;              // the output takes TMA stores (rows on 16 bytes)
+  bool out_tma;              // the output takes TMA stores (rows start and end on 16 bytes)
   uint32_t *err;
   bool test_wait;
 };
@@ -887,9 +887,12 @@ cudaError_t launch_fp8_matmul(const kda_fp8_matmul_args &p, cudaStream_t st) {
   a.stage_bytes = LANE_BYTES + ((a.col_box_bytes + 1023) & ~1023u);
   const bool f32 = p.out_dtype == KDA_F32;
   const bool spans = f32 || a.kblocks > a.span;  // kernels that add up spans of k
-  // sums of spans in bf16 leave by plain stores: over so long a k that costs nothing
-  a.out_tma = pair && f32 == spans && p.ldo * (f32 ? 4 : 2) % 16 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
-              p.ldo <= INT32_MAX;
+  // TMA stores clip a row at 16 bytes, not at elements: rows that end inside of
+  // 16 leave by plain stores, or they would reach into what lies beside them.
+  // So do sums of spans in bf16: over so long a k that costs nothing.
+  const int64_t es = f32 ? 4 : 2;
+  a.out_tma = pair && f32 == spans && p.n * es % 16 == 0 && p.ldo * es % 16 == 0 && p.ldo <= INT32_MAX &&
+              reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
   // A pair has its SMs to itself, and so do split CTAs when all of them fit that
   // way; else two share one.  A cluster stays within a group of SMs, whose number
   // is no multiple of it: of 152 SMs fours fill 144, eights surely 64 (1 x 2048 x
