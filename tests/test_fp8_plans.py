@@ -1,12 +1,19 @@
-"""The matrix product of scaled 8-bit matrices in the plans that it gives
-large problems, on the GPU."""
+"""The matrix product of scaled 8-bit matrices in every tile width, output
+path and number of spans that its plan gives large problems, and the norm's
+and the binding's less common ways, on the GPU."""
+import numpy as np
 import pytest
 import torch
 
 import fp8_testutil as ref
-from test_fp8_path import _operands, _product
+from test_fp8_path import NORM_SHAPES, U32, _bwd_ref, _np, _operands, _product, _rand
 
 pytestmark = pytest.mark.gpu
+
+# Pairs of CTAs in tiles of 160, 192, 128 and 224 rows, each with rows of the
+# result on 16 bytes and not.  k: three blocks; two spans of fp32 sums, the
+# second one short; four.
+PAIR_SHAPES = [(2900, 2048), (2901, 2047), (3500, 2048), (3501, 2047), (2200, 2048), (2201, 2047), (2500, 2600), (2501, 2599)]
 
 
 def _integers(shape, seed):
@@ -20,6 +27,17 @@ def _integers(shape, seed):
 
 def _exact(form, a, b):
     return _product(form, *(torch.from_numpy(ref.values(x)).cuda() for x in (a, b)))
+
+
+@pytest.mark.parametrize("k", [272, 1736, 5000])
+@pytest.mark.parametrize("m,n", PAIR_SHAPES)
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+def test_pairs_in_every_width_are_exact(cuda_lib, form, m, n, k):
+    a, b = _operands(cuda_lib, form, m, n, k, 200, _integers)
+    want = _exact(form, a, b)
+    assert torch.equal(cuda_lib.kda_fp8_matmul(a, b, form, out_dtype=torch.float32).double(), want)
+    assert torch.equal(cuda_lib.kda_fp8_matmul(a, b, form), want.bfloat16())
+    assert cuda_lib.kda_fp8_matmul_status() == cuda_lib.KDA_OK
 
 
 @pytest.mark.parametrize("left,pitch", [(5, 2063), (8, 2072)])
@@ -38,3 +56,62 @@ def test_pairs_write_only_their_result(cuda_lib, form, m, left, pitch):
         assert torch.equal(out, want.to(dtype))
         out.fill_(7.0)
         assert torch.all(buf == 7.0)
+
+
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(700, 256), (1300, 100)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_bwd_weight_gradient(cuda_lib, rows, cols, dtype):
+    """A column of dweight adds rows / 608 in a thread, up to 1,216 partial
+    rows over 64 lanes (19 each), the lanes of a warp that share it (two
+    exchanges) and 16 warps; up to eight warps before that; 45 in n itself."""
+    h, g = _rand((rows, cols), dtype, 7), _rand((rows, cols), dtype, 8)
+    w = 1 + 0.1 * torch.randn(cols, device="cuda")
+    _, dw = cuda_lib.kda_rms_norm_bwd(g, h, w, eps=1e-6)
+    _, want, _, mag = _bwd_ref(_np(g), _np(h), _np(w), 0.0, float(np.float32(1e-6)))
+    assert np.all(np.abs(_np(dw) - want) <= mag * (rows / 608 + 1 + 19 + 2 + 16 + 8 + 45) * U32 + 1e-38)
+
+
+@pytest.mark.parametrize("cols", [264, 1111, 4096])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_residual_sums_at_the_ends_of_the_range(cuda_lib, cols, dtype):
+    """The stream's addition rounds once, also among the smallest numbers,
+    with zeros of either sign, infinities and NaN."""
+    x, r = (_rand((9, cols), torch.float32, s) for s in (220, 221))
+    x[0] *= 1e-38
+    r[0] *= 1e-38
+    x[1], r[1] = x[1] * 1e-40, r[1] * 1e-42
+    r[2] = -x[2]
+    x[3], r[3] = 0.0, -0.0
+    x[4], r[4] = -0.0, -0.0
+    x[5, 3], r[5, 3], x[6, 4], x[7, 5] = float("inf"), float("-inf"), float("inf"), float("nan")
+    x[8], r[8] = 3e38, 3e38
+    x, r = x.to(dtype), r.to(dtype)
+    got = cuda_lib.kda_rms_norm(x, None, r).residual_out
+    want = (x.double() + r.double()).to(torch.float32).to(dtype) if dtype == torch.bfloat16 else x + r
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    assert torch.equal(got.view(bits)[fine], want.view(bits)[fine])
+
+
+def test_binding_without_the_short_allocator(cuda_lib, monkeypatch):
+    """Where torch lacks the allocation that the binding prefers, its public
+    one gives the same results."""
+    x = _rand((300, 1000), torch.bfloat16, 230)
+
+    def calls():
+        n = cuda_lib.kda_rms_norm(x, None, x, fp8=True)
+        w, = cuda_lib.kda_fp8_quantize(x, "tile")
+        dx, dw = cuda_lib.kda_rms_norm_bwd(n.out, n.residual_out)
+        y = cuda_lib.kda_fp8_matmul(n.fp8, w)
+        return [n.out, n.residual_out, n.fp8.data.view(torch.uint8), n.fp8.scales.view(torch.uint8), dx, dw, y]
+
+    want = calls()
+    before = cuda_lib._alloc
+    monkeypatch.setattr(cuda_lib, "_F8", None)
+    monkeypatch.setattr(cuda_lib, "_alloc", before)  # put back afterwards
+    monkeypatch.delattr(torch._C._dynamo.guards, "_empty_strided_cuda", raising=False)
+    got = calls()
+    assert cuda_lib._alloc is not before
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert [t.stride() for t in got] == [t.stride() for t in want]
