@@ -1,6 +1,8 @@
 """The matrix product of scaled 8-bit matrices in every tile width, output
 path and number of spans that its plan gives large problems, and the norm's
 and the binding's less common ways, on the GPU."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -115,3 +117,85 @@ def test_binding_without_the_short_allocator(cuda_lib, monkeypatch):
     assert cuda_lib._alloc is not before
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert [t.stride() for t in got] == [t.stride() for t in want]
+
+
+@pytest.mark.parametrize("m,n", [(5, 130), (2201, 2047), (2901, 2048)])
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+def test_operands_inside_of_wider_buffers(cuda_lib, form, m, n):
+    """What stands beside an operand's rows is NaN: none of it is read into a
+    sum, in either operand, also where a row ends inside of 16 bytes."""
+    k = 1741
+    a, b = _operands(cuda_lib, form, m, n, k, 240, _integers)
+    want = _exact(form, a, b)
+
+    def widened(x):
+        rows, cols = x.data.shape
+        buf = torch.full((rows + 2, (cols + 31) // 16 * 16), 0x7F, dtype=torch.uint8, device="cuda")
+        buf[1:1 + rows, :cols] = x.data.view(torch.uint8)
+        return cuda_lib.Fp8Matrix(buf.view(torch.float8_e4m3fn)[1:1 + rows, :cols], x.scales, x.kind)
+
+    for dtype in (torch.float32, torch.bfloat16):
+        assert torch.equal(cuda_lib.kda_fp8_matmul(widened(a), widened(b), form, out_dtype=dtype), want.to(dtype))
+
+
+class _Guarded:
+    """Device buffers between bands of 4,096 bytes of 0xA5."""
+
+    def __init__(self):
+        self.bands = []
+
+    def new(self, nbytes):
+        buf = torch.full((8192 + (nbytes + 15) // 16 * 16,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.bands.append((buf, nbytes))
+        return buf[4096:4096 + nbytes]
+
+    def intact(self):
+        return all(bool((b[:4096] == 0xA5).all()) and bool((b[4096 + n:] == 0xA5).all()) for b, n in self.bands)
+
+
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(20001, 903)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_and_quantiser_write_only_their_results(cuda_lib, rows, cols, dtype):
+    """Guard bands around every output, and a pitch of the 8-bit values with
+    room beside each row."""
+    k, lib = cuda_lib, cuda_lib.load_library()
+    code, es = (k.KDA_BF16, 2) if dtype == torch.bfloat16 else (k.KDA_F32, 4)
+    x, r, g = (_rand((rows, cols), dtype, s) for s in (250, 251, 252))
+    stream = torch.cuda.current_stream().cuda_stream
+    ld = (cols + 15) // 16 * 16 + 32
+    rb, cb = ref.blocks(rows), ref.blocks(cols)
+    buf = _Guarded()
+
+    def beside(q):
+        """The bytes to the right of the values have not been written."""
+        return bool((q.view(rows, ld)[:, cols:] == 0xA5).all())
+
+    want = k.kda_rms_norm(x, None, r, fp8=True)
+    h, out, q, s = buf.new(rows * cols * es), buf.new(rows * cols * es), buf.new(rows * ld), buf.new((cb + 3) // 4 * rows * 4)
+    a = k.kda_rms_norm_args(rows, cols, code, x.data_ptr(), r.data_ptr(), None, 1e-6, h.data_ptr(), out.data_ptr(),
+                            q.data_ptr(), ld, s.data_ptr())
+    assert lib.kda_rms_norm(ctypes.byref(a), stream) == k.KDA_OK
+    assert buf.intact() and beside(q)
+    assert torch.equal(h.view(dtype).view(rows, cols), want.residual_out) and torch.equal(out.view(dtype).view(rows, cols), want.out)
+    assert torch.equal(q.view(rows, ld)[:, :cols], want.fp8.data.view(torch.uint8))
+    assert torch.equal(s, want.fp8.scales.view(torch.uint8).flatten())
+
+    want_dx, want_dw = k.kda_rms_norm_bwd(g, x, None, r)
+    need = lib.kda_rms_norm_bwd_workspace_size(rows, cols)
+    dx, dw, ws = buf.new(rows * cols * es), buf.new(cols * 4), buf.new(need)
+    a = k.kda_rms_norm_bwd_args(rows, cols, code, g.data_ptr(), x.data_ptr(), None, r.data_ptr(), 1e-6, dx.data_ptr(),
+                                dw.data_ptr(), ws.data_ptr(), need)
+    assert lib.kda_rms_norm_bwd(ctypes.byref(a), stream) == k.KDA_OK
+    assert buf.intact()
+    assert torch.equal(dx.view(dtype).view(rows, cols), want_dx) and torch.equal(dw.view(torch.float32), want_dw)
+
+    kinds = ("row", "col", "tile")
+    parts = k.kda_fp8_quantize(x, kinds)
+    vals = [buf.new(rows * ld) for _ in kinds]
+    scales = [buf.new((cb + 3) // 4 * rows * 4), buf.new((rb + 3) // 4 * cols * 4), buf.new(rb * cb)]
+    a = k.kda_fp8_quantize_args(rows, cols, code, x.data_ptr(), ld, *(t.data_ptr() for t in vals), *(t.data_ptr() for t in scales))
+    assert lib.kda_fp8_quantize(ctypes.byref(a), stream) == k.KDA_OK
+    assert buf.intact()
+    for p, v, e in zip(parts, vals, scales):
+        assert beside(v) and torch.equal(v.view(rows, ld)[:, :cols], p.data.view(torch.uint8))
+        assert torch.equal(e, p.scales.view(torch.uint8).flatten())
