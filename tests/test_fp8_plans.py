@@ -60,6 +60,81 @@ def test_pairs_write_only_their_result(cuda_lib, form, m, left, pitch):
         assert torch.all(buf == 7.0)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 130, 4096), (5, 1000, 8200), (33, 257, 2064), (64, 129, 8192)])
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+def test_split_products_write_only_their_result(cuda_lib, form, m, n, k):
+    """The same where k is split over a cluster."""
+    a, b = _operands(cuda_lib, form, m, n, k, 260, _integers)
+    want = _exact(form, a, b)
+    for dtype in (torch.float32, torch.bfloat16):
+        for left in (5, 8):
+            buf = torch.full((m + 6, n + 16), 7.0, dtype=dtype, device="cuda")
+            out = buf[3:3 + m, left:left + n]
+            cuda_lib.kda_fp8_matmul(a, b, form, out=out)
+            assert torch.equal(out, want.to(dtype))
+            out.fill_(7.0)
+            assert torch.all(buf == 7.0)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 130, 1100), (300, 200, 300), (2201, 2047, 300)])
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+def test_scales_at_both_ends(cuda_lib, form, m, n, k):
+    """One operand about 2^-121, with scale bytes down to 0, the other about
+    2^122: the products are of ordinary size and exact."""
+    a, b = _operands(cuda_lib, form, m, n, k, 270,
+                     lambda s, seed: _integers(s, seed) * (2.0 ** -121 if seed == 270 else 2.0 ** 122))
+    assert int(a.scales.view(torch.uint8).min()) == 0
+    want = _exact(form, a, b)
+    assert float(want.abs().max()) > 1
+    assert torch.equal(cuda_lib.kda_fp8_matmul(a, b, form, out_dtype=torch.float32).double(), want)
+
+
+@pytest.mark.parametrize("m,n", [(70, 200), (2201, 2047)])
+def test_scale_that_is_nan(cuda_lib, m, n):
+    """Byte 255 stands for NaN: it reaches the results of its row, or of its
+    tile's columns, and no others."""
+    k = 700
+    a, b = _operands(cuda_lib, "nt", m, n, k, 280, _integers)
+    want = _exact("nt", a, b)
+    a.scales.view(torch.uint8)[1, 17, 0] = 255       # row 17, columns 512 to 639
+    b.scales.view(torch.uint8)[1, 2] = 255           # rows 128 and on, columns 256 to 383
+    got = cuda_lib.kda_fp8_matmul(a, b, out_dtype=torch.float32).double()
+    bad = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    bad[17], bad[:, 128:256] = True, True
+    assert torch.equal(torch.isnan(got), bad)
+    assert torch.equal(got[~bad], want[~bad])
+
+
+def test_products_and_layers_on_several_streams(cuda_lib):
+    """Products of both kernels, norms, quantisers and the chunked forward at
+    once on streams of their own, whose kernels share SMs and tensor memory:
+    the results are those of each alone."""
+    g = torch.Generator(device="cuda").manual_seed(290)
+    q, k, v = (torch.randn(2, 512, 8, 128, device="cuda", generator=g).bfloat16() for _ in range(3))
+    gate, beta = -torch.rand(2, 512, 8, 128, device="cuda", generator=g), torch.rand(2, 512, 8, device="cuda", generator=g)
+    large = _operands(cuda_lib, "nt", 2500, 2600, 1024, 291, _integers)
+    few = _operands(cuda_lib, "nt", 3, 2048, 4096, 293, _integers)
+    some = _operands(cuda_lib, "tn", 300, 1000, 2000, 295, _integers)
+    x = _rand((3000, 2048), torch.bfloat16, 297)
+    calls = [lambda: cuda_lib.kda_fp8_matmul(*large), lambda: cuda_lib.kda_fp8_matmul(*few),
+             lambda: cuda_lib.kda_fp8_matmul(*some, "tn", out_dtype=torch.float32),
+             lambda: cuda_lib.kda_chunk_fwd(q, k, v, gate, beta)[0], lambda: cuda_lib.kda_rms_norm(x, None, x).out,
+             lambda: cuda_lib.kda_fp8_quantize(x, ("row", "col"))[1].data.view(torch.uint8)]
+    want = [f() for f in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for f, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    out = f()
+                got.append(out)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert cuda_lib.kda_fp8_matmul_status() == cuda_lib.KDA_OK
+
+
 @pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(700, 256), (1300, 100)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_norm_bwd_weight_gradient(cuda_lib, rows, cols, dtype):
