@@ -23,8 +23,9 @@
 // an entry to tensor memory ahead of them (tcgen05.cp, which orders itself
 // before the MMAs and repeats the entry for the four quarters).  Storing the
 // words to tensor memory from registers instead (tcgen05.st by four warps)
-// took 2,400 cycles a word against the 1,800 of its MMAs: 2.9 PFLOP/s at
-// 32768 x 4096 x 4096 where this reaches 3.5 PFLOP/s.
+// took 2,400 cycles a word against the 1,800 of its MMAs: 2.9 PFLOP/s from rest
+// at 32768 x 4096 x 4096 where this reaches 3.5 (3.0 in a stream of calls under
+// the power cap).
 #include <cuda_bf16.h>
 
 #include "kda_fp8.cuh"
@@ -367,10 +368,11 @@ __device__ __forceinline__ void settle() {
 // What bounds it is the way of the operands: a block of k brings 30.7 KB to
 // an SM, 480 cycles at 64 bytes a cycle from L2 (and again 480 for shared
 // memory to take them in and give them to the MMAs at 128), against 448
-// cycles of MMAs; measured about 560 at 32768 x 4096 x 4096 (306 us, 3.6
-// PFLOP/s from rest, 363 to 368 us back to back under the power cap; tensor pipe 78%
-// busy).  Half of the MMAs left out changed little (314 to 300 us), 26% less
-// read from L2 by multicast of the lane side to a second pair nothing at all.
+// cycles of MMAs; measured about 560 at 32768 x 4096 x 4096 (354 to 363 us,
+// 3.0 to 3.1 PFLOP/s, back to back under the power cap at 1,395 to 1,460 MHz;
+// 315 us over the first 30 calls after a rest; tensor pipe 79% busy).  Half of
+// the MMAs left out changed little (314 to 300 us), 26% less read from L2 by
+// multicast of the lane side to a second pair nothing at all.
 // Warps 0-7 epilogue, 8 scales, 9 TMA, 10 MMA (first CTA of the pair).
 constexpr int PAIR_THREADS = 352;
 constexpr int PAIR_MAX_WIDTH = 224;  // two accumulators and the scale ring fill the 512 columns
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1) fp8_matmul_pair_kernel(const 
 // each with its own range of k; the partial sums meet through distributed
 // shared memory and are added in the order of k.
 // What bounds it is latency, from the launch over one pass of loads and MMAs
-// to the meeting of the sums: 1 x 4096 x 4096 takes 6.3 us where the weight's
+// to the meeting of the sums: 1 x 4096 x 4096 takes 6.6 us where the weight's
 // bytes take 2.5.
 // Warps 0-3 epilogue, 4 scales, 5 TMA, 6 MMA.
 constexpr int SPLIT_THREADS = 224;
