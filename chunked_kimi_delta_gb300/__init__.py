@@ -165,6 +165,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kda_chunk_fwd_host_workspace_size": ([P], ctypes.c_size_t),
         "kda_chunk_fwd_host": ([P, vp], ctypes.c_int),
         "kda_recurrent_step": ([ctypes.POINTER(kda_decode_args), vp], ctypes.c_int),
+        "kda_gdn_chunk_fwd_workspace_size": ([P], ctypes.c_size_t),
+        "kda_gdn_chunk_fwd": ([P, vp], ctypes.c_int),
+        "kda_gdn_recurrent_step": ([ctypes.POINTER(kda_decode_args), vp], ctypes.c_int),
         "kda_chunk_fwd_stages": ([P, ctypes.POINTER(ctypes.c_char_p), i32], i32),
         "kda_chunk_fwd_profiled": ([P, vp, ctypes.POINTER(vp), i32], ctypes.c_int),
         "kda_chunk_bwd_workspace_size": ([ctypes.POINTER(kda_bwd_args)], ctypes.c_size_t),
@@ -1137,3 +1140,140 @@ def kda_fp8_matmul_status(stream=None) -> int:
     read."""
     word = _fp8_status_word(_torch().cuda.current_device())
     return load_library().kda_get_device_status(word, _stream(stream))
+
+
+# ------------------------------------------- gated delta rule, one gate per head
+
+def _gdn_problem(q, k, v, g, beta, a_log, dt_bias, states, cu_seqlens, head_major, v_first, gate_in_kernel):
+    """Shapes and types of a chunked call's tensors (the kernels trust them).
+    ``states``: (name, tensor or None) of the recurrent states.  Returns
+    (sequences, heads, key heads, tokens per sequence or in all, batch)."""
+    torch = _torch()
+    nd = q.dim()
+    if nd not in (3, 4) or k.dim() != nd or v.dim() != nd:
+        raise ValueError("q/k/v are [B, T, H, D] or [T_total, H, D] (head-major: [B, H, T, D], [H, T_total, D])")
+    if cu_seqlens is not None and nd != 3:
+        raise ValueError("with cu_seqlens, q/k/v have one token axis")
+    th, tt = (-3, -2) if head_major else (-2, -3)  # axes of heads and tokens
+    H, Hk, T = v.shape[th], q.shape[th], v.shape[tt]
+    B = v.shape[0] if nd == 4 else 1
+    if k.shape != q.shape or q.shape[tt] != T or (nd == 4 and q.shape[0] != B):
+        raise ValueError("q and k must have v's leading dims and token count")
+    if Hk < 1 or H % Hk:
+        raise ValueError("the key heads of q/k must divide the value heads of v")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    if tuple(g.shape) != tuple(v.shape[:-1]) or tuple(beta.shape) != tuple(v.shape[:-1]):
+        raise ValueError("g and beta must have v's layout without the channel axis")
+    if gate_in_kernel and a_log is None:
+        raise ValueError("gate_in_kernel needs a_log")
+    for name, t in (("a_log", a_log), ("dt_bias", dt_bias)):
+        if t is not None and (tuple(t.shape) != (H,) or t.dtype != torch.float32):
+            raise ValueError(f"{name} must be fp32 [H]")
+    if g.dtype != torch.float32 or beta.dtype != torch.float32:
+        raise TypeError("g and beta must be fp32")
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or cu_seqlens.dtype != torch.int32:
+            raise ValueError("cu_seqlens must be int32 [sequences + 1]")
+        N = cu_seqlens.numel() - 1
+    shape = _state_shape(N, q, v, v_first, head_major)
+    for name, t in states:
+        if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32):
+            raise ValueError(f"{name} must be fp32 {list(shape)}")
+    return N, H, Hk, T, B
+
+
+def _gdn_args(q, k, v, g, beta, dims, scale, eps, a_log, dt_bias, initial_state, cu_seqlens, l2norm_qk, beta_sigmoid,
+              gate_in_kernel, v_first, head_major, extra_flags, out, final_state):
+    N, H, Hk, T, B = dims
+    flags = ((KDA_L2NORM_QK if l2norm_qk else 0) | (KDA_BETA_SIGMOID if beta_sigmoid else 0)
+             | (KDA_GATE_IN_KERNEL if gate_in_kernel else 0) | (KDA_STATE_V_FIRST if v_first else 0)
+             | (KDA_LAYOUT_HEAD_MAJOR if head_major else 0) | extra_flags)
+    a = kda_fwd_args(B, T, H, q.shape[-1], v.shape[-1], CHUNK, _dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                     _ptr(a_log), _ptr(dt_bias), _ptr(beta), q.shape[-1] ** -0.5 if scale is None else scale, eps,
+                     _ptr(initial_state), _ptr(cu_seqlens), N if cu_seqlens is not None else 0, flags, _ptr(out),
+                     _ptr(final_state))
+    a.Hk = Hk
+    return a
+
+
+def kda_gdn_chunk_fwd(q, k, v, g, beta, *, scale=None, eps=1e-6, a_log=None, dt_bias=None, initial_state=None,
+                      cu_seqlens=None, l2norm_qk=True, beta_sigmoid=False, gate_in_kernel=False,
+                      output_final_state=True, out=None, final_state=None, workspace=None, stream=None,
+                      state_v_first=False, head_major=False, extra_flags=0):
+    """Chunked forward of the gated delta rule with one gate per head:
+    arguments as :func:`kda_chunk_fwd`, but ``g`` has beta's shape ([B, T, H]
+    or [T, H]; head-major [B, H, T] or [H, T]) and ``dt_bias`` is [H].
+    Returns ``(out, final_state)``.  See ``kda_gdn_chunk_fwd`` in
+    include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_gdn_chunk_fwd(q, k, v, g, beta, scale=scale, eps=eps, a_log=a_log, dt_bias=dt_bias,
+                                     initial_state=initial_state, cu_seqlens=cu_seqlens, l2norm_qk=l2norm_qk,
+                                     beta_sigmoid=beta_sigmoid, gate_in_kernel=gate_in_kernel,
+                                     output_final_state=output_final_state, out=out, final_state=final_state,
+                                     workspace=workspace, state_v_first=state_v_first, head_major=head_major,
+                                     extra_flags=extra_flags)
+    lib = _ready()
+    dims = _gdn_problem(q, k, v, g, beta, a_log, dt_bias, (("initial_state", initial_state), ("final_state", final_state)),
+                        cu_seqlens, head_major, state_v_first, gate_in_kernel)
+    if out is not None and (out.shape != v.shape or out.dtype != v.dtype):
+        raise ValueError("out must have v's shape and dtype")
+    dev = _launch_device(q, k, v, g, beta, a_log, dt_bias, initial_state, cu_seqlens, out, final_state, workspace)
+    if out is None:
+        out = _alloc(tuple(v.shape), v.stride(), v.dtype)
+    if output_final_state and final_state is None:
+        shape = _state_shape(dims[0], q, v, state_v_first, head_major)
+        final_state = _alloc(shape, (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1), _F32)
+    a = _gdn_args(q, k, v, g, beta, dims, scale, eps, a_log, dt_bias, initial_state, cu_seqlens, l2norm_qk, beta_sigmoid,
+                  gate_in_kernel, state_v_first, head_major, extra_flags, out, final_state)
+    need = lib.kda_gdn_chunk_fwd_workspace_size(ctypes.byref(a))
+    ws = _alloc(((need + 3) // 4,), (1,), _F32) if workspace is None else _workspace(need, q.device, workspace)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    status = lib.kda_gdn_chunk_fwd(ctypes.byref(a), _raw_stream(dev))
+    if status:
+        raise KdaError(status, "kda_gdn_chunk_fwd")
+    return out, final_state
+
+
+def kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags=None, *, scale=None, eps=1e-6, a_log=None,
+                           dt_bias=None, l2norm_qk=True, beta_sigmoid=False, gate_in_kernel=False,
+                           state_v_first=False, out=None, stream=None):
+    """Recurrent step of the gated delta rule with one gate per head on pool
+    states, in place: as :func:`kda_recurrent_step` with ``g`` [N, T, H] and
+    ``dt_bias`` [H].  Returns out [N, T, H, dv].  See
+    ``kda_gdn_recurrent_step`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags, scale=scale, eps=eps, a_log=a_log,
+                                          dt_bias=dt_bias, l2norm_qk=l2norm_qk, beta_sigmoid=beta_sigmoid,
+                                          gate_in_kernel=gate_in_kernel, state_v_first=state_v_first, out=out)
+    lib = _ready()
+    if q.dim() != 4:
+        raise ValueError("q/k/v are [N, T, H, D]")
+    N, H, Hk, T, _ = _gdn_problem(q, k, v, g, beta, a_log, dt_bias, (), None, False, state_v_first, gate_in_kernel)
+    if tuple(cache.shape[1:]) != _state_shape(N, q, v, state_v_first)[1:]:
+        raise ValueError("cache must be [rows, H, dk, dv] ([rows, H, dv, dk] V-first)")
+    if idx.numel() != N:
+        raise ValueError("idx must have one row of the pool for each sequence")
+    if init_flags is not None and (init_flags.dtype != _torch_module.bool or init_flags.numel() != N):
+        raise TypeError("init_flags must be bool [N]")
+    if out is not None and (out.shape != v.shape or out.dtype != v.dtype):
+        raise ValueError("out must have v's shape and dtype")
+    rows, stride, _ = _rows(cache)
+    dev = _launch_device(q, k, v, g, beta, a_log, dt_bias, idx, init_flags, out)
+    if cache.get_device() != dev:
+        _on_device(q, cache)
+    if out is None:
+        out = _alloc(tuple(v.shape), v.stride(), v.dtype)
+    flags = ((KDA_L2NORM_QK if l2norm_qk else 0) | (KDA_BETA_SIGMOID if beta_sigmoid else 0)
+             | (KDA_GATE_IN_KERNEL if gate_in_kernel else 0) | (KDA_STATE_V_FIRST if state_v_first else 0))
+    a = kda_decode_args(N, T, H, q.shape[3], v.shape[3], _dtype_code(q), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                        g.data_ptr(), _ptr(a_log), _ptr(dt_bias), beta.data_ptr(),
+                        q.shape[3] ** -0.5 if scale is None else scale, eps, flags, out.data_ptr(), cache.data_ptr(),
+                        _dtype_code(cache), rows, stride, idx.data_ptr(), _idx_code(idx), _ptr(init_flags), Hk)
+    status = lib.kda_gdn_recurrent_step(ctypes.byref(a), _raw_stream(dev))
+    if status:
+        raise KdaError(status, "kda_gdn_recurrent_step")
+    return out

@@ -1,0 +1,127 @@
+// kda_api_gdn.cu - C ABI of the gated delta rule with one gate per head:
+// host-side argument checks, the workspace plan, then the launches.
+#include "kda_gdn.cuh"
+
+using namespace kda;
+
+namespace {
+
+inline bool mis16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+inline kda_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+constexpr uint32_t kFlags = KDA_L2NORM_QK | KDA_BETA_SIGMOID | KDA_GATE_IN_KERNEL | KDA_USE_EXP2 | KDA_STATE_V_FIRST |
+                            KDA_LAYOUT_HEAD_MAJOR;
+constexpr uint32_t kRefused = KDA_REUSE_PREP | KDA_SAFE_GATE | KDA_ALLOW_NEG_EIGVAL;
+
+inline int key_heads(const kda_fwd_args *a) { return a->Hk > 0 ? a->Hk : a->H; }
+inline int64_t tokens(const kda_fwd_args *a) { return (int64_t)a->B * a->T; }
+
+kda_status check(const kda_fwd_args *a) {
+  if (!a || a->B < 1 || a->T < 0 || a->H < 1) return KDA_ERR_INVALID_ARG;
+  if (a->Hk < 0 || (a->Hk > 0 && a->H % a->Hk != 0)) return KDA_ERR_INVALID_ARG;
+  if (a->flags & ~(kFlags | kRefused)) return KDA_ERR_INVALID_ARG;
+  if (a->qkv_dtype != KDA_F32 && a->qkv_dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  if (tokens(a) > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta)) return KDA_ERR_INVALID_ARG;
+  if ((a->flags & KDA_GATE_IN_KERNEL) && !a->a_log) return KDA_ERR_INVALID_ARG;
+  if (a->cu_seqlens && (a->B != 1 || a->num_seqs < 1)) return KDA_ERR_INVALID_ARG;
+  if ((a->dk != 64 && a->dk != 128) || (a->dv != 64 && a->dv != 128) || a->chunk != BT) return KDA_ERR_UNSUPPORTED;
+  if ((a->flags & kRefused) || a->h_out || a->v_new_out) return KDA_ERR_UNSUPPORTED;
+  if (tokens(a) > INT32_MAX) return KDA_ERR_UNSUPPORTED;  // token ids are 32-bit
+  const int64_t n = a->cu_seqlens ? a->num_seqs : a->B;
+  // one CTA per (chunk, head) and per (sequence, head)
+  if ((tokens(a) / BT + n) * a->H > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (mis16(a->q) || mis16(a->k) || mis16(a->v) || mis16(a->g) || mis16(a->beta) || mis16(a->a_log) || mis16(a->dt_bias) ||
+      mis16(a->initial_state) || mis16(a->cu_seqlens))
+    return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
+kda_status check_fwd(const kda_fwd_args *a) {
+  const kda_status s = check(a);
+  if (s != KDA_OK) return s;
+  if (!a->out && tokens(a) > 0) return KDA_ERR_INVALID_ARG;
+  return mis16(a->out) || mis16(a->final_state) ? KDA_ERR_ALIGNMENT : KDA_OK;
+}
+
+gdn::Problem problem(const kda_fwd_args *a) {
+  gdn::Problem p{};
+  p.s.bounds = a->cu_seqlens;
+  p.s.T_tot = tokens(a);
+  p.s.T = a->T;
+  p.s.N = a->cu_seqlens ? a->num_seqs : a->B;
+  p.H = a->H;
+  p.Hk = key_heads(a);
+  p.dk = a->dk;
+  p.dv = a->dv;
+  p.nchunks = (int32_t)chunks_upper_bound(p.s.T_tot, p.s.N, a->cu_seqlens != nullptr, a->T);
+  const bool hm = (a->flags & KDA_LAYOUT_HEAD_MAJOR) != 0;
+  auto strides = [&](int64_t heads, int64_t d) {
+    const int64_t T = a->T;
+    return hm ? gdn::Strides{heads * T * d, d, T * d} : gdn::Strides{T * heads * d, heads * d, d};
+  };
+  p.qk = strides(p.Hk, a->dk);
+  p.v = strides(a->H, a->dv);
+  p.gate = strides(a->H, 1);
+  p.q = a->q; p.k = a->k; p.val = a->v;
+  p.g = a->g; p.beta = a->beta;
+  p.gp.a_log = a->a_log;
+  p.gp.dt_bias = a->dt_bias;
+  p.gp.scale = a->scale;
+  p.gp.eps = a->eps;
+  p.gp.flags = a->flags;
+  p.v_first = (a->flags & KDA_STATE_V_FIRST) != 0;
+  return p;
+}
+
+// Chunk offsets of packed sequences (p.s.chunk_off), then the preparation.
+cudaError_t prepare(const kda_fwd_args *a, bool bwd, gdn::Problem &p, char *ws, const gdn::Plan &pl, cudaStream_t st) {
+  int32_t *co = reinterpret_cast<int32_t *>(ws + pl.off_chunks);
+  p.s.chunk_off = co;
+  cudaError_t e = p.s.bounds ? launch_chunk_map(p.s, co, st) : cudaSuccess;
+  if (e == cudaSuccess) e = gdn::launch_gdn_prep(a->qkv_dtype, bwd, p, ws, pl, st);
+  return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_gdn_chunk_fwd_workspace_size(const kda_fwd_args *a) {
+  if (check_fwd(a) != KDA_OK) return 0;
+  const gdn::Problem p = problem(a);
+  return gdn::make_gdn_plan(a->qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, false).total;
+}
+
+kda_status kda_gdn_chunk_fwd(const kda_fwd_args *a, kda_stream_t stream) {
+  const kda_status s = check_fwd(a);
+  if (s != KDA_OK) return s;
+  gdn::Problem p = problem(a);
+  const gdn::Plan pl = gdn::make_gdn_plan(a->qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, false);
+  if (!a->workspace || a->workspace_bytes < pl.total) return KDA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return KDA_ERR_ALIGNMENT;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char *ws = static_cast<char *>(a->workspace);
+  cudaError_t e = prepare(a, false, p, ws, pl, st);
+  if (e == cudaSuccess)
+    e = gdn::launch_gdn_chain(a->qkv_dtype, p, ws, pl, gdn::ChainOut{a->out, a->initial_state, a->final_state}, st);
+  return cuda_status(e);
+}
+
+kda_status kda_gdn_recurrent_step(const kda_decode_args *a, kda_stream_t stream) {
+  if (!a || a->N < 0 || a->T < 1 || a->H < 1) return KDA_ERR_INVALID_ARG;
+  if (a->Hk < 0 || (a->Hk > 0 && a->H % a->Hk != 0)) return KDA_ERR_INVALID_ARG;
+  if (a->flags & ~(kFlags | kRefused)) return KDA_ERR_INVALID_ARG;
+  if (a->flags & (kRefused | KDA_LAYOUT_HEAD_MAJOR)) return KDA_ERR_UNSUPPORTED;
+  if ((a->dk != 64 && a->dk != 128) || (a->dv != 64 && a->dv != 128)) return KDA_ERR_UNSUPPORTED;
+  if (a->qkv_dtype != KDA_F32 && a->qkv_dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  if (a->cache_dtype != KDA_F32 && a->cache_dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+  if (a->idx_dtype != KDA_I32 && a->idx_dtype != KDA_I64) return KDA_ERR_INVALID_ARG;
+  if (a->num_rows < 1 || a->row_stride_elems < (int64_t)a->H * a->dk * a->dv) return KDA_ERR_INVALID_ARG;
+  if ((a->flags & KDA_GATE_IN_KERNEL) && !a->a_log) return KDA_ERR_INVALID_ARG;
+  if (a->N == 0) return KDA_OK;
+  if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->out || !a->cache || !a->idx) return KDA_ERR_INVALID_ARG;
+  if ((int64_t)a->N * a->H > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  return cuda_status(gdn::launch_gdn_step(*a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

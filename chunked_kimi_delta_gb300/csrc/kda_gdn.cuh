@@ -1,0 +1,171 @@
+// kda_gdn.cuh - the gated delta rule with one gate per head: what its kernels
+// share.
+//
+//   S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// With G the running sum of g inside a chunk of 64 tokens and S the state
+// entering it,
+//   L_ij = beta_i e^{G_i - G_j} k_i.k_j (j < i),   A = (I + L)^-1
+//   Y  = beta (V - e^G K S),   W = A Y             (the corrected values)
+//   O  = scale e^G Q S + P W,  P_ij = scale e^{G_i - G_j} q_i.k_j (j <= i)
+//   S' = e^{G_C} S + (e^{G_C - G} K)^T W
+// A gate of one number per head commutes with every product over channels, so
+// k and q enter the products as the caller gave them and the gates, norms and
+// the scale are numbers per token, applied to sums.
+//
+// Arithmetic.  Products run on the tensor cores as fp16 pieces with fp32
+// sums: a value x is s x = hi + lo + (at most 2^-23 |s x|), s a power of two that takes
+// the largest of its row to [2^13, 2^14) (28 binades below it keep their
+// bits), and a product of two such values is hi hi + hi lo + lo hi.  bf16
+// inputs are one piece (8 bits fit fp16's 11), so the state, held in fp32,
+// costs two products with them and keeps fp32's accuracy; bf16 pieces would
+// lose 2^-17 of it at the same cost.  What only leads to a bf16 result (o, dq,
+// dk) takes the first piece alone: 2^-12, an eighth of bf16's own rounding.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace gdn {
+
+constexpr int C = BT;
+
+// Element strides of a [.., tokens, heads, channels] tensor.
+struct Strides {
+  int64_t b, t, h;
+};
+
+// One problem, as every kernel of the family takes it.
+struct Problem {
+  SeqInfo s;
+  int H, Hk, dk, dv;
+  int32_t nchunks;         // upper bound
+  Strides qk, v, gate;     // q and k; v, out and their gradients; g and beta (no channels)
+  const void *q, *k, *val;
+  const float *g, *beta;
+  GateParams gp;
+  bool v_first;            // states are [dv, dk]
+};
+
+// Chunk c's first token: batch row and token inside it, as the strides want
+// them, and the tokens it holds (false: none).
+__device__ __forceinline__ bool chunk_at(const SeqInfo &s, int64_t c, int &n, int64_t &batch, int64_t &tok, int &len) {
+  int64_t t0;
+  if (!chunk_lookup(s, c, n, t0, len)) return false;
+  batch = s.bounds ? 0 : n;
+  tok = s.bounds ? t0 : t0 - (int64_t)n * s.T;
+  return true;
+}
+
+// ---------------------------------------------------------------- workspace
+// Per (chunk, key head): the fp16 pieces of k, then of q, each [64, dk] as the
+// bytes of a shared-memory tile (16-byte units XOR-swizzled by row, so that
+// eight rows' units of one column lie in different banks).
+// Per (chunk, value head): numbers per token, then the pieces of A, then of P
+// ([64, 64] tiles; blocks of 16 above the diagonal are not written).
+constexpr int NUM_MISC = 0, NUM_BETA = 16, NUM_EK = 80, NUM_EQ = 144, NUM_FK = 208, NUM_K = 272, NUM_Q = 336, NUM_GH = 400,
+              NUM_GL = 464, NUM_FLOATS = 528;
+// misc: 0 e^{G_C}, 1 what a unit of A's pieces stands for, 2 the same of P's
+constexpr int NUM_BYTES = NUM_FLOATS * 4;
+constexpr int MAT_BYTES = C * C * 2;
+
+template <typename T> constexpr int pieces() { return sizeof(T) == 2 ? 1 : 2; }
+
+inline int in_pieces(kda_dtype d) { return d == KDA_BF16 ? 1 : 2; }
+inline size_t kq_bytes(kda_dtype d, int dk) { return (size_t)2 * in_pieces(d) * C * dk * 2; }
+// P in two pieces where the backward reads it (its products lead to fp32 results)
+inline size_t ap_bytes(kda_dtype d, bool bwd) { return NUM_BYTES + (size_t)MAT_BYTES * (2 + (bwd ? 2 : in_pieces(d))); }
+
+struct Plan {
+  size_t off_chunks, off_kq, off_ap, total;
+};
+inline Plan make_gdn_plan(kda_dtype d, int64_t nchunks, int N, int H, int Hk, int dk, bool bwd) {
+  Plan p{};
+  size_t o = 256;
+  p.off_chunks = o; o = align256(o + sizeof(int32_t) * ((size_t)N + 1));
+  p.off_kq = o; o = align256(o + (size_t)nchunks * Hk * kq_bytes(d, dk));
+  p.off_ap = o; o = align256(o + (size_t)nchunks * H * ap_bytes(d, bwd));
+  p.total = o;
+  return p;
+}
+
+// ---------------------------------------------------------------- primitives
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros (src is then not read)
+__device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool fill) {
+  const int n = fill ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Byte offset of 16-byte unit u of row r, rows of U units (8 or 16).
+template <int U> __device__ __forceinline__ uint32_t unit_at(int r, int u) { return (uint32_t)((r * U + (u ^ (r & 7))) * 16); }
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+// hi and lo pieces of two values that are in range already
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = pack_half(a - f.x, b - f.y);
+}
+// The power of two s that takes m (>= 0) to [2^13, 2^14), and 1 / s.  Both
+// are normal numbers; a maximum below 2^-113 stays smaller, one of zero takes any.
+__device__ __forceinline__ float2 piece_scale(float m) {
+  int e = (int)(__float_as_uint(m) >> 23);
+  int sb = 267 - e;
+  sb = sb > 253 ? 253 : sb;
+  return make_float2(__uint_as_float((uint32_t)sb << 23), __uint_as_float((uint32_t)(254 - sb) << 23));
+}
+// Log-decay of one token and head from what the caller gave.  From -256 on
+// (e^-256 is zero in fp32) it is held there: -inf, a decay to nothing, would
+// make NaN of the differences of running sums.
+__device__ __forceinline__ float log_decay(float x, const GateParams &gp, float neg_exp_alog, float bias) {
+  if (gp.flags & KDA_GATE_IN_KERNEL) {
+    const float z = x + bias;
+    x = neg_exp_alog * (fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
+  }
+  return x < -256.f ? -256.f : x;
+}
+
+// ---------------------------------------------------------------- launchers
+cudaError_t launch_gdn_prep(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, cudaStream_t st);
+
+struct ChainOut {
+  void *out;
+  const float *initial;
+  float *final_state;
+};
+cudaError_t launch_gdn_chain(kda_dtype dt, const Problem &p, const char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st);
+
+cudaError_t launch_gdn_step(const kda_decode_args &a, cudaStream_t st);
+
+}  // namespace gdn
+}  // namespace kda

@@ -1,0 +1,381 @@
+// kda_gdn_chain.cu - from chunk to chunk: the state, the corrected values and
+// the outputs of the gated delta rule with one gate per head (kda_gdn.cuh).
+//
+// A value channel's column of the state never meets another one, so a warp
+// takes 16 of them and walks the chunks alone: it holds S^T [16, dk] in the
+// accumulator layout of the tensor-core instruction, which is at once (rounded
+// to pieces) the layout of a left operand, and so do Y^T and W^T, its
+// intermediates.  Nothing of the recurrence passes through shared memory;
+// that holds only what the warps of a CTA read in common (k, q, A, P of the
+// chunk, double-buffered).
+#include "kda_gdn.cuh"
+
+namespace kda {
+namespace gdn {
+namespace {
+
+// Largest of |c0|, |c1| (row lane / 4) and of |c2|, |c3| (row + 8) over a row's
+// four lanes, as scales.
+template <int N>
+__device__ __forceinline__ void row_scales(const float (&x)[N][4], float2 &lo, float2 &hi) {
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a = fmaxf(a, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
+    b = fmaxf(b, fmaxf(fabsf(x[i][2]), fabsf(x[i][3])));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+    b = fmaxf(b, __shfl_xor_sync(~0u, b, o));
+  }
+  lo = piece_scale(a);
+  hi = piece_scale(b);
+}
+
+// Columns 16 ks .. of an accumulator as the left operand, in pieces.
+template <int N>
+__device__ __forceinline__ void as_left(const float (&x)[N][4], int ks, float s0, float s1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    split2(x[2 * ks + i][0] * s0, x[2 * ks + i][1] * s0, hi[2 * i], lo[2 * i]);
+    split2(x[2 * ks + i][2] * s1, x[2 * ks + i][3] * s1, hi[2 * i + 1], lo[2 * i + 1]);
+  }
+}
+
+template <typename T, int DK, int WARPS> struct Shape {
+  static constexpr int NI = pieces<T>();
+  static constexpr int STAGES = NI == 1 ? 2 : 1;
+  static constexpr uint32_t TILE = C * DK * 2;
+  static constexpr uint32_t S_K = 0, S_Q = NI * TILE, S_NUM = 2 * NI * TILE, S_A = S_NUM + NUM_BYTES,
+                            S_P = S_A + 2 * MAT_BYTES, S_V = S_P + NI * MAT_BYTES;
+  static constexpr uint32_t V_STRIP = C * 16 * sizeof(T);
+  static constexpr uint32_t STAGE = (S_V + WARPS * V_STRIP + 127) / 128 * 128;
+  static constexpr uint32_t S_OUT = STAGES * STAGE;  // a strip a warp, bf16 only
+  static constexpr uint32_t BYTES = S_OUT + (NI == 1 ? WARPS * V_STRIP : 0);
+};
+
+template <typename T, int DK, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1)
+gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, size_t ap_stride, ChainOut io) {
+  using Sh = Shape<T, DK, WARPS>;
+  constexpr int NI = Sh::NI, U = DK / 8, NK = DK / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = (lane & 3) * 2;
+  const int slices = p.dv / (16 * WARPS);
+  const int slice = blockIdx.x % slices;
+  const int h = (int)(blockIdx.x / slices % p.H);
+  const int n = (int)(blockIdx.x / slices / p.H);
+  const int hk = h / (p.H / p.Hk);
+  const int v0 = (slice * WARPS + warp) * 16;  // this warp's first value channel
+  int64_t t0, t1;
+  seq_range(p.s, n, t0, t1);
+  const int64_t c0 = seq_first_chunk(p.s, n);
+  // offsets that overlap (a broken cu_seqlens) could ask for more chunks than there are
+  const int nc = (int)max((int64_t)0, min((t1 - t0 + C - 1) / C, p.nchunks - c0));
+  const int64_t batch = p.s.bounds ? 0 : n, tok = p.s.bounds ? t0 : 0;
+  const int64_t v_off = batch * p.v.b + tok * p.v.t + h * p.v.h + v0;
+  const T *v = static_cast<const T *>(p.val) + v_off;
+  T *out = static_cast<T *>(io.out) + v_off;
+
+  // S^T: channel of k along the columns.  (row, column) of a state in memory
+  const int64_t s_off = ((int64_t)n * p.H + h) * DK * p.dv;
+  const int64_t sk = p.v_first ? 1 : p.dv, sv = p.v_first ? DK : 1;
+  float S[NK][4];
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      S[i][e] = io.initial ? io.initial[s_off + (8 * i + t + (e & 1)) * sk + (v0 + g + (e >> 1) * 8) * sv] : 0.f;
+
+  const uint32_t base = smem_addr(smem);
+  auto load = [&](int c, uint32_t stage) {
+    const char *a = kq + ((size_t)(c0 + c) * p.Hk + hk) * kq_stride, *b = ap + ((size_t)(c0 + c) * p.H + h) * ap_stride;
+    for (uint32_t x = tid * 16; x < Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_K + x, a + x);
+    for (uint32_t x = tid * 16; x < Sh::S_V - Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_NUM + x, b + x);
+    constexpr int PER = 16 * sizeof(T) / 16;  // 16-byte units of a row of the strip
+    const uint32_t strip = stage + Sh::S_V + warp * Sh::V_STRIP;
+#pragma unroll
+    for (int x = lane; x < C * PER; x += 32) {
+      const int64_t r = (int64_t)c * C + x / PER;
+      const bool in = r < t1 - t0;
+      cp16z(strip + x * 16, v + (in ? r * p.v.t : 0) + x % PER * (16 / sizeof(T)), in);
+    }
+    cp_commit();
+  };
+
+  const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;  // right operand, rows are its columns
+  const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;  // right operand, transposed on the way
+  if (Sh::STAGES == 2 && nc > 0) load(0, base);
+  for (int c = 0; c < nc; ++c) {
+    const uint32_t st = base + (Sh::STAGES == 2 ? (c & 1) * Sh::STAGE : 0);
+    if (Sh::STAGES == 1) {
+      load(c, st);
+      cp_wait<0>();
+    } else if (c + 1 < nc) {
+      load(c + 1, base + ((c + 1) & 1) * Sh::STAGE);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncthreads();
+    const float *num = reinterpret_cast<const float *>(smem + (st - base) + Sh::S_NUM);
+
+    // ---- S^T k^T and S^T q^T
+    float2 z0, z1;
+    row_scales(S, z0, z1);
+    float Y[8][4], O[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Y[i][e] = O[i][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      uint32_t ah[4], al[4];
+      as_left(S, ks, z0.x, z1.x, ah, al);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t at = unit_at<U>(16 * q + rb, 2 * ks + ub);
+        uint32_t b[4];
+        ldsm4(b, st + Sh::S_K + at);
+        mma16(Y[2 * q], al, b[0], b[1]);
+        mma16(Y[2 * q + 1], al, b[2], b[3]);
+        mma16(Y[2 * q], ah, b[0], b[1]);
+        mma16(Y[2 * q + 1], ah, b[2], b[3]);
+        if constexpr (NI == 2) {
+          ldsm4(b, st + Sh::S_K + Sh::TILE + at);
+          mma16(Y[2 * q], ah, b[0], b[1]);
+          mma16(Y[2 * q + 1], ah, b[2], b[3]);
+        }
+        ldsm4(b, st + Sh::S_Q + at);
+        mma16(O[2 * q], ah, b[0], b[1]);
+        mma16(O[2 * q + 1], ah, b[2], b[3]);
+        if constexpr (NI == 2) {
+          mma16(O[2 * q], al, b[0], b[1]);
+          mma16(O[2 * q + 1], al, b[2], b[3]);
+          ldsm4(b, st + Sh::S_Q + Sh::TILE + at);
+          mma16(O[2 * q], ah, b[0], b[1]);
+          mma16(O[2 * q + 1], ah, b[2], b[3]);
+        }
+      }
+    }
+
+    // ---- Y = beta (v - e^G k S); the part of o that the state gives
+    const unsigned char *strip = smem + (st - base) + Sh::S_V + warp * Sh::V_STRIP;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float x[2][4];
+      if constexpr (NI == 1) {
+        uint32_t r[4];
+        ldsm4t(r, smem_addr(strip) + (16 * q + ((lane >> 4) << 3) + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i >> 1][2 * (i & 1)] = __uint_as_float(r[i] << 16);
+          x[i >> 1][2 * (i & 1) + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        }
+      } else {
+        const float *f = reinterpret_cast<const float *>(strip);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = f[(16 * q + 8 * i + t + (e & 1)) * 16 + g + (e >> 1) * 8];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int nt = 2 * q + i, j = 8 * nt + t;
+        const float2 be = *reinterpret_cast<const float2 *>(num + NUM_BETA + j), ek = *reinterpret_cast<const float2 *>(num + NUM_EK + j),
+                     eq = *reinterpret_cast<const float2 *>(num + NUM_EQ + j);
+        Y[nt][0] = be.x * (x[i][0] - Y[nt][0] * ek.x * z0.y);
+        Y[nt][1] = be.y * (x[i][1] - Y[nt][1] * ek.y * z0.y);
+        Y[nt][2] = be.x * (x[i][2] - Y[nt][2] * ek.x * z1.y);
+        Y[nt][3] = be.y * (x[i][3] - Y[nt][3] * ek.y * z1.y);
+        // factor by factor: the factors' product may be too small for fp32 where the result is not
+        O[nt][0] = O[nt][0] * eq.x * z0.y;
+        O[nt][1] = O[nt][1] * eq.y * z0.y;
+        O[nt][2] = O[nt][2] * eq.x * z1.y;
+        O[nt][3] = O[nt][3] * eq.y * z1.y;
+      }
+    }
+
+    // ---- W^T = Y^T A^T
+    float W[8][4];
+    row_scales(Y, z0, z1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) W[i][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint32_t ah[4], al[4];
+      as_left(Y, ks, z0.x, z1.x, ah, al);
+#pragma unroll
+      for (int q = ks; q < 4; ++q) {
+        const uint32_t at = unit_at<8>(16 * q + rb, 2 * ks + ub);
+        uint32_t b[4];
+        ldsm4(b, st + Sh::S_A + MAT_BYTES + at);
+        mma16(W[2 * q], ah, b[0], b[1]);
+        mma16(W[2 * q + 1], ah, b[2], b[3]);
+        ldsm4(b, st + Sh::S_A + at);
+        mma16(W[2 * q], al, b[0], b[1]);
+        mma16(W[2 * q + 1], al, b[2], b[3]);
+        mma16(W[2 * q], ah, b[0], b[1]);
+        mma16(W[2 * q + 1], ah, b[2], b[3]);
+      }
+    }
+    {
+      const float a = num[NUM_MISC + 1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        W[i][0] = W[i][0] * a * z0.y;
+        W[i][1] = W[i][1] * a * z0.y;
+        W[i][2] = W[i][2] * a * z1.y;
+        W[i][3] = W[i][3] * a * z1.y;
+      }
+    }
+
+    // ---- o += P W
+    row_scales(W, z0, z1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Y[i][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint32_t ah[4], al[4];
+      as_left(W, ks, z0.x, z1.x, ah, al);
+#pragma unroll
+      for (int q = ks; q < 4; ++q) {
+        const uint32_t at = unit_at<8>(16 * q + rb, 2 * ks + ub);
+        uint32_t b[4];
+        ldsm4(b, st + Sh::S_P + at);
+        mma16(Y[2 * q], ah, b[0], b[1]);
+        mma16(Y[2 * q + 1], ah, b[2], b[3]);
+        if constexpr (NI == 2) {
+          mma16(Y[2 * q], al, b[0], b[1]);
+          mma16(Y[2 * q + 1], al, b[2], b[3]);
+          ldsm4(b, st + Sh::S_P + MAT_BYTES + at);
+          mma16(Y[2 * q], ah, b[0], b[1]);
+          mma16(Y[2 * q + 1], ah, b[2], b[3]);
+        }
+      }
+    }
+    const int64_t r0 = (int64_t)c * C;
+    const int len = (int)(t1 - t0 - r0 < C ? t1 - t0 - r0 : C);
+    {
+      const float a = num[NUM_MISC + 2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        O[i][0] += Y[i][0] * a * z0.y;
+        O[i][1] += Y[i][1] * a * z0.y;
+        O[i][2] += Y[i][2] * a * z1.y;
+        O[i][3] += Y[i][3] * a * z1.y;
+      }
+    }
+    if constexpr (NI == 1) {
+      const uint32_t os = base + Sh::S_OUT + warp * Sh::V_STRIP;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(O[2 * q + (i >> 1)][2 * (i & 1)], O[2 * q + (i >> 1)][2 * (i & 1) + 1]);
+          r[i] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        stsm4t(os + (16 * q + ((lane >> 4) << 3) + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16, r[0], r[1], r[2], r[3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int x = lane; x < C * 2; x += 32)
+        if ((x >> 1) < len)
+          *reinterpret_cast<uint4 *>(out + (r0 + (x >> 1)) * p.v.t + (x & 1) * 8) =
+              *reinterpret_cast<const uint4 *>(smem + Sh::S_OUT + warp * Sh::V_STRIP + x * 16);
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 8 * i + t + (e & 1);
+          if (j < len) out[(r0 + j) * p.v.t + g + (e >> 1) * 8] = O[i][e];
+        }
+    }
+
+    // ---- S^T = e^{G_C} S^T + (e^{G_C - G} W)^T k
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 fk = *reinterpret_cast<const float2 *>(num + NUM_FK + 8 * i + t);
+      W[i][0] *= fk.x;
+      W[i][1] *= fk.y;
+      W[i][2] *= fk.x;
+      W[i][3] *= fk.y;
+    }
+    row_scales(W, z0, z1);
+    uint32_t wh[4][4], wl[4][4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) as_left(W, ks, z0.x, z1.x, wh[ks], wl[ks]);
+    const float ec = num[NUM_MISC];
+#pragma unroll
+    for (int q = 0; q < NK / 2; ++q) {
+      float acc[2][4] = {};
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t at = unit_at<U>(16 * ks + rt, 2 * q + ut);
+        uint32_t b[4];
+        ldsm4t(b, st + Sh::S_K + at);
+        mma16(acc[0], wl[ks], b[0], b[1]);
+        mma16(acc[1], wl[ks], b[2], b[3]);
+        mma16(acc[0], wh[ks], b[0], b[1]);
+        mma16(acc[1], wh[ks], b[2], b[3]);
+        if constexpr (NI == 2) {
+          ldsm4t(b, st + Sh::S_K + Sh::TILE + at);
+          mma16(acc[0], wh[ks], b[0], b[1]);
+          mma16(acc[1], wh[ks], b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        S[2 * q + i][0] = ec * S[2 * q + i][0] + acc[i][0] * z0.y;
+        S[2 * q + i][1] = ec * S[2 * q + i][1] + acc[i][1] * z0.y;
+        S[2 * q + i][2] = ec * S[2 * q + i][2] + acc[i][2] * z1.y;
+        S[2 * q + i][3] = ec * S[2 * q + i][3] + acc[i][3] * z1.y;
+      }
+    }
+    __syncthreads();  // the buffer may be refilled
+  }
+
+  if (io.final_state) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        io.final_state[s_off + (8 * i + t + (e & 1)) * sk + (v0 + g + (e >> 1) * 8) * sv] = S[i][e];
+  }
+}
+
+template <typename T, int DK, int WARPS>
+cudaError_t go(const Problem &p, const char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
+  auto kernel = gdn_chain_kernel<T, DK, WARPS>;
+  constexpr int smem = Shape<T, DK, WARPS>::BYTES;
+  const kda_dtype dt = sizeof(T) == 2 ? KDA_BF16 : KDA_F32;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = (int64_t)p.s.N * p.H * (p.dv / (16 * WARPS));
+  kernel<<<(unsigned)grid, WARPS * 32, smem, st>>>(p, ws + pl.off_kq, ws + pl.off_ap, kq_bytes(dt, p.dk), ap_bytes(dt, false), io);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_chain(kda_dtype dt, const Problem &p, const char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
+  const bool w = p.dk == 128;
+#define GDN_GO(T) \
+  if (p.dv == 128) return w ? go<T, 128, 8>(p, ws, pl, io, st) : go<T, 64, 8>(p, ws, pl, io, st); \
+  return w ? go<T, 128, 4>(p, ws, pl, io, st) : go<T, 64, 4>(p, ws, pl, io, st)
+  if (dt == KDA_BF16) { GDN_GO(__nv_bfloat16); }
+  GDN_GO(float);
+#undef GDN_GO
+}
+
+}  // namespace gdn
+}  // namespace kda

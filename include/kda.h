@@ -8,8 +8,9 @@
  * in chunks of 64 tokens, together with the segment affine summary (M, S~)
  * of a token range, the ordered prefix scan S <- M_j S + S~_j that composes
  * summaries, and the gather/scatter of per-request states between a cache
- * pool and packed rows; and, around such a layer, the 8-bit projection path
- * (RMS norm, quantiser, matrix product).
+ * pool and packed rows; the same delta rule with one gate per head; and,
+ * around such a layer, the 8-bit projection path (RMS norm, quantiser, matrix
+ * product).
  *
  * Conventions shared by every call
  *  - All tensor pointers are DEVICE pointers unless a comment says "host".
@@ -476,6 +477,38 @@ kda_status kda_segment_bwd_summary(const kda_fwd_args *args, const void *d_out,
 kda_status kda_state_grad_scan(const float *M, const float *E, const float *dS_final,
                                int32_t num_chains, int32_t num_segments, int32_t H, int32_t dk,
                                int32_t dv, float *dS_out, float *dS_initial, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The gated delta rule with one gate per head,
+ *     S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,
+ *     o_t = scale * S_t^T q_t,
+ * for models whose decay is one number per token and value head.  It equals
+ * KDA with g repeated over the key channels, and takes the argument
+ * structures of the KDA calls, read as there except for the gate:
+ *   g       [.., H] fp32 (head-major: [B, H, T]), no channel axis
+ *   dt_bias [H] fp32 or NULL;  a_log [H] as before:
+ *           with KDA_GATE_IN_KERNEL  g = -exp(a_log[h]) softplus(x + dt_bias[h])
+ * Arithmetic: q, k, v (and d_out) of either type enter the products exactly
+ * (fp32 ones to 2^-23 of a row's largest) and everything derived from them, the
+ * state above all, keeps at least 22 bits, so fp32 results are good to a few
+ * 1e-7 of their size whatever the inputs' type, under any decay.  Results of
+ * the inputs' type are rounded once (bf16: from values good to 2^-12).
+ * Every sum runs in a fixed order: results do not change from call to call.
+ * ------------------------------------------------------------------------ */
+size_t kda_gdn_chunk_fwd_workspace_size(const kda_fwd_args *args);
+
+/* The chunked forward: out, and final_state when given.  Fields, layouts
+ * (packed sequences, grouped key heads, KDA_LAYOUT_HEAD_MAJOR,
+ * KDA_STATE_V_FIRST: no copies are made for either), limits and errors as
+ * kda_chunk_fwd; KDA_USE_EXP2 changes nothing.  KDA_ERR_UNSUPPORTED also for
+ * h_out, v_new_out and KDA_REUSE_PREP, and where (B T / 64 + sequences) * H
+ * exceeds 2^31 - 1; KDA_ERR_INVALID_ARG for KDA_TEST_WAIT_TIMEOUT (the kernels
+ * wait for nothing).  final_state may be initial_state in place. */
+kda_status kda_gdn_chunk_fwd(const kda_fwd_args *args, kda_stream_t stream);
+
+/* The recurrent step on pool states, in fp32, as kda_recurrent_step (any
+ * pool alignment; KDA_STATE_V_FIRST pools are [H, dv, dk]). */
+kda_status kda_gdn_recurrent_step(const kda_decode_args *args, kda_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The 8-bit projection path around a KDA layer: RMS norm with the residual's
