@@ -167,6 +167,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kda_recurrent_step": ([ctypes.POINTER(kda_decode_args), vp], ctypes.c_int),
         "kda_gdn_chunk_fwd_workspace_size": ([P], ctypes.c_size_t),
         "kda_gdn_chunk_fwd": ([P, vp], ctypes.c_int),
+        "kda_gdn_chunk_bwd_workspace_size": ([ctypes.POINTER(kda_bwd_args)], ctypes.c_size_t),
+        "kda_gdn_chunk_bwd": ([ctypes.POINTER(kda_bwd_args), vp], ctypes.c_int),
         "kda_gdn_recurrent_step": ([ctypes.POINTER(kda_decode_args), vp], ctypes.c_int),
         "kda_chunk_fwd_stages": ([P, ctypes.POINTER(ctypes.c_char_p), i32], i32),
         "kda_chunk_fwd_profiled": ([P, vp, ctypes.POINTER(vp), i32], ctypes.c_int),
@@ -1235,6 +1237,53 @@ def kda_gdn_chunk_fwd(q, k, v, g, beta, *, scale=None, eps=1e-6, a_log=None, dt_
     if status:
         raise KdaError(status, "kda_gdn_chunk_fwd")
     return out, final_state
+
+
+def kda_gdn_chunk_bwd(q, k, v, g, beta, d_out, *, d_final_state=None, scale=None, eps=1e-6, a_log=None, dt_bias=None,
+                      initial_state=None, cu_seqlens=None, l2norm_qk=True, beta_sigmoid=False, gate_in_kernel=False,
+                      want_d_initial_state=None, workspace=None, stream=None, state_v_first=False, head_major=False,
+                      extra_flags=0):
+    """Backward of :func:`kda_gdn_chunk_fwd`: gradients of <d_out, out> +
+    <d_final_state, final_state> (either may be None) with respect to the
+    inputs as given.  Returns a dict of dq, dk, dv (q's dtype), dg, dbeta
+    ([.., H] fp32), da_log, ddt_bias ([H]; None without ``gate_in_kernel``)
+    and d_initial_state (by default where there is an initial state).  See
+    ``kda_gdn_chunk_bwd`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_gdn_chunk_bwd(q, k, v, g, beta, d_out, d_final_state=d_final_state, scale=scale, eps=eps,
+                                     a_log=a_log, dt_bias=dt_bias, initial_state=initial_state, cu_seqlens=cu_seqlens,
+                                     l2norm_qk=l2norm_qk, beta_sigmoid=beta_sigmoid, gate_in_kernel=gate_in_kernel,
+                                     want_d_initial_state=want_d_initial_state, workspace=workspace,
+                                     state_v_first=state_v_first, head_major=head_major, extra_flags=extra_flags)
+    lib = _ready()
+    dims = _gdn_problem(q, k, v, g, beta, a_log, dt_bias,
+                        (("initial_state", initial_state), ("d_final_state", d_final_state)), cu_seqlens, head_major,
+                        state_v_first, gate_in_kernel)
+    if d_out is not None and (d_out.shape != v.shape or d_out.dtype != v.dtype):
+        raise ValueError("d_out must have v's shape and dtype")
+    dev = _launch_device(q, k, v, g, beta, d_out, d_final_state, a_log, dt_bias, initial_state, cu_seqlens, workspace)
+    if want_d_initial_state is None:
+        want_d_initial_state = initial_state is not None
+    H = dims[1]
+    grads = {"d" + n: _alloc(tuple(t.shape), t.stride(), t.dtype)
+             for n, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta))}
+    for n in ("da_log", "ddt_bias"):
+        grads[n] = _alloc((H,), (1,), _F32) if gate_in_kernel else None
+    shape = _state_shape(dims[0], q, v, state_v_first, head_major)
+    grads["d_initial_state"] = (_alloc(shape, (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1), _F32)
+                                if want_d_initial_state else None)
+    b = kda_bwd_args(_gdn_args(q, k, v, g, beta, dims, scale, eps, a_log, dt_bias, initial_state, cu_seqlens, l2norm_qk,
+                               beta_sigmoid, gate_in_kernel, state_v_first, head_major, extra_flags, None, None),
+                     _ptr(d_out), _ptr(d_final_state), *[_ptr(grads[n]) for n in (
+                         "dq", "dk", "dv", "dg", "dbeta", "da_log", "ddt_bias", "d_initial_state")])
+    need = lib.kda_gdn_chunk_bwd_workspace_size(ctypes.byref(b))
+    ws = _alloc(((need + 3) // 4,), (1,), _F32) if workspace is None else _workspace(need, q.device, workspace)
+    b.workspace, b.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    status = lib.kda_gdn_chunk_bwd(ctypes.byref(b), _raw_stream(dev))
+    if status:
+        raise KdaError(status, "kda_gdn_chunk_bwd")
+    return grads
 
 
 def kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags=None, *, scale=None, eps=1e-6, a_log=None,

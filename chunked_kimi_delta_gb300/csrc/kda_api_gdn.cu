@@ -89,21 +89,57 @@ extern "C" {
 size_t kda_gdn_chunk_fwd_workspace_size(const kda_fwd_args *a) {
   if (check_fwd(a) != KDA_OK) return 0;
   const gdn::Problem p = problem(a);
-  return gdn::make_gdn_plan(a->qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, false).total;
+  return gdn::make_gdn_plan(a->qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, p.dv, false).total;
 }
 
 kda_status kda_gdn_chunk_fwd(const kda_fwd_args *a, kda_stream_t stream) {
   const kda_status s = check_fwd(a);
   if (s != KDA_OK) return s;
   gdn::Problem p = problem(a);
-  const gdn::Plan pl = gdn::make_gdn_plan(a->qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, false);
+  const gdn::Plan pl = gdn::make_gdn_plan(a->qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, p.dv, false);
   if (!a->workspace || a->workspace_bytes < pl.total) return KDA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return KDA_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(a->workspace);
   cudaError_t e = prepare(a, false, p, ws, pl, st);
   if (e == cudaSuccess)
-    e = gdn::launch_gdn_chain(a->qkv_dtype, p, ws, pl, gdn::ChainOut{a->out, a->initial_state, a->final_state}, st);
+    e = gdn::launch_gdn_chain(a->qkv_dtype, false, p, ws, pl, gdn::ChainOut{a->out, a->initial_state, a->final_state}, st);
+  return cuda_status(e);
+}
+
+static kda_status check_bwd(const kda_bwd_args *b) {
+  if (!b) return KDA_ERR_INVALID_ARG;
+  const kda_status s = check(&b->fwd);
+  if (s != KDA_OK) return s;
+  if (tokens(&b->fwd) > 0 && (!b->dq || !b->dk || !b->dv || !b->dg || !b->dbeta)) return KDA_ERR_INVALID_ARG;
+  if (mis16(b->d_out) || mis16(b->d_final_state) || mis16(b->dq) || mis16(b->dk) || mis16(b->dv) || mis16(b->dg) ||
+      mis16(b->dbeta) || mis16(b->da_log) || mis16(b->ddt_bias) || mis16(b->d_initial_state))
+    return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
+size_t kda_gdn_chunk_bwd_workspace_size(const kda_bwd_args *b) {
+  if (check_bwd(b) != KDA_OK) return 0;
+  const gdn::Problem p = problem(&b->fwd);
+  return gdn::make_gdn_plan(b->fwd.qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, p.dv, true).total;
+}
+
+kda_status kda_gdn_chunk_bwd(const kda_bwd_args *b, kda_stream_t stream) {
+  const kda_status s = check_bwd(b);
+  if (s != KDA_OK) return s;
+  const kda_fwd_args *a = &b->fwd;
+  gdn::Problem p = problem(a);
+  const gdn::Plan pl = gdn::make_gdn_plan(a->qkv_dtype, p.nchunks, p.s.N, p.H, p.Hk, p.dk, p.dv, true);
+  if (!b->workspace || b->workspace_bytes < pl.total) return KDA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(b->workspace) & 255u) return KDA_ERR_ALIGNMENT;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char *ws = static_cast<char *>(b->workspace);
+  cudaError_t e = prepare(a, true, p, ws, pl, st);
+  if (e == cudaSuccess) e = gdn::launch_gdn_chain(a->qkv_dtype, true, p, ws, pl, gdn::ChainOut{nullptr, a->initial_state, nullptr}, st);
+  if (e == cudaSuccess)
+    e = gdn::launch_gdn_bwd(a->qkv_dtype, p, ws, pl,
+                            gdn::GradOut{b->d_out, b->d_final_state, b->dq, b->dk, b->dv, b->dg, b->dbeta, b->da_log,
+                                         b->ddt_bias, b->d_initial_state}, st);
   return cuda_status(e);
 }
 

@@ -65,9 +65,12 @@ __device__ __forceinline__ bool chunk_at(const SeqInfo &s, int64_t c, int &n, in
 // eight rows' units of one column lie in different banks).
 // Per (chunk, value head): numbers per token, then the pieces of A, then of P
 // ([64, 64] tiles; blocks of 16 above the diagonal are not written).
+// Numbers: beta; e^G, e^{G_C - G} with the norms' factors (and the scale, for q)
+// in them; those factors alone, times what a unit of the pieces stands for (no
+// scale) and by themselves; G in two floats.  misc: 0 e^{G_C}, 1 what a unit of
+// A's pieces stands for, 2 the same of P's.
 constexpr int NUM_MISC = 0, NUM_BETA = 16, NUM_EK = 80, NUM_EQ = 144, NUM_FK = 208, NUM_K = 272, NUM_Q = 336, NUM_GH = 400,
-              NUM_GL = 464, NUM_FLOATS = 528;
-// misc: 0 e^{G_C}, 1 what a unit of A's pieces stands for, 2 the same of P's
+              NUM_GL = 464, NUM_RK = 528, NUM_RQ = 592, NUM_FLOATS = 656;
 constexpr int NUM_BYTES = NUM_FLOATS * 4;
 constexpr int MAT_BYTES = C * C * 2;
 
@@ -78,15 +81,34 @@ inline size_t kq_bytes(kda_dtype d, int dk) { return (size_t)2 * in_pieces(d) * 
 // P in two pieces where the backward reads it (its products lead to fp32 results)
 inline size_t ap_bytes(kda_dtype d, bool bwd) { return NUM_BYTES + (size_t)MAT_BYTES * (2 + (bwd ? 2 : in_pieces(d))); }
 
+// What the backward's kernels hand on, per (chunk, value head), in fp32 and in
+// the order in which a warp's lanes hold it ([16 value channels][8 columns]
+// tiles, four values a lane): the state entering the chunk and the gradient of
+// the one leaving it ([dv, dk]), W, e^G k S and dY ([dv, 64]); the largest of
+// each of S, dS, W, dY, dO in each warp's 16 channels; sums over the channels
+// for each token; the sums of a_log's and dt_bias's gradients.
 struct Plan {
-  size_t off_chunks, off_kq, off_ap, total;
+  size_t off_chunks, off_kq, off_ap, off_s, off_ds, off_w, off_e, off_dy, off_max, off_dots, off_part, total;
 };
-inline Plan make_gdn_plan(kda_dtype d, int64_t nchunks, int N, int H, int Hk, int dk, bool bwd) {
+constexpr int MAX_S = 0, MAX_DS = 8, MAX_W = 16, MAX_DY = 24, MAX_DO = 32, MAX_FLOATS = 64;
+constexpr int DOT_BETA = 0, DOT_K = 64, DOT_Y = 128, DOT_FLOATS = 192;
+inline Plan make_gdn_plan(kda_dtype d, int64_t nchunks, int N, int H, int Hk, int dk, int dv, bool bwd) {
   Plan p{};
   size_t o = 256;
   p.off_chunks = o; o = align256(o + sizeof(int32_t) * ((size_t)N + 1));
   p.off_kq = o; o = align256(o + (size_t)nchunks * Hk * kq_bytes(d, dk));
   p.off_ap = o; o = align256(o + (size_t)nchunks * H * ap_bytes(d, bwd));
+  if (bwd) {
+    const size_t u = (size_t)nchunks * H;
+    p.off_s = o; o = align256(o + u * dk * dv * 4);
+    p.off_ds = o; o = align256(o + u * dk * dv * 4);
+    p.off_w = o; o = align256(o + u * C * dv * 4);
+    p.off_e = o; o = align256(o + u * C * dv * 4);
+    p.off_dy = o; o = align256(o + u * C * dv * 4);
+    p.off_max = o; o = align256(o + u * MAX_FLOATS * 4);
+    p.off_dots = o; o = align256(o + u * DOT_FLOATS * 4);
+    p.off_part = o; o = align256(o + u * 2 * 4);
+  }
   p.total = o;
   return p;
 }
@@ -144,6 +166,62 @@ __device__ __forceinline__ float2 piece_scale(float m) {
   sb = sb > 253 ? 253 : sb;
   return make_float2(__uint_as_float((uint32_t)sb << 23), __uint_as_float((uint32_t)(254 - sb) << 23));
 }
+// Largest of |c0|, |c1| (row lane / 4) and of |c2|, |c3| (row + 8) over a row's
+// four lanes, as scales.
+template <int N>
+__device__ __forceinline__ void row_scales(const float (&x)[N][4], float2 &lo, float2 &hi) {
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a = fmaxf(a, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
+    b = fmaxf(b, fmaxf(fabsf(x[i][2]), fabsf(x[i][3])));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+    b = fmaxf(b, __shfl_xor_sync(~0u, b, o));
+  }
+  lo = piece_scale(a);
+  hi = piece_scale(b);
+}
+
+// Largest |x| of a warp's accumulators.
+template <int N>
+__device__ __forceinline__ float warp_max(const float (&x)[N][4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, fmaxf(fmaxf(fabsf(x[i][0]), fabsf(x[i][1])), fmaxf(fabsf(x[i][2]), fabsf(x[i][3]))));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  return m;
+}
+
+// Columns 16 ks .. of an accumulator as the left operand, in pieces.
+template <int N>
+__device__ __forceinline__ void as_left(const float (&x)[N][4], int ks, float s0, float s1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    split2(x[2 * ks + i][0] * s0, x[2 * ks + i][1] * s0, hi[2 * i], lo[2 * i]);
+    split2(x[2 * ks + i][2] * s1, x[2 * ks + i][3] * s1, hi[2 * i + 1], lo[2 * i + 1]);
+  }
+}
+
+// 8 values of a row as fp32
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
 // Log-decay of one token and head from what the caller gave.  From -256 on
 // (e^-256 is zero in fp32) it is held there: -inf, a decay to nothing, would
 // make NaN of the differences of running sums.
@@ -158,12 +236,22 @@ __device__ __forceinline__ float log_decay(float x, const GateParams &gp, float 
 // ---------------------------------------------------------------- launchers
 cudaError_t launch_gdn_prep(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, cudaStream_t st);
 
+// The forward's chain writes out and final_state; the backward's first one (out
+// null) S, W, e^G k S and their largest values instead.
 struct ChainOut {
   void *out;
   const float *initial;
   float *final_state;
 };
-cudaError_t launch_gdn_chain(kda_dtype dt, const Problem &p, const char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st);
+cudaError_t launch_gdn_chain(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st);
+
+struct GradOut {
+  const void *d_out;        // or null: zeros
+  const float *d_final;     // or null: zeros
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *da_log, *ddt_bias, *d_initial;
+};
+cudaError_t launch_gdn_bwd(kda_dtype dt, const Problem &p, char *ws, const Plan &pl, const GradOut &io, cudaStream_t st);
 
 cudaError_t launch_gdn_step(const kda_decode_args &a, cudaStream_t st);
 

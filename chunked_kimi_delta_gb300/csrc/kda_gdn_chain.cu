@@ -14,53 +14,25 @@ namespace kda {
 namespace gdn {
 namespace {
 
-// Largest of |c0|, |c1| (row lane / 4) and of |c2|, |c3| (row + 8) over a row's
-// four lanes, as scales.
-template <int N>
-__device__ __forceinline__ void row_scales(const float (&x)[N][4], float2 &lo, float2 &hi) {
-  float a = 0.f, b = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    a = fmaxf(a, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
-    b = fmaxf(b, fmaxf(fabsf(x[i][2]), fabsf(x[i][3])));
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
-    b = fmaxf(b, __shfl_xor_sync(~0u, b, o));
-  }
-  lo = piece_scale(a);
-  hi = piece_scale(b);
-}
-
-// Columns 16 ks .. of an accumulator as the left operand, in pieces.
-template <int N>
-__device__ __forceinline__ void as_left(const float (&x)[N][4], int ks, float s0, float s1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    split2(x[2 * ks + i][0] * s0, x[2 * ks + i][1] * s0, hi[2 * i], lo[2 * i]);
-    split2(x[2 * ks + i][2] * s1, x[2 * ks + i][3] * s1, hi[2 * i + 1], lo[2 * i + 1]);
-  }
-}
-
-template <typename T, int DK, int WARPS> struct Shape {
-  static constexpr int NI = pieces<T>();
+template <typename T, int DK, int WARPS, bool STORE> struct Shape {
+  static constexpr int NI = pieces<T>(), NP = STORE ? 2 : NI;
   static constexpr int STAGES = NI == 1 ? 2 : 1;
   static constexpr uint32_t TILE = C * DK * 2;
   static constexpr uint32_t S_K = 0, S_Q = NI * TILE, S_NUM = 2 * NI * TILE, S_A = S_NUM + NUM_BYTES,
-                            S_P = S_A + 2 * MAT_BYTES, S_V = S_P + NI * MAT_BYTES;
+                            S_P = S_A + 2 * MAT_BYTES, S_V = S_P + NP * MAT_BYTES;
   static constexpr uint32_t V_STRIP = C * 16 * sizeof(T);
   static constexpr uint32_t STAGE = (S_V + WARPS * V_STRIP + 127) / 128 * 128;
   static constexpr uint32_t S_OUT = STAGES * STAGE;  // a strip a warp, bf16 only
-  static constexpr uint32_t BYTES = S_OUT + (NI == 1 ? WARPS * V_STRIP : 0);
+  static constexpr uint32_t BYTES = S_OUT + (NI == 1 && !STORE ? WARPS * V_STRIP : 0);
 };
 
-template <typename T, int DK, int WARPS>
+template <typename T, int DK, int WARPS, bool STORE>
 __global__ void __launch_bounds__(WARPS * 32, 1)
-gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, size_t ap_stride, ChainOut io) {
-  using Sh = Shape<T, DK, WARPS>;
+gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_stride, ChainOut io) {
+  using Sh = Shape<T, DK, WARPS, STORE>;
   constexpr int NI = Sh::NI, U = DK / 8, NK = DK / 8;
   extern __shared__ __align__(128) unsigned char smem[];
+  const char *kq = ws + pl.off_kq, *ap = ws + pl.off_ap;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = (lane & 3) * 2;
   const int slices = p.dv / (16 * WARPS);
@@ -77,7 +49,7 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
   const int64_t batch = p.s.bounds ? 0 : n, tok = p.s.bounds ? t0 : 0;
   const int64_t v_off = batch * p.v.b + tok * p.v.t + h * p.v.h + v0;
   const T *v = static_cast<const T *>(p.val) + v_off;
-  T *out = static_cast<T *>(io.out) + v_off;
+  T *out = STORE ? nullptr : static_cast<T *>(io.out) + v_off;
 
   // S^T: channel of k along the columns.  (row, column) of a state in memory
   const int64_t s_off = ((int64_t)n * p.H + h) * DK * p.dv;
@@ -92,8 +64,8 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
   const uint32_t base = smem_addr(smem);
   auto load = [&](int c, uint32_t stage) {
     const char *a = kq + ((size_t)(c0 + c) * p.Hk + hk) * kq_stride, *b = ap + ((size_t)(c0 + c) * p.H + h) * ap_stride;
-    for (uint32_t x = tid * 16; x < Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_K + x, a + x);
-    for (uint32_t x = tid * 16; x < Sh::S_V - Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_NUM + x, b + x);
+    for (uint32_t x = tid * 16; x < (STORE ? Sh::S_Q : Sh::S_NUM); x += WARPS * 512) cp16(stage + Sh::S_K + x, a + x);
+    for (uint32_t x = tid * 16; x < (STORE ? Sh::S_P : Sh::S_V) - Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_NUM + x, b + x);
     constexpr int PER = 16 * sizeof(T) / 16;  // 16-byte units of a row of the strip
     const uint32_t strip = stage + Sh::S_V + warp * Sh::V_STRIP;
 #pragma unroll
@@ -125,6 +97,14 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
     // ---- S^T k^T and S^T q^T
     float2 z0, z1;
     row_scales(S, z0, z1);
+    const int64_t unit = (c0 + c) * p.H + h;  // of what the backward is handed
+    auto keep = [&](size_t off, const auto &x, int n, float top, int which) {
+      float4 *to = reinterpret_cast<float4 *>(ws + off) + (unit * (p.dv / 16) + warp) * n * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(x) / 16); ++i) to[i * 32] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+      if (which >= 0 && lane == 0) reinterpret_cast<float *>(ws + pl.off_max)[unit * MAX_FLOATS + which + warp] = top;
+    };
+    if constexpr (STORE) keep(pl.off_s, S, NK, warp_max(S), MAX_S);
     float Y[8][4], O[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -148,6 +128,7 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
           mma16(Y[2 * q], ah, b[0], b[1]);
           mma16(Y[2 * q + 1], ah, b[2], b[3]);
         }
+        if constexpr (STORE) continue;
         ldsm4(b, st + Sh::S_Q + at);
         mma16(O[2 * q], ah, b[0], b[1]);
         mma16(O[2 * q + 1], ah, b[2], b[3]);
@@ -186,10 +167,18 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
         const int nt = 2 * q + i, j = 8 * nt + t;
         const float2 be = *reinterpret_cast<const float2 *>(num + NUM_BETA + j), ek = *reinterpret_cast<const float2 *>(num + NUM_EK + j),
                      eq = *reinterpret_cast<const float2 *>(num + NUM_EQ + j);
-        Y[nt][0] = be.x * (x[i][0] - Y[nt][0] * ek.x * z0.y);
-        Y[nt][1] = be.y * (x[i][1] - Y[nt][1] * ek.y * z0.y);
-        Y[nt][2] = be.x * (x[i][2] - Y[nt][2] * ek.x * z1.y);
-        Y[nt][3] = be.y * (x[i][3] - Y[nt][3] * ek.y * z1.y);
+        Y[nt][0] = Y[nt][0] * ek.x * z0.y;
+        Y[nt][1] = Y[nt][1] * ek.y * z0.y;
+        Y[nt][2] = Y[nt][2] * ek.x * z1.y;
+        Y[nt][3] = Y[nt][3] * ek.y * z1.y;
+        if constexpr (STORE)
+          reinterpret_cast<float4 *>(ws + pl.off_e)[((unit * (p.dv / 16) + warp) * 8 + nt) * 32 + lane] =
+              make_float4(Y[nt][0], Y[nt][1], Y[nt][2], Y[nt][3]);
+        Y[nt][0] = be.x * (x[i][0] - Y[nt][0]);
+        Y[nt][1] = be.y * (x[i][1] - Y[nt][1]);
+        Y[nt][2] = be.x * (x[i][2] - Y[nt][2]);
+        Y[nt][3] = be.y * (x[i][3] - Y[nt][3]);
+        if constexpr (STORE) continue;
         // factor by factor: the factors' product may be too small for fp32 where the result is not
         O[nt][0] = O[nt][0] * eq.x * z0.y;
         O[nt][1] = O[nt][1] * eq.y * z0.y;
@@ -234,6 +223,9 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
       }
     }
 
+    if constexpr (STORE) {
+      keep(pl.off_w, W, 8, warp_max(W), MAX_W);
+    } else {
     // ---- o += P W
     row_scales(W, z0, z1);
 #pragma unroll
@@ -300,6 +292,7 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
           if (j < len) out[(r0 + j) * p.v.t + g + (e >> 1) * 8] = O[i][e];
         }
     }
+    }
 
     // ---- S^T = e^{G_C} S^T + (e^{G_C - G} W)^T k
 #pragma unroll
@@ -353,28 +346,31 @@ gdn_chain_kernel(Problem p, const char *kq, const char *ap, size_t kq_stride, si
   }
 }
 
-template <typename T, int DK, int WARPS>
-cudaError_t go(const Problem &p, const char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
-  auto kernel = gdn_chain_kernel<T, DK, WARPS>;
-  constexpr int smem = Shape<T, DK, WARPS>::BYTES;
+template <typename T, int DK, int WARPS, bool STORE>
+cudaError_t go(const Problem &p, char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
+  auto kernel = gdn_chain_kernel<T, DK, WARPS, STORE>;
+  constexpr int smem = Shape<T, DK, WARPS, STORE>::BYTES;
   const kda_dtype dt = sizeof(T) == 2 ? KDA_BF16 : KDA_F32;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)p.s.N * p.H * (p.dv / (16 * WARPS));
-  kernel<<<(unsigned)grid, WARPS * 32, smem, st>>>(p, ws + pl.off_kq, ws + pl.off_ap, kq_bytes(dt, p.dk), ap_bytes(dt, false), io);
+  kernel<<<(unsigned)grid, WARPS * 32, smem, st>>>(p, ws, pl, kq_bytes(dt, p.dk), ap_bytes(dt, STORE), io);
   return cudaGetLastError();
+}
+
+template <typename T, bool STORE>
+cudaError_t go_dims(const Problem &p, char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
+  const bool w = p.dk == 128;
+  if (p.dv == 128) return w ? go<T, 128, 8, STORE>(p, ws, pl, io, st) : go<T, 64, 8, STORE>(p, ws, pl, io, st);
+  return w ? go<T, 128, 4, STORE>(p, ws, pl, io, st) : go<T, 64, 4, STORE>(p, ws, pl, io, st);
 }
 
 }  // namespace
 
-cudaError_t launch_gdn_chain(kda_dtype dt, const Problem &p, const char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
-  const bool w = p.dk == 128;
-#define GDN_GO(T) \
-  if (p.dv == 128) return w ? go<T, 128, 8>(p, ws, pl, io, st) : go<T, 64, 8>(p, ws, pl, io, st); \
-  return w ? go<T, 128, 4>(p, ws, pl, io, st) : go<T, 64, 4>(p, ws, pl, io, st)
-  if (dt == KDA_BF16) { GDN_GO(__nv_bfloat16); }
-  GDN_GO(float);
-#undef GDN_GO
+cudaError_t launch_gdn_chain(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
+  if (dt == KDA_BF16)
+    return bwd ? go_dims<__nv_bfloat16, true>(p, ws, pl, io, st) : go_dims<__nv_bfloat16, false>(p, ws, pl, io, st);
+  return bwd ? go_dims<float, true>(p, ws, pl, io, st) : go_dims<float, false>(p, ws, pl, io, st);
 }
 
 }  // namespace gdn

@@ -19,22 +19,6 @@ namespace {
 constexpr int NT = 128;
 constexpr int LP = 68;  // floats a row of L
 
-// 8 values of a row as fp32
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
 // (hi, lo) + (h, l) with the rounding error of the sum kept
 __device__ __forceinline__ void add2(float &hi, float &lo, float h, float l) {
   const float s = hi + h, v = s - hi;
@@ -92,7 +76,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   constexpr uint32_t TILE = C * DK * 2;
   extern __shared__ __align__(128) unsigned char smem[];
   float *Ls = reinterpret_cast<float *>(smem + 2 * NI * TILE);
-  __shared__ float s_num[2][C], s_g[2][C], s_beta[C];  // 1 / norm (times the pieces' unit) of k and q; G; beta
+  __shared__ float s_num[2][C], s_r[2][C], s_g[2][C], s_beta[C];  // 1 / norm of k and q, with and without the pieces' unit; G; beta
   __shared__ int s_max[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -140,9 +124,9 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
         }
         if (u == 0) {
           // x / norm = (unit / norm) (x / unit); rows past the end are zero
-          float f = (p.gp.flags & KDA_L2NORM_QK) ? 1.f / sqrtf(ss + p.gp.eps) : 1.f;
-          if (which) f *= p.gp.scale;
+          const float f = (p.gp.flags & KDA_L2NORM_QK) ? 1.f / sqrtf(ss + p.gp.eps) : 1.f;
           s_num[which][r] = r < len ? f * sc.y : 0.f;
+          s_r[which][r] = f;
         }
       }
     }
@@ -228,12 +212,14 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
         s_beta[r] = b[i];
         num[NUM_BETA + r] = b[i];
         num[NUM_EK + r] = e * kn;
-        num[NUM_EQ + r] = e * qn;
+        num[NUM_EQ + r] = e * qn * p.gp.scale;
         num[NUM_FK + r] = f * kn;
         num[NUM_K + r] = kn;
         num[NUM_Q + r] = qn;
         num[NUM_GH + r] = Gh[i];
         num[NUM_GL + r] = Gl[i];
+        num[NUM_RK + r] = s_r[0][r];
+        num[NUM_RQ + r] = s_r[1][r];
       }
       if (lane == 0) num[NUM_MISC] = expf(Ch + Cl);
     }
@@ -251,7 +237,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
         float lv = 0.f, pv = 0.f;
         if (j <= i) {
           const float y = expf((s_g[0][i] - s_g[0][j]) + (s_g[1][i] - s_g[1][j])) * s_num[0][j];
-          pv = qk[nt][e] * s_num[1][i] * y;
+          pv = qk[nt][e] * s_num[1][i] * y * p.gp.scale;
           if (j < i) lv = kk[nt][e] * s_num[0][i] * y * s_beta[i];
         }
         P[nt][e] = pv;

@@ -506,6 +506,16 @@ size_t kda_gdn_chunk_fwd_workspace_size(const kda_fwd_args *args);
  * wait for nothing).  final_state may be initial_state in place. */
 kda_status kda_gdn_chunk_fwd(const kda_fwd_args *args, kda_stream_t stream);
 
+/* Its backward: the gradients of <d_out, out> + <d_final_state, final_state>
+ * with respect to the inputs as given; fields as kda_chunk_bwd, except that dg
+ * is [.., H] and ddt_bias [H], fp32.  The forward's intermediates are computed
+ * anew; the workspace holds the states entering and the state gradients
+ * leaving every chunk (fp32).  Where the decay is held at e^-256 (zero in
+ * fp32) the gate's gradient is that of a decay of zero.  Errors as the forward,
+ * and KDA_ERR_INVALID_ARG for null dq, dk, dv, dg or dbeta with tokens. */
+size_t kda_gdn_chunk_bwd_workspace_size(const kda_bwd_args *args);
+kda_status kda_gdn_chunk_bwd(const kda_bwd_args *args, kda_stream_t stream);
+
 /* The recurrent step on pool states, in fp32, as kda_recurrent_step (any
  * pool alignment; KDA_STATE_V_FIRST pools are [H, dv, dk]). */
 kda_status kda_gdn_recurrent_step(const kda_decode_args *args, kda_stream_t stream);

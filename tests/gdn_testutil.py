@@ -77,6 +77,11 @@ def off(got, ref):
 
 def check(got, ref, what, tol=None):
     e, tol = off(got, ref), TOL[got.dtype] if tol is None else tol
+    # below 2^-126 fp32 has no relative precision left (and below 2^-149 nothing but zero): each value may be
+    # off by that much, the 2-norm of n of them by sqrt(n) 2^-126
+    norm = np.linalg.norm(ref)
+    if norm > 0:
+        tol += np.sqrt(np.size(ref)) * 2.0 ** -126 / norm
     assert e <= tol, f"{what}: off by {e:.3g} of its norm, at most {tol:.3g} is wanted"
     return e
 
