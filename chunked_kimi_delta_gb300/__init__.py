@@ -35,6 +35,7 @@ KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGNMENT = 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_DEVICE_TIMEOUT = 4, 5, 6
 KDA_FP8_NT, KDA_FP8_NN, KDA_FP8_TN = 0, 1, 2
 KDA_FP8_MATMUL_WORKSPACE_BYTES = 256
+KDA_LORA_MAX_RANK = 128
 CHUNK = 64
 
 
@@ -135,6 +136,28 @@ class kda_fp8_matmul_args(ctypes.Structure):
     ]
 
 
+class kda_lora_args(ctypes.Structure):
+    """Mirror of ``kda_lora_args`` in include/kda.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32), ("rank", ctypes.c_int32),
+        ("adapters", ctypes.c_int32), ("dtype", ctypes.c_int), ("x", ctypes.c_void_p), ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("idx_dtype", ctypes.c_int), ("num_requests", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("y", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
+class kda_lora_bwd_args(ctypes.Structure):
+    """Mirror of ``kda_lora_bwd_args`` in include/kda.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32), ("rank", ctypes.c_int32),
+        ("adapters", ctypes.c_int32), ("dtype", ctypes.c_int), ("d_out", ctypes.c_void_p), ("x", ctypes.c_void_p),
+        ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("idx_dtype", ctypes.c_int),
+        ("num_requests", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("d_x_in", ctypes.c_void_p), ("d_x", ctypes.c_void_p), ("d_a", ctypes.c_void_p), ("d_b", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -182,6 +205,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kda_rms_norm_bwd": ([ctypes.POINTER(kda_rms_norm_bwd_args), vp], ctypes.c_int),
         "kda_fp8_quantize": ([ctypes.POINTER(kda_fp8_quantize_args), vp], ctypes.c_int),
         "kda_fp8_matmul": ([ctypes.POINTER(kda_fp8_matmul_args), vp], ctypes.c_int),
+        "kda_lora": ([ctypes.POINTER(kda_lora_args), vp], ctypes.c_int),
+        "kda_lora_bwd_workspace_size": ([ctypes.POINTER(kda_lora_bwd_args)], ctypes.c_size_t),
+        "kda_lora_bwd": ([ctypes.POINTER(kda_lora_bwd_args), vp], ctypes.c_int),
         "kda_fp8_matmul_shared_workspace": ([ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
     }
     for name, (argt, rest) in sigs.items():
@@ -1326,3 +1352,97 @@ def kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags=None, *, sca
     if status:
         raise KdaError(status, "kda_gdn_recurrent_step")
     return out
+
+
+# ------------------------------------------------ low-rank adapters of many requests
+
+def _lora_problem(x, a, b, idx, cu_seqlens, scale, wide):
+    """Checks the tensors both calls take (the kernels trust them); ``wide``:
+    (name, tensor or None, width) of the other [rows, width] tensors."""
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x is [rows, n_in], a [adapters, rank, n_in], b [adapters, n_out, rank]")
+    rows, n_in = x.shape
+    L, r, n_a = a.shape
+    if n_a != n_in or b.shape[0] != L or b.shape[2] != r:
+        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} do not go with x {tuple(x.shape)}")
+    code = _in_code(x.dtype)
+    if a.dtype is not x.dtype or b.dtype is not x.dtype:
+        raise TypeError("x, a and b must have one dtype")
+    n_out = b.shape[1]
+    for name, t, n in wide:
+        if t is not None and (tuple(t.shape) != (rows, n_in if n == "n_in" else n_out) or t.dtype is not x.dtype):
+            raise ValueError(f"{name} must be [rows, {n}] in x's dtype")
+    n_req = idx.numel()
+    if idx.dim() != 1:
+        raise ValueError("idx is [requests]")
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() != n_req + 1 or cu_seqlens.dtype != _torch_module.int32:
+            raise ValueError("cu_seqlens must be int32 [requests + 1]")
+    elif n_req == 0 and rows or n_req and rows % n_req:
+        raise ValueError(f"{rows} rows cannot be shared out among {n_req} requests: give cu_seqlens")
+    if scale is not None and (tuple(scale.shape) != (L,) or scale.dtype is not _F32):
+        raise ValueError("scale must be fp32 [adapters]")
+    return rows, n_in, n_out, r, L, code, _idx_code(idx), n_req
+
+
+def kda_lora(x, a, b, idx, y, *, cu_seqlens=None, scale=None, out=None, stream=None):
+    """Low-rank adapters of many requests beside a shared projection: for the
+    rows of request i and adapter ``l = idx[i]``
+    ``out = y + scale[l] * (x a[l]^T) b[l]^T``; rows of requests whose index
+    is no adapter's get y.  x [rows, n_in], a [adapters, rank, n_in],
+    b [adapters, n_out, rank], y [rows, n_out] (the projection's result, bf16
+    or fp32 as x); requests are packed rows given by ``cu_seqlens`` or have
+    rows / len(idx) rows each.  Returns out (``out=y`` works in place).  See
+    ``kda_lora`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_lora(x, a, b, idx, y, cu_seqlens=cu_seqlens, scale=scale, out=out)
+    lib = _ready()
+    rows, n_in, n_out, r, L, code, icode, n_req = _lora_problem(
+        x, a, b, idx, cu_seqlens, scale, (("y", y, "n_out"), ("out", out, "n_out")))
+    dev = _launch_device(x, a, b, idx, y, cu_seqlens, scale, out)
+    if out is None:
+        out = _alloc((rows, n_out), (n_out, 1), y.dtype)
+    p = kda_lora_args(rows, n_in, n_out, r, L, code, x.data_ptr(), a.data_ptr(), b.data_ptr(), idx.data_ptr(), icode, n_req,
+                      _ptr(cu_seqlens), _ptr(scale), y.data_ptr(), out.data_ptr())
+    status = lib.kda_lora(ctypes.byref(p), _raw_stream(dev))
+    if status:
+        raise KdaError(status, "kda_lora")
+    return out
+
+
+def kda_lora_bwd(d_out, x, a, b, idx, d_x=None, *, cu_seqlens=None, scale=None, want_dx=True, want_weights=True,
+                 dx=None, workspace=None, stream=None):
+    """Gradients of :func:`kda_lora`: ``(dx, da, db)`` with
+    ``dx = d_x + scale[l] (d_out b[l]) a[l]`` (``d_x``: the projection's own
+    gradient of x, None for zeros; ``dx=d_x`` works in place) in x's dtype and
+    da, db fp32 in the shapes of a and b, summed over each adapter's rows.
+    ``want_dx=False`` or ``want_weights=False`` leave their part out (None).
+    See ``kda_lora_bwd`` in include/kda.h."""
+    if stream is not None:
+        with _under(stream):
+            return kda_lora_bwd(d_out, x, a, b, idx, d_x, cu_seqlens=cu_seqlens, scale=scale, want_dx=want_dx,
+                                want_weights=want_weights, dx=dx, workspace=workspace)
+    lib = _ready()
+    if not want_dx and not want_weights:
+        raise ValueError("no gradient is wanted")
+    rows, n_in, n_out, r, L, code, icode, n_req = _lora_problem(
+        x, a, b, idx, cu_seqlens, scale,
+        (("d_out", d_out, "n_out"), ("d_x", d_x, "n_in"), ("dx", dx, "n_in")))
+    dev = _launch_device(x, d_out, a, b, idx, d_x, dx, cu_seqlens, scale, workspace)
+    if want_dx and dx is None:
+        dx = _alloc((rows, n_in), (n_in, 1), x.dtype)
+    if not want_dx:
+        dx = None
+    da = db = None
+    if want_weights:
+        da, db = _alloc((L, r, n_in), (r * n_in, n_in, 1), _F32), _alloc((L, n_out, r), (n_out * r, r, 1), _F32)
+    p = kda_lora_bwd_args(rows, n_in, n_out, r, L, code, d_out.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(),
+                          idx.data_ptr(), icode, n_req, _ptr(cu_seqlens), _ptr(scale), _ptr(d_x), _ptr(dx), _ptr(da), _ptr(db))
+    need = lib.kda_lora_bwd_workspace_size(ctypes.byref(p))
+    ws = _alloc(((need + 3) // 4,), (1,), _F32) if workspace is None else _workspace(need, x.device, workspace)
+    p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    status = lib.kda_lora_bwd(ctypes.byref(p), _raw_stream(dev))
+    if status:
+        raise KdaError(status, "kda_lora_bwd")
+    return dx, da, db

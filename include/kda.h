@@ -678,6 +678,74 @@ kda_status kda_fp8_matmul(const kda_fp8_matmul_args *args, kda_stream_t stream);
  * stream capture.  Errors: KDA_ERR_INVALID_ARG (null), KDA_ERR_CUDA. */
 kda_status kda_fp8_matmul_shared_workspace(void **workspace);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.
+ *
+ * The rows of request i take adapter l = idx[i] (with 0 <= l < adapters; any
+ * other index: none).  For each of them
+ *   out = y + scale[l] * (x A[l]^T) B[l]^T
+ * with y the projection's result, A [adapters, rank, n_in] and
+ * B [adapters, n_out, rank] in the type of x; rows without an adapter get y.
+ * Requests are packed rows [cu_seqlens[i], cu_seqlens[i+1]) (rows behind the
+ * last request have no adapter), or, without cu_seqlens, rows / num_requests
+ * rows each (a decode batch: one).  The sum is held in fp32 and rounded once;
+ * u = x A^T keeps 16 bits for bf16 results, 24 for fp32 ones.  out may be y.
+ * Any n_in, n_out and rank up to KDA_LORA_MAX_RANK; widths that are multiples
+ * of 8 (then of 4) elements are read fastest.  Deterministic.
+ * Errors: KDA_ERR_INVALID_ARG (sizes below 1, rows < 0, null pointers, rows
+ * not a multiple of num_requests without cu_seqlens), KDA_ERR_UNSUPPORTED
+ * (rank above KDA_LORA_MAX_RANK, more than 65,535 adapters, more than 2^31 - 1
+ * rows or 2^28 - 1 tiles of them), KDA_ERR_ALIGNMENT, KDA_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+#define KDA_LORA_MAX_RANK 128
+
+typedef struct {
+  int64_t rows;
+  int32_t n_in, n_out, rank, adapters;
+  kda_dtype dtype;          /* of x, a, b, y and out                           */
+  const void *x;            /* [rows, n_in]                                    */
+  const void *a, *b;        /* [adapters, rank, n_in], [adapters, n_out, rank] */
+  const void *idx;          /* [num_requests] adapter of each request          */
+  kda_index_dtype idx_dtype;
+  int32_t num_requests;
+  const int32_t *cu_seqlens; /* [num_requests + 1] or NULL                     */
+  const float *scale;       /* [adapters] or NULL (= ones)                     */
+  const void *y;            /* [rows, n_out]                                   */
+  void *out;                /* [rows, n_out], may be y                         */
+} kda_lora_args;
+
+kda_status kda_lora(const kda_lora_args *args, kda_stream_t stream);
+
+/*
+ * Its gradients.  d_x = d_x_in + scale[l] (d_out B[l]) A[l] (d_x_in: the
+ * projection's own gradient of x; NULL: zeros; d_x may be d_x_in), and in fp32
+ *   d_a[l] = sum over l's rows of scale[l] (d_out B[l])^T x     [adapters, rank, n_in]
+ *   d_b[l] = sum over l's rows of scale[l] d_out^T (x A[l]^T)   [adapters, n_out, rank]
+ * (zeros for adapters without rows).  Any of d_x, d_a, d_b may be NULL, not all.
+ * Sums run in a fixed order.  Errors as kda_lora, plus KDA_ERR_WORKSPACE.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t n_in, n_out, rank, adapters;
+  kda_dtype dtype;          /* of d_out, x, a, b, d_x_in and d_x               */
+  const void *d_out;        /* [rows, n_out]                                   */
+  const void *x;            /* [rows, n_in]                                    */
+  const void *a, *b;
+  const void *idx;
+  kda_index_dtype idx_dtype;
+  int32_t num_requests;
+  const int32_t *cu_seqlens;
+  const float *scale;
+  const void *d_x_in;       /* [rows, n_in] or NULL                            */
+  void *d_x;                /* [rows, n_in] or NULL                            */
+  float *d_a, *d_b;         /* or NULL                                         */
+  void *workspace;          /* kda_lora_bwd_workspace_size bytes, 256-byte     */
+  size_t workspace_bytes;   /* aligned                                         */
+} kda_lora_bwd_args;
+
+size_t kda_lora_bwd_workspace_size(const kda_lora_bwd_args *args);
+kda_status kda_lora_bwd(const kda_lora_bwd_args *args, kda_stream_t stream);
+
 /* Reads and clears the device error word kept at the start of a forward or
  * summary workspace: synchronises the stream, returns KDA_OK or
  * KDA_ERR_DEVICE_TIMEOUT when a bounded device-side wait gave up.  Every
