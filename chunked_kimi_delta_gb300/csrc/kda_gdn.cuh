@@ -120,6 +120,16 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// c[2 q], c[2 q + 1] += a b[q] for a row of tiles, from tile pair q0 to q1.
+template <int N, int M>
+__device__ __forceinline__ void mma_row(float (&c)[N][4], const uint32_t (&a)[4], const uint32_t (&b)[M][4], int q0 = 0, int q1 = N / 2) {
+#pragma unroll
+  for (int q = 0; q < N / 2; ++q)
+    if (q >= q0 && q < q1) {
+      mma16(c[2 * q], a, b[q][0], b[q][1]);
+      mma16(c[2 * q + 1], a, b[q][2], b[q][3]);
+    }
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");

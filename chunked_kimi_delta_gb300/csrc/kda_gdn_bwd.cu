@@ -159,20 +159,15 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     for (int ks = 0; ks < DK / 16; ++ks) {
       uint32_t ah[4], al[4];
       as_left(D, ks, z0.x, z1.x, ah, al);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t at = unit_at<U>(16 * q + rb, 2 * ks + ub);
-        uint32_t b[4];
-        ldsm4(b, st + Sh::S_K + at);
-        mma16(X[2 * q], al, b[0], b[1]);
-        mma16(X[2 * q + 1], al, b[2], b[3]);
-        mma16(X[2 * q], ah, b[0], b[1]);
-        mma16(X[2 * q + 1], ah, b[2], b[3]);
-        if constexpr (NI == 2) {
-          ldsm4(b, st + Sh::S_K + Sh::TILE + at);
-          mma16(X[2 * q], ah, b[0], b[1]);
-          mma16(X[2 * q + 1], ah, b[2], b[3]);
-        }
+      for (int q = 0; q < 4; ++q) ldsm4(b[q], st + Sh::S_K + unit_at<U>(16 * q + rb, 2 * ks + ub));
+      mma_row(X, al, b);
+      mma_row(X, ah, b);
+      if constexpr (NI == 2) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ldsm4(b[q], st + Sh::S_K + Sh::TILE + unit_at<U>(16 * q + rb, 2 * ks + ub));
+        mma_row(X, ah, b);
       }
     }
 #pragma unroll
@@ -201,21 +196,14 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t ah[4], al[4];
       as_left(O, ks, z0.x, z1.x, ah, al);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int q = 0; q <= ks; ++q) {
-        const uint32_t at = unit_at<8>(16 * ks + rt, 2 * q + ut);
-        uint32_t b[4];
-        ldsm4t(b, st + Sh::S_P + MAT_BYTES + at);
-        mma16(Y[2 * q], ah, b[0], b[1]);
-        mma16(Y[2 * q + 1], ah, b[2], b[3]);
-        ldsm4t(b, st + Sh::S_P + at);
-        if constexpr (NI == 2) {
-          mma16(Y[2 * q], al, b[0], b[1]);
-          mma16(Y[2 * q + 1], al, b[2], b[3]);
-        }
-        mma16(Y[2 * q], ah, b[0], b[1]);
-        mma16(Y[2 * q + 1], ah, b[2], b[3]);
-      }
+      for (int q = 0; q <= ks; ++q) ldsm4t(b[q], st + Sh::S_P + MAT_BYTES + unit_at<8>(16 * ks + rt, 2 * q + ut));
+      mma_row(Y, ah, b, 0, ks + 1);
+#pragma unroll
+      for (int q = 0; q <= ks; ++q) ldsm4t(b[q], st + Sh::S_P + unit_at<8>(16 * ks + rt, 2 * q + ut));
+      if constexpr (NI == 2) mma_row(Y, al, b, 0, ks + 1);
+      mma_row(Y, ah, b, 0, ks + 1);
     }
     {
       const float a = num[NUM_MISC + 2];
@@ -244,19 +232,14 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t ah[4], al[4];
       as_left(X, ks, z0.x, z1.x, ah, al);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int q = 0; q <= ks; ++q) {
-        const uint32_t at = unit_at<8>(16 * ks + rt, 2 * q + ut);
-        uint32_t b[4];
-        ldsm4t(b, st + Sh::S_A + MAT_BYTES + at);
-        mma16(Y[2 * q], ah, b[0], b[1]);
-        mma16(Y[2 * q + 1], ah, b[2], b[3]);
-        ldsm4t(b, st + Sh::S_A + at);
-        mma16(Y[2 * q], al, b[0], b[1]);
-        mma16(Y[2 * q + 1], al, b[2], b[3]);
-        mma16(Y[2 * q], ah, b[0], b[1]);
-        mma16(Y[2 * q + 1], ah, b[2], b[3]);
-      }
+      for (int q = 0; q <= ks; ++q) ldsm4t(b[q], st + Sh::S_A + MAT_BYTES + unit_at<8>(16 * ks + rt, 2 * q + ut));
+      mma_row(Y, ah, b, 0, ks + 1);
+#pragma unroll
+      for (int q = 0; q <= ks; ++q) ldsm4t(b[q], st + Sh::S_A + unit_at<8>(16 * ks + rt, 2 * q + ut));
+      mma_row(Y, al, b, 0, ks + 1);
+      mma_row(Y, ah, b, 0, ks + 1);
     }
     load_strip<T>(smem + so + Sh::S_V + warp * Sh::STRIP, lane, O);  // v, for R = v - e^G k S
     float4 *dy_to = tiles(pl.off_dy, 8);
@@ -342,25 +325,23 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
       for (int ks = 0; ks < 4; ++ks) as_left(O, ks, z0.x, z1.x, xh[ks], xl[ks]);
       const uint32_t right = st + (which ? Sh::S_K : Sh::S_Q);
 #pragma unroll
-      for (int q = 0; q < NK / 2; ++q) {
-        float acc[2][4] = {};
+      for (int q = 0; q < NK / 2; q += 2) {
+        float acc[4][4] = {};
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          const uint32_t at = unit_at<U>(16 * ks + rt, 2 * q + ut);
-          uint32_t b[4];
-          ldsm4t(b, right + at);
-          mma16(acc[0], xl[ks], b[0], b[1]);
-          mma16(acc[1], xl[ks], b[2], b[3]);
-          mma16(acc[0], xh[ks], b[0], b[1]);
-          mma16(acc[1], xh[ks], b[2], b[3]);
+          uint32_t b[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ldsm4t(b[i], right + unit_at<U>(16 * ks + rt, 2 * (q + i) + ut));
+          mma_row(acc, xl[ks], b);
+          mma_row(acc, xh[ks], b);
           if constexpr (NI == 2) {
-            ldsm4t(b, right + Sh::TILE + at);
-            mma16(acc[0], xh[ks], b[0], b[1]);
-            mma16(acc[1], xh[ks], b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ldsm4t(b[i], right + Sh::TILE + unit_at<U>(16 * ks + rt, 2 * (q + i) + ut));
+            mma_row(acc, xh[ks], b);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
           float(&d)[4] = D[2 * q + i];
           const float f = which ? 1.f : ec;
           d[0] = f * d[0] + acc[i][0] * z0.y;
@@ -398,10 +379,12 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
 }
 
 // ---------------------------------------------------------------- chunks by themselves
-// Eight warps: warp w has rows 16 (w % 4) .. of every product and half w / 4 of
-// its columns; of the two pairs of [64, 64] products, q k^T with dO W^T or
-// k k^T with dY W^T.  The value heads of a key head take turns, dQ and dK stay
+// Sixteen warps: warp w has rows 16 (w % 4) .. of every product and quarter
+// w / 4 of its columns; of the two pairs of [64, 64] products, half of q k^T
+// with dO W^T or of k k^T with dY W^T.  The value heads of a key head take turns, dQ and dK stay
 // in registers meanwhile.
+constexpr int NT = 512;  // of the intra kernel
+
 template <typename T, int DK, int DV> struct IntraShape {
   static constexpr int NI = pieces<T>();
   static constexpr int DH = NI == 1 ? DK : 64;  // key channels of S and dS' held at once
@@ -410,7 +393,7 @@ template <typename T, int DK, int DV> struct IntraShape {
                             S_S = S_DO + NI * VT, S_DS = S_S + 2 * ST, END = S_DS + NI * ST;
   // over S and dS' once these are used: the coefficients of k and q, then the pairs of dg
   static constexpr uint32_t S_T = S_S, S_X = S_T + 3 * NI * MAT_BYTES, END2 = S_X + C * C * 4;
-  static constexpr uint32_t S_NUM = END > END2 ? END : END2, BYTES = S_NUM + 10 * C * 4 + 64;
+  static constexpr uint32_t S_NUM = END > END2 ? END : END2, BYTES = S_NUM + 11 * C * 4 + 128;
 };
 
 template <int N> __device__ __forceinline__ void zero(float (&x)[N][4]) {
@@ -428,17 +411,18 @@ __device__ __forceinline__ void mma_pieces(float (&c)[4], const uint32_t (&a)[NA
 }
 
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(NT, 1)
 gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_stride, GradOut io) {
   using Sh = IntraShape<T, DK, DV>;
-  constexpr int NI = Sh::NI, DH = Sh::DH, PASSES = DK / DH, NW = DH / 16;  // n-tiles of a warp in a pass
+  constexpr int NI = Sh::NI, DH = Sh::DH, PASSES = DK / DH, NW = DH / 32;  // n-tiles of a warp in a pass
   constexpr int UK = DK / 8, UV = DV / 8, US = DH / 8;
   extern __shared__ __align__(128) unsigned char smem[];
   float *s_beta = reinterpret_cast<float *>(smem + Sh::S_NUM), *s_kn = s_beta + C, *s_qn = s_kn + C, *s_gh = s_qn + C,
-        *s_gl = s_gh + C, *s_e = s_gl + C, *s_f = s_e + C, *s_iq = s_f + C /* [2][C] */, *s_db = s_iq + 2 * C;
-  int *s_max = reinterpret_cast<int *>(s_db + C);  // [3]
-  float *s_z = s_db + C + 4;                       // [8]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mt = warp & 3, half = warp >> 2;
+        *s_gl = s_gh + C, *s_e = s_gl + C, *s_f = s_e + C, *s_iq = s_f + C /* [4][C] */,
+        *s_db = s_e;  // [2][C], once e^G is used
+  int *s_max = reinterpret_cast<int *>(s_iq + 4 * C);  // [3]
+  float *s_z = s_iq + 4 * C + 4;                       // [16]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mt = warp & 3, quarter = warp >> 2, half = quarter >> 1, side = quarter & 1;
   const int g = lane >> 2, t = (lane & 3) * 2;
   const int hk = (int)(blockIdx.x % p.Hk);
   const int64_t c = blockIdx.x / p.Hk;
@@ -448,7 +432,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
   const uint32_t base = smem_addr(smem);
   {
     const char *a = ws + pl.off_kq + (size_t)blockIdx.x * kq_stride;
-    for (uint32_t x = tid * 16; x < 2 * NI * Sh::KT; x += 256 * 16) cp16(base + x, a + x);
+    for (uint32_t x = tid * 16; x < 2 * NI * Sh::KT; x += NT * 16) cp16(base + x, a + x);
     cp_commit();
     cp_wait<0>();
   }
@@ -499,7 +483,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       const float4 *w = reinterpret_cast<const float4 *>(ws + pl.off_w) + unit * (DV / 16) * 8 * 32;
       const float4 *y = reinterpret_cast<const float4 *>(ws + pl.off_dy) + unit * (DV / 16) * 8 * 32;
 #pragma unroll 4
-      for (int x = tid; x < DV / 16 * 8 * 32; x += 256) {
+      for (int x = tid; x < DV / 16 * 8 * 32; x += NT) {
         const int l = x & 31, nt = (x >> 5) & 7, r = (x >> 8) * 16 + (l >> 2);
         const uint32_t at = unit_at<8>(r, nt) + (l & 3) * 4, at8 = unit_at<8>(r + 8, nt) + (l & 3) * 4;
         uint32_t hi, lo;
@@ -519,7 +503,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       }
       const T *o = static_cast<const T *>(io.d_out) + batch * p.v.b + tok * p.v.t + h * p.v.h;
 #pragma unroll 4
-      for (int x = tid; x < C * UV; x += 256) {
+      for (int x = tid; x < C * UV; x += NT) {
         const int r = x / UV, u = x % UV;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (r < len && io.d_out) load8(o + r * p.v.t + u * 8, v);
@@ -542,7 +526,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         const float4 *s = reinterpret_cast<const float4 *>(ws + pl.off_s) + unit * (DV / 16) * UK * 32;
         const float4 *d = reinterpret_cast<const float4 *>(ws + pl.off_ds) + unit * (DV / 16) * UK * 32;
 #pragma unroll 4
-        for (int x = tid; x < DV / 16 * US * 32; x += 256) {
+        for (int x = tid; x < DV / 16 * US * 32; x += NT) {
           const int l = x & 31, nt = (x >> 5) % US, w = (x >> 5) / US, r = w * 16 + (l >> 2);
           const int from = (w * UK + pass * US + nt) * 32 + l;
           const uint32_t at = unit_at<US>(r, nt) + (l & 3) * 4, at8 = unit_at<US>(r + 8, nt) + (l & 3) * 4;
@@ -579,7 +563,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         for (int q = 0; q < NW / 2; ++q) {
           uint32_t b[2][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) ldsm4t(b[i], base + Sh::S_S + i * Sh::ST + unit_at<US>(16 * ks + rt, half * NW + 2 * q + ut));
+          for (int i = 0; i < 2; ++i) ldsm4t(b[i], base + Sh::S_S + i * Sh::ST + unit_at<US>(16 * ks + rt, quarter * NW + 2 * q + ut));
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             mma_pieces<NI, 2>(x[2 * q + e], o, b, e);
@@ -594,7 +578,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         const float eq = s_e[i] * scale, ek = s_e[i] * s_beta[i];
 #pragma unroll
         for (int nt = 0; nt < NW; ++nt) {
-          const uint32_t at = unit_at<UK>(i, pass * US + half * NW + nt) + t * 2;
+          const uint32_t at = unit_at<UK>(i, pass * US + quarter * NW + nt) + t * 2;
           float2 q = __half22float2(*reinterpret_cast<const __half2 *>(smem + Sh::S_Q + at));
           if constexpr (NI == 2) {
             const float2 ql = __half22float2(*reinterpret_cast<const __half2 *>(smem + Sh::S_Q + Sh::KT + at));
@@ -619,7 +603,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         for (int q = 0; q < NW / 2; ++q) {
           uint32_t b[NI][4];
 #pragma unroll
-          for (int i = 0; i < NI; ++i) ldsm4t(b[i], base + Sh::S_DS + i * Sh::ST + unit_at<US>(16 * ks + rt, half * NW + 2 * q + ut));
+          for (int i = 0; i < NI; ++i) ldsm4t(b[i], base + Sh::S_DS + i * Sh::ST + unit_at<US>(16 * ks + rt, quarter * NW + 2 * q + ut));
 #pragma unroll
           for (int e = 0; e < 2; ++e) mma_pieces<NI, NI>(x[2 * q + e], w, b, e);
         }
@@ -638,14 +622,14 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     for (int rr = 0; rr < 2; ++rr) {
       iq[rr] += __shfl_xor_sync(~0u, iq[rr], 1);
       iq[rr] += __shfl_xor_sync(~0u, iq[rr], 2);
-      if ((lane & 3) == 0) s_iq[half * C + row0 + 8 * rr] = iq[rr] * s_e[row0 + 8 * rr] * s_qn[row0 + 8 * rr] * scale;
+      if ((lane & 3) == 0) s_iq[quarter * C + row0 + 8 * rr] = iq[rr] * s_e[row0 + 8 * rr] * s_qn[row0 + 8 * rr] * scale;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) zsum += __shfl_xor_sync(~0u, zsum, o);
     if (lane == 0) s_z[warp] = zsum;
 
     // ---- inside the chunk: half 0 has q k^T and dP, half 1 k k^T and dL
-    float x[8][4], m[8][4];
+    float x[4][4], m[4][4];  // tile pairs `side` and `side` + 2
     zero(x);
     zero(m);
 #pragma unroll 2
@@ -654,13 +638,14 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
 #pragma unroll
       for (int i = 0; i < NI; ++i) ldsm4(a[i], base + (half ? Sh::S_K : Sh::S_Q) + i * Sh::KT + unit_at<UK>(ra, 2 * ks + ua));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int qi = 0; qi < 2; ++qi) {
+        const int q = side + 2 * qi;
         if (q > mt) continue;
         uint32_t b[NI][4];
 #pragma unroll
         for (int i = 0; i < NI; ++i) ldsm4(b[i], base + Sh::S_K + i * Sh::KT + unit_at<UK>(16 * q + rb, 2 * ks + ub));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) mma_pieces<NI, NI>(x[2 * q + e], a, b, e);
+        for (int e = 0; e < 2; ++e) mma_pieces<NI, NI>(x[2 * qi + e], a, b, e);
       }
     }
 #pragma unroll 2
@@ -675,26 +660,28 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         if constexpr (NI == 1) a[1][0] = a[1][1] = a[1][2] = a[1][3] = 0u;
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int qi = 0; qi < 2; ++qi) {
+        const int q = side + 2 * qi;
         if (q > mt) continue;
         uint32_t b[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) ldsm4t(b[i], base + Sh::S_W + i * Sh::VT + unit_at<8>(16 * ks + rt, 2 * q + ut));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (NI == 2 || half) mma16(m[2 * q + e], a[1], b[0][2 * e], b[0][2 * e + 1]);
-          mma16(m[2 * q + e], a[0], b[1][2 * e], b[1][2 * e + 1]);
-          mma16(m[2 * q + e], a[0], b[0][2 * e], b[0][2 * e + 1]);
+          if (NI == 2 || half) mma16(m[2 * qi + e], a[1], b[0][2 * e], b[0][2 * e + 1]);
+          mma16(m[2 * qi + e], a[0], b[1][2 * e], b[1][2 * e + 1]);
+          mma16(m[2 * qi + e], a[0], b[0][2 * e], b[0][2 * e + 1]);
         }
       }
     }
+    auto col_of = [&](int nt) { return 16 * (side + (nt & 2)) + 8 * (nt & 1) + t; };
     float db[2] = {0.f, 0.f}, top0 = 0.f, top1 = 0.f;
     const float un = half ? -sc[3].y : sc[4].y;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
+    for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = row0 + 8 * (e >> 1), j = 8 * nt + t + (e & 1);
+        const int i = row0 + 8 * (e >> 1), j = col_of(nt) + (e & 1);
         float mv = 0.f, xv = 0.f;
         if (half ? j < i : j <= i) {
           const float gam = expf((s_gh[i] - s_gh[j]) + (s_gl[i] - s_gl[j]));
@@ -723,15 +710,15 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       atomicMax(&s_max[half ? 2 : 0], __float_as_int(top0));
       if (!half) atomicMax(&s_max[1], __float_as_int(top1));
     }
+    __syncthreads();  // the states' place is free, the largest values are known
     if (half) {
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         db[rr] += __shfl_xor_sync(~0u, db[rr], 1);
         db[rr] += __shfl_xor_sync(~0u, db[rr], 2);
-        if ((lane & 3) == 0) s_db[row0 + 8 * rr] = db[rr];
+        if ((lane & 3) == 0) s_db[side * C + row0 + 8 * rr] = db[rr];
       }
     }
-    __syncthreads();  // the states' place is free, the largest values are known
     const float2 s1 = piece_scale(__int_as_float(s_max[0])), s2 = piece_scale(__int_as_float(s_max[1])),
                  s3 = piece_scale(__int_as_float(s_max[2]));
     auto put = [&](int which, int i, int j, float v) {  // one element of a tile
@@ -743,11 +730,11 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     float *Xs = reinterpret_cast<float *>(smem + Sh::S_X);
     auto x_at = [&](int i, int j) -> float & { return Xs[i * C + (j ^ (i & 31))]; };
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      if (nt >= 2 * mt + 2) continue;
+    for (int nt = 0; nt < 4; ++nt) {
+      if (side + (nt & 2) > mt) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = row0 + 8 * (e >> 1), j = 8 * nt + t + (e & 1);
+        const int i = row0 + 8 * (e >> 1), j = col_of(nt) + (e & 1);
         const float mv = m[nt][e];
         if (half) {
           if (j < i) {
@@ -766,10 +753,10 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     __syncthreads();
     if (half) {
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        if (nt >= 2 * mt + 2) continue;
+      for (int nt = 0; nt < 4; ++nt) {
+        if (side + (nt & 2) > mt) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x_at(row0 + 8 * (e >> 1), 8 * nt + t + (e & 1)) += x[nt][e];
+        for (int e = 0; e < 4; ++e) x_at(row0 + 8 * (e >> 1), col_of(nt) + (e & 1)) += x[nt][e];
       }
     }
     // dQ += dP.. k, dK += (dP..)^T q + (M + M^T) k
@@ -791,7 +778,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
 #pragma unroll
         for (int q = 0; q < NW / 2; ++q) {
           uint32_t r[NI][4];
-          const uint32_t at = unit_at<UK>(16 * ks + rt, pass * US + half * NW + 2 * q + ut);
+          const uint32_t at = unit_at<UK>(16 * ks + rt, pass * US + quarter * NW + 2 * q + ut);
 #pragma unroll
           for (int i = 0; i < NI; ++i) ldsm4t(r[i], base + Sh::S_K + i * Sh::KT + at);
 #pragma unroll
@@ -836,7 +823,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
 #pragma unroll 8
         for (int j = 0; j < r; ++j) s += x_at(r, j);
         F[i] = s;
-        I[i] = s_iq[r] + s_iq[C + r] + dots[DOT_K + r];
+        I[i] = (s_iq[r] + s_iq[C + r]) + (s_iq[2 * C + r] + s_iq[3 * C + r]) + dots[DOT_K + r];
         Y[i] = dots[DOT_Y + r];
       }
       float si = I[0] + I[1], sy = Y[0] + Y[1];
@@ -851,7 +838,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       if (lane == 31) after = 0.f;
       float z = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) z += s_z[w];
+      for (int w = 0; w < NT / 32; ++w) z += s_z[w];
       z *= num[NUM_MISC];
       const float dg[2] = {F[0] + si + before + z, F[1] + (I[1] + after) + (before + Y[0]) + z};
       const bool gate = (p.gp.flags & KDA_GATE_IN_KERNEL) != 0;
@@ -870,7 +857,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
             dt += dx;
           }
           io.dg[off + r * p.gate.t] = dx;
-          float d = dots[DOT_BETA + r] + s_db[r];
+          float d = dots[DOT_BETA + r] + (s_db[r] + s_db[C + r]);
           if (p.gp.flags & KDA_BETA_SIGMOID) d *= be * (1.f - be);
           io.dbeta[off + r * p.gate.t] = d;
         }
@@ -892,7 +879,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     const uint32_t tile = which ? Sh::S_K : Sh::S_Q;
     float dot[2] = {0.f, 0.f};
     auto hat = [&](int pass, int nt, int rr) {  // two values of x^, without the unit's factor
-      const uint32_t at = unit_at<UK>(row0 + 8 * rr, pass * US + half * NW + nt) + t * 2;
+      const uint32_t at = unit_at<UK>(row0 + 8 * rr, pass * US + quarter * NW + nt) + t * 2;
       float2 v = __half22float2(*reinterpret_cast<const __half2 *>(smem + tile + at));
       if constexpr (NI == 2) {
         const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(smem + tile + Sh::KT + at));
@@ -918,8 +905,8 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       }
       __syncthreads();
       if ((lane & 3) == 0) {
-        s_iq[half * C + row0] = dot[0];
-        s_iq[half * C + row0 + 8] = dot[1];
+        s_iq[quarter * C + row0] = dot[0];
+        s_iq[quarter * C + row0 + 8] = dot[1];
       }
       __syncthreads();
     }
@@ -929,7 +916,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       const int i = row0 + 8 * rr;
       if (i >= len) continue;
       const float xn = which ? s_kn[i] : s_qn[i], r = num[(which ? NUM_RK : NUM_RQ) + i];
-      const float full = l2 ? (s_iq[i] + s_iq[C + i]) * xn * xn : 0.f;
+      const float full = l2 ? ((s_iq[i] + s_iq[C + i]) + (s_iq[2 * C + i] + s_iq[3 * C + i])) * xn * xn : 0.f;
 #pragma unroll
       for (int pass = 0; pass < PASSES; ++pass)
 #pragma unroll
@@ -940,7 +927,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
             a = r * (a - v.x * full);
             b = r * (b - v.y * full);
           }
-          T *to = out + i * p.qk.t + pass * DH + half * NW * 8 + nt * 8 + t;
+          T *to = out + i * p.qk.t + pass * DH + quarter * NW * 8 + nt * 8 + t;
           if constexpr (NI == 1) *reinterpret_cast<__nv_bfloat162 *>(to) = __floats2bfloat162_rn(a, b);
           else *reinterpret_cast<float2 *>(to) = make_float2(a, b);
         }
@@ -983,7 +970,7 @@ template <typename T, int DK, int DV> cudaError_t go(const Problem &p, char *ws,
   reverse<<<(unsigned)((int64_t)p.s.N * p.H), DV * 2, rev_smem, st>>>(p, ws, pl, kqs, aps, io);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.nchunks > 0) {
-    intra<<<(unsigned)((int64_t)p.nchunks * p.Hk), 256, in_smem, st>>>(p, ws, pl, kqs, aps, io);
+    intra<<<(unsigned)((int64_t)p.nchunks * p.Hk), NT, in_smem, st>>>(p, ws, pl, kqs, aps, io);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (io.da_log || io.ddt_bias)

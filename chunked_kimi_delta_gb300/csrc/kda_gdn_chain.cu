@@ -114,31 +114,27 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     for (int ks = 0; ks < DK / 16; ++ks) {
       uint32_t ah[4], al[4];
       as_left(S, ks, z0.x, z1.x, ah, al);
+      // eight products of one kind in a row: none waits for the sum of the one before
+      uint32_t b[4][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t at = unit_at<U>(16 * q + rb, 2 * ks + ub);
-        uint32_t b[4];
-        ldsm4(b, st + Sh::S_K + at);
-        mma16(Y[2 * q], al, b[0], b[1]);
-        mma16(Y[2 * q + 1], al, b[2], b[3]);
-        mma16(Y[2 * q], ah, b[0], b[1]);
-        mma16(Y[2 * q + 1], ah, b[2], b[3]);
-        if constexpr (NI == 2) {
-          ldsm4(b, st + Sh::S_K + Sh::TILE + at);
-          mma16(Y[2 * q], ah, b[0], b[1]);
-          mma16(Y[2 * q + 1], ah, b[2], b[3]);
-        }
-        if constexpr (STORE) continue;
-        ldsm4(b, st + Sh::S_Q + at);
-        mma16(O[2 * q], ah, b[0], b[1]);
-        mma16(O[2 * q + 1], ah, b[2], b[3]);
-        if constexpr (NI == 2) {
-          mma16(O[2 * q], al, b[0], b[1]);
-          mma16(O[2 * q + 1], al, b[2], b[3]);
-          ldsm4(b, st + Sh::S_Q + Sh::TILE + at);
-          mma16(O[2 * q], ah, b[0], b[1]);
-          mma16(O[2 * q + 1], ah, b[2], b[3]);
-        }
+      for (int q = 0; q < 4; ++q) ldsm4(b[q], st + Sh::S_K + unit_at<U>(16 * q + rb, 2 * ks + ub));
+      mma_row(Y, al, b);
+      mma_row(Y, ah, b);
+      if constexpr (NI == 2) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ldsm4(b[q], st + Sh::S_K + Sh::TILE + unit_at<U>(16 * q + rb, 2 * ks + ub));
+        mma_row(Y, ah, b);
+      }
+      if constexpr (!STORE) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) ldsm4(b[q], st + Sh::S_Q + unit_at<U>(16 * q + rb, 2 * ks + ub));
+      mma_row(O, ah, b);
+      if constexpr (NI == 2) {
+        mma_row(O, al, b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ldsm4(b[q], st + Sh::S_Q + Sh::TILE + unit_at<U>(16 * q + rb, 2 * ks + ub));
+        mma_row(O, ah, b);
+      }
       }
     }
 
@@ -178,7 +174,7 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         Y[nt][1] = be.y * (x[i][1] - Y[nt][1]);
         Y[nt][2] = be.x * (x[i][2] - Y[nt][2]);
         Y[nt][3] = be.y * (x[i][3] - Y[nt][3]);
-        if constexpr (STORE) continue;
+        if constexpr (STORE) continue;  // no outputs
         // factor by factor: the factors' product may be too small for fp32 where the result is not
         O[nt][0] = O[nt][0] * eq.x * z0.y;
         O[nt][1] = O[nt][1] * eq.y * z0.y;
@@ -198,19 +194,14 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t ah[4], al[4];
       as_left(Y, ks, z0.x, z1.x, ah, al);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int q = ks; q < 4; ++q) {
-        const uint32_t at = unit_at<8>(16 * q + rb, 2 * ks + ub);
-        uint32_t b[4];
-        ldsm4(b, st + Sh::S_A + MAT_BYTES + at);
-        mma16(W[2 * q], ah, b[0], b[1]);
-        mma16(W[2 * q + 1], ah, b[2], b[3]);
-        ldsm4(b, st + Sh::S_A + at);
-        mma16(W[2 * q], al, b[0], b[1]);
-        mma16(W[2 * q + 1], al, b[2], b[3]);
-        mma16(W[2 * q], ah, b[0], b[1]);
-        mma16(W[2 * q + 1], ah, b[2], b[3]);
-      }
+      for (int q = ks; q < 4; ++q) ldsm4(b[q], st + Sh::S_A + MAT_BYTES + unit_at<8>(16 * q + rb, 2 * ks + ub));
+      mma_row(W, ah, b, ks);
+#pragma unroll
+      for (int q = ks; q < 4; ++q) ldsm4(b[q], st + Sh::S_A + unit_at<8>(16 * q + rb, 2 * ks + ub));
+      mma_row(W, al, b, ks);
+      mma_row(W, ah, b, ks);
     }
     {
       const float a = num[NUM_MISC + 1];
@@ -236,20 +227,15 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t ah[4], al[4];
       as_left(W, ks, z0.x, z1.x, ah, al);
+      uint32_t b[4][4];
 #pragma unroll
-      for (int q = ks; q < 4; ++q) {
-        const uint32_t at = unit_at<8>(16 * q + rb, 2 * ks + ub);
-        uint32_t b[4];
-        ldsm4(b, st + Sh::S_P + at);
-        mma16(Y[2 * q], ah, b[0], b[1]);
-        mma16(Y[2 * q + 1], ah, b[2], b[3]);
-        if constexpr (NI == 2) {
-          mma16(Y[2 * q], al, b[0], b[1]);
-          mma16(Y[2 * q + 1], al, b[2], b[3]);
-          ldsm4(b, st + Sh::S_P + MAT_BYTES + at);
-          mma16(Y[2 * q], ah, b[0], b[1]);
-          mma16(Y[2 * q + 1], ah, b[2], b[3]);
-        }
+      for (int q = ks; q < 4; ++q) ldsm4(b[q], st + Sh::S_P + unit_at<8>(16 * q + rb, 2 * ks + ub));
+      mma_row(Y, ah, b, ks);
+      if constexpr (NI == 2) {
+        mma_row(Y, al, b, ks);
+#pragma unroll
+        for (int q = ks; q < 4; ++q) ldsm4(b[q], st + Sh::S_P + MAT_BYTES + unit_at<8>(16 * q + rb, 2 * ks + ub));
+        mma_row(Y, ah, b, ks);
       }
     }
     const int64_t r0 = (int64_t)c * C;
@@ -309,25 +295,23 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     for (int ks = 0; ks < 4; ++ks) as_left(W, ks, z0.x, z1.x, wh[ks], wl[ks]);
     const float ec = num[NUM_MISC];
 #pragma unroll
-    for (int q = 0; q < NK / 2; ++q) {
-      float acc[2][4] = {};
+    for (int q = 0; q < NK / 2; q += 2) {
+      float acc[4][4] = {};
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t at = unit_at<U>(16 * ks + rt, 2 * q + ut);
-        uint32_t b[4];
-        ldsm4t(b, st + Sh::S_K + at);
-        mma16(acc[0], wl[ks], b[0], b[1]);
-        mma16(acc[1], wl[ks], b[2], b[3]);
-        mma16(acc[0], wh[ks], b[0], b[1]);
-        mma16(acc[1], wh[ks], b[2], b[3]);
+        uint32_t b[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ldsm4t(b[i], st + Sh::S_K + unit_at<U>(16 * ks + rt, 2 * (q + i) + ut));
+        mma_row(acc, wl[ks], b);
+        mma_row(acc, wh[ks], b);
         if constexpr (NI == 2) {
-          ldsm4t(b, st + Sh::S_K + Sh::TILE + at);
-          mma16(acc[0], wh[ks], b[0], b[1]);
-          mma16(acc[1], wh[ks], b[2], b[3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ldsm4t(b[i], st + Sh::S_K + Sh::TILE + unit_at<U>(16 * ks + rt, 2 * (q + i) + ut));
+          mma_row(acc, wh[ks], b);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         S[2 * q + i][0] = ec * S[2 * q + i][0] + acc[i][0] * z0.y;
         S[2 * q + i][1] = ec * S[2 * q + i][1] + acc[i][1] * z0.y;
         S[2 * q + i][2] = ec * S[2 * q + i][2] + acc[i][2] * z1.y;

@@ -3,13 +3,14 @@
 // token, A = (I + L)^-1 and P (kda_gdn.cuh).
 //
 // One CTA of four warps per (chunk, key head); the value heads of its group
-// take turns on the products q k^T and k k^T, which are theirs in common.
-// Warp w holds rows 16 w .. of both products in registers.  The inverse: the
-// four diagonal blocks of 16 by substitution (a lane per column, fp32), then
-// block column c by warp c alone, A_bc = -D_b (sum over m of L_bm A_mc), as
-// three-term products of fp16 pieces.  A block is kept transposed in the
-// half of L's array above the diagonal: the layout in which the next product
-// reads it.
+// take turns on q k^T and k k^T, which are theirs in common and lie in shared
+// memory where the pieces of q and k were.  The inverse: the four diagonal
+// blocks of 16 by substitution (a lane per column, fp32), then two blocks of 16
+// and one of 32 below them, A_21 = -A_22 (L_21 A_11), a warp to every eight
+// columns: these never meet another warp's.  Their products take tf32 operands
+// in two pieces (22 bits; tf32 has fp32's range, so no scaling has to be found).
+// A is kept transposed in the half of L's array above the diagonal: the layout
+// in which the next product reads it.
 #include "kda_gdn.cuh"
 
 namespace kda {
@@ -18,6 +19,7 @@ namespace {
 
 constexpr int NT = 128;
 constexpr int LP = 68;  // floats a row of L
+constexpr int HEADS = 4;  // value heads whose gates are computed at once, a warp each
 
 // (hi, lo) + (h, l) with the rounding error of the sum kept
 __device__ __forceinline__ void add2(float &hi, float &lo, float h, float l) {
@@ -26,58 +28,72 @@ __device__ __forceinline__ void add2(float &hi, float &lo, float h, float l) {
   hi = s;
 }
 
-// Block (rows 16 b.., columns 16 m..) of L as the A operand, in pieces.
-__device__ __forceinline__ void block_a(const float *M, int lane, float s, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  const int g = lane >> 2, t = (lane & 3) * 2;
+// A value's two tf32 pieces.
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  const float r = x - __uint_as_float(hi);
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(r));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c[16 MT, 8] += M [16 MT, K] X [K, 8].  M: element (i, k) at M[i LP + k], or
+// kept transposed at M[k LP + i]; where TRI its blocks above the diagonal, whose
+// place holds L, are left out.  X: element (k, j) at X[j LP + k], from k = k0 on
+// (likewise).
+template <int MT, int K, bool TRANSPOSED, bool TRI>
+__device__ __forceinline__ void block_product(float (&c)[MT][4], const float *M, const float *X, int lane, float sign, int k0 = 0) {
+  const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = *reinterpret_cast<const float2 *>(M + (g + (i & 1) * 8) * LP + t + (i >> 1) * 8);
-    split2(x.x * s, x.y * s, hi[i], lo[i]);
+  for (int ks = 0; ks < K / 8; ++ks) {
+    if (8 * ks < k0) continue;
+    uint32_t bh[2], bl[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) split_tf32(X[g * LP + 8 * ks + t + 4 * i], bh[i], bl[i]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (TRI && 8 * ks >= 16 * (m + 1)) continue;
+      uint32_t ah[4], al[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * m + g + 8 * (i & 1), k = 8 * ks + t + 4 * (i >> 1);
+        split_tf32(sign * (TRANSPOSED ? M[k * LP + r] : M[r * LP + k]), ah[i], al[i]);
+      }
+      mma_tf32(c[m], al, bh[0], bh[1]);
+      mma_tf32(c[m], ah, bl[0], bl[1]);
+      mma_tf32(c[m], ah, bh[0], bh[1]);
+    }
   }
 }
-// The same of a block that is kept transposed.
-__device__ __forceinline__ void block_at(const float *M, int lane, float s, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+// The accumulators to where X is read from, element (k, j) at X[j LP + k].
+template <int MT> __device__ __forceinline__ void put_columns(const float (&c)[MT][4], float *X, int lane) {
   const int g = lane >> 2, t = (lane & 3) * 2;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float *x = M + (t + (i >> 1) * 8) * LP + g + (i & 1) * 8;
-    split2(x[0] * s, x[LP] * s, hi[i], lo[i]);
-  }
-}
-// Column tile nt of a transposed block as the B operand.
-__device__ __forceinline__ void block_b(const float *M, int lane, int nt, float s, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
-  const int g = lane >> 2, t = (lane & 3) * 2;
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 x = *reinterpret_cast<const float2 *>(M + (8 * nt + g) * LP + t + i * 8);
-    split2(x.x * s, x.y * s, hi[i], lo[i]);
-  }
+    for (int e = 0; e < 4; ++e) X[(t + (e & 1)) * LP + 16 * m + g + 8 * (e >> 1)] = c[m][e];
 }
-__device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[2],
-                                     const uint32_t (&bl)[2]) {
-  mma16(c, al, bh[0], bh[1]);
-  mma16(c, ah, bl[0], bl[1]);
-  mma16(c, ah, bh[0], bh[1]);
-}
-// Largest |x| of a 16 x 16 block over the warp.
-__device__ __forceinline__ float block_max(const float *M, int lane) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(M[(lane >> 1) * LP + (lane & 1) * 8 + i]));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  return m;
-}
+
+template <typename T, int DK> struct PrepShape {
+  static constexpr uint32_t TILES = 2 * pieces<T>() * C * DK * 2, PRODUCTS = 2 * C * LP * 4;
+  static constexpr uint32_t S_L = TILES > PRODUCTS ? TILES : PRODUCTS, BYTES = S_L + C * LP * 4;
+};
 
 template <typename T, int DK, bool BWD>
 __global__ void __launch_bounds__(NT)
 gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_stride) {
+  using Sh = PrepShape<T, DK>;
   constexpr int NI = pieces<T>(), U = DK / 8, NP = BWD ? 2 : NI;
   constexpr uint32_t TILE = C * DK * 2;
   extern __shared__ __align__(128) unsigned char smem[];
-  float *Ls = reinterpret_cast<float *>(smem + 2 * NI * TILE);
-  __shared__ float s_num[2][C], s_r[2][C], s_g[2][C], s_beta[C];  // 1 / norm of k and q, with and without the pieces' unit; G; beta
-  __shared__ int s_max[2];
+  // the pieces of k and q, and over them, once used, their products [64][LP]
+  float *s_kk = reinterpret_cast<float *>(smem), *s_qk = s_kk + C * LP, *Ls = reinterpret_cast<float *>(smem + Sh::S_L);
+  __shared__ float s_num[2][C], s_r[2][C];       // 1 / norm of k and q, with and without the pieces' unit
+  __shared__ float s_g[HEADS][2][C], s_beta[HEADS][C], s_top[2][4];
+  __shared__ int s_max;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.x % p.Hk;
@@ -91,6 +107,8 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   {
     constexpr int RW = 32 / U;  // rows a warp takes at once
     const int u = lane % U;
+    float top[2] = {0.f, 0.f};
+#pragma unroll
     for (int which = 0; which < 2; ++which) {
       const T *src = static_cast<const T *>(which ? p.q : p.k) + batch * p.qk.b + tok * p.qk.t + hk * p.qk.h;
 #pragma unroll 4
@@ -128,7 +146,11 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
           s_num[which][r] = r < len ? f * sc.y : 0.f;
           s_r[which][r] = f;
         }
+        top[which] = fmaxf(top[which], ss * ((p.gp.flags & KDA_L2NORM_QK) ? 1.f / (ss + p.gp.eps) : 1.f));
       }
+#pragma unroll
+      for (int o = U; o < 32; o <<= 1) top[which] = fmaxf(top[which], __shfl_xor_sync(~0u, top[which], o));
+      if (lane == 0) s_top[which][warp] = top[which];
     }
   }
   __syncthreads();
@@ -172,162 +194,187 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
     }
   }
 
+  __syncthreads();  // the pieces are used
+  {
+    const int g = lane >> 2, t = (lane & 3) * 2;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      if (nt >= 2 * warp + 2) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = (16 * warp + g + 8 * h) * LP + 8 * nt + t;
+        *reinterpret_cast<float2 *>(s_kk + at) = make_float2(kk[nt][2 * h], kk[nt][2 * h + 1]);
+        *reinterpret_cast<float2 *>(s_qk + at) = make_float2(qk[nt][2 * h], qk[nt][2 * h + 1]);
+      }
+    }
+  }
+  // |P| is at most the scale times the largest norms: a unit for its pieces
+  // without looking at P itself (28 binades below it keep their bits)
+  const float bound = fabsf(p.gp.scale) * sqrtf(fmaxf(fmaxf(s_top[0][0], s_top[0][1]), fmaxf(s_top[0][2], s_top[0][3]))) *
+                      sqrtf(fmaxf(fmaxf(s_top[1][0], s_top[1][1]), fmaxf(s_top[1][2], s_top[1][3])));
+  const float2 sP = piece_scale(bound);
+
   const int group = p.H / p.Hk;
-  for (int hi_ = 0; hi_ < group; ++hi_) {
-    const int h = hk * group + hi_;
+  for (int hv = 0; hv < group; ++hv) {
+    const int h = hk * group + hv;
+    if (hv % HEADS == 0) {
+      __syncthreads();
+      if (hv + warp < group) {
+        // ---- the gate of head h + warp: two tokens a lane, running sum in two floats
+        const int hw = h + warp;
+        float *num = reinterpret_cast<float *>(ap + ((size_t)c * p.H + hw) * ap_stride);
+        const float nea = (p.gp.flags & KDA_GATE_IN_KERNEL) ? -expf(p.gp.a_log[hw]) : 0.f;
+        const float bias = p.gp.dt_bias ? p.gp.dt_bias[hw] : 0.f;
+        const int64_t off = batch * p.gate.b + tok * p.gate.t + hw * p.gate.h;
+        float g[2], b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 2 * lane + i;
+          g[i] = r < len ? log_decay(p.g[off + r * p.gate.t], p.gp, nea, bias) : 0.f;
+          b[i] = r < len ? p.beta[off + r * p.gate.t] : 0.f;
+          if ((p.gp.flags & KDA_BETA_SIGMOID) && r < len) b[i] = 1.f / (1.f + expf(-b[i]));
+        }
+        float sh = g[0], sl = 0.f;
+        add2(sh, sl, g[1], 0.f);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float h_ = __shfl_up_sync(~0u, sh, o), l_ = __shfl_up_sync(~0u, sl, o);
+          if (lane >= o) add2(sh, sl, h_, l_);
+        }
+        float Gh[2] = {sh, sh}, Gl[2] = {sl, sl};
+        add2(Gh[0], Gl[0], -g[1], 0.f);
+        const float Ch = __shfl_sync(~0u, sh, 31), Cl = __shfl_sync(~0u, sl, 31);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 2 * lane + i;
+          const float kn = s_num[0][r], qn = s_num[1][r];
+          const float e = expf(Gh[i] + Gl[i]), f = expf((Ch - Gh[i]) + (Cl - Gl[i]));
+          s_g[warp][0][r] = Gh[i];
+          s_g[warp][1][r] = Gl[i];
+          s_beta[warp][r] = b[i];
+          num[NUM_BETA + r] = b[i];
+          num[NUM_EK + r] = e * kn;
+          num[NUM_EQ + r] = e * qn * p.gp.scale;
+          num[NUM_FK + r] = f * kn;
+          num[NUM_K + r] = kn;
+          num[NUM_Q + r] = qn;
+          num[NUM_GH + r] = Gh[i];
+          num[NUM_GL + r] = Gl[i];
+          num[NUM_RK + r] = s_r[0][r];
+          num[NUM_RQ + r] = s_r[1][r];
+        }
+        if (lane == 0) {
+          num[NUM_MISC] = expf(Ch + Cl);
+          num[NUM_MISC + 2] = sP.y;
+        }
+      }
+    }
+    __syncthreads();  // the gates; the last head's A is out
     char *ap_out = ap + ((size_t)c * p.H + h) * ap_stride;
-    float *num = reinterpret_cast<float *>(ap_out);
-    if (hi_) __syncthreads();  // the last head's reads of shared memory are done
-    if (tid < 2) s_max[tid] = 0;
-    if (warp == 0) {
-      // ---- the gate: two tokens a lane, running sum in two floats
-      const float nea = (p.gp.flags & KDA_GATE_IN_KERNEL) ? -expf(p.gp.a_log[h]) : 0.f;
-      const float bias = p.gp.dt_bias ? p.gp.dt_bias[h] : 0.f;
-      const int64_t off = batch * p.gate.b + tok * p.gate.t + h * p.gate.h;
-      float g[2], b[2];
+    char *A = ap_out + NUM_BYTES, *Pm = A + 2 * MAT_BYTES;
+    const float *gh = s_g[hv % HEADS][0], *gl = s_g[hv % HEADS][1], *beta = s_beta[hv % HEADS];
+    if (tid == 0) s_max = 0;
+
+    // ---- L, and P on its way out: eight columns a thread, blocks of 16 down to the diagonal alone
+    for (int x = tid; x < 320; x += NT) {
+      // block row b has 2 (b + 1) units in each of its 16 rows: 32, 64, 96, 128 of them
+      const int b = x < 32 ? 0 : x < 96 ? 1 : x < 192 ? 2 : 3, y = x - 16 * b * (b + 1);
+      const int i = 16 * b + y % 16, u = y / 16;
+      const float hi_i = gh[i], lo_i = gl[i], ki = s_num[0][i] * beta[i], qi = s_num[1][i] * p.gp.scale * sP.x;
+      float pv[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * lane + i;
-        g[i] = r < len ? log_decay(p.g[off + r * p.gate.t], p.gp, nea, bias) : 0.f;
-        b[i] = r < len ? p.beta[off + r * p.gate.t] : 0.f;
-        if ((p.gp.flags & KDA_BETA_SIGMOID) && r < len) b[i] = 1.f / (1.f + expf(-b[i]));
+      for (int e = 0; e < 8; ++e) {
+        const int j = 8 * u + e;
+        float lv = 0.f;
+        pv[e] = 0.f;
+        if (j <= i) {
+          const float gam = expf((hi_i - gh[j]) + (lo_i - gl[j])) * s_num[0][j];
+          pv[e] = s_qk[i * LP + j] * gam * qi;
+          if (j < i) lv = s_kk[i * LP + j] * gam * ki;
+        }
+        Ls[i * LP + j] = lv;
       }
-      float sh = g[0], sl = 0.f;
-      add2(sh, sl, g[1], 0.f);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float h_ = __shfl_up_sync(~0u, sh, o), l_ = __shfl_up_sync(~0u, sl, o);
-        if (lane >= o) add2(sh, sl, h_, l_);
-      }
-      float Gh[2] = {sh, sh}, Gl[2] = {sl, sl};
-      add2(Gh[0], Gl[0], -g[1], 0.f);
-      const float Ch = __shfl_sync(~0u, sh, 31), Cl = __shfl_sync(~0u, sl, 31);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * lane + i;
-        const float kn = s_num[0][r], qn = s_num[1][r];
-        const float e = expf(Gh[i] + Gl[i]), f = expf((Ch - Gh[i]) + (Cl - Gl[i]));
-        s_g[0][r] = Gh[i];
-        s_g[1][r] = Gl[i];
-        s_beta[r] = b[i];
-        num[NUM_BETA + r] = b[i];
-        num[NUM_EK + r] = e * kn;
-        num[NUM_EQ + r] = e * qn * p.gp.scale;
-        num[NUM_FK + r] = f * kn;
-        num[NUM_K + r] = kn;
-        num[NUM_Q + r] = qn;
-        num[NUM_GH + r] = Gh[i];
-        num[NUM_GL + r] = Gl[i];
-        num[NUM_RK + r] = s_r[0][r];
-        num[NUM_RQ + r] = s_r[1][r];
-      }
-      if (lane == 0) num[NUM_MISC] = expf(Ch + Cl);
+      uint4 hi, lo;
+      split2(pv[0], pv[1], hi.x, lo.x);
+      split2(pv[2], pv[3], hi.y, lo.y);
+      split2(pv[4], pv[5], hi.z, lo.z);
+      split2(pv[6], pv[7], hi.w, lo.w);
+      *reinterpret_cast<uint4 *>(Pm + unit_at<8>(i, u)) = hi;
+      if constexpr (NP == 2) *reinterpret_cast<uint4 *>(Pm + MAT_BYTES + unit_at<8>(i, u)) = lo;
     }
     __syncthreads();
 
-    // ---- L into shared memory, P in registers
-    const int g = lane >> 2, t = (lane & 3) * 2;
-    float P[8][4];
-    float pm = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * warp + g + (e >> 1) * 8, j = 8 * nt + t + (e & 1);
-        float lv = 0.f, pv = 0.f;
-        if (j <= i) {
-          const float y = expf((s_g[0][i] - s_g[0][j]) + (s_g[1][i] - s_g[1][j])) * s_num[0][j];
-          pv = qk[nt][e] * s_num[1][i] * y * p.gp.scale;
-          if (j < i) lv = kk[nt][e] * s_num[0][i] * y * s_beta[i];
-        }
-        P[nt][e] = pv;
-        pm = fmaxf(pm, fabsf(pv));
-        if (nt < 2 * warp + 2) Ls[i * LP + j] = lv;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) pm = fmaxf(pm, __shfl_xor_sync(~0u, pm, o));
-    if (lane == 0) atomicMax(&s_max[1], __float_as_int(pm));
-    __syncwarp();
-
-    // ---- D_w, transposed into its own place
+    // ---- diagonal blocks, transposed into their own places
+    float top = 1.f;  // A's own diagonal
     {
       float x[16];
-      const float *Lw = Ls + 16 * warp * LP + 16 * warp;
+      const float *Lw = Ls + 16 * warp * (LP + 1);
       if (lane < 16) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          float s = i == lane ? 1.f : 0.f;
+          float s[2] = {i == lane ? 1.f : 0.f, 0.f};
 #pragma unroll
           for (int l = 0; l < 16; ++l)
-            if (l < i) s = fmaf(-Lw[i * LP + l], x[l], s);
-          x[i] = s;
+            if (l < i) s[l & 1] = fmaf(-Lw[i * LP + l], x[l], s[l & 1]);
+          x[i] = s[0] + s[1];
+          top = fmaxf(top, fabsf(x[i]));
         }
       }
       __syncwarp();
       if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) Ls[(16 * warp + lane) * LP + 16 * warp + i] = x[i];
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4 *>(Ls + (16 * warp + lane) * LP + 16 * warp + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
       }
     }
     __syncthreads();
-
-    // ---- block column `warp`
-    float am = block_max(Ls + 16 * warp * (LP + 1), lane);
-    for (int b = warp + 1; b < 4; ++b) {
+    // ---- blocks (1, 0) and (3, 2): a pair of warps each, eight columns a warp
+    {
+      const int d = 32 * (warp >> 1), col = 8 * (warp & 1);
+      float acc[1][4] = {};
+      block_product<1, 16, false, false>(acc, Ls + (d + 16) * LP + d, Ls + (d + col) * LP + d, lane, 1.f);
+      float *X = Ls + (d + col) * LP + d + 16;  // rows: columns of A; where block (1, 0) is kept
+      put_columns(acc, X, lane);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][e] = 0.f;
+      block_product<1, 16, true, false>(acc, Ls + (d + 16) * (LP + 1), X, lane, -1.f);
+      __syncwarp();
+      put_columns(acc, X, lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(acc[0][e]));
+    }
+    __syncthreads();
+    // ---- the block of 32 below: eight columns a warp
+    {
       float acc[2][4] = {};
-      // one unit for the products of this block row, from the largest of each side
-      float lm = 0.f;
-      for (int m = warp; m < b; ++m) lm = fmaxf(lm, block_max(Ls + 16 * b * LP + 16 * m, lane));
-      const float2 sl = piece_scale(lm), sa = piece_scale(am);
-      for (int m = warp; m < b; ++m) {
-        uint32_t lh[4], ll[4];
-        block_a(Ls + 16 * b * LP + 16 * m, lane, sl.x, lh, ll);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          uint32_t bh[2], bl[2];
-          block_b(Ls + 16 * warp * LP + 16 * m, lane, nt, sa.x, bh, bl);
-          mma3(acc[nt], lh, ll, bh, bl);
-        }
-      }
-      // M = sum over m, transposed to where A_bc will be, then A_bc = -D_b M
-      float *At = Ls + 16 * warp * LP + 16 * b;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) At[(8 * nt + t + (e & 1)) * LP + g + (e >> 1) * 8] = acc[nt][e] * sl.y * sa.y;
-      __syncwarp();
-      const float2 sm = piece_scale(block_max(At, lane)), sd = piece_scale(block_max(Ls + 16 * b * (LP + 1), lane));
-      uint32_t dh[4], dl[4], mh[2][2], ml[2][2];
-      block_at(Ls + 16 * b * (LP + 1), lane, -sd.x, dh, dl);
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        block_b(At, lane, nt, sm.x, mh[nt], ml[nt]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-        mma3(acc[nt], dh, dl, mh[nt], ml[nt]);
-      }
+      block_product<2, 32, false, false>(acc, Ls + 32 * LP, Ls + 8 * warp * LP, lane, 1.f, 16 * (warp >> 1));
+      float *X = Ls + 8 * warp * LP + 32;
+      put_columns(acc, X, lane);
       __syncwarp();
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) At[(8 * nt + t + (e & 1)) * LP + g + (e >> 1) * 8] = acc[nt][e] * sd.y * sm.y;
+        for (int e = 0; e < 4; ++e) acc[m][e] = 0.f;
+      block_product<2, 32, true, true>(acc, Ls + 32 * (LP + 1), X, lane, -1.f);
       __syncwarp();
-      am = fmaxf(am, block_max(At, lane));
+      put_columns(acc, X, lane);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(acc[m][e]));
     }
-    if (lane == 0) atomicMax(&s_max[0], __float_as_int(am));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) atomicMax(&s_max, __float_as_int(top));
     __syncthreads();
 
-    // ---- out: A (from its transposed blocks) and P
-    const float2 sA = piece_scale(__int_as_float(s_max[0])), sP = piece_scale(__int_as_float(s_max[1]));
-    char *A = ap_out + NUM_BYTES, *Pm = A + 2 * MAT_BYTES;
-    if (tid == 0) {
-      num[NUM_MISC + 1] = sA.y;
-      num[NUM_MISC + 2] = sP.y;
-    }
-    for (int x = tid; x < C * 8; x += NT) {
-      const int i = x & 63, u = x >> 6;
-      if ((u >> 1) > (i >> 4)) continue;
+    // ---- A out, from its transpose
+    const float2 sA = piece_scale(__int_as_float(s_max));
+    if (tid == 0) reinterpret_cast<float *>(ap_out)[NUM_MISC + 1] = sA.y;
+    for (int x = tid; x < 320; x += NT) {
+      const int b = x < 32 ? 0 : x < 96 ? 1 : x < 192 ? 2 : 3, y = x - 16 * b * (b + 1);
+      const int i = 16 * b + y % 16, u = y / 16;
       uint4 hi, lo;
       const float *col = Ls + 8 * u * LP + i;
       split2(col[0] * sA.x, col[LP] * sA.x, hi.x, lo.x);
@@ -337,18 +384,6 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
       *reinterpret_cast<uint4 *>(A + unit_at<8>(i, u)) = hi;
       *reinterpret_cast<uint4 *>(A + MAT_BYTES + unit_at<8>(i, u)) = lo;
     }
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      if (nt >= 2 * warp + 2) continue;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t at = unit_at<8>(16 * warp + g + 8 * r, nt) + t * 2;
-        uint32_t hi, lo;
-        split2(P[nt][2 * r] * sP.x, P[nt][2 * r + 1] * sP.x, hi, lo);
-        *reinterpret_cast<uint32_t *>(Pm + at) = hi;
-        if constexpr (NP == 2) *reinterpret_cast<uint32_t *>(Pm + MAT_BYTES + at) = lo;
-      }
-    }
   }
 }
 
@@ -357,8 +392,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
 cudaError_t launch_gdn_prep(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, cudaStream_t st) {
   if (p.nchunks == 0) return cudaSuccess;
   const size_t kqs = kq_bytes(dt, p.dk), aps = ap_bytes(dt, bwd);
-  const int smem = (int)kqs + C * LP * 4;
-  auto go = [&](auto kernel) {
+  auto go = [&](auto kernel, int smem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(p.nchunks * (int64_t)p.Hk), NT, smem, st>>>(p, ws + pl.off_kq, ws + pl.off_ap, kqs, aps);
@@ -366,11 +400,11 @@ cudaError_t launch_gdn_prep(kda_dtype dt, bool bwd, const Problem &p, char *ws, 
   };
   const bool w = p.dk == 128;
   if (dt == KDA_BF16) {
-    if (bwd) return w ? go(gdn_prep_kernel<__nv_bfloat16, 128, true>) : go(gdn_prep_kernel<__nv_bfloat16, 64, true>);
-    return w ? go(gdn_prep_kernel<__nv_bfloat16, 128, false>) : go(gdn_prep_kernel<__nv_bfloat16, 64, false>);
+    if (bwd) return w ? go(gdn_prep_kernel<__nv_bfloat16, 128, true>, PrepShape<__nv_bfloat16, 128>::BYTES) : go(gdn_prep_kernel<__nv_bfloat16, 64, true>, PrepShape<__nv_bfloat16, 64>::BYTES);
+    return w ? go(gdn_prep_kernel<__nv_bfloat16, 128, false>, PrepShape<__nv_bfloat16, 128>::BYTES) : go(gdn_prep_kernel<__nv_bfloat16, 64, false>, PrepShape<__nv_bfloat16, 64>::BYTES);
   }
-  if (bwd) return w ? go(gdn_prep_kernel<float, 128, true>) : go(gdn_prep_kernel<float, 64, true>);
-  return w ? go(gdn_prep_kernel<float, 128, false>) : go(gdn_prep_kernel<float, 64, false>);
+  if (bwd) return w ? go(gdn_prep_kernel<float, 128, true>, PrepShape<float, 128>::BYTES) : go(gdn_prep_kernel<float, 64, true>, PrepShape<float, 64>::BYTES);
+  return w ? go(gdn_prep_kernel<float, 128, false>, PrepShape<float, 128>::BYTES) : go(gdn_prep_kernel<float, 64, false>, PrepShape<float, 64>::BYTES);
 }
 
 }  // namespace gdn
