@@ -85,8 +85,8 @@ inline size_t ap_bytes(kda_dtype d, bool bwd) { return NUM_BYTES + (size_t)MAT_B
 // the order in which a warp's lanes hold it ([16 value channels][8 columns]
 // tiles, four values a lane): the state entering the chunk and the gradient of
 // the one leaving it ([dv, dk]), W, e^G k S and dY ([dv, 64]); the largest of
-// each of S, dS, W, dY, dO in each warp's 16 channels; sums over the channels
-// for each token; the sums of a_log's and dt_bias's gradients.
+// each of S, dS, W, dY, dO in each warp's 16 channels; sums over each 64
+// channels for each token; the sums of a_log's and dt_bias's gradients.
 struct Plan {
   size_t off_chunks, off_kq, off_ap, off_s, off_ds, off_w, off_e, off_dy, off_max, off_dots, off_part, total;
 };
@@ -106,7 +106,7 @@ inline Plan make_gdn_plan(kda_dtype d, int64_t nchunks, int N, int H, int Hk, in
     p.off_e = o; o = align256(o + u * C * dv * 4);
     p.off_dy = o; o = align256(o + u * C * dv * 4);
     p.off_max = o; o = align256(o + u * MAX_FLOATS * 4);
-    p.off_dots = o; o = align256(o + u * DOT_FLOATS * 4);
+    p.off_dots = o; o = align256(o + u * 2 * DOT_FLOATS * 4);
     p.off_part = o; o = align256(o + u * 2 * 4);
   }
   p.total = o;
@@ -153,6 +153,62 @@ __device__ __forceinline__ void cp16z(uint32_t dst, const void *src, bool fill) 
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Named barriers of a CTA: `threads` of them arrive, some of these wait.
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// The chains' two buffers (bf16): four more warps fill them, groups of four
+// warps, one on each of the SM's schedulers, empty them.  The groups never meet
+// each other, so that one can be at its products while the other is at its
+// elementwise work: together, as a barrier for all keeps them, they wait for
+// the same unit at a time (measured on the training batch: 774 us, 12 k cycles
+// a chunk, of which the tensor cores' share is 6.4 k).
+// The second group starts this much later where there are chunks enough for it.
+constexpr int SKEW_CHUNKS = 8, SKEW_NS = 3000;
+constexpr int GROUP = 128, FILL = 128, BAR_FULL = 1, BAR_EMPTY = 5, BAR_GROUP = 9;
+__device__ __forceinline__ int bar_full(int stage, int group) { return BAR_FULL + 2 * stage + group; }
+__device__ __forceinline__ int bar_empty(int stage, int group) { return BAR_EMPTY + 2 * stage + group; }
+
+// Registers: the launch gives each of 12 warps 168 a thread; the four that fill
+// give up what the eight that compute need, 128 * 40 + 256 * 232 = 384 * 168.
+// With four computing warps there is room without.
+template <int WARPS> __device__ __forceinline__ void registers_to_fill() {
+  if constexpr (WARPS == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+}
+template <int WARPS> __device__ __forceinline__ void registers_to_compute() {
+  if constexpr (WARPS == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+}
+
+// The filling warps: load(c) starts chunk c's copies (c counts from 0 in the
+// order of use).
+template <int GROUPS, typename F> __device__ __forceinline__ void fill_buffers(int nc, F load) {
+  for (int c = 0; c <= nc; ++c) {
+    if (c >= 1) {  // the one before has arrived: first of all this is told
+      cp_wait<0>();
+      __threadfence_block();
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) bar_arrive(bar_full((c - 1) & 1, g), GROUP + FILL);
+    }
+    if (c == nc) break;
+    if (c >= 2) {
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) bar_sync(bar_empty(c & 1, g), GROUP + FILL);
+    }
+    load(c);
+    cp_commit();
+  }
+}
+// [64 tokens][16 W channels] of bf16 as W strips [64][16] (a warp's), rows past
+// the end zero (src is then not read).
+template <int W> __device__ __forceinline__ void load_strips(uint32_t dst, const __nv_bfloat16 *src, int64_t stride, int64_t rows, int first) {
+#pragma unroll 4
+  for (int x = first; x < C * 2 * W; x += FILL) {
+    const int r = x / (2 * W), u = x % (2 * W);
+    const bool in = src && r < rows;
+    cp16z(dst + (u >> 1) * (C * 32) + r * 32 + (u & 1) * 16, in ? src + r * stride + u * 8 : src, in);
+  }
+}
 
 // Byte offset of 16-byte unit u of row r, rows of U units (8 or 16).
 template <int U> __device__ __forceinline__ uint32_t unit_at(int r, int u) { return (uint32_t)((r * U + (u ^ (r & 7))) * 16); }

@@ -24,7 +24,7 @@ namespace {
 
 // ---------------------------------------------------------------- chain, backwards
 template <typename T, int DK, int WARPS> struct RevShape {
-  static constexpr int NI = pieces<T>(), STAGES = NI == 1 ? 2 : 1;
+  static constexpr int NI = pieces<T>(), STAGES = NI == 1 ? 2 : 1, THREADS = WARPS * 32 + (STAGES == 2 ? FILL : 0);
   static constexpr uint32_t TILE = C * DK * 2, STRIP = C * 16 * sizeof(T);
   static constexpr uint32_t S_K = 0, S_Q = NI * TILE, S_NUM = 2 * NI * TILE, S_A = S_NUM + NUM_BYTES, S_P = S_A + 2 * MAT_BYTES,
                             S_DO = S_P + 2 * MAT_BYTES, S_V = S_DO + WARPS * STRIP, STAGE = (S_V + WARPS * STRIP + 127) / 128 * 128;
@@ -55,18 +55,26 @@ template <typename T> __device__ __forceinline__ void load_strip(const unsigned 
   }
 }
 
-// Sums over a warp's 16 channels for tokens t, t + 1 of a tile, to shared memory.
-__device__ __forceinline__ void channel_sums(float a, float b, int lane, float *to) {
+// Sums over a warp's 16 channels for all 64 tokens: x[2 tile + e] is this
+// lane's part (two channels) for token 8 tile + 2 (lane % 4) + e.  The lanes
+// share out the tiles as they add, so that 14 exchanges do.
+__device__ __forceinline__ void channel_sums(float (&x)[16], int lane, float *to) {
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    a += __shfl_xor_sync(~0u, a, o);
-    b += __shfl_xor_sync(~0u, b, o);
+  for (int n = 8; n >= 2; n >>= 1) {
+    const int bit = 2 * n;  // lanes 16, 8, 4 apart
+    const bool up = lane & bit;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+      x[i] = keep + __shfl_xor_sync(~0u, send, bit);
+    }
   }
-  if (lane < 4) *reinterpret_cast<float2 *>(to + lane * 2) = make_float2(a, b);
+  const int tile = (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
+  *reinterpret_cast<float2 *>(to + 8 * tile + 2 * (lane & 3)) = make_float2(x[0], x[1]);
 }
 
 template <typename T, int DK, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 1)
+__global__ void __launch_bounds__(RevShape<T, DK, WARPS>::THREADS, 1)
 gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_stride, GradOut io) {
   using Sh = RevShape<T, DK, WARPS>;
   constexpr int NI = Sh::NI, U = DK / 8, NK = DK / 8;
@@ -88,6 +96,40 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
   T *dv = static_cast<T *>(io.dv) + v_off;
   float *s_dots = reinterpret_cast<float *>(smem + Sh::S_DOTS) + warp * DOT_FLOATS;
 
+  const uint32_t base = smem_addr(smem);
+  auto load = [&](int c, uint32_t stage, uint32_t first, uint32_t step) {
+    const char *a = kq + ((size_t)(c0 + c) * p.Hk + hk) * kq_stride, *b = ap + ((size_t)(c0 + c) * p.H + h) * ap_stride;
+#pragma unroll 4
+    for (uint32_t x = first; x < Sh::S_NUM; x += step) cp16(stage + Sh::S_K + x, a + x);
+#pragma unroll 4
+    for (uint32_t x = first; x < Sh::S_DO - Sh::S_NUM; x += step) cp16(stage + Sh::S_NUM + x, b + x);
+  };
+  if constexpr (Sh::STAGES == 2) {
+    if (warp >= WARPS) {
+      registers_to_fill<WARPS>();
+      const int first = tid - WARPS * 32;
+      const T *vs = v - warp * 16, *os = d_out ? d_out - warp * 16 : nullptr;
+      fill_buffers<WARPS / 4>(nc, [&](int i) {
+        const int c = nc - 1 - i;
+        const uint32_t stage = base + (i & 1) * Sh::STAGE;
+        const int64_t r0 = (int64_t)c * C;
+        load(c, stage, first * 16, FILL * 16);
+        load_strips<WARPS>(stage + Sh::S_DO, os ? os + r0 * p.v.t : nullptr, p.v.t, t1 - t0 - r0, first);
+        load_strips<WARPS>(stage + Sh::S_V, vs + r0 * p.v.t, p.v.t, t1 - t0 - r0, first);
+        // what this chunk's warps read themselves is on its way to L2 as well
+        const int64_t unit = (c0 + c) * p.H + h;
+        const char *w = ws + pl.off_w + unit * (WARPS * 16 * C * 4), *e = ws + pl.off_e + unit * (WARPS * 16 * C * 4);
+        for (int x = first * 128; x < WARPS * 16 * C * 4; x += FILL * 128) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(w + x));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(e + x));
+        }
+      });
+      return;
+    }
+    registers_to_compute<WARPS>();
+  }
+  const int group = warp >> 2;
+
   const int64_t s_off = ((int64_t)n * p.H + h) * DK * p.dv;
   const int64_t sk = p.v_first ? 1 : p.dv, sv = p.v_first ? DK : 1;
   float D[NK][4];
@@ -97,38 +139,28 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     for (int e = 0; e < 4; ++e)
       D[i][e] = io.d_final ? io.d_final[s_off + (8 * i + t + (e & 1)) * sk + (v0 + g + (e >> 1) * 8) * sv] : 0.f;
 
-  const uint32_t base = smem_addr(smem);
-  auto load = [&](int c, uint32_t stage) {
-    const char *a = kq + ((size_t)(c0 + c) * p.Hk + hk) * kq_stride, *b = ap + ((size_t)(c0 + c) * p.H + h) * ap_stride;
-    for (uint32_t x = tid * 16; x < Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_K + x, a + x);
-    for (uint32_t x = tid * 16; x < Sh::S_DO - Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_NUM + x, b + x);
-    constexpr int PER = sizeof(T);  // 16-byte units of a row of the strip
-#pragma unroll
-    for (int x = lane; x < C * PER; x += 32) {
-      const int64_t r = (int64_t)c * C + x / PER;
-      const bool in = r < t1 - t0;
-      const int64_t at = (in ? r * p.v.t : 0) + x % PER * (16 / sizeof(T));
-      cp16z(stage + Sh::S_V + warp * Sh::STRIP + x * 16, v + at, in);
-      cp16z(stage + Sh::S_DO + warp * Sh::STRIP + x * 16, d_out ? d_out + at : v + at, in && d_out);
-    }
-    cp_commit();
-  };
-
   const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;
   const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;
-  if (Sh::STAGES == 2 && nc > 0) load(nc - 1, base + ((nc - 1) & 1) * Sh::STAGE);
+  if (Sh::STAGES == 2 && group == 1 && nc >= SKEW_CHUNKS) __nanosleep(SKEW_NS);
   for (int c = nc - 1; c >= 0; --c) {
-    const uint32_t so = Sh::STAGES == 2 ? (c & 1) * Sh::STAGE : 0, st = base + so;
-    if (Sh::STAGES == 1) {
-      load(c, st);
-      cp_wait<0>();
-    } else if (c > 0) {
-      load(c - 1, base + ((c - 1) & 1) * Sh::STAGE);
-      cp_wait<1>();
+    const int stage = (nc - 1 - c) & 1;
+    const uint32_t so = Sh::STAGES == 2 ? stage * Sh::STAGE : 0, st = base + so;
+    if constexpr (Sh::STAGES == 2) {
+      bar_sync(bar_full(stage, group), GROUP + FILL);
     } else {
+      load(c, st, tid * 16, WARPS * 512);
+#pragma unroll
+      for (int x = lane; x < C * 4; x += 32) {
+        const int64_t r = (int64_t)c * C + x / 4;
+        const bool in = r < t1 - t0;
+        const int64_t at = (in ? r * p.v.t : 0) + x % 4 * 4;
+        cp16z(st + Sh::S_V + warp * Sh::STRIP + x * 16, v + at, in);
+        cp16z(st + Sh::S_DO + warp * Sh::STRIP + x * 16, d_out ? d_out + at : v + at, in && d_out);
+      }
+      cp_commit();
       cp_wait<0>();
+      __syncthreads();
     }
-    __syncthreads();
     const float *num = reinterpret_cast<const float *>(smem + so + Sh::S_NUM);
     const int64_t unit = (c0 + c) * p.H + h;
     float *maxes = reinterpret_cast<float *>(ws + pl.off_max) + unit * MAX_FLOATS + warp;
@@ -170,6 +202,7 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
         mma_row(X, ah, b);
       }
     }
+    float dots[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 fk = *reinterpret_cast<const float2 *>(num + NUM_FK + 8 * i + t);
@@ -177,8 +210,10 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
       X[i][1] = X[i][1] * fk.y * z0.y;
       X[i][2] = X[i][2] * fk.x * z1.y;
       X[i][3] = X[i][3] * fk.y * z1.y;
-      channel_sums(wv[i].x * X[i][0] + wv[i].z * X[i][2], wv[i].y * X[i][1] + wv[i].w * X[i][3], lane, s_dots + DOT_Y + 8 * i);
+      dots[2 * i] = wv[i].x * X[i][0] + wv[i].z * X[i][2];
+      dots[2 * i + 1] = wv[i].y * X[i][1] + wv[i].w * X[i][3];
     }
+    channel_sums(dots, lane, s_dots + DOT_Y);
 
     // ---- dW = X + P^T dO
     float O[8][4], Y[8][4];
@@ -253,16 +288,21 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
       Y[i][3] = Y[i][3] * a * z1.y;
       ym = fmaxf(ym, fmaxf(fmaxf(fabsf(Y[i][0]), fabsf(Y[i][1])), fmaxf(fabsf(Y[i][2]), fabsf(Y[i][3]))));
       dy_to[i * 32] = make_float4(Y[i][0], Y[i][1], Y[i][2], Y[i][3]);
+      dots[2 * i] = Y[i][0] * (O[i][0] - ev[i].x) + Y[i][2] * (O[i][2] - ev[i].z);
+      dots[2 * i + 1] = Y[i][1] * (O[i][1] - ev[i].y) + Y[i][3] * (O[i][3] - ev[i].w);
+    }
+    channel_sums(dots, lane, s_dots + DOT_BETA);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       const float2 be = *reinterpret_cast<const float2 *>(num + NUM_BETA + 8 * i + t);
-      channel_sums(Y[i][0] * (O[i][0] - ev[i].x) + Y[i][2] * (O[i][2] - ev[i].z),
-                   Y[i][1] * (O[i][1] - ev[i].y) + Y[i][3] * (O[i][3] - ev[i].w), lane, s_dots + DOT_BETA + 8 * i);
       Y[i][0] *= be.x;
       Y[i][1] *= be.y;
       Y[i][2] *= be.x;
       Y[i][3] *= be.y;
-      channel_sums(-(Y[i][0] * ev[i].x + Y[i][2] * ev[i].z), -(Y[i][1] * ev[i].y + Y[i][3] * ev[i].w), lane,
-                   s_dots + DOT_K + 8 * i);
+      dots[2 * i] = -(Y[i][0] * ev[i].x + Y[i][2] * ev[i].z);
+      dots[2 * i + 1] = -(Y[i][1] * ev[i].y + Y[i][3] * ev[i].w);
     }
+    channel_sums(dots, lane, s_dots + DOT_K);
 #pragma unroll
     for (int o = 16; o; o >>= 1) ym = fmaxf(ym, __shfl_xor_sync(~0u, ym, o));
     if (lane == 0) maxes[MAX_DY] = ym;
@@ -351,22 +391,15 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
         }
       }
     }
-    __syncthreads();  // the buffer may be refilled; all warps' sums are there
-    if (tid < DOT_FLOATS) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) s += reinterpret_cast<const float *>(smem + Sh::S_DOTS)[w * DOT_FLOATS + tid];
-      reinterpret_cast<float *>(ws + pl.off_dots)[unit * DOT_FLOATS + tid] = s;
-    }
-    if constexpr (WARPS * 32 < DOT_FLOATS) {
-      const int x = WARPS * 32 + tid;
-      if (x < DOT_FLOATS) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += reinterpret_cast<const float *>(smem + Sh::S_DOTS)[w * DOT_FLOATS + x];
-        reinterpret_cast<float *>(ws + pl.off_dots)[unit * DOT_FLOATS + x] = s;
-      }
-    }
+    // the buffer may be refilled; a group's four warps add their sums
+    if constexpr (Sh::STAGES == 1) __syncthreads();
+    else if (c >= 2) bar_arrive(bar_empty(stage, group), GROUP + FILL);
+    bar_sync(BAR_GROUP + group, GROUP);
+    float *to = reinterpret_cast<float *>(ws + pl.off_dots) + (unit * 2 + group) * DOT_FLOATS;
+    const float *from = reinterpret_cast<const float *>(smem + Sh::S_DOTS) + group * 4 * DOT_FLOATS;
+    for (int x = tid & (GROUP - 1); x < DOT_FLOATS; x += GROUP)
+      to[x] = (from[x] + from[DOT_FLOATS + x]) + (from[2 * DOT_FLOATS + x] + from[3 * DOT_FLOATS + x]);
+    if constexpr (Sh::STAGES == 1) __syncthreads();
   }
 
   if (io.d_initial) {
@@ -422,7 +455,8 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         *s_db = s_e;  // [2][C], once e^G is used
   int *s_max = reinterpret_cast<int *>(s_iq + 4 * C);  // [3]
   float *s_z = s_iq + 4 * C + 4;                       // [16]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mt = warp & 3, quarter = warp >> 2, half = quarter >> 1, side = quarter & 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quarter = warp >> 2, half = quarter >> 1, side = quarter & 1;
+  const int mt = side ? 3 - (warp & 3) : warp & 3;  // later rows have more to do: each scheduler gets early and late ones
   const int g = lane >> 2, t = (lane & 3) * 2;
   const int hk = (int)(blockIdx.x % p.Hk);
   const int64_t c = blockIdx.x / p.Hk;
@@ -814,7 +848,8 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     }
     __syncthreads();
     if (warp == 0) {
-      const float *dots = reinterpret_cast<const float *>(ws + pl.off_dots) + unit * DOT_FLOATS;
+      const float *sums = reinterpret_cast<const float *>(ws + pl.off_dots) + unit * 2 * DOT_FLOATS;
+      auto dots = [&](int at) { return DV == 128 ? sums[at] + sums[DOT_FLOATS + at] : sums[at]; };
       float F[2], I[2], Y[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -823,8 +858,8 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
 #pragma unroll 8
         for (int j = 0; j < r; ++j) s += x_at(r, j);
         F[i] = s;
-        I[i] = (s_iq[r] + s_iq[C + r]) + (s_iq[2 * C + r] + s_iq[3 * C + r]) + dots[DOT_K + r];
-        Y[i] = dots[DOT_Y + r];
+        I[i] = (s_iq[r] + s_iq[C + r]) + (s_iq[2 * C + r] + s_iq[3 * C + r]) + dots(DOT_K + r);
+        Y[i] = dots(DOT_Y + r);
       }
       float si = I[0] + I[1], sy = Y[0] + Y[1];
 #pragma unroll
@@ -857,7 +892,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
             dt += dx;
           }
           io.dg[off + r * p.gate.t] = dx;
-          float d = dots[DOT_BETA + r] + (s_db[r] + s_db[C + r]);
+          float d = dots(DOT_BETA + r) + (s_db[r] + s_db[C + r]);
           if (p.gp.flags & KDA_BETA_SIGMOID) d *= be * (1.f - be);
           io.dbeta[off + r * p.gate.t] = d;
         }
@@ -967,7 +1002,7 @@ template <typename T, int DK, int DV> cudaError_t go(const Problem &p, char *ws,
   cudaError_t e = cudaFuncSetAttribute(reverse, cudaFuncAttributeMaxDynamicSharedMemorySize, rev_smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(intra, cudaFuncAttributeMaxDynamicSharedMemorySize, in_smem);
   if (e != cudaSuccess) return e;
-  reverse<<<(unsigned)((int64_t)p.s.N * p.H), DV * 2, rev_smem, st>>>(p, ws, pl, kqs, aps, io);
+  reverse<<<(unsigned)((int64_t)p.s.N * p.H), RevShape<T, DK, DV / 16>::THREADS, rev_smem, st>>>(p, ws, pl, kqs, aps, io);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.nchunks > 0) {
     intra<<<(unsigned)((int64_t)p.nchunks * p.Hk), NT, in_smem, st>>>(p, ws, pl, kqs, aps, io);

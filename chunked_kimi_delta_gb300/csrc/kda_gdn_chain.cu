@@ -16,7 +16,7 @@ namespace {
 
 template <typename T, int DK, int WARPS, bool STORE> struct Shape {
   static constexpr int NI = pieces<T>(), NP = STORE ? 2 : NI;
-  static constexpr int STAGES = NI == 1 ? 2 : 1;
+  static constexpr int STAGES = NI == 1 ? 2 : 1, THREADS = WARPS * 32 + (STAGES == 2 ? FILL : 0);
   static constexpr uint32_t TILE = C * DK * 2;
   static constexpr uint32_t S_K = 0, S_Q = NI * TILE, S_NUM = 2 * NI * TILE, S_A = S_NUM + NUM_BYTES,
                             S_P = S_A + 2 * MAT_BYTES, S_V = S_P + NP * MAT_BYTES;
@@ -27,7 +27,7 @@ template <typename T, int DK, int WARPS, bool STORE> struct Shape {
 };
 
 template <typename T, int DK, int WARPS, bool STORE>
-__global__ void __launch_bounds__(WARPS * 32, 1)
+__global__ void __launch_bounds__(Shape<T, DK, WARPS, STORE>::THREADS, 1)
 gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_stride, ChainOut io) {
   using Sh = Shape<T, DK, WARPS, STORE>;
   constexpr int NI = Sh::NI, U = DK / 8, NK = DK / 8;
@@ -51,6 +51,31 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
   const T *v = static_cast<const T *>(p.val) + v_off;
   T *out = STORE ? nullptr : static_cast<T *>(io.out) + v_off;
 
+  const uint32_t base = smem_addr(smem);
+  const uint32_t kq_part = STORE ? Sh::S_Q : Sh::S_NUM, ap_part = (STORE ? Sh::S_P : Sh::S_V) - Sh::S_NUM;  // q and P are for o alone
+  auto load = [&](int c, uint32_t stage, uint32_t first, uint32_t step) {
+    const char *a = kq + ((size_t)(c0 + c) * p.Hk + hk) * kq_stride, *b = ap + ((size_t)(c0 + c) * p.H + h) * ap_stride;
+#pragma unroll 4
+    for (uint32_t x = first; x < kq_part; x += step) cp16(stage + Sh::S_K + x, a + x);
+#pragma unroll 4
+    for (uint32_t x = first; x < ap_part; x += step) cp16(stage + Sh::S_NUM + x, b + x);
+  };
+  if constexpr (Sh::STAGES == 2) {
+    if (warp >= WARPS) {
+      registers_to_fill<WARPS>();
+      const int first = tid - WARPS * 32;
+      const T *vs = v - warp * 16;
+      fill_buffers<WARPS / 4>(nc, [&](int c) {
+        const uint32_t stage = base + (c & 1) * Sh::STAGE;
+        load(c, stage, first * 16, FILL * 16);
+        load_strips<WARPS>(stage + Sh::S_V, vs + (int64_t)c * C * p.v.t, p.v.t, t1 - t0 - (int64_t)c * C, first);
+      });
+      return;
+    }
+    registers_to_compute<WARPS>();
+  }
+  const int group = warp >> 2;
+
   // S^T: channel of k along the columns.  (row, column) of a state in memory
   const int64_t s_off = ((int64_t)n * p.H + h) * DK * p.dv;
   const int64_t sk = p.v_first ? 1 : p.dv, sv = p.v_first ? DK : 1;
@@ -61,37 +86,26 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     for (int e = 0; e < 4; ++e)
       S[i][e] = io.initial ? io.initial[s_off + (8 * i + t + (e & 1)) * sk + (v0 + g + (e >> 1) * 8) * sv] : 0.f;
 
-  const uint32_t base = smem_addr(smem);
-  auto load = [&](int c, uint32_t stage) {
-    const char *a = kq + ((size_t)(c0 + c) * p.Hk + hk) * kq_stride, *b = ap + ((size_t)(c0 + c) * p.H + h) * ap_stride;
-    for (uint32_t x = tid * 16; x < (STORE ? Sh::S_Q : Sh::S_NUM); x += WARPS * 512) cp16(stage + Sh::S_K + x, a + x);
-    for (uint32_t x = tid * 16; x < (STORE ? Sh::S_P : Sh::S_V) - Sh::S_NUM; x += WARPS * 512) cp16(stage + Sh::S_NUM + x, b + x);
-    constexpr int PER = 16 * sizeof(T) / 16;  // 16-byte units of a row of the strip
-    const uint32_t strip = stage + Sh::S_V + warp * Sh::V_STRIP;
-#pragma unroll
-    for (int x = lane; x < C * PER; x += 32) {
-      const int64_t r = (int64_t)c * C + x / PER;
-      const bool in = r < t1 - t0;
-      cp16z(strip + x * 16, v + (in ? r * p.v.t : 0) + x % PER * (16 / sizeof(T)), in);
-    }
-    cp_commit();
-  };
-
   const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;  // right operand, rows are its columns
   const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;  // right operand, transposed on the way
-  if (Sh::STAGES == 2 && nc > 0) load(0, base);
+  if (Sh::STAGES == 2 && group == 1 && nc >= SKEW_CHUNKS) __nanosleep(SKEW_NS);
   for (int c = 0; c < nc; ++c) {
     const uint32_t st = base + (Sh::STAGES == 2 ? (c & 1) * Sh::STAGE : 0);
-    if (Sh::STAGES == 1) {
-      load(c, st);
-      cp_wait<0>();
-    } else if (c + 1 < nc) {
-      load(c + 1, base + ((c + 1) & 1) * Sh::STAGE);
-      cp_wait<1>();
+    if constexpr (Sh::STAGES == 2) {
+      bar_sync(bar_full(c & 1, group), GROUP + FILL);
     } else {
+      load(c, st, tid * 16, WARPS * 512);
+      const uint32_t strip = st + Sh::S_V + warp * Sh::V_STRIP;
+#pragma unroll
+      for (int x = lane; x < C * 4; x += 32) {
+        const int64_t r = (int64_t)c * C + x / 4;
+        const bool in = r < t1 - t0;
+        cp16z(strip + x * 16, v + (in ? r * p.v.t : 0) + x % 4 * 4, in);
+      }
+      cp_commit();
       cp_wait<0>();
+      __syncthreads();
     }
-    __syncthreads();
     const float *num = reinterpret_cast<const float *>(smem + (st - base) + Sh::S_NUM);
 
     // ---- S^T k^T and S^T q^T
@@ -318,7 +332,9 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         S[2 * q + i][3] = ec * S[2 * q + i][3] + acc[i][3] * z1.y;
       }
     }
-    __syncthreads();  // the buffer may be refilled
+    // the buffer may be refilled
+    if constexpr (Sh::STAGES == 1) __syncthreads();
+    else if (c + 2 < nc) bar_arrive(bar_empty(c & 1, group), GROUP + FILL);
   }
 
   if (io.final_state) {
@@ -338,7 +354,7 @@ cudaError_t go(const Problem &p, char *ws, const Plan &pl, const ChainOut &io, c
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)p.s.N * p.H * (p.dv / (16 * WARPS));
-  kernel<<<(unsigned)grid, WARPS * 32, smem, st>>>(p, ws, pl, kq_bytes(dt, p.dk), ap_bytes(dt, STORE), io);
+  kernel<<<(unsigned)grid, Shape<T, DK, WARPS, STORE>::THREADS, smem, st>>>(p, ws, pl, kq_bytes(dt, p.dk), ap_bytes(dt, STORE), io);
   return cudaGetLastError();
 }
 
