@@ -100,21 +100,6 @@ template <typename T, int V> struct Eight {
       for (int i = 0; i < 8; ++i) f[i] = left > i ? p[i] : 0.f;
     }
   }
-  // The values themselves (one piece, or fp32).
-  static __device__ __forceinline__ void values(const T *p, int64_t left, float (&f)[8]) {
-    if constexpr (sizeof(T) == 2) {
-      Eight e;
-      e.load(p, left);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack2(e.x[0][i]);
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-      }
-    } else {
-      load_f32(p, left, f);
-    }
-  }
   static __device__ __forceinline__ void store(T *p, int64_t left, const float (&f)[8]) {
     if constexpr (sizeof(T) == 2) {
       const uint32_t w[4] = {pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
@@ -136,6 +121,37 @@ template <typename T, int V> struct Eight {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (left > i) p[i] = f[i];
+    }
+  }
+};
+
+// Eight neighbouring values as they are stored.
+template <typename T, int V> struct Raw {
+  uint32_t w[2 * sizeof(T)];
+  __device__ __forceinline__ void load(const T *p, int64_t left) {
+    if constexpr (sizeof(T) == 2) {
+      Eight<T, V> e;
+      e.load(p, left);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = e.x[0][i];
+    } else {
+      float f[8];
+      Eight<T, V>::load_f32(p, left, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[i]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2(w[i]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
     }
   }
 };
@@ -245,17 +261,17 @@ template <int M> __device__ __forceinline__ void find_tile(const Args &a, int64_
   }
 }
 
-// M rows a tile, RP ranks.  Warps share the sum over n_in KW ways; a warp has
-// MT tiles of 16 rows.
+// M rows a tile, RP ranks.  A warp has 16 rows; warps share the sum over n_in
+// KW ways.
 template <int M, int RP> struct Shape {
-  static constexpr int MT = M == 16 || RP == 128 ? 1 : 2, MG = M / (16 * MT), KW = 8 / MG;
+  static constexpr int MT = 1, MG = M / (16 * MT), KW = 8 / MG;
   static constexpr int PITCH = RP + 8;  // elements a row of u's pieces
   static constexpr size_t PART = (size_t)KW * M * RP * 4, U = (size_t)M * RP * 4, PIECES = (size_t)3 * M * PITCH * 2;
   static constexpr size_t BYTES = U + (PART > PIECES ? PART : PIECES);
 };
 
 template <typename T, int M, int RP, int V>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 && RP <= 32 ? 2 : 1) lora_kernel(Args a) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 && RP <= 64 ? 2 : 1) lora_kernel(Args a) {
   using Sh = Shape<M, RP>;
   constexpr int MT = Sh::MT, KW = Sh::KW, NI = Type<T>::IN, NU = Type<T>::U, RT = RP / 8, PITCH = Sh::PITCH;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -431,14 +447,24 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && RP <= 32 ? 2 : 1) lora_k
         }
       }
     }
+    // y of all rows on its way before the first product
+    Raw<T, V> yr[M / 16][2];
+    if (y) {
+#pragma unroll
+      for (int m = 0; m < M / 16; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = m * 16 + g + 8 * h;
+          yr[m][h].load(y + (int64_t)r * a.n_out + col, r < len ? left : 0);
+        }
+    }
 #pragma unroll
     for (int m = 0; m < M / 16; ++m) {
       if (m * 16 >= len) break;
       float v[2][8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = m * 16 + g + 8 * h;
-        if (y) Eight<T, V>::values(y + (int64_t)(r < len ? r : len - 1) * a.n_out + col, left, v[h]);
+        if (y) yr[m][h].get(v[h]);
         else
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[h][i] = 0.f;
@@ -754,13 +780,21 @@ cudaError_t grad_rank(int rp, const void *wide, int n, const void *narrow, const
   }
 }
 
-// Shares of the rows: until there are two CTAs an SM, at least 512 rows each.
+// Shares of the rows, at least 512 in each: of up to eight the number that
+// leaves the fewest SMs idle in its last round, the smaller of two alike.
 int shares_of(int n, int rp, int L, int64_t rows, int sms) {
   const int64_t cols = rp == 128 ? 128 : 256, ctas = (n + cols - 1) / cols * L;
-  int64_t s = (2 * sms + ctas - 1) / ctas;
-  const int64_t most = (rows + 511) / 512;
-  s = s < most ? s : most;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  int best = 1;
+  double most = 0;
+  for (int s = 1; s <= 8 && (s == 1 || rows >= 512 * (int64_t)s); ++s) {
+    const int64_t rounds = (ctas * s + sms - 1) / sms;
+    const double busy = (double)(ctas * s) / (double)(rounds * sms);
+    if (busy > most * 1.02) {
+      most = busy;
+      best = s;
+    }
+  }
+  return best;
 }
 
 }  // namespace
