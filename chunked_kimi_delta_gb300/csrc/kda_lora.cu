@@ -6,11 +6,12 @@
 // columns of the result.  So u never leaves the chip, one launch does it all,
 // and a decode batch of single rows still uses every SM.
 //
-// Operands go from global memory to the tensor cores' registers directly: a
-// sum does not care for the order of its terms, so a lane takes eight
-// neighbouring values of a row (16 bytes) as its share of two k steps of 16,
-// on both sides alike; and the columns of a result tile are dealt so that a
-// lane ends up with eight neighbouring ones of y.
+// x and A pass through a ring in shared memory (read straight into registers,
+// two steps ahead, u of 32,768 x 4,096 took 150 us and more: too few bytes in
+// flight).  B and y go to registers directly: a sum does not care for the order
+// of its terms, so a lane takes four neighbouring ranks as its share of a step
+// of 16, on both sides alike; and the columns of a result tile are dealt so that
+// a lane ends up with eight neighbouring ones of y.
 //
 // bf16 values are exact operands; u is carried in two of them (16 bits; three
 // where an fp32 gradient comes of it), fp32 inputs in three (24 bits, six
@@ -32,6 +33,10 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -261,22 +266,55 @@ template <int M> __device__ __forceinline__ void find_tile(const Args &a, int64_
   }
 }
 
-// M rows a tile, RP ranks.  A warp has 16 rows; warps share the sum over n_in
-// KW ways.
-template <int M, int RP> struct Shape {
-  static constexpr int MT = 1, MG = M / (16 * MT), KW = 8 / MG;
+// M rows a tile, RP ranks.  x and A pass through a ring in shared memory, KC
+// columns at a time; a warp has 16 rows and KS of the steps of 16 columns (the
+// warps share these KW ways).
+template <typename T, int M, int RP> struct Shape {
+  static constexpr int NI = Type<T>::IN;
+  static constexpr int MG = M / 16, KW = 8 / MG, KC = M == 16 ? 128 : 64, UX = KC / 8, KS = KC / 16 / KW;
+  static constexpr int STAGES = NI == 1 ? 4 : 2;
+  static constexpr uint32_t X = M * KC * 2, A = RP * KC * 2, STAGE = NI * (X + A);
   static constexpr int PITCH = RP + 8;  // elements a row of u's pieces
-  static constexpr size_t PART = (size_t)KW * M * RP * 4, U = (size_t)M * RP * 4, PIECES = (size_t)3 * M * PITCH * 2;
-  static constexpr size_t BYTES = U + (PART > PIECES ? PART : PIECES);
+  static constexpr size_t U = (size_t)M * RP * 4, RING = (size_t)STAGES * STAGE, PART = (size_t)KW * M * RP * 4,
+                          PIECES = (size_t)3 * M * PITCH * 2, OVER = RING > PART ? RING : PART;
+  static constexpr size_t BYTES = U + (OVER > PIECES ? OVER : PIECES);
 };
+
+// Byte offset of 16-byte unit u of row r in rows of U units, eight rows' units
+// of a column in different banks.
+template <int U> __device__ __forceinline__ uint32_t unit_at(int r, int u) { return (uint32_t)((r * U + (u ^ (r & 7))) * 16); }
+
+// Eight neighbouring values, of which `left` exist, to shared memory (zeros for
+// the others): asynchronously where they can be read 8 or 16 bytes at a time.
+template <typename T, int V>
+__device__ __forceinline__ void stage8(unsigned char *to, uint32_t piece, const T *from, int64_t left, const void *any) {
+  if constexpr (sizeof(T) == 2 && V == 8) {
+    const int n = left > 0 ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(n ? (const void *)from : any), "r"(n) : "memory");
+  } else if constexpr (sizeof(T) == 2 && V == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = left > 4 * i ? 8 : 0;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to + 8 * i)),
+                   "l"(n ? (const void *)(from + 4 * i) : any), "r"(n) : "memory");
+    }
+  } else {
+    Eight<T, V> e;
+    e.load(from, left);
+#pragma unroll
+    for (int j = 0; j < Type<T>::IN; ++j) *reinterpret_cast<uint4 *>(to + j * piece) = make_uint4(e.x[j][0], e.x[j][1], e.x[j][2], e.x[j][3]);
+  }
+}
 
 template <typename T, int M, int RP, int V>
 __global__ void __launch_bounds__(NT, sizeof(T) == 2 && RP <= 64 ? 2 : 1) lora_kernel(Args a) {
-  using Sh = Shape<M, RP>;
-  constexpr int MT = Sh::MT, KW = Sh::KW, NI = Type<T>::IN, NU = Type<T>::U, RT = RP / 8, PITCH = Sh::PITCH;
-  extern __shared__ __align__(16) unsigned char smem[];
-  float *u_s = reinterpret_cast<float *>(smem), *part = u_s + M * RP;
-  uint16_t *pieces = reinterpret_cast<uint16_t *>(part);  // over the parts, once they are summed
+  using Sh = Shape<T, M, RP>;
+  constexpr int KW = Sh::KW, NI = Type<T>::IN, NU = Type<T>::U, RT = RP / 8, PITCH = Sh::PITCH;
+  extern __shared__ __align__(128) unsigned char smem[];
+  float *u_s = reinterpret_cast<float *>(smem), *part = u_s + M * RP;  // the ring, then the warps' parts, then u's pieces
+  unsigned char *ring = reinterpret_cast<unsigned char *>(part);
+  uint16_t *pieces = reinterpret_cast<uint16_t *>(part);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_rank(), size = cluster_size();
   int64_t row0 = 0;
@@ -287,84 +325,83 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && RP <= 64 ? 2 : 1) lora_k
   if (l >= 0) {
     // ---- u = x A^T over this CTA's and warp's part of n_in
     const int mg = warp / KW, kw = warp % KW;
-    const T *A = static_cast<const T *>(a.a) + l * a.a_adapter;
-    const int chunks = (a.n_in + 31) / 32;
-    const int c0 = (int)((int64_t)chunks * rank / size), c1 = (int)((int64_t)chunks * (rank + 1) / size);
-    const T *xr[MT][2];
+    const T *A = static_cast<const T *>(a.a) + l * a.a_adapter, *X = static_cast<const T *>(a.x) + row0 * a.n_in;
+    const int chunks = (a.n_in + Sh::KC - 1) / Sh::KC;
+    const int c0 = (int)((int64_t)chunks * rank / size), nc = (int)((int64_t)chunks * (rank + 1) / size) - c0;
+    auto load = [&](int c) {
+      unsigned char *st = ring + (c % Sh::STAGES) * Sh::STAGE;
+      const int k0 = (c0 + c) * Sh::KC;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int r = (mg * MT + m) * 16 + g + 8 * h;
-        r = r < len ? r : len - 1;  // rows past the end: any, their u is not used
-        xr[m][h] = static_cast<const T *>(a.x) + (row0 + r) * a.n_in;
+      for (int i = 0; i < ((M + RP) * Sh::UX + NT - 1) / NT; ++i) {
+        const int x = tid + i * NT, r = x / Sh::UX, u = x % Sh::UX, k = k0 + u * 8;
+        if (r >= M + RP) break;
+        if (r < M) {  // rows past the end: nothing, their u is not used
+          if (r < len) stage8<T, V>(st + unit_at<Sh::UX>(r, u), Sh::X, X + (int64_t)r * a.n_in + k, a.n_in - k, a.x);
+        } else {
+          const int q = r - M;
+          stage8<T, V>(st + NI * Sh::X + unit_at<Sh::UX>(q, u), Sh::A, A + (q < a.rank ? q * a.a_ld : 0) + k, q < a.rank ? a.n_in - k : 0, a.a);
+        }
       }
-    float sum[MT][RT][4], acc[MT][RT][4];
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float sum[RT][4], acc[RT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int e = 0; e < 4; ++e) sum[i][e] = acc[i][e] = 0.f;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    const int ra = 16 * mg + (lane & 15), ua = lane >> 4, rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[m][i][e] = acc[m][i][e] = 0.f;
-    if (mg * MT * 16 < len) {
-      int n = 0;
-#pragma unroll 2
-      for (int c = c0 + kw; c < c1; c += KW) {
-        const int k = c * 32 + t * 8;
-        const int64_t left = a.n_in - k;
-        Eight<T, V> x[MT][2];
+    for (int c = 0; c < Sh::STAGES - 1; ++c) {
+      if (c < nc) load(c);
+      else asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int c = 0; c < nc; ++c) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(Sh::STAGES - 2) : "memory");
+      __syncthreads();  // chunk c is there; every warp is done with chunk c - 1, whose place is next
+      if (c + Sh::STAGES - 1 < nc) load(c + Sh::STAGES - 1);
+      else asm volatile("cp.async.commit_group;" ::: "memory");
+      const uint32_t x_at = ring_at + (c % Sh::STAGES) * Sh::STAGE, a_at = x_at + NI * Sh::X;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int ks = 0; ks < Sh::KS; ++ks) {
+        const int u0 = 2 * (kw * Sh::KS + ks);
+        uint32_t f[NI][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) x[m][h].load(xr[m][h] + k, left);
+        for (int j = 0; j < NI; ++j) ldsm4(f[j], x_at + j * Sh::X + unit_at<Sh::UX>(ra, u0 + ua));
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const int r = 8 * i + g;
-          Eight<T, V> b;
-          b.load(A + (r < a.rank ? r * a.a_ld : 0) + k, r < a.rank ? left : 0);
+        for (int q = 0; q < RT / 2; ++q) {
+          uint32_t b[NI][4];
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
+          for (int j = 0; j < NI; ++j) ldsm4(b[j], a_at + j * Sh::A + unit_at<Sh::UX>(16 * q + rb, u0 + ub));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
             uint32_t b0[NI], b1[NI];
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
-              b0[j] = b.x[j][2 * s];
-              b1[j] = b.x[j][2 * s + 1];
+              b0[j] = b[j][2 * e];
+              b1[j] = b[j][2 * e + 1];
             }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              uint32_t f[NI][4];
-#pragma unroll
-              for (int j = 0; j < NI; ++j) {
-                f[j][0] = x[m][0].x[j][2 * s];
-                f[j][1] = x[m][1].x[j][2 * s];
-                f[j][2] = x[m][0].x[j][2 * s + 1];
-                f[j][3] = x[m][1].x[j][2 * s + 1];
-              }
-              mma_pieces<NI, NI>(acc[m][i], f, b0, b1);
-            }
+            mma_pieces<NI, NI>(acc[2 * q + e], f, b0, b1);
           }
         }
-        if ((++n & 3) == 0) {
+      }
+      if ((c + 1) % (8 / Sh::KS) == 0) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                sum[m][i][e] += acc[m][i][e];
-                acc[m][i][e] = 0.f;
-              }
-        }
+          for (int e = 0; e < 4; ++e) {
+            sum[i][e] += acc[i][e];
+            acc[i][e] = 0.f;
+          }
       }
     }
+    __syncthreads();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2 *>(part + ((size_t)kw * M + (mg * MT + m) * 16 + g + 8 * h) * RP + 8 * i + 2 * t) =
-              make_float2(sum[m][i][2 * h] + acc[m][i][2 * h], sum[m][i][2 * h + 1] + acc[m][i][2 * h + 1]);
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2 *>(part + ((size_t)kw * M + mg * 16 + g + 8 * h) * RP + 8 * i + 2 * t) =
+            make_float2(sum[i][2 * h] + acc[i][2 * h], sum[i][2 * h + 1] + acc[i][2 * h + 1]);
     __syncthreads();
     for (int i = tid; i < M * RP; i += NT) {
       float s = part[i];
@@ -514,7 +551,7 @@ template <typename T> int vec_of(int64_t n) { return sizeof(T) == 2 && n % 8 == 
 template <typename T, int M, int RP, int V>
 cudaError_t go(const Args &a, int64_t tiles, int size, cudaStream_t st) {
   auto kernel = lora_kernel<T, M, RP, V>;
-  constexpr size_t smem = Shape<M, RP>::BYTES;
+  constexpr size_t smem = Shape<T, M, RP>::BYTES;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -584,11 +621,11 @@ template <typename T> cudaError_t transpose(const void *src, void *dst, int L, i
   return cudaGetLastError();
 }
 
-// Row tiles of 64 of every adapter, in the order of the requests: a thread an
-// adapter, requests looked at 1,024 at a time.
+// Row tiles of 64 of every adapter, in the order of the requests: a warp an
+// adapter, requests looked at 1,024 at a time, a lane to a tile.
 __global__ void __launch_bounds__(128) tiles_kernel(Args a, int32_t *count, int2 *list, int64_t cap) {
   __shared__ int s_l[1024], s_r0[1024], s_r1[1024];
-  const int l = blockIdx.x * 128 + threadIdx.x;
+  const int lane = threadIdx.x & 31, l = blockIdx.x * 4 + (threadIdx.x >> 5);
   int64_t n = 0;
   for (int n0 = 0; n0 < a.requests; n0 += 1024) {
     __syncthreads();
@@ -601,12 +638,20 @@ __global__ void __launch_bounds__(128) tiles_kernel(Args a, int32_t *count, int2
       s_r1[i] = (int)r1;
     }
     __syncthreads();
-    if (l < a.adapters)
-      for (int i = 0; i < here; ++i)
-        if (s_l[i] == l)
-          for (int r = s_r0[i]; r < s_r1[i] && n < cap; r += TM) list[l * cap + n++] = make_int2(r, min(TM, s_r1[i] - r));
+    if (l >= a.adapters) continue;
+    for (int i0 = 0; i0 < here; i0 += 32) {
+      uint32_t mine = __ballot_sync(~0u, i0 + lane < here && s_l[min(i0 + lane, 1023)] == l);
+      while (mine) {
+        const int i = i0 + __ffs(mine) - 1;
+        mine &= mine - 1;
+        const int r0 = s_r0[i], r1 = s_r1[i], tiles = (r1 - r0 + TM - 1) / TM;
+        for (int k = lane; k < tiles && n + k < cap; k += 32)
+          list[l * cap + n + k] = make_int2(r0 + k * TM, min(TM, r1 - r0 - k * TM));
+        n = min(n + tiles, cap);
+      }
+    }
   }
-  if (l < a.adapters) count[l] = (int32_t)n;
+  if (l < a.adapters && lane == 0) count[l] = (int32_t)n;
 }
 
 // Sum over an adapter's rows of wide[row, col] narrow[row, r] (narrow in three
@@ -867,7 +912,7 @@ cudaError_t launch_lora_bwd(const kda_lora_bwd_args &x, const BwdPlan &p, cudaSt
   int32_t *count = reinterpret_cast<int32_t *>(ws + p.off_count);
   int2 *list = reinterpret_cast<int2 *>(ws + p.off_list);
   if (e == cudaSuccess && (x.d_a || x.d_b)) {
-    tiles_kernel<<<(unsigned)((L + 127) / 128), 128, 0, st>>>(a, count, list, p.tiles);
+    tiles_kernel<<<(unsigned)((L + 3) / 4), 128, 0, st>>>(a, count, list, p.tiles);
     e = cudaGetLastError();
   }
   float *part = reinterpret_cast<float *>(ws + p.off_part);
