@@ -435,17 +435,28 @@ template <int N> __device__ __forceinline__ void zero(float (&x)[N][4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
 }
-// c += a b over pieces: NA of a, NB of b, the smallest products left out
-template <int NA, int NB>
-__device__ __forceinline__ void mma_pieces(float (&c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4], int h) {
-  if constexpr (NA == 2) mma16(c, a[1], b[0][2 * h], b[0][2 * h + 1]);
-  if constexpr (NB == 2) mma16(c, a[0], b[1][2 * h], b[1][2 * h + 1]);
-  mma16(c, a[0], b[0][2 * h], b[0][2 * h + 1]);
+// c[2 q + e] += a b[q] over pieces, NA of a and NB of b with the smallest
+// products left out, for tile pairs q below n: one pair of pieces on all tiles in
+// a row, so that no product waits for the sum of the one before.
+template <int NA, int NB, int N, int Q>
+__device__ __forceinline__ void mma_tiles(float (&c)[N][4], const uint32_t (&a)[NA][4], const uint32_t (&b)[Q][NB][4], int n = Q) {
+  constexpr int M = NA > NB ? NA : NB;
+#pragma unroll
+  for (int s = M - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          if (q < n) {
+            mma16(c[2 * q], a[i], b[q][s - i][0], b[q][s - i][1]);
+            mma16(c[2 * q + 1], a[i], b[q][s - i][2], b[q][s - i][3]);
+          }
 }
 
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(NT, 1)
-gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_stride, GradOut io) {
+gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_stride, GradOut io, int sms) {
   using Sh = IntraShape<T, DK, DV>;
   constexpr int NI = Sh::NI, DH = Sh::DH, PASSES = DK / DH, NW = DH / 32;  // n-tiles of a warp in a pass
   constexpr int UK = DK / 8, UV = DV / 8, US = DH / 8;
@@ -551,6 +562,22 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       }
     }
 
+    // the next head's share of memory on its way to L2: of this CTA, or of the one
+    // that will take its place
+    {
+      const int64_t after = (int64_t)blockIdx.x + sms;
+      const int64_t next = hv + 1 < group ? unit + 1 : after < gridDim.x ? after / p.Hk * p.H + after % p.Hk * group : -1;
+      if (next >= 0) {
+        constexpr int SB = DK * DV * 4, WB = C * DV * 4;
+        for (int x = tid * 128; x < 2 * SB + 2 * WB; x += NT * 128) {
+          const char *at = x < SB ? ws + pl.off_s + next * SB + x
+                         : x < 2 * SB ? ws + pl.off_ds + next * SB + (x - SB)
+                         : x < 2 * SB + WB ? ws + pl.off_w + next * WB + (x - 2 * SB) : ws + pl.off_dy + next * WB + (x - 2 * SB - WB);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
+      }
+    }
+
     // ---- what meets the states
     float zsum = 0.f, iq[2] = {0.f, 0.f};
 #pragma unroll
@@ -593,16 +620,19 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
           ldsm4(o[i], base + Sh::S_DO + i * Sh::VT + unit_at<UV>(ra, 2 * ks + ua));
           ldsm4t(r[i], base + Sh::S_DY + i * Sh::VT + unit_at<8>(16 * ks + rat, uat));
         }
+        uint32_t b[NW / 2][2][4];
 #pragma unroll
-        for (int q = 0; q < NW / 2; ++q) {
-          uint32_t b[2][4];
+        for (int q = 0; q < NW / 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) ldsm4t(b[i], base + Sh::S_S + i * Sh::ST + unit_at<US>(16 * ks + rt, quarter * NW + 2 * q + ut));
+          for (int i = 0; i < 2; ++i) ldsm4t(b[q][i], base + Sh::S_S + i * Sh::ST + unit_at<US>(16 * ks + rt, quarter * NW + 2 * q + ut));
+        mma_tiles<NI, 2>(x, o, b);
+        if constexpr (NI == 2) {
+          mma_tiles<2, 2>(y, r, b);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mma_pieces<NI, 2>(x[2 * q + e], o, b, e);
-            if constexpr (NI == 2) mma_pieces<2, 2>(y[2 * q + e], r, b, e);
-            else mma16(y[2 * q + e], r[0], b[0][2 * e], b[0][2 * e + 1]);
+          for (int q = 0; q < NW / 2; ++q) {
+            mma16(y[2 * q], r[0], b[q][0][0], b[q][0][1]);
+            mma16(y[2 * q + 1], r[0], b[q][0][2], b[q][0][3]);
           }
         }
       }
@@ -633,14 +663,12 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         uint32_t w[NI][4];
 #pragma unroll
         for (int i = 0; i < NI; ++i) ldsm4t(w[i], base + Sh::S_W + i * Sh::VT + unit_at<8>(16 * ks + rat, uat));
+        uint32_t b[NW / 2][NI][4];
 #pragma unroll
-        for (int q = 0; q < NW / 2; ++q) {
-          uint32_t b[NI][4];
+        for (int q = 0; q < NW / 2; ++q)
 #pragma unroll
-          for (int i = 0; i < NI; ++i) ldsm4t(b[i], base + Sh::S_DS + i * Sh::ST + unit_at<US>(16 * ks + rt, quarter * NW + 2 * q + ut));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) mma_pieces<NI, NI>(x[2 * q + e], w, b, e);
-        }
+          for (int i = 0; i < NI; ++i) ldsm4t(b[q][i], base + Sh::S_DS + i * Sh::ST + unit_at<US>(16 * ks + rt, quarter * NW + 2 * q + ut));
+        mma_tiles<NI, NI>(x, w, b);
       }
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
@@ -663,6 +691,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     if (lane == 0) s_z[warp] = zsum;
 
     // ---- inside the chunk: half 0 has q k^T and dP, half 1 k k^T and dL
+    const int pairs = mt < side ? 0 : mt < side + 2 ? 1 : 2;  // down to the diagonal
     float x[4][4], m[4][4];  // tile pairs `side` and `side` + 2
     zero(x);
     zero(m);
@@ -671,16 +700,13 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       uint32_t a[NI][4];
 #pragma unroll
       for (int i = 0; i < NI; ++i) ldsm4(a[i], base + (half ? Sh::S_K : Sh::S_Q) + i * Sh::KT + unit_at<UK>(ra, 2 * ks + ua));
+      uint32_t b[2][NI][4];
 #pragma unroll
-      for (int qi = 0; qi < 2; ++qi) {
-        const int q = side + 2 * qi;
-        if (q > mt) continue;
-        uint32_t b[NI][4];
+      for (int qi = 0; qi < 2; ++qi)
+        if (qi < pairs)
 #pragma unroll
-        for (int i = 0; i < NI; ++i) ldsm4(b[i], base + Sh::S_K + i * Sh::KT + unit_at<UK>(16 * q + rb, 2 * ks + ub));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) mma_pieces<NI, NI>(x[2 * qi + e], a, b, e);
-      }
+          for (int i = 0; i < NI; ++i) ldsm4(b[qi][i], base + Sh::S_K + i * Sh::KT + unit_at<UK>(16 * (side + 2 * qi) + rb, 2 * ks + ub));
+      mma_tiles<NI, NI>(x, a, b, pairs);
     }
 #pragma unroll 2
     for (int ks = 0; ks < DV / 16; ++ks) {
@@ -691,21 +717,18 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       } else {
 #pragma unroll
         for (int i = 0; i < NI; ++i) ldsm4(a[i], base + Sh::S_DO + i * Sh::VT + unit_at<UV>(ra, 2 * ks + ua));
-        if constexpr (NI == 1) a[1][0] = a[1][1] = a[1][2] = a[1][3] = 0u;
       }
+      uint32_t b[2][2][4];
 #pragma unroll
-      for (int qi = 0; qi < 2; ++qi) {
-        const int q = side + 2 * qi;
-        if (q > mt) continue;
-        uint32_t b[2][4];
+      for (int qi = 0; qi < 2; ++qi)
+        if (qi < pairs)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ldsm4t(b[i], base + Sh::S_W + i * Sh::VT + unit_at<8>(16 * ks + rt, 2 * q + ut));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (NI == 2 || half) mma16(m[2 * qi + e], a[1], b[0][2 * e], b[0][2 * e + 1]);
-          mma16(m[2 * qi + e], a[0], b[1][2 * e], b[1][2 * e + 1]);
-          mma16(m[2 * qi + e], a[0], b[0][2 * e], b[0][2 * e + 1]);
-        }
+          for (int i = 0; i < 2; ++i) ldsm4t(b[qi][i], base + Sh::S_W + i * Sh::VT + unit_at<8>(16 * ks + rt, 2 * (side + 2 * qi) + ut));
+      if (NI == 2 || half) {
+        mma_tiles<2, 2>(m, a, b, pairs);
+      } else {
+        const uint32_t one[1][4] = {{a[0][0], a[0][1], a[0][2], a[0][3]}};
+        mma_tiles<1, 2>(m, one, b, pairs);
       }
     }
     auto col_of = [&](int nt) { return 16 * (side + (nt & 2)) + 8 * (nt & 1) + t; };
@@ -809,23 +832,21 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
           if (ks >= mt) ldsm4t(l2[i], base + Sh::S_T + (NI + i) * MAT_BYTES + unit_at<8>(16 * ks + rat, uat));
           ldsm4(l3[i], base + Sh::S_T + (2 * NI + i) * MAT_BYTES + unit_at<8>(ra, 2 * ks + ua));
         }
+        uint32_t r[NW / 2][NI][4];
 #pragma unroll
-        for (int q = 0; q < NW / 2; ++q) {
-          uint32_t r[NI][4];
-          const uint32_t at = unit_at<UK>(16 * ks + rt, pass * US + quarter * NW + 2 * q + ut);
+        for (int q = 0; q < NW / 2; ++q)
 #pragma unroll
-          for (int i = 0; i < NI; ++i) ldsm4t(r[i], base + Sh::S_K + i * Sh::KT + at);
+          for (int i = 0; i < NI; ++i)
+            ldsm4t(r[q][i], base + Sh::S_K + i * Sh::KT + unit_at<UK>(16 * ks + rt, pass * US + quarter * NW + 2 * q + ut));
+        if (ks <= mt) mma_tiles<NI, NI>(a, l1, r);
+        mma_tiles<NI, NI>(d, l3, r);
+        if (ks >= mt) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (ks <= mt) mma_pieces<NI, NI>(a[2 * q + e], l1, r, e);
-            mma_pieces<NI, NI>(d[2 * q + e], l3, r, e);
-          }
-          if (ks >= mt) {
+          for (int q = 0; q < NW / 2; ++q)
 #pragma unroll
-            for (int i = 0; i < NI; ++i) ldsm4t(r[i], base + Sh::S_Q + i * Sh::KT + at);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) mma_pieces<NI, NI>(b[2 * q + e], l2, r, e);
-          }
+            for (int i = 0; i < NI; ++i)
+              ldsm4t(r[q][i], base + Sh::S_Q + i * Sh::KT + unit_at<UK>(16 * ks + rt, pass * US + quarter * NW + 2 * q + ut));
+          mma_tiles<NI, NI>(b, l2, r);
         }
       }
 #pragma unroll
@@ -836,30 +857,55 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
           dk[pass][nt][e] += scale * (b[nt][e] * s2.y) + d[nt][e] * s3.y;
         }
     }
-    __syncthreads();
-    // sums over i >= r of the pairs, in place, then over j < r
-    if (tid < C) {
-      float s = 0.f;
-#pragma unroll 8
-      for (int i = C - 1; i > tid; --i) {
-        s += x_at(i, tid);
-        x_at(i, tid) = s;
-      }
-    }
-    __syncthreads();
+    // what the last step wants from memory, on its way meanwhile
+    float I[2], Y[2], B[2], xg[2];
+    const int64_t g_off = batch * p.gate.b + tok * p.gate.t + h * p.gate.h;
     if (warp == 0) {
       const float *sums = reinterpret_cast<const float *>(ws + pl.off_dots) + unit * 2 * DOT_FLOATS;
       auto dots = [&](int at) { return DV == 128 ? sums[at] + sums[DOT_FLOATS + at] : sums[at]; };
-      float F[2], I[2], Y[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 2 * lane + i;
-        float s = 0.f;
-#pragma unroll 8
-        for (int j = 0; j < r; ++j) s += x_at(r, j);
-        F[i] = s;
-        I[i] = (s_iq[r] + s_iq[C + r]) + (s_iq[2 * C + r] + s_iq[3 * C + r]) + dots(DOT_K + r);
+        I[i] = dots(DOT_K + r);
         Y[i] = dots(DOT_Y + r);
+        B[i] = dots(DOT_BETA + r);
+        xg[i] = r < len ? p.g[g_off + r * p.gate.t] : 0.f;
+      }
+    }
+    __syncthreads();
+    // sums over i >= r of the pairs, in place: first within eight rows, a thread a column
+    float *s_tot = reinterpret_cast<float *>(smem + Sh::S_T), *s_pairs = s_tot + NT;  // over the coefficients
+    {
+      const int j = tid & (C - 1), seg = tid / C;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 8 * seg + 7; i >= 8 * seg; --i) {
+        if (i > j) sum += x_at(i, j);
+        x_at(i, j) = sum;
+      }
+      s_tot[tid] = sum;
+    }
+    __syncthreads();
+    // then over j < r, eight lanes a row, with the totals of the later rows
+    {
+      const int r = tid >> 3;
+      float sum = 0.f;
+      for (int j = tid & 7; j < r; j += 8) {
+        sum += x_at(r, j);
+        for (int seg = r / 8 + 1; seg < 8; ++seg) sum += s_tot[seg * C + j];
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      if ((tid & 7) == 0) s_pairs[r] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float F[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * lane + i;
+        F[i] = s_pairs[r];
+        I[i] += (s_iq[r] + s_iq[C + r]) + (s_iq[2 * C + r] + s_iq[3 * C + r]);
       }
       float si = I[0] + I[1], sy = Y[0] + Y[1];
 #pragma unroll
@@ -878,23 +924,22 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       const float dg[2] = {F[0] + si + before + z, F[1] + (I[1] + after) + (before + Y[0]) + z};
       const bool gate = (p.gp.flags & KDA_GATE_IN_KERNEL) != 0;
       const float ea = gate ? expf(p.gp.a_log[h]) : 0.f, bias = p.gp.dt_bias ? p.gp.dt_bias[h] : 0.f;
-      const int64_t off = batch * p.gate.b + tok * p.gate.t + h * p.gate.h;
       float da = 0.f, dt = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 2 * lane + i;
         if (r < len) {
-          const float xg = p.g[off + r * p.gate.t], be = s_beta[r];
+          const float be = s_beta[r];
           float dx = dg[i];
           if (gate) {
-            da = fmaf(log_decay(xg, p.gp, -ea, bias), dg[i], da);
-            dx = -ea * dg[i] / (1.f + expf(-(xg + bias)));
+            da = fmaf(log_decay(xg[i], p.gp, -ea, bias), dg[i], da);
+            dx = -ea * dg[i] / (1.f + expf(-(xg[i] + bias)));
             dt += dx;
           }
-          io.dg[off + r * p.gate.t] = dx;
-          float d = dots(DOT_BETA + r) + (s_db[r] + s_db[C + r]);
+          io.dg[g_off + r * p.gate.t] = dx;
+          float d = B[i] + (s_db[r] + s_db[C + r]);
           if (p.gp.flags & KDA_BETA_SIGMOID) d *= be * (1.f - be);
-          io.dbeta[off + r * p.gate.t] = d;
+          io.dbeta[g_off + r * p.gate.t] = d;
         }
       }
 #pragma unroll
@@ -1005,7 +1050,10 @@ template <typename T, int DK, int DV> cudaError_t go(const Problem &p, char *ws,
   reverse<<<(unsigned)((int64_t)p.s.N * p.H), RevShape<T, DK, DV / 16>::THREADS, rev_smem, st>>>(p, ws, pl, kqs, aps, io);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.nchunks > 0) {
-    intra<<<(unsigned)((int64_t)p.nchunks * p.Hk), NT, in_smem, st>>>(p, ws, pl, kqs, aps, io);
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+      return e;
+    intra<<<(unsigned)((int64_t)p.nchunks * p.Hk), NT, in_smem, st>>>(p, ws, pl, kqs, aps, io, sms);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (io.da_log || io.ddt_bias)

@@ -520,16 +520,14 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && RP <= 64 ? 2 : 1) lora_k
             f[j][2] = lo.y;
             f[j][3] = hi.y;
           }
+          constexpr int N = NU > NI ? NU : NI;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t b0[NI], b1[NI];
+          for (int w = N - 1; w >= 0; --w)
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              b0[i] = b[j][s][i][0];
-              b1[i] = b[j][s][i][1];
-            }
-            mma_pieces<NU, NI>(c[j], f, b0, b1);
-          }
+            for (int i = 0; i < NU; ++i)
+              if (w - i >= 0 && w - i < NI)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma(c[j], f[i], b[j][s][w - i][0], b[j][s][w - i][1]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -748,17 +746,25 @@ grad_kernel(const T *wide, int n, const uint16_t *narrow, const int32_t *count, 
 #pragma unroll
         for (int j = 0; j < NI; ++j)
           ldsm4t(f[m][j], w0 + ((j * TM + 16 * ks + ra) * Sh::WP + warp * Sh::W + 16 * m + 8 * ua) * 2);
+      // products of one pair of pieces on all tiles in a row: none waits for the sum of the one before
+      constexpr int Q = RT == 2 ? 1 : 2;
 #pragma unroll
-      for (int q = 0; q < RT / 2; ++q) {
-        uint32_t b[3][4];
+      for (int q0 = 0; q0 < RT / 2; q0 += Q) {
+        uint32_t b[Q][3][4];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) ldsm4t(b[j], n0 + ((16 * ks + rb) * Sh::NP + j * RP + 16 * q + 8 * ub) * 2);
+        for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t b0[3] = {b[0][2 * e], b[1][2 * e], b[2][2 * e]}, b1[3] = {b[0][2 * e + 1], b[1][2 * e + 1], b[2][2 * e + 1]};
+          for (int j = 0; j < 3; ++j) ldsm4t(b[q][j], n0 + ((16 * ks + rb) * Sh::NP + j * RP + 16 * (q0 + q) + 8 * ub) * 2);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma_pieces<NI, 3>(acc[m][2 * q + e], f[m], b0, b1);
-        }
+        for (int s = 2; s >= 0; --s)
+#pragma unroll
+          for (int i = 0; i < NI && i <= s; ++i)
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma(acc[m][2 * (q0 + q) + e], f[m][i], b[q][s - i][2 * e], b[q][s - i][2 * e + 1]);
       }
     }
 #pragma unroll
