@@ -21,6 +21,20 @@ constexpr int NT = 128;
 constexpr int LP = 68;  // floats a row of L
 constexpr int HEADS = 4;  // value heads whose gates are computed at once, a warp each
 
+// 8 values as they lie in memory
+__device__ __forceinline__ void unpack8(const float4 (&r)[1], float (&x)[8]) {
+  const uint32_t w[4] = {__float_as_uint(r[0].x), __float_as_uint(r[0].y), __float_as_uint(r[0].z), __float_as_uint(r[0].w)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack8(const float4 (&r)[2], float (&x)[8]) {
+  x[0] = r[0].x; x[1] = r[0].y; x[2] = r[0].z; x[3] = r[0].w;
+  x[4] = r[1].x; x[5] = r[1].y; x[6] = r[1].z; x[7] = r[1].w;
+}
+
 // (hi, lo) + (h, l) with the rounding error of the sum kept
 __device__ __forceinline__ void add2(float &hi, float &lo, float h, float l) {
   const float s = hi + h, v = s - hi;
@@ -91,8 +105,8 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   extern __shared__ __align__(128) unsigned char smem[];
   // the pieces of k and q, and over them, once used, their products [64][LP]
   float *s_kk = reinterpret_cast<float *>(smem), *s_qk = s_kk + C * LP, *Ls = reinterpret_cast<float *>(smem + Sh::S_L);
-  __shared__ float s_num[2][C], s_r[2][C];       // 1 / norm of k and q, with and without the pieces' unit
-  __shared__ float s_g[HEADS][2][C], s_beta[HEADS][C], s_top[2][4];
+  __shared__ __align__(16) float s_num[2][C], s_r[2][C];  // 1 / norm of k and q, with and without the pieces' unit
+  __shared__ __align__(16) float s_g[HEADS][2][C], s_beta[HEADS][C], s_top[2][4];
   __shared__ int s_max;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -111,11 +125,21 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const T *src = static_cast<const T *>(which ? p.q : p.k) + batch * p.qk.b + tok * p.qk.t + hk * p.qk.h;
-#pragma unroll 4
-      for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += RW) {
-        const int r = r0 + lane / U;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r < len) load8(src + r * p.qk.t + u * 8, x);
+      // all rows on their way before the first is used: no store to memory may come between, the compiler
+      // could not tell it from what is read
+      float4 raw[16 / RW][sizeof(T) / 2];
+#pragma unroll
+      for (int k = 0; k < 16 / RW; ++k) {
+        const int r = warp * 16 + k * RW + lane / U;
+#pragma unroll
+        for (int w = 0; w < (int)sizeof(T) / 2; ++w)
+          raw[k][w] = r < len ? reinterpret_cast<const float4 *>(src + r * p.qk.t + u * 8)[w] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 16 / RW; ++k) {
+        const int r = warp * 16 + k * RW + lane / U;
+        float x[8];
+        unpack8(raw[k], x);
         float ss = 0.f, m = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -281,18 +305,23 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
       const int b = x < 32 ? 0 : x < 96 ? 1 : x < 192 ? 2 : 3, y = x - 16 * b * (b + 1);
       const int i = 16 * b + y % 16, u = y / 16;
       const float hi_i = gh[i], lo_i = gl[i], ki = s_num[0][i] * beta[i], qi = s_num[1][i] * p.gp.scale * sP.x;
-      float pv[8];
+      float pv[8], lv[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = 8 * u + e;
-        float lv = 0.f;
-        pv[e] = 0.f;
-        if (j <= i) {
-          const float gam = expf((hi_i - gh[j]) + (lo_i - gl[j])) * s_num[0][j];
-          pv[e] = s_qk[i * LP + j] * gam * qi;
-          if (j < i) lv = s_kk[i * LP + j] * gam * ki;
+      for (int w = 0; w < 2; ++w) {
+        const int j0 = 8 * u + 4 * w;
+        const float4 kk4 = *reinterpret_cast<const float4 *>(s_kk + i * LP + j0), qk4 = *reinterpret_cast<const float4 *>(s_qk + i * LP + j0),
+                     h4 = *reinterpret_cast<const float4 *>(gh + j0), l4 = *reinterpret_cast<const float4 *>(gl + j0),
+                     n4 = *reinterpret_cast<const float4 *>(s_num[0] + j0);
+        const float kkv[4] = {kk4.x, kk4.y, kk4.z, kk4.w}, qkv[4] = {qk4.x, qk4.y, qk4.z, qk4.w}, hv4[4] = {h4.x, h4.y, h4.z, h4.w},
+                    lv4[4] = {l4.x, l4.y, l4.z, l4.w}, nv[4] = {n4.x, n4.y, n4.z, n4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + e;
+          const float gam = j <= i ? expf((hi_i - hv4[e]) + (lo_i - lv4[e])) * nv[e] : 0.f;
+          pv[4 * w + e] = j <= i ? qkv[e] * gam * qi : 0.f;
+          lv[4 * w + e] = j < i ? kkv[e] * gam * ki : 0.f;
         }
-        Ls[i * LP + j] = lv;
+        *reinterpret_cast<float4 *>(Ls + i * LP + j0) = make_float4(lv[4 * w], lv[4 * w + 1], lv[4 * w + 2], lv[4 * w + 3]);
       }
       uint4 hi, lo;
       split2(pv[0], pv[1], hi.x, lo.x);
