@@ -67,7 +67,7 @@ __device__ __forceinline__ bool chunk_at(const SeqInfo &s, int64_t c, int &n, in
 // ([64, 64] tiles; blocks of 16 above the diagonal are not written).
 // Numbers: beta; e^G, e^{G_C - G} with the norms' factors (and the scale, for q)
 // in them; those factors alone, times what a unit of the pieces stands for (no
-// scale) and by themselves; G in two floats.  misc: 0 e^{G_C}, 1 what a unit of
+// scale) and by themselves; G to base 2 in two floats.  misc: 0 e^{G_C}, 1 what a unit of
 // A's pieces stands for, 2 the same of P's.
 constexpr int NUM_MISC = 0, NUM_BETA = 16, NUM_EK = 80, NUM_EQ = 144, NUM_FK = 208, NUM_K = 272, NUM_Q = 336, NUM_GH = 400,
               NUM_GL = 464, NUM_RK = 528, NUM_RQ = 592, NUM_FLOATS = 656;
@@ -287,6 +287,8 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
+
+constexpr float LOG2E = 1.4426950408889634f;
 
 // Log-decay of one token and head from what the caller gave.  From -256 on
 // (e^-256 is zero in fp32) it is held there: -inf, a decay to nothing, would

@@ -509,8 +509,8 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       s_qn[tid] = num[NUM_Q + tid];
       s_gh[tid] = gh;
       s_gl[tid] = gl;
-      s_e[tid] = expf(gh + gl);
-      s_f[tid] = expf((num[NUM_GH + C - 1] - gh) + (num[NUM_GL + C - 1] - gl));
+      s_e[tid] = exp2f(gh + gl);
+      s_f[tid] = exp2f((num[NUM_GH + C - 1] - gh) + (num[NUM_GL + C - 1] - gl));
     }
     if (tid < 3) s_max[tid] = 0;
     float2 sc[5];  // S, dS', W, dY, dO: one unit of pieces for the whole of each
@@ -741,7 +741,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         const int i = row0 + 8 * (e >> 1), j = col_of(nt) + (e & 1);
         float mv = 0.f, xv = 0.f;
         if (half ? j < i : j <= i) {
-          const float gam = expf((s_gh[i] - s_gh[j]) + (s_gl[i] - s_gl[j]));
+          const float gam = exp2f((s_gh[i] - s_gh[j]) + (s_gl[i] - s_gl[j]));
           mv = m[nt][e] * un * sc[2].y * gam;
           if (half) {
             const float kk = x[nt][e] * s_kn[i] * s_kn[j];
@@ -784,26 +784,39 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       *reinterpret_cast<__half *>(smem + at) = hi;
       if constexpr (NI == 2) *reinterpret_cast<__half *>(smem + at + MAT_BYTES) = __float2half_rn(v - __half2float(hi));
     };
+    auto put2 = [&](int which, int i, int j, float v, float w) {  // two of a row, j even
+      uint32_t hi, lo;
+      split2(v, w, hi, lo);
+      const uint32_t at = Sh::S_T + which * NI * MAT_BYTES + unit_at<8>(i, j >> 3) + (j & 7) * 2;
+      *reinterpret_cast<uint32_t *>(smem + at) = hi;
+      if constexpr (NI == 2) *reinterpret_cast<uint32_t *>(smem + at + MAT_BYTES) = lo;
+    };
     float *Xs = reinterpret_cast<float *>(smem + Sh::S_X);
     auto x_at = [&](int i, int j) -> float & { return Xs[i * C + (j ^ (i & 31))]; };
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       if (side + (nt & 2) > mt) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = row0 + 8 * (e >> 1), j = col_of(nt) + (e & 1);
-        const float mv = m[nt][e];
+      for (int e = 0; e < 4; e += 2) {
+        const int i = row0 + 4 * e, j = col_of(nt);
+        const float mv = m[nt][e], mw = m[nt][e + 1];
         if (half) {
-          if (j < i) {
-            put(2, i, j, mv * s_kn[j] * s3.x);
-            put(2, j, i, mv * s_kn[i] * s3.x);
-          } else if (j == i) {
-            put(2, i, i, 0.f);
+          // M + M^T times k's factors: its own pair in a block below the diagonal blocks, one by one in these
+          const float kj = s_kn[j] * s3.x, kw = s_kn[j + 1] * s3.x, ki = s_kn[i] * s3.x;
+          if (side + (nt & 2) < mt) {
+            put2(2, i, j, mv * kj, mw * kw);
+          } else {
+            if (j <= i) put(2, i, j, mv * kj);  // zero on the diagonal
+            if (j + 1 <= i) put(2, i, j + 1, mw * kw);
           }
+          if (j < i) put(2, j, i, mv * ki);
+          if (j + 1 < i) put(2, j + 1, i, mw * ki);
         } else {
-          put(0, i, j, mv * s_kn[j] * s1.x);
-          put(1, i, j, mv * s_qn[i] * s2.x);
+          const float qi = s_qn[i] * s2.x;
+          put2(0, i, j, mv * (s_kn[j] * s1.x), mw * (s_kn[j + 1] * s1.x));
+          put2(1, i, j, mv * qi, mw * qi);
           x_at(i, j) = x[nt][e];
+          x_at(i, j + 1) = x[nt][e + 1];
         }
       }
     }

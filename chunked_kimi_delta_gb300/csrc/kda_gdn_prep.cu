@@ -97,7 +97,7 @@ template <typename T, int DK> struct PrepShape {
 };
 
 template <typename T, int DK, bool BWD>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 4)
 gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_stride) {
   using Sh = PrepShape<T, DK>;
   constexpr int NI = pieces<T>(), U = DK / 8, NP = BWD ? 2 : NI;
@@ -106,7 +106,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   // the pieces of k and q, and over them, once used, their products [64][LP]
   float *s_kk = reinterpret_cast<float *>(smem), *s_qk = s_kk + C * LP, *Ls = reinterpret_cast<float *>(smem + Sh::S_L);
   __shared__ __align__(16) float s_num[2][C], s_r[2][C];  // 1 / norm of k and q, with and without the pieces' unit
-  __shared__ __align__(16) float s_g[HEADS][2][C], s_beta[HEADS][C], s_top[2][4];
+  __shared__ __align__(16) float s_g[HEADS][2][C], s_beta[HEADS][C], s_top[2][2];
   __shared__ int s_max;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -121,37 +121,45 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   {
     constexpr int RW = 32 / U;  // rows a warp takes at once
     const int u = lane % U;
-    float top[2] = {0.f, 0.f};
+    constexpr int K = 16 / RW;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const T *src = static_cast<const T *>(which ? p.q : p.k) + batch * p.qk.b + tok * p.qk.t + hk * p.qk.h;
       // all rows on their way before the first is used: no store to memory may come between, the compiler
       // could not tell it from what is read
-      float4 raw[16 / RW][sizeof(T) / 2];
+      float4 raw[K][sizeof(T) / 2];
 #pragma unroll
-      for (int k = 0; k < 16 / RW; ++k) {
+      for (int k = 0; k < K; ++k) {
         const int r = warp * 16 + k * RW + lane / U;
 #pragma unroll
         for (int w = 0; w < (int)sizeof(T) / 2; ++w)
           raw[k][w] = r < len ? reinterpret_cast<const float4 *>(src + r * p.qk.t + u * 8)[w] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      float ss[K], m[K];
 #pragma unroll
-      for (int k = 0; k < 16 / RW; ++k) {
-        const int r = warp * 16 + k * RW + lane / U;
+      for (int k = 0; k < K; ++k) {
         float x[8];
         unpack8(raw[k], x);
-        float ss = 0.f, m = 0.f;
+        ss[k] = m[k] = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          m = fmaxf(m, fabsf(x[i]));
+          ss[k] = fmaf(x[i], x[i], ss[k]);
+          m[k] = fmaxf(m[k], fabsf(x[i]));
+        }
+      }
+#pragma unroll
+      for (int o = U / 2; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          ss[k] += __shfl_xor_sync(~0u, ss[k], o);
+          m[k] = fmaxf(m[k], __shfl_xor_sync(~0u, m[k], o));
         }
 #pragma unroll
-        for (int o = U / 2; o; o >>= 1) {
-          ss += __shfl_xor_sync(~0u, ss, o);
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        }
-        const float2 sc = piece_scale(m);
+      for (int k = 0; k < K; ++k) {
+        const int r = warp * 16 + k * RW + lane / U;
+        const float2 sc = piece_scale(m[k]);
+        float x[8];
+        unpack8(raw[k], x);
         uint4 hi, lo;
         split2(x[0] * sc.x, x[1] * sc.x, hi.x, lo.x);
         split2(x[2] * sc.x, x[3] * sc.x, hi.y, lo.y);
@@ -165,19 +173,26 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
           *reinterpret_cast<uint4 *>(kq_out + at + TILE) = lo;
         }
         if (u == 0) {
-          // x / norm = (unit / norm) (x / unit); rows past the end are zero
-          const float f = (p.gp.flags & KDA_L2NORM_QK) ? 1.f / sqrtf(ss + p.gp.eps) : 1.f;
-          s_num[which][r] = r < len ? f * sc.y : 0.f;
-          s_r[which][r] = f;
+          s_r[which][r] = ss[k];
+          s_num[which][r] = r < len ? sc.y : 0.f;
         }
-        top[which] = fmaxf(top[which], ss * ((p.gp.flags & KDA_L2NORM_QK) ? 1.f / (ss + p.gp.eps) : 1.f));
       }
-#pragma unroll
-      for (int o = U; o < 32; o <<= 1) top[which] = fmaxf(top[which], __shfl_xor_sync(~0u, top[which], o));
-      if (lane == 0) s_top[which][warp] = top[which];
     }
   }
   __syncthreads();
+  {
+    // a thread a row: x / norm = (unit / norm) (x / unit); rows past the end are zero
+    const int which = tid / C, r = tid % C;
+    const float ss = s_r[which][r];
+    const bool l2 = (p.gp.flags & KDA_L2NORM_QK) != 0;
+    const float f = l2 ? 1.f / sqrtf(ss + p.gp.eps) : 1.f;
+    s_r[which][r] = f;
+    s_num[which][r] *= f;
+    float top = l2 ? ss * (f * f) : ss;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) s_top[which][warp & 1] = top;
+  }
 
   // ---- k k^T and q k^T, rows 16 warp ..
   float kk[8][4], qk[8][4];
@@ -234,8 +249,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   }
   // |P| is at most the scale times the largest norms: a unit for its pieces
   // without looking at P itself (28 binades below it keep their bits)
-  const float bound = fabsf(p.gp.scale) * sqrtf(fmaxf(fmaxf(s_top[0][0], s_top[0][1]), fmaxf(s_top[0][2], s_top[0][3]))) *
-                      sqrtf(fmaxf(fmaxf(s_top[1][0], s_top[1][1]), fmaxf(s_top[1][2], s_top[1][3])));
+  const float bound = fabsf(p.gp.scale) * sqrtf(fmaxf(s_top[0][0], s_top[0][1])) * sqrtf(fmaxf(s_top[1][0], s_top[1][1]));
   const float2 sP = piece_scale(bound);
 
   const int group = p.H / p.Hk;
@@ -244,7 +258,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
     if (hv % HEADS == 0) {
       __syncthreads();
       if (hv + warp < group) {
-        // ---- the gate of head h + warp: two tokens a lane, running sum in two floats
+        // ---- the gate of head h + warp: two tokens a lane, running sum in two floats, to base 2
         const int hw = h + warp;
         float *num = reinterpret_cast<float *>(ap + ((size_t)c * p.H + hw) * ap_stride);
         const float nea = (p.gp.flags & KDA_GATE_IN_KERNEL) ? -expf(p.gp.a_log[hw]) : 0.f;
@@ -254,7 +268,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = 2 * lane + i;
-          g[i] = r < len ? log_decay(p.g[off + r * p.gate.t], p.gp, nea, bias) : 0.f;
+          g[i] = r < len ? LOG2E * log_decay(p.g[off + r * p.gate.t], p.gp, nea, bias) : 0.f;
           b[i] = r < len ? p.beta[off + r * p.gate.t] : 0.f;
           if ((p.gp.flags & KDA_BETA_SIGMOID) && r < len) b[i] = 1.f / (1.f + expf(-b[i]));
         }
@@ -272,7 +286,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
         for (int i = 0; i < 2; ++i) {
           const int r = 2 * lane + i;
           const float kn = s_num[0][r], qn = s_num[1][r];
-          const float e = expf(Gh[i] + Gl[i]), f = expf((Ch - Gh[i]) + (Cl - Gl[i]));
+          const float e = exp2f(Gh[i] + Gl[i]), f = exp2f((Ch - Gh[i]) + (Cl - Gl[i]));
           s_g[warp][0][r] = Gh[i];
           s_g[warp][1][r] = Gl[i];
           s_beta[warp][r] = b[i];
@@ -288,7 +302,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
           num[NUM_RQ + r] = s_r[1][r];
         }
         if (lane == 0) {
-          num[NUM_MISC] = expf(Ch + Cl);
+          num[NUM_MISC] = exp2f(Ch + Cl);
           num[NUM_MISC + 2] = sP.y;
         }
       }
@@ -317,7 +331,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = j0 + e;
-          const float gam = j <= i ? expf((hi_i - hv4[e]) + (lo_i - lv4[e])) * nv[e] : 0.f;
+          const float gam = j <= i ? exp2f((hi_i - hv4[e]) + (lo_i - lv4[e])) * nv[e] : 0.f;
           pv[4 * w + e] = j <= i ? qkv[e] * gam * qi : 0.f;
           lv[4 * w + e] = j < i ? kkv[e] * gam * ki : 0.f;
         }
