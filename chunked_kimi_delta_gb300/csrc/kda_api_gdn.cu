@@ -73,11 +73,17 @@ gdn::Problem problem(const kda_fwd_args *a) {
   return p;
 }
 
-// Chunk offsets of packed sequences (p.s.chunk_off), then the preparation.
+// Chunk offsets of packed sequences (p.s.chunk_off) and their order, then the preparation.
 cudaError_t prepare(const kda_fwd_args *a, bool bwd, gdn::Problem &p, char *ws, const gdn::Plan &pl, cudaStream_t st) {
   int32_t *co = reinterpret_cast<int32_t *>(ws + pl.off_chunks);
   p.s.chunk_off = co;
-  cudaError_t e = p.s.bounds ? launch_chunk_map(p.s, co, st) : cudaSuccess;
+  cudaError_t e = cudaSuccess;
+  if (p.s.bounds && p.s.N <= gdn::ORDERED) {
+    p.order = co + p.s.N + 1;
+    e = gdn::launch_gdn_map(p.s, co, co + p.s.N + 1, st);
+  } else if (p.s.bounds) {
+    e = launch_chunk_map(p.s, co, st);
+  }
   if (e == cudaSuccess) e = gdn::launch_gdn_prep(a->qkv_dtype, bwd, p, ws, pl, st);
   return e;
 }
@@ -156,7 +162,7 @@ kda_status kda_gdn_recurrent_step(const kda_decode_args *a, kda_stream_t stream)
   if ((a->flags & KDA_GATE_IN_KERNEL) && !a->a_log) return KDA_ERR_INVALID_ARG;
   if (a->N == 0) return KDA_OK;
   if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->out || !a->cache || !a->idx) return KDA_ERR_INVALID_ARG;
-  if ((int64_t)a->N * a->H > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)a->N * a->H > INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;  // two CTAs a state
   return cuda_status(gdn::launch_gdn_step(*a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

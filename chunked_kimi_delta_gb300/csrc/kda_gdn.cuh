@@ -47,7 +47,12 @@ struct Problem {
   const float *g, *beta;
   GateParams gp;
   bool v_first;            // states are [dv, dk]
+  const int32_t *order;    // packed sequences from the longest to the shortest, or null: as they come
 };
+
+// Up to so many packed sequences are taken in the order of their lengths: the
+// chains' time is their longest's, if that does not start last.
+constexpr int ORDERED = 1024;
 
 // Chunk c's first token: batch row and token inside it, as the strides want
 // them, and the tokens it holds (false: none).
@@ -95,7 +100,7 @@ constexpr int DOT_BETA = 0, DOT_K = 64, DOT_Y = 128, DOT_FLOATS = 192;
 inline Plan make_gdn_plan(kda_dtype d, int64_t nchunks, int N, int H, int Hk, int dk, int dv, bool bwd) {
   Plan p{};
   size_t o = 256;
-  p.off_chunks = o; o = align256(o + sizeof(int32_t) * ((size_t)N + 1));
+  p.off_chunks = o; o = align256(o + sizeof(int32_t) * (2 * (size_t)N + 1));
   p.off_kq = o; o = align256(o + (size_t)nchunks * Hk * kq_bytes(d, dk));
   p.off_ap = o; o = align256(o + (size_t)nchunks * H * ap_bytes(d, bwd));
   if (bwd) {
@@ -302,6 +307,8 @@ __device__ __forceinline__ float log_decay(float x, const GateParams &gp, float 
 }
 
 // ---------------------------------------------------------------- launchers
+// Chunk offsets [N + 1] and order [N] of at most ORDERED packed sequences.
+cudaError_t launch_gdn_map(const SeqInfo &s, int32_t *chunk_off, int32_t *order, cudaStream_t st);
 cudaError_t launch_gdn_prep(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, cudaStream_t st);
 
 // The forward's chain writes out and final_state; the backward's first one (out

@@ -82,7 +82,7 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
   const char *kq = ws + pl.off_kq, *ap = ws + pl.off_ap;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = (lane & 3) * 2;
-  const int h = (int)(blockIdx.x % p.H), n = (int)(blockIdx.x / p.H);
+  const int h = (int)(blockIdx.x % p.H), at = (int)(blockIdx.x / p.H), n = p.order ? p.order[at] : at;
   const int hk = h / (p.H / p.Hk);
   const int v0 = warp * 16;
   int64_t t0, t1;

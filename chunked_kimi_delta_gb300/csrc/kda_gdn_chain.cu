@@ -38,7 +38,7 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
   const int slices = p.dv / (16 * WARPS);
   const int slice = blockIdx.x % slices;
   const int h = (int)(blockIdx.x / slices % p.H);
-  const int n = (int)(blockIdx.x / slices / p.H);
+  const int at = (int)(blockIdx.x / slices / p.H), n = p.order ? p.order[at] : at;
   const int hk = h / (p.H / p.Hk);
   const int v0 = (slice * WARPS + warp) * 16;  // this warp's first value channel
   int64_t t0, t1;

@@ -430,7 +430,40 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   }
 }
 
+// A thread a sequence.
+__global__ void __launch_bounds__(ORDERED) gdn_map_kernel(SeqInfo s, int32_t *chunk_off, int32_t *order) {
+  __shared__ int s_n[ORDERED], s_w[ORDERED / 32];
+  const int n = threadIdx.x, lane = n & 31, warp = n >> 5;
+  int chunks = 0;
+  if (n < s.N) {
+    int64_t t0, t1;
+    seq_range(s, n, t0, t1);
+    chunks = (int)((t1 - t0 + C - 1) / C);
+  }
+  s_n[n] = chunks;
+  int sum = chunks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) s_w[warp] = sum;
+  __syncthreads();
+  if (n >= s.N) return;
+  for (int w = 0; w < warp; ++w) sum += s_w[w];
+  if (n == 0) chunk_off[0] = 0;
+  chunk_off[n + 1] = sum;
+  int rank = 0;
+  for (int m = 0; m < s.N; ++m) rank += s_n[m] > chunks || (s_n[m] == chunks && m < n);
+  order[rank] = n;
+}
+
 }  // namespace
+
+cudaError_t launch_gdn_map(const SeqInfo &s, int32_t *chunk_off, int32_t *order, cudaStream_t st) {
+  gdn_map_kernel<<<1, ORDERED, 0, st>>>(s, chunk_off, order);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_gdn_prep(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, cudaStream_t st) {
   if (p.nchunks == 0) return cudaSuccess;
