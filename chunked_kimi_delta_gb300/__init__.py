@@ -1325,29 +1325,43 @@ def kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags=None, *, sca
                                           dt_bias=dt_bias, l2norm_qk=l2norm_qk, beta_sigmoid=beta_sigmoid,
                                           gate_in_kernel=gate_in_kernel, state_v_first=state_v_first, out=out)
     lib = _ready()
-    if q.dim() != 4:
+    qs, vs, dtype = q.shape, v.shape, q.dtype
+    if len(qs) != 4 or len(vs) != 4:
         raise ValueError("q/k/v are [N, T, H, D]")
-    N, H, Hk, T, _ = _gdn_problem(q, k, v, g, beta, a_log, dt_bias, (), None, False, state_v_first, gate_in_kernel)
-    if tuple(cache.shape[1:]) != _state_shape(N, q, v, state_v_first)[1:]:
+    N, T, Hk, dk = qs
+    H, dv = vs[2], vs[3]
+    gs, hs = vs[:3], (H,)
+    # every call of a decode step passes here: a few comparisons, and the general checks to name what is wrong
+    fine = (k.shape == qs and vs[:2] == qs[:2] and Hk >= 1 and H % Hk == 0 and k.dtype is dtype and v.dtype is dtype
+            and g.shape == gs and beta.shape == gs and g.dtype is _F32 and beta.dtype is _F32
+            and (a_log is None or (a_log.shape == hs and a_log.dtype is _F32))
+            and (dt_bias is None or (dt_bias.shape == hs and dt_bias.dtype is _F32)) and (a_log is not None or not gate_in_kernel))
+    if not fine:
+        _gdn_problem(q, k, v, g, beta, a_log, dt_bias, (), None, False, state_v_first, gate_in_kernel)
+    a_, b_ = (dv, dk) if state_v_first else (dk, dv)
+    cs, strides = cache.shape, cache.stride()
+    if cs[1:] != (H, a_, b_):
         raise ValueError("cache must be [rows, H, dk, dv] ([rows, H, dv, dk] V-first)")
+    rows, stride = cs[0], strides[0]
+    if strides[1:] != (a_ * b_, b_, 1):
+        _rows(cache)
     if idx.numel() != N:
         raise ValueError("idx must have one row of the pool for each sequence")
-    if init_flags is not None and (init_flags.dtype != _torch_module.bool or init_flags.numel() != N):
+    if init_flags is not None and (init_flags.dtype is not _torch_module.bool or init_flags.numel() != N):
         raise TypeError("init_flags must be bool [N]")
-    if out is not None and (out.shape != v.shape or out.dtype != v.dtype):
+    if out is not None and (out.shape != vs or out.dtype is not dtype):
         raise ValueError("out must have v's shape and dtype")
-    rows, stride, _ = _rows(cache)
     dev = _launch_device(q, k, v, g, beta, a_log, dt_bias, idx, init_flags, out)
     if cache.get_device() != dev:
         _on_device(q, cache)
     if out is None:
-        out = _alloc(tuple(v.shape), v.stride(), v.dtype)
+        out = _alloc(tuple(vs), v.stride(), dtype)
     flags = ((KDA_L2NORM_QK if l2norm_qk else 0) | (KDA_BETA_SIGMOID if beta_sigmoid else 0)
              | (KDA_GATE_IN_KERNEL if gate_in_kernel else 0) | (KDA_STATE_V_FIRST if state_v_first else 0))
-    a = kda_decode_args(N, T, H, q.shape[3], v.shape[3], _dtype_code(q), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    a = kda_decode_args(N, T, H, dk, dv, _in_code(dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                         g.data_ptr(), _ptr(a_log), _ptr(dt_bias), beta.data_ptr(),
-                        q.shape[3] ** -0.5 if scale is None else scale, eps, flags, out.data_ptr(), cache.data_ptr(),
-                        _dtype_code(cache), rows, stride, idx.data_ptr(), _idx_code(idx), _ptr(init_flags), Hk)
+                        dk ** -0.5 if scale is None else scale, eps, flags, out.data_ptr(), cache.data_ptr(),
+                        _in_code(cache.dtype), rows, stride, idx.data_ptr(), _idx_code(idx), _ptr(init_flags), Hk)
     status = lib.kda_gdn_recurrent_step(ctypes.byref(a), _raw_stream(dev))
     if status:
         raise KdaError(status, "kda_gdn_recurrent_step")

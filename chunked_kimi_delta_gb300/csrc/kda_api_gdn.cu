@@ -70,6 +70,9 @@ gdn::Problem problem(const kda_fwd_args *a) {
   p.gp.eps = a->eps;
   p.gp.flags = a->flags;
   p.v_first = (a->flags & KDA_STATE_V_FIRST) != 0;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    p.halves = p.dv == 128 && (int64_t)p.s.N * p.H * 2 <= sms;
   return p;
 }
 

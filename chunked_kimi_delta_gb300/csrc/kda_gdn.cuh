@@ -47,6 +47,7 @@ struct Problem {
   const float *g, *beta;
   GateParams gp;
   bool v_first;            // states are [dv, dk]
+  bool halves;             // chains of 128 value channels as two CTAs: with few of them, each chunk is done sooner
   const int32_t *order;    // packed sequences from the longest to the shortest, or null: as they come
 };
 

@@ -82,9 +82,10 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
   const char *kq = ws + pl.off_kq, *ap = ws + pl.off_ap;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = (lane & 3) * 2;
-  const int h = (int)(blockIdx.x % p.H), at = (int)(blockIdx.x / p.H), n = p.order ? p.order[at] : at;
+  const int slices = p.dv / (16 * WARPS), slice = blockIdx.x % slices;
+  const int h = (int)(blockIdx.x / slices % p.H), at = (int)(blockIdx.x / slices / p.H), n = p.order ? p.order[at] : at;
   const int hk = h / (p.H / p.Hk);
-  const int v0 = warp * 16;
+  const int v0 = (slice * WARPS + warp) * 16;
   int64_t t0, t1;
   seq_range(p.s, n, t0, t1);
   const int64_t c0 = seq_first_chunk(p.s, n);
@@ -118,7 +119,8 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
         load_strips<WARPS>(stage + Sh::S_V, vs + r0 * p.v.t, p.v.t, t1 - t0 - r0, first);
         // what this chunk's warps read themselves is on its way to L2 as well
         const int64_t unit = (c0 + c) * p.H + h;
-        const char *w = ws + pl.off_w + unit * (WARPS * 16 * C * 4), *e = ws + pl.off_e + unit * (WARPS * 16 * C * 4);
+        const size_t part = (unit * p.dv + slice * WARPS * 16) * (C * 4);
+        const char *w = ws + pl.off_w + part, *e = ws + pl.off_e + part;
         for (int x = first * 128; x < WARPS * 16 * C * 4; x += FILL * 128) {
           asm volatile("prefetch.global.L2 [%0];" ::"l"(w + x));
           asm volatile("prefetch.global.L2 [%0];" ::"l"(e + x));
@@ -163,8 +165,8 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     }
     const float *num = reinterpret_cast<const float *>(smem + so + Sh::S_NUM);
     const int64_t unit = (c0 + c) * p.H + h;
-    float *maxes = reinterpret_cast<float *>(ws + pl.off_max) + unit * MAX_FLOATS + warp;
-    auto tiles = [&](size_t off, int n_) { return reinterpret_cast<float4 *>(ws + off) + (unit * WARPS + warp) * n_ * 32 + lane; };
+    float *maxes = reinterpret_cast<float *>(ws + pl.off_max) + unit * MAX_FLOATS + v0 / 16;
+    auto tiles = [&](size_t off, int n_) { return reinterpret_cast<float4 *>(ws + off) + (unit * (p.dv / 16) + v0 / 16) * n_ * 32 + lane; };
 
     // ---- dS' out; X = e^{G_C - G} k dS' and its sums with W
     float4 *ds_to = tiles(pl.off_ds, NK);
@@ -395,7 +397,7 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     if constexpr (Sh::STAGES == 1) __syncthreads();
     else if (c >= 2) bar_arrive(bar_empty(stage, group), GROUP + FILL);
     bar_sync(BAR_GROUP + group, GROUP);
-    float *to = reinterpret_cast<float *>(ws + pl.off_dots) + (unit * 2 + group) * DOT_FLOATS;
+    float *to = reinterpret_cast<float *>(ws + pl.off_dots) + (unit * 2 + slice * (WARPS / 4) + group) * DOT_FLOATS;
     const float *from = reinterpret_cast<const float *>(smem + Sh::S_DOTS) + group * 4 * DOT_FLOATS;
     for (int x = tid & (GROUP - 1); x < DOT_FLOATS; x += GROUP)
       to[x] = (from[x] + from[DOT_FLOATS + x]) + (from[2 * DOT_FLOATS + x] + from[3 * DOT_FLOATS + x]);
@@ -1050,18 +1052,28 @@ __global__ void __launch_bounds__(32) gdn_param_kernel(Problem p, const float2 *
   }
 }
 
+template <typename T, int DK, int WARPS>
+cudaError_t go_reverse(const Problem &p, char *ws, const Plan &pl, const GradOut &io, cudaStream_t st) {
+  const kda_dtype dt = sizeof(T) == 2 ? KDA_BF16 : KDA_F32;
+  auto kernel = gdn_reverse_kernel<T, DK, WARPS>;
+  constexpr int smem = RevShape<T, DK, WARPS>::BYTES;
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = (int64_t)p.s.N * p.H * (p.dv / (16 * WARPS));
+  kernel<<<(unsigned)grid, RevShape<T, DK, WARPS>::THREADS, smem, st>>>(p, ws, pl, kq_bytes(dt, p.dk), ap_bytes(dt, true), io);
+  return cudaGetLastError();
+}
+
 template <typename T, int DK, int DV> cudaError_t go(const Problem &p, char *ws, const Plan &pl, const GradOut &io, cudaStream_t st) {
   const kda_dtype dt = sizeof(T) == 2 ? KDA_BF16 : KDA_F32;
   const size_t kqs = kq_bytes(dt, p.dk), aps = ap_bytes(dt, true);
-  auto reverse = gdn_reverse_kernel<T, DK, DV / 16>;
   auto intra = gdn_intra_kernel<T, DK, DV>;
-  constexpr int rev_smem = RevShape<T, DK, DV / 16>::BYTES, in_smem = IntraShape<T, DK, DV>::BYTES;
-  static_assert(rev_smem <= 232448 && in_smem <= 232448, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(reverse, cudaFuncAttributeMaxDynamicSharedMemorySize, rev_smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(intra, cudaFuncAttributeMaxDynamicSharedMemorySize, in_smem);
+  constexpr int in_smem = IntraShape<T, DK, DV>::BYTES;
+  static_assert(in_smem <= 232448, "shared memory of a CTA");
+  cudaError_t e = DV == 128 && !p.halves ? go_reverse<T, DK, 8>(p, ws, pl, io, st) : go_reverse<T, DK, 4>(p, ws, pl, io, st);
   if (e != cudaSuccess) return e;
-  reverse<<<(unsigned)((int64_t)p.s.N * p.H), RevShape<T, DK, DV / 16>::THREADS, rev_smem, st>>>(p, ws, pl, kqs, aps, io);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(intra, cudaFuncAttributeMaxDynamicSharedMemorySize, in_smem)) != cudaSuccess) return e;
   if (p.nchunks > 0) {
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)

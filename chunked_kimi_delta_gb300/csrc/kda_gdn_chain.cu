@@ -113,10 +113,10 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     row_scales(S, z0, z1);
     const int64_t unit = (c0 + c) * p.H + h;  // of what the backward is handed
     auto keep = [&](size_t off, const auto &x, int n, float top, int which) {
-      float4 *to = reinterpret_cast<float4 *>(ws + off) + (unit * (p.dv / 16) + warp) * n * 32 + lane;
+      float4 *to = reinterpret_cast<float4 *>(ws + off) + (unit * (p.dv / 16) + v0 / 16) * n * 32 + lane;
 #pragma unroll
       for (int i = 0; i < (int)(sizeof(x) / 16); ++i) to[i * 32] = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
-      if (which >= 0 && lane == 0) reinterpret_cast<float *>(ws + pl.off_max)[unit * MAX_FLOATS + which + warp] = top;
+      if (which >= 0 && lane == 0) reinterpret_cast<float *>(ws + pl.off_max)[unit * MAX_FLOATS + which + v0 / 16] = top;
     };
     if constexpr (STORE) keep(pl.off_s, S, NK, warp_max(S), MAX_S);
     float Y[8][4], O[8][4];
@@ -182,7 +182,7 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         Y[nt][2] = Y[nt][2] * ek.x * z1.y;
         Y[nt][3] = Y[nt][3] * ek.y * z1.y;
         if constexpr (STORE)
-          reinterpret_cast<float4 *>(ws + pl.off_e)[((unit * (p.dv / 16) + warp) * 8 + nt) * 32 + lane] =
+          reinterpret_cast<float4 *>(ws + pl.off_e)[((unit * (p.dv / 16) + v0 / 16) * 8 + nt) * 32 + lane] =
               make_float4(Y[nt][0], Y[nt][1], Y[nt][2], Y[nt][3]);
         Y[nt][0] = be.x * (x[i][0] - Y[nt][0]);
         Y[nt][1] = be.y * (x[i][1] - Y[nt][1]);
@@ -361,7 +361,7 @@ cudaError_t go(const Problem &p, char *ws, const Plan &pl, const ChainOut &io, c
 template <typename T, bool STORE>
 cudaError_t go_dims(const Problem &p, char *ws, const Plan &pl, const ChainOut &io, cudaStream_t st) {
   const bool w = p.dk == 128;
-  if (p.dv == 128) return w ? go<T, 128, 8, STORE>(p, ws, pl, io, st) : go<T, 64, 8, STORE>(p, ws, pl, io, st);
+  if (p.dv == 128 && !p.halves) return w ? go<T, 128, 8, STORE>(p, ws, pl, io, st) : go<T, 64, 8, STORE>(p, ws, pl, io, st);
   return w ? go<T, 128, 4, STORE>(p, ws, pl, io, st) : go<T, 64, 4, STORE>(p, ws, pl, io, st);
 }
 
