@@ -1373,30 +1373,31 @@ def kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags=None, *, sca
 def _lora_problem(x, a, b, idx, cu_seqlens, scale, wide):
     """Checks the tensors both calls take (the kernels trust them); ``wide``:
     (name, tensor or None, width) of the other [rows, width] tensors."""
-    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+    xs, as_, bs, dtype = x.shape, a.shape, b.shape, x.dtype
+    if len(xs) != 2 or len(as_) != 3 or len(bs) != 3:
         raise ValueError("x is [rows, n_in], a [adapters, rank, n_in], b [adapters, n_out, rank]")
-    rows, n_in = x.shape
-    L, r, n_a = a.shape
-    if n_a != n_in or b.shape[0] != L or b.shape[2] != r:
-        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} do not go with x {tuple(x.shape)}")
-    code = _in_code(x.dtype)
-    if a.dtype is not x.dtype or b.dtype is not x.dtype:
+    rows, n_in = xs
+    L, r, n_a = as_
+    n_out = bs[1]
+    if n_a != n_in or bs[0] != L or bs[2] != r:
+        raise ValueError(f"a {tuple(as_)} and b {tuple(bs)} do not go with x {tuple(xs)}")
+    if a.dtype is not dtype or b.dtype is not dtype:
         raise TypeError("x, a and b must have one dtype")
-    n_out = b.shape[1]
     for name, t, n in wide:
-        if t is not None and (tuple(t.shape) != (rows, n_in if n == "n_in" else n_out) or t.dtype is not x.dtype):
+        if t is not None and (t.shape != (rows, n_in if n == "n_in" else n_out) or t.dtype is not dtype):
             raise ValueError(f"{name} must be [rows, {n}] in x's dtype")
-    n_req = idx.numel()
-    if idx.dim() != 1:
+    ids = idx.shape
+    if len(ids) != 1:
         raise ValueError("idx is [requests]")
+    n_req = ids[0]
     if cu_seqlens is not None:
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() != n_req + 1 or cu_seqlens.dtype != _torch_module.int32:
+        if cu_seqlens.shape != (n_req + 1,) or cu_seqlens.dtype is not _torch_module.int32:
             raise ValueError("cu_seqlens must be int32 [requests + 1]")
     elif n_req == 0 and rows or n_req and rows % n_req:
         raise ValueError(f"{rows} rows cannot be shared out among {n_req} requests: give cu_seqlens")
-    if scale is not None and (tuple(scale.shape) != (L,) or scale.dtype is not _F32):
+    if scale is not None and (scale.shape != (L,) or scale.dtype is not _F32):
         raise ValueError("scale must be fp32 [adapters]")
-    return rows, n_in, n_out, r, L, code, _idx_code(idx), n_req
+    return rows, n_in, n_out, r, L, _in_code(dtype), _idx_code(idx), n_req
 
 
 def kda_lora(x, a, b, idx, y, *, cu_seqlens=None, scale=None, out=None, stream=None):

@@ -588,9 +588,12 @@ cudaError_t run(kda_dtype dt, const Args &a, cudaStream_t st) {
   const int64_t per = a.rows / a.requests;
   const int m = per <= 16 ? 16 : 64;
   const int64_t tiles = a.cu ? a.rows / m + a.requests + 1 : a.requests * ((per + m - 1) / m);
-  // two CTAs an SM, if the tiles alone are too few for that
+  // CTAs a tile.  Tiles of 64 rows: until every SM has its two (115 tiles of 2,048 -> 4,196: 48.5 us with 4 of
+  // them, 51.4 with 2; 512 tiles of 4,096 -> 4,096, enough by themselves: 230 us with 1, 277 with 4, which fill the
+  // last round better but add their parts).  Tiles of 16, a few rows each, are the start and end of a CTA more
+  // than anything: as many as run at once (64 tiles of 4,096 -> 4,096: 12.5 us with 4, 17.8 with 8).
   int size = 1;
-  while (size < 8 && tiles * size < 2 * sms) size *= 2;
+  while (size < 8 && (m == 64 ? tiles * size < 2 * sms : tiles * size * 2 <= 2 * sms)) size *= 2;
   if (dt == KDA_BF16)
     return m == 16 ? go_rank<__nv_bfloat16, 16>(a, tiles, size, st) : go_rank<__nv_bfloat16, 64>(a, tiles, size, st);
   return m == 16 ? go_rank<float, 16>(a, tiles, size, st) : go_rank<float, 64>(a, tiles, size, st);
@@ -676,8 +679,11 @@ grad_kernel(const T *wide, int n, const uint16_t *narrow, const int32_t *count, 
   const int tiles = count[l];
   const int i0 = (int)((int64_t)tiles * share / shares), i1 = (int)((int64_t)tiles * (share + 1) / shares);
 
+  // the next tile's place in memory is read one tile ahead
+  int2 next = i0 < i1 ? list[l * cap + i0] : make_int2(0, 0);
   auto load = [&](int i, unsigned char *st) {
-    const int2 rl = list[l * cap + i];
+    const int2 rl = next;
+    if (i + 1 < i1) next = list[l * cap + i + 1];
     constexpr int UW = Sh::COLS / 8, UN = 3 * RP / 8;
     for (int x = tid; x < TM * UW; x += NT) {
       const int r = x / UW, u = x % UW;
