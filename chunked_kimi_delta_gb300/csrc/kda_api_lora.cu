@@ -30,6 +30,8 @@ kda_status check_bwd(const kda_lora_bwd_args *a) {
   const kda_status s = check(a);
   if (s != KDA_OK) return s;
   if (!a->d_x && !a->d_a && !a->d_b) return KDA_ERR_INVALID_ARG;
+  // 32 x 32 elements of every matrix a block of the transposes
+  if ((int64_t)a->adapters * 4 * ((int64_t)a->n_in / 32 + a->n_out / 32 + 3) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
   if (a->rows > 0 && !a->d_out) return KDA_ERR_INVALID_ARG;
   return mis16(a->d_out) || mis16(a->d_x_in) || mis16(a->d_x) || mis16(a->d_a) || mis16(a->d_b) ? KDA_ERR_ALIGNMENT : KDA_OK;
 }

@@ -18,7 +18,7 @@ inline int padded(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <=
 struct BwdPlan {
   size_t off_at, off_bt, off_u, off_du, off_count, off_list, off_part, total;
   int64_t tiles;  // at most so many row tiles
-  int shares_a, shares_b;
+  int shares;     // of the rows, for the gradients' sums
 };
 BwdPlan bwd_plan(const kda_lora_bwd_args &a, int sms);
 
