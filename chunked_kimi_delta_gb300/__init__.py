@@ -1347,6 +1347,7 @@ def kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags=None, *, sca
         _rows(cache)
     if idx.numel() != N:
         raise ValueError("idx must have one row of the pool for each sequence")
+    icode = _idx_code(idx)
     if init_flags is not None and (init_flags.dtype is not _torch_module.bool or init_flags.numel() != N):
         raise TypeError("init_flags must be bool [N]")
     if out is not None and (out.shape != vs or out.dtype is not dtype):
@@ -1361,7 +1362,7 @@ def kda_gdn_recurrent_step(q, k, v, g, beta, cache, idx, init_flags=None, *, sca
     a = kda_decode_args(N, T, H, dk, dv, _in_code(dtype), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                         g.data_ptr(), _ptr(a_log), _ptr(dt_bias), beta.data_ptr(),
                         dk ** -0.5 if scale is None else scale, eps, flags, out.data_ptr(), cache.data_ptr(),
-                        _in_code(cache.dtype), rows, stride, idx.data_ptr(), _idx_code(idx), _ptr(init_flags), Hk)
+                        _in_code(cache.dtype), rows, stride, idx.data_ptr(), icode, _ptr(init_flags), Hk)
     status = lib.kda_gdn_recurrent_step(ctypes.byref(a), _raw_stream(dev))
     if status:
         raise KdaError(status, "kda_gdn_recurrent_step")

@@ -46,6 +46,28 @@ def test_fwd_packed(cuda_lib, dtype, hk, h):
     _check_fwd(cuda_lib, problem([0, 1, 64, 129, 0, 200, 3, 0], hk=hk, h=h, dtype=dtype, seed=h))
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_fwd_many_heads(cuda_lib, dtype, dk, dv):
+    """More chains than half the SMs (a CTA has all 128 value channels), long enough for its two groups to part."""
+    _check_fwd(cuda_lib, problem([600, 0, 1, 577, 64, 128, 129, 640, 63, 511, 90, 7], hk=4, h=8, dk=dk, dv=dv, dtype=dtype, seed=dk))
+
+
+def test_more_packed_sequences_than_are_ordered(cuda_lib):
+    _check_fwd(cuda_lib, problem([1, 0, 2] * 400, hk=1, h=1, dk=64, dv=64, seed=2))
+
+
+def test_tokens_behind_the_last_sequence_are_left_alone(cuda_lib):
+    p = problem([70, 33], seed=3)
+    want = _fwd(cuda_lib, p)
+    d = cuda(p)
+    for n in ("q", "k", "v", "g", "beta"):  # what is not read may hold anything
+        d[n] = torch.cat([d[n], torch.full_like(d[n][:50], float("nan"))])
+    out = torch.full_like(d["v"], 7.0)
+    got = cuda_lib.kda_gdn_chunk_fwd(*args(d), **dict(d["kw"], out=out))
+    assert torch.equal(got[0][:103], want[0]) and torch.equal(got[1], want[1]) and bool((out[103:] == 7).all())
+
+
 def test_fwd_long(cuda_lib):
     _check_fwd(cuda_lib, problem([4096], hk=1, h=2, seed=3))
 

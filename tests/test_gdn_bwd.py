@@ -71,6 +71,13 @@ def test_bwd_one_gradient_given(cuda_lib, dtype, which):
     _check_bwd(cuda_lib, problem([200], dtype=dtype, seed=3), **which)
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_bwd_many_heads(cuda_lib, dtype, dk, dv):
+    """More chains than half the SMs (a CTA has all 128 value channels), long enough for its two groups to part."""
+    _check_bwd(cuda_lib, problem([600, 0, 1, 577, 64, 128, 129, 640, 63, 511, 90, 7], hk=4, h=8, dk=dk, dv=dv, dtype=dtype, seed=dk))
+
+
 def test_bwd_long(cuda_lib):
     _check_bwd(cuda_lib, problem([2048], hk=1, h=2, seed=3))
 
