@@ -515,16 +515,28 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       s_f[tid] = exp2f((num[NUM_GH + C - 1] - gh) + (num[NUM_GL + C - 1] - gl));
     }
     if (tid < 3) s_max[tid] = 0;
-    float2 sc[5];  // S, dS', W, dY, dO: one unit of pieces for the whole of each
+    float2 sc[5];  // S, dS', W, dY, dO: one unit of pieces for the whole of each, eight lanes to find its largest
     {
       const float *m = reinterpret_cast<const float *>(ws + pl.off_max) + unit * MAX_FLOATS;
+      const bool mine = (lane & 7) < DV / 16;
+      float a = mine ? m[lane] : 0.f, b = mine && lane < 8 ? m[MAX_DO + lane] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        float x = 0.f;
-#pragma unroll
-        for (int w = 0; w < DV / 16; ++w) x = fmaxf(x, m[8 * i + w]);
-        sc[i] = piece_scale(x);
+      for (int o = 1; o < 8; o <<= 1) {
+        a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
+        b = fmaxf(b, __shfl_xor_sync(~0u, b, o));
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[i] = piece_scale(__shfl_sync(~0u, a, 8 * i));
+      sc[4] = piece_scale(__shfl_sync(~0u, b, 0));
+    }
+    // the states' first share on its way before the rest is worked on
+    constexpr int ROUNDS = DV / 16 * US * 32 / NT, EARLY = ROUNDS < 4 ? ROUNDS : 4;
+    float4 sv[EARLY], dv_[EARLY];
+#pragma unroll
+    for (int e = 0; e < EARLY; ++e) {
+      const int x = tid + e * NT, from = (((x >> 5) / US) * UK + (x >> 5) % US) * 32 + (x & 31);
+      sv[e] = reinterpret_cast<const float4 *>(ws + pl.off_s)[unit * (DV / 16) * UK * 32 + from];
+      dv_[e] = reinterpret_cast<const float4 *>(ws + pl.off_ds)[unit * (DV / 16) * UK * 32 + from];
     }
     {
       const float4 *w = reinterpret_cast<const float4 *>(ws + pl.off_w) + unit * (DV / 16) * 8 * 32;
@@ -588,13 +600,23 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       {
         const float4 *s = reinterpret_cast<const float4 *>(ws + pl.off_s) + unit * (DV / 16) * UK * 32;
         const float4 *d = reinterpret_cast<const float4 *>(ws + pl.off_ds) + unit * (DV / 16) * UK * 32;
-#pragma unroll 4
-        for (int x = tid; x < DV / 16 * US * 32; x += NT) {
-          const int l = x & 31, nt = (x >> 5) % US, w = (x >> 5) / US, r = w * 16 + (l >> 2);
-          const int from = (w * UK + pass * US + nt) * 32 + l;
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+          const int x = tid + k * NT, l = x & 31, nt = (x >> 5) % US, w = (x >> 5) / US, r = w * 16 + (l >> 2);
+          if (k >= EARLY || pass > 0) {
+            if ((k - (pass ? 0 : EARLY)) % EARLY == 0) {
+#pragma unroll
+              for (int e = 0; e < EARLY; ++e)
+                if (k + e < ROUNDS) {
+                  const int x2 = x + e * NT, from2 = (((x2 >> 5) / US) * UK + pass * US + (x2 >> 5) % US) * 32 + l;
+                  sv[e] = s[from2];
+                  dv_[e] = d[from2];
+                }
+            }
+          }
           const uint32_t at = unit_at<US>(r, nt) + (l & 3) * 4, at8 = unit_at<US>(r + 8, nt) + (l & 3) * 4;
           uint32_t hi, lo;
-          const float4 a = s[from], b = d[from];
+          const float4 a = sv[k % EARLY], b = dv_[k % EARLY];
           zsum += (a.x * b.x + a.y * b.y) + (a.z * b.z + a.w * b.w);
           split2(a.x * sc[0].x, a.y * sc[0].x, hi, lo);
           *reinterpret_cast<uint32_t *>(smem + Sh::S_S + at) = hi;
@@ -873,7 +895,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         }
     }
     // what the last step wants from memory, on its way meanwhile
-    float I[2], Y[2], B[2], xg[2];
+    float I[2], Y[2], B[2], xg[2], alog = 0.f, bias = 0.f, ec = 0.f;
     const int64_t g_off = batch * p.gate.b + tok * p.gate.t + h * p.gate.h;
     if (warp == 0) {
       const float *sums = reinterpret_cast<const float *>(ws + pl.off_dots) + unit * 2 * DOT_FLOATS;
@@ -886,6 +908,9 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         B[i] = dots(DOT_BETA + r);
         xg[i] = r < len ? p.g[g_off + r * p.gate.t] : 0.f;
       }
+      if (p.gp.flags & KDA_GATE_IN_KERNEL) alog = p.gp.a_log[h];
+      if (p.gp.dt_bias) bias = p.gp.dt_bias[h];
+      ec = num[NUM_MISC];
     }
     __syncthreads();
     // sums over i >= r of the pairs, in place: first within eight rows, a thread a column
@@ -935,10 +960,10 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       float z = 0.f;
 #pragma unroll
       for (int w = 0; w < NT / 32; ++w) z += s_z[w];
-      z *= num[NUM_MISC];
+      z *= ec;
       const float dg[2] = {F[0] + si + before + z, F[1] + (I[1] + after) + (before + Y[0]) + z};
       const bool gate = (p.gp.flags & KDA_GATE_IN_KERNEL) != 0;
-      const float ea = gate ? expf(p.gp.a_log[h]) : 0.f, bias = p.gp.dt_bias ? p.gp.dt_bias[h] : 0.f;
+      const float ea = gate ? expf(alog) : 0.f;
       float da = 0.f, dt = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
