@@ -143,7 +143,6 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
 
   const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;
   const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;
-  if (Sh::STAGES == 2 && group == 1 && nc >= SKEW_CHUNKS) __nanosleep(SKEW_NS);
   for (int c = nc - 1; c >= 0; --c) {
     const int stage = (nc - 1 - c) & 1;
     const uint32_t so = Sh::STAGES == 2 ? stage * Sh::STAGE : 0, st = base + so;

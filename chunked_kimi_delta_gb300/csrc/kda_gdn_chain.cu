@@ -88,7 +88,6 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
 
   const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;  // right operand, rows are its columns
   const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;  // right operand, transposed on the way
-  if (Sh::STAGES == 2 && group == 1 && nc >= SKEW_CHUNKS) __nanosleep(SKEW_NS);
   for (int c = 0; c < nc; ++c) {
     const uint32_t st = base + (Sh::STAGES == 2 ? (c & 1) * Sh::STAGE : 0);
     if constexpr (Sh::STAGES == 2) {

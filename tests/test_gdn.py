@@ -49,7 +49,7 @@ def test_fwd_packed(cuda_lib, dtype, hk, h):
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_fwd_many_heads(cuda_lib, dtype, dk, dv):
-    """More chains than half the SMs (a CTA has all 128 value channels), long enough for its two groups to part."""
+    """More chains than half the SMs (a CTA has all 128 value channels) of many chunks."""
     _check_fwd(cuda_lib, problem([600, 0, 1, 577, 64, 128, 129, 640, 63, 511, 90, 7], hk=4, h=8, dk=dk, dv=dv, dtype=dtype, seed=dk))
 
 

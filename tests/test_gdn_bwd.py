@@ -74,7 +74,7 @@ def test_bwd_one_gradient_given(cuda_lib, dtype, which):
 @pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_bwd_many_heads(cuda_lib, dtype, dk, dv):
-    """More chains than half the SMs (a CTA has all 128 value channels), long enough for its two groups to part."""
+    """More chains than half the SMs (a CTA has all 128 value channels) of many chunks."""
     _check_bwd(cuda_lib, problem([600, 0, 1, 577, 64, 128, 129, 640, 63, 511, 90, 7], hk=4, h=8, dk=dk, dv=dv, dtype=dtype, seed=dk))
 
 
