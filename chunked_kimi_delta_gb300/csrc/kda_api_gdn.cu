@@ -121,6 +121,8 @@ static kda_status check_bwd(const kda_bwd_args *b) {
   const kda_status s = check(&b->fwd);
   if (s != KDA_OK) return s;
   if (tokens(&b->fwd) > 0 && (!b->dq || !b->dk || !b->dv || !b->dg || !b->dbeta)) return KDA_ERR_INVALID_ARG;
+  // d_out is read again after dv, and by chunks beside those whose dq and dk are written
+  if (b->d_out && tokens(&b->fwd) > 0 && (b->d_out == b->dq || b->d_out == b->dk || b->d_out == b->dv)) return KDA_ERR_INVALID_ARG;
   if (mis16(b->d_out) || mis16(b->d_final_state) || mis16(b->dq) || mis16(b->dk) || mis16(b->dv) || mis16(b->dg) ||
       mis16(b->dbeta) || mis16(b->da_log) || mis16(b->ddt_bias) || mis16(b->d_initial_state))
     return KDA_ERR_ALIGNMENT;

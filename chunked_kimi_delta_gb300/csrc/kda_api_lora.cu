@@ -33,6 +33,7 @@ kda_status check_bwd(const kda_lora_bwd_args *a) {
   // 32 x 32 elements of every matrix a block of the transposes
   if ((int64_t)a->adapters * 4 * ((int64_t)a->n_in / 32 + a->n_out / 32 + 3) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
   if (a->rows > 0 && !a->d_out) return KDA_ERR_INVALID_ARG;
+  if (a->rows > 0 && a->d_x && (a->d_x == a->d_out || a->d_x == a->x)) return KDA_ERR_INVALID_ARG;  // both are read after it
   return mis16(a->d_out) || mis16(a->d_x_in) || mis16(a->d_x) || mis16(a->d_a) || mis16(a->d_b) ? KDA_ERR_ALIGNMENT : KDA_OK;
 }
 
@@ -51,7 +52,7 @@ extern "C" {
 kda_status kda_lora(const kda_lora_args *a, kda_stream_t stream) {
   const kda_status s = check(a);
   if (s != KDA_OK) return s;
-  if (a->rows > 0 && (!a->y || !a->out)) return KDA_ERR_INVALID_ARG;
+  if (a->rows > 0 && (!a->y || !a->out || a->out == a->x)) return KDA_ERR_INVALID_ARG;  // x is read by others meanwhile
   if (mis16(a->y) || mis16(a->out)) return KDA_ERR_ALIGNMENT;
   if (a->rows == 0) return KDA_OK;
   return cuda_status(lora::launch_lora(*a, reinterpret_cast<cudaStream_t>(stream)));

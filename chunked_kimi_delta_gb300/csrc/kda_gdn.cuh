@@ -204,13 +204,13 @@ template <int GROUPS, typename F> __device__ __forceinline__ void fill_buffers(i
     cp_commit();
   }
 }
-// [64 tokens][16 W channels] of bf16 as W strips [64][16] (a warp's), rows past
-// the end zero (src is then not read).
+// [64 tokens][16 W channels] of bf16 as W strips [64][16] (a warp's); rows from
+// `rows` on are zero and not read.
 template <int W> __device__ __forceinline__ void load_strips(uint32_t dst, const __nv_bfloat16 *src, int64_t stride, int64_t rows, int first) {
 #pragma unroll 4
   for (int x = first; x < C * 2 * W; x += FILL) {
     const int r = x / (2 * W), u = x % (2 * W);
-    const bool in = src && r < rows;
+    const bool in = r < rows;
     cp16z(dst + (u >> 1) * (C * 32) + r * 32 + (u & 1) * 16, in ? src + r * stride + u * 8 : src, in);
   }
 }

@@ -109,13 +109,13 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     if (warp >= WARPS) {
       registers_to_fill<WARPS>();
       const int first = tid - WARPS * 32;
-      const T *vs = v - warp * 16, *os = d_out ? d_out - warp * 16 : nullptr;
+      const T *vs = v - warp * 16, *os = d_out ? d_out - warp * 16 : vs;  // without d_out zeros, and nothing is read
       fill_buffers<WARPS / 4>(nc, [&](int i) {
         const int c = nc - 1 - i;
         const uint32_t stage = base + (i & 1) * Sh::STAGE;
         const int64_t r0 = (int64_t)c * C;
         load(c, stage, first * 16, FILL * 16);
-        load_strips<WARPS>(stage + Sh::S_DO, os ? os + r0 * p.v.t : nullptr, p.v.t, t1 - t0 - r0, first);
+        load_strips<WARPS>(stage + Sh::S_DO, os + r0 * p.v.t, p.v.t, d_out ? t1 - t0 - r0 : 0, first);
         load_strips<WARPS>(stage + Sh::S_V, vs + r0 * p.v.t, p.v.t, t1 - t0 - r0, first);
         // what this chunk's warps read themselves is on its way to L2 as well
         const int64_t unit = (c0 + c) * p.H + h;

@@ -500,7 +500,9 @@ size_t kda_gdn_chunk_fwd_workspace_size(const kda_fwd_args *args);
 /* The chunked forward: out, and final_state when given.  Fields, layouts
  * (packed sequences, grouped key heads, KDA_LAYOUT_HEAD_MAJOR,
  * KDA_STATE_V_FIRST: no copies are made for either), limits and errors as
- * kda_chunk_fwd; KDA_USE_EXP2 changes nothing.  KDA_ERR_UNSUPPORTED also for
+ * kda_chunk_fwd; KDA_USE_EXP2 changes nothing; g must not be positive.  Tokens
+ * of a packed batch behind the last sequence are neither read nor written.
+ * KDA_ERR_UNSUPPORTED also for
  * h_out, v_new_out and KDA_REUSE_PREP, and where (B T / 64 + sequences) * H
  * exceeds 2^31 - 1; KDA_ERR_INVALID_ARG for KDA_TEST_WAIT_TIMEOUT (the kernels
  * wait for nothing).  final_state may be initial_state in place. */
@@ -512,7 +514,8 @@ kda_status kda_gdn_chunk_fwd(const kda_fwd_args *args, kda_stream_t stream);
  * anew; the workspace holds the states entering and the state gradients
  * leaving every chunk (fp32).  Where the decay is held at e^-256 (zero in
  * fp32) the gate's gradient is that of a decay of zero.  Errors as the forward,
- * and KDA_ERR_INVALID_ARG for null dq, dk, dv, dg or dbeta with tokens. */
+ * and KDA_ERR_INVALID_ARG for null dq, dk, dv, dg or dbeta with tokens, or one
+ * of the first three being d_out. */
 size_t kda_gdn_chunk_bwd_workspace_size(const kda_bwd_args *args);
 kda_status kda_gdn_chunk_bwd(const kda_bwd_args *args, kda_stream_t stream);
 
@@ -689,7 +692,8 @@ kda_status kda_fp8_matmul_shared_workspace(void **workspace);
  * Requests are packed rows [cu_seqlens[i], cu_seqlens[i+1]) (rows behind the
  * last request have no adapter), or, without cu_seqlens, rows / num_requests
  * rows each (a decode batch: one).  The sum is held in fp32 and rounded once;
- * u = x A^T keeps 16 bits for bf16 results, 24 for fp32 ones.  out may be y.
+ * u = x A^T keeps 16 bits for bf16 results, 24 for fp32 ones.  out may be y,
+ * not x.
  * Any n_in, n_out and rank up to KDA_LORA_MAX_RANK; widths that are multiples
  * of 8 (then of 4) elements are read fastest.  Deterministic.
  * Errors: KDA_ERR_INVALID_ARG (sizes below 1, rows < 0, null pointers, rows
@@ -718,7 +722,8 @@ kda_status kda_lora(const kda_lora_args *args, kda_stream_t stream);
 
 /*
  * Its gradients.  d_x = d_x_in + scale[l] (d_out B[l]) A[l] (d_x_in: the
- * projection's own gradient of x; NULL: zeros; d_x may be d_x_in), and in fp32
+ * projection's own gradient of x; NULL: zeros; d_x may be d_x_in, not x or
+ * d_out), and in fp32
  *   d_a[l] = sum over l's rows of scale[l] (d_out B[l])^T x     [adapters, rank, n_in]
  *   d_b[l] = sum over l's rows of scale[l] d_out^T (x A[l]^T)   [adapters, n_out, rank]
  * (zeros for adapters without rows).  Any of d_x, d_a, d_b may be NULL, not all.

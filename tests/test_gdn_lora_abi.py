@@ -69,6 +69,7 @@ def test_bwd_refuses_what_the_forward_does(lib, kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(dq=None), INVALID), (dict(dk=None), INVALID), (dict(dv=None), INVALID), (dict(dg=None), INVALID), (dict(dbeta=None), INVALID),
+    (dict(d_out=3 * BASE), INVALID), (dict(d_out=4 * BASE), INVALID), (dict(d_out=5 * BASE), INVALID),
     (dict(d_out=BASE + 2), ALIGNMENT), (dict(d_initial_state=BASE + 4), ALIGNMENT), (dict(workspace=None), WORKSPACE),
     (dict(workspace=BASE + 128), ALIGNMENT)])
 def test_bwd_refusals(lib, kw, want):
@@ -129,7 +130,7 @@ LORA_COMMON = [(dict(rows=-1), INVALID), (dict(n_in=0), INVALID), (dict(n_out=0)
 
 
 @pytest.mark.parametrize("kw,want", LORA_COMMON + [
-    (dict(y=None), INVALID), (dict(out=None), INVALID), (dict(y=BASE + 2), ALIGNMENT), (dict(out=BASE + 2), ALIGNMENT),
+    (dict(y=None), INVALID), (dict(out=None), INVALID), (dict(out=BASE), INVALID), (dict(y=BASE + 2), ALIGNMENT), (dict(out=BASE + 2), ALIGNMENT),
     (dict(rows=0), 0), (dict(rows=0, num_requests=0), 0)])
 def test_lora_refusals(lib, kw, want):
     assert lib.kda_lora(ctypes.byref(_lora(**kw)), None) == want
@@ -137,7 +138,7 @@ def test_lora_refusals(lib, kw, want):
 
 
 @pytest.mark.parametrize("kw,want", LORA_COMMON + [
-    (dict(d_out=None), INVALID), (dict(d_x=None, d_a=None, d_b=None), INVALID), (dict(d_out=BASE + 2), ALIGNMENT),
+    (dict(d_out=None), INVALID), (dict(d_x=BASE), INVALID), (dict(d_x=6 * BASE), INVALID), (dict(d_x=None, d_a=None, d_b=None), INVALID), (dict(d_out=BASE + 2), ALIGNMENT),
     (dict(d_x=BASE + 2), ALIGNMENT), (dict(d_a=BASE + 4), ALIGNMENT), (dict(workspace=None), WORKSPACE),
     (dict(workspace=BASE + 64), ALIGNMENT), (dict(adapters=65535, n_in=1 << 18, n_out=1 << 18), UNSUPPORTED)])
 def test_lora_bwd_refusals(lib, kw, want):
