@@ -164,7 +164,7 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// The chains' two buffers (bf16): four more warps fill them, groups of four
+// The chains' two buffers, where they fit: four more warps fill them, groups of four
 // warps, one on each of the SM's schedulers, empty them.  The groups never meet
 // each other, so that one can be at its products while the other is at its
 // elementwise work; a barrier for all after every chunk, with the computing
@@ -204,14 +204,15 @@ template <int GROUPS, typename F> __device__ __forceinline__ void fill_buffers(i
     cp_commit();
   }
 }
-// [64 tokens][16 W channels] of bf16 as W strips [64][16] (a warp's); rows from
-// `rows` on are zero and not read.
-template <int W> __device__ __forceinline__ void load_strips(uint32_t dst, const __nv_bfloat16 *src, int64_t stride, int64_t rows, int first) {
+// [64 tokens][16 W channels] as W strips [64][16] (a warp's); rows from `rows` on
+// are zero and not read.
+template <int W, typename T> __device__ __forceinline__ void load_strips(uint32_t dst, const T *src, int64_t stride, int64_t rows, int first) {
+  constexpr int U = sizeof(T);  // 16-byte units of a strip's row
 #pragma unroll 4
-  for (int x = first; x < C * 2 * W; x += FILL) {
-    const int r = x / (2 * W), u = x % (2 * W);
+  for (int x = first; x < C * U * W; x += FILL) {
+    const int r = x / (U * W), u = x % (U * W);
     const bool in = r < rows;
-    cp16z(dst + (u >> 1) * (C * 32) + r * 32 + (u & 1) * 16, in ? src + r * stride + u * 8 : src, in);
+    cp16z(dst + (u / U) * (C * U * 16) + (r * U + u % U) * 16, in ? src + r * stride + u * (16 / sizeof(T)) : src, in);
   }
 }
 
@@ -294,6 +295,13 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
 }
 
 constexpr float LOG2E = 1.4426950408889634f;
+
+// 2^x, x <= 0, to 2^-22 of its size; below 2^-126 zero.
+__device__ __forceinline__ float exp2_neg(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Log-decay of one token and head from what the caller gave.  From -256 on
 // (e^-256 is zero in fp32) it is held there: -inf, a decay to nothing, would

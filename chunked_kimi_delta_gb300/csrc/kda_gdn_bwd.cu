@@ -24,10 +24,13 @@ namespace {
 
 // ---------------------------------------------------------------- chain, backwards
 template <typename T, int DK, int WARPS> struct RevShape {
-  static constexpr int NI = pieces<T>(), STAGES = NI == 1 ? 2 : 1, THREADS = WARPS * 32 + (STAGES == 2 ? FILL : 0);
+  static constexpr int NI = pieces<T>();
   static constexpr uint32_t TILE = C * DK * 2, STRIP = C * 16 * sizeof(T);
   static constexpr uint32_t S_K = 0, S_Q = NI * TILE, S_NUM = 2 * NI * TILE, S_A = S_NUM + NUM_BYTES, S_P = S_A + 2 * MAT_BYTES,
-                            S_DO = S_P + 2 * MAT_BYTES, S_V = S_DO + WARPS * STRIP, STAGE = (S_V + WARPS * STRIP + 127) / 128 * 128;
+                            S_DO = S_P + 2 * MAT_BYTES, S_V = S_DO + WARPS * STRIP, STAGE = (S_V + WARPS * STRIP + 127) / 128 * 128,
+                            REST = (NI == 1 ? WARPS * STRIP : 0) + WARPS * DOT_FLOATS * 4;
+  static constexpr int STAGES = 2 * STAGE + REST <= 232448 ? 2 : 1;
+  static constexpr int THREADS = WARPS * 32 + (STAGES == 2 ? FILL : 0);
   static constexpr uint32_t S_OUT = STAGES * STAGE, S_DOTS = S_OUT + (NI == 1 ? WARPS * STRIP : 0),
                             BYTES = S_DOTS + WARPS * DOT_FLOATS * 4;
 };
@@ -764,7 +767,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         const int i = row0 + 8 * (e >> 1), j = col_of(nt) + (e & 1);
         float mv = 0.f, xv = 0.f;
         if (half ? j < i : j <= i) {
-          const float gam = exp2f((s_gh[i] - s_gh[j]) + (s_gl[i] - s_gl[j]));
+          const float gam = exp2_neg((s_gh[i] - s_gh[j]) + (s_gl[i] - s_gl[j]));
           mv = m[nt][e] * un * sc[2].y * gam;
           if (half) {
             const float kk = x[nt][e] * s_kn[i] * s_kn[j];

@@ -16,12 +16,13 @@ namespace {
 
 template <typename T, int DK, int WARPS, bool STORE> struct Shape {
   static constexpr int NI = pieces<T>(), NP = STORE ? 2 : NI;
-  static constexpr int STAGES = NI == 1 ? 2 : 1, THREADS = WARPS * 32 + (STAGES == 2 ? FILL : 0);
   static constexpr uint32_t TILE = C * DK * 2;
   static constexpr uint32_t S_K = 0, S_Q = NI * TILE, S_NUM = 2 * NI * TILE, S_A = S_NUM + NUM_BYTES,
                             S_P = S_A + 2 * MAT_BYTES, S_V = S_P + NP * MAT_BYTES;
   static constexpr uint32_t V_STRIP = C * 16 * sizeof(T);
   static constexpr uint32_t STAGE = (S_V + WARPS * V_STRIP + 127) / 128 * 128;
+  static constexpr int STAGES = 2 * STAGE + (NI == 1 ? WARPS * V_STRIP : 0) <= 232448 ? 2 : 1;  // fp32 of 128 key channels: one
+  static constexpr int THREADS = WARPS * 32 + (STAGES == 2 ? FILL : 0);
   static constexpr uint32_t S_OUT = STAGES * STAGE;  // a strip a warp, bf16 only
   static constexpr uint32_t BYTES = S_OUT + (NI == 1 && !STORE ? WARPS * V_STRIP : 0);
 };

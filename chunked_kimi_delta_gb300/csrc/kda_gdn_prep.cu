@@ -331,7 +331,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = j0 + e;
-          const float gam = j <= i ? exp2f((hi_i - hv4[e]) + (lo_i - lv4[e])) * nv[e] : 0.f;
+          const float gam = j <= i ? exp2_neg((hi_i - hv4[e]) + (lo_i - lv4[e])) * nv[e] : 0.f;
           pv[4 * w + e] = j <= i ? qkv[e] * gam * qi : 0.f;
           lv[4 * w + e] = j < i ? kkv[e] * gam * ki : 0.f;
         }
