@@ -169,8 +169,7 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("
 // each other, so that one can be at its products while the other is at its
 // elementwise work; a barrier for all after every chunk, with the computing
 // warps copying themselves, took 774 us for 4 x 8192 tokens of 32 heads (12 k
-// cycles a chunk), this 665 to 690.  A start of the second group up to 7 us
-// later changes nothing: they part by themselves.
+// cycles a chunk), this 665 to 685.
 constexpr int GROUP = 128, FILL = 128, BAR_FULL = 1, BAR_EMPTY = 5, BAR_GROUP = 9;
 __device__ __forceinline__ int bar_full(int stage, int group) { return BAR_FULL + 2 * stage + group; }
 __device__ __forceinline__ int bar_empty(int stage, int group) { return BAR_EMPTY + 2 * stage + group; }
