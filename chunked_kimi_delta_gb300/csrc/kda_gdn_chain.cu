@@ -7,7 +7,9 @@
 // to pieces) the layout of a left operand, and so do Y^T and W^T, its
 // intermediates.  Nothing of the recurrence passes through shared memory;
 // that holds only what the warps of a CTA read in common (k, q, A, P of the
-// chunk, double-buffered).
+// chunk, double-buffered where that fits, by warps of their own: with the
+// computing warps copying and a barrier for all after every chunk, 4 x 8192 tokens
+// of 32 heads took 774 us (12 k cycles a chunk), now 670.
 #include "kda_gdn.cuh"
 
 namespace kda {

@@ -3,6 +3,7 @@
 // du and dX are the forward's kernel with the matrices' roles changed (both
 // transposed once), u = x A^T is it again in the same launch.  dA and dB share a
 // launch too: tiles of 64 rows of one adapter, [columns, ranks] in registers.
+#include "kda_fill.cuh"
 #include "kda_lora_kernel.cuh"
 
 namespace kda {
@@ -85,6 +86,7 @@ template <typename T, int RP> struct GradShape {
   static constexpr size_t WIDE = (size_t)NI * TM * WP * 2, NARROW = (size_t)TM * NP * 2, STAGE = WIDE + NARROW;
   static constexpr int STAGES = NI == 1 ? 2 : 1;
   static constexpr size_t BYTES = STAGES * STAGE;
+  static constexpr int THREADS = NT + (STAGES == 2 ? FILL : 0);
 };
 
 // One of the two gradients a launch makes.
@@ -98,7 +100,7 @@ struct Grad {
 };
 
 template <typename T, int RP, int V>
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __launch_bounds__(GradShape<T, RP>::THREADS, 1)
 grad_kernel(Grad g0, Grad g1, const int32_t *count, const int2 *list, int64_t cap, int shares, int rank) {
   using Sh = GradShape<T, RP>;
   constexpr int NI = Sh::NI, MT = Sh::MT, RT = RP / 8;
@@ -114,30 +116,16 @@ grad_kernel(Grad g0, Grad g1, const int32_t *count, const int2 *list, int64_t ca
   const int tiles = count[l];
   const int i0 = (int)((int64_t)tiles * share / shares), i1 = (int)((int64_t)tiles * (share + 1) / shares);
 
-  // the next tile's place in memory is read one tile ahead
-  int2 next = i0 < i1 ? list[l * cap + i0] : make_int2(0, 0);
-  auto load = [&](int i, unsigned char *st) {
-    const int2 rl = next;
-    if (i + 1 < i1) next = list[l * cap + i + 1];
+  auto load = [&](int2 rl, unsigned char *st, int first, int step) {
     constexpr int UW = Sh::COLS / 8, UN = 3 * RP / 8;
-    for (int x = tid; x < TM * UW; x += NT) {
+#pragma unroll 4
+    for (int x = first; x < TM * UW; x += step) {
       const int r = x / UW, u = x % UW;
       const T *from = wide + ((int64_t)rl.x + (r < rl.y ? r : 0)) * n + col0 + u * 8;
-      const int64_t left = r < rl.y ? (int64_t)n - col0 - u * 8 : 0;
-      unsigned char *to = st + (r * Sh::WP + u * 8) * 2;
-      if constexpr (sizeof(T) == 2 && V == 8) {
-        const int bytes = left > 0 ? 16 : 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
-                     "l"(bytes ? from : wide), "r"(bytes) : "memory");
-      } else {
-        Eight<T, V> e;
-        e.load(from, left);
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          *reinterpret_cast<uint4 *>(to + j * TM * Sh::WP * 2) = make_uint4(e.x[j][0], e.x[j][1], e.x[j][2], e.x[j][3]);
-      }
+      stage8<T, V>(st + (r * Sh::WP + u * 8) * 2, TM * Sh::WP * 2, from, r < rl.y ? (int64_t)n - col0 - u * 8 : 0, wide);
     }
-    for (int x = tid; x < TM * UN; x += NT) {
+#pragma unroll 4
+    for (int x = first; x < TM * UN; x += step) {
       const int r = x / UN, u = x % UN;
       const int bytes = r < rl.y ? 16 : 0;
       const uint16_t *from = narrow + ((int64_t)rl.x + (r < rl.y ? r : 0)) * 3 * RP + u * 8;
@@ -145,8 +133,20 @@ grad_kernel(Grad g0, Grad g1, const int32_t *count, const int2 *list, int64_t ca
                        (uint32_t)__cvta_generic_to_shared(st + Sh::WIDE + (r * Sh::NP + u * 8) * 2)),
                    "l"(from), "r"(bytes) : "memory");
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  if constexpr (Sh::STAGES == 2) {
+    if (warp >= 8) {
+      registers_to_fill<8>();
+      int2 next = i0 < i1 ? list[l * cap + i0] : make_int2(0, 0);  // a tile's place in memory is read one tile ahead
+      fill_buffers<2>(i1 - i0, [&](int i) {
+        const int2 rl = next;
+        if (i0 + i + 1 < i1) next = list[l * cap + i0 + i + 1];
+        load(rl, smem + (i & 1) * Sh::STAGE, tid - NT, FILL);
+      });
+      return;
+    }
+    registers_to_compute<8>();
+  }
 
   float sum[MT][RT][4];
 #pragma unroll
@@ -158,19 +158,17 @@ grad_kernel(Grad g0, Grad g1, const int32_t *count, const int2 *list, int64_t ca
   // transposed on the way: left operand [columns, rows], right operand [rows, ranks]
   const int ra = ((lane >> 4) << 3) + (lane & 7), ua = (lane >> 3) & 1;
   const int rb = (((lane >> 3) & 1) << 3) + (lane & 7), ub = lane >> 4;
-  if (Sh::STAGES == 2 && i0 < i1) load(i0, smem);
   for (int i = i0; i < i1; ++i) {
-    unsigned char *st = smem + (Sh::STAGES == 2 ? (i - i0) & 1 : 0) * Sh::STAGE;
-    if (Sh::STAGES == 1) {
-      load(i, st);
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else if (i + 1 < i1) {
-      load(i + 1, smem + ((i + 1 - i0) & 1) * Sh::STAGE);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const int stage = Sh::STAGES == 2 ? (i - i0) & 1 : 0;
+    unsigned char *st = smem + stage * Sh::STAGE;
+    if constexpr (Sh::STAGES == 2) {
+      bar_sync(bar_full(stage, warp >> 2), GROUP + FILL);
     } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      load(list[l * cap + i], st, tid, NT);
+      cp_commit();
+      cp_wait<0>();
+      __syncthreads();
     }
-    __syncthreads();
     const uint32_t w0 = (uint32_t)__cvta_generic_to_shared(st), n0 = w0 + (uint32_t)Sh::WIDE;
     float acc[MT][RT][4];
 #pragma unroll
@@ -214,7 +212,8 @@ grad_kernel(Grad g0, Grad g1, const int32_t *count, const int2 *list, int64_t ca
       for (int j = 0; j < RT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[m][j][e] += acc[m][j][e];
-    __syncthreads();
+    if constexpr (Sh::STAGES == 1) __syncthreads();
+    else if (i + 2 < i1) bar_arrive(bar_empty(stage, warp >> 2), GROUP + FILL);
   }
   float *to = gr.grad + share * gr.share + (int64_t)l * n * rank;
 #pragma unroll
@@ -248,7 +247,7 @@ cudaError_t grad_go(Grad g0, Grad g1, const int32_t *count, const int2 *list, in
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::BYTES);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((g0.cols + g1.cols) * shares), (unsigned)L);
-  kernel<<<grid, NT, Sh::BYTES, st>>>(g0, g1, count, list, cap, shares, rank);
+  kernel<<<grid, Sh::THREADS, Sh::BYTES, st>>>(g0, g1, count, list, cap, shares, rank);
   return cudaGetLastError();
 }
 template <typename T, int RP>
