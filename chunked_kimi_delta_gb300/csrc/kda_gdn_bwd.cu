@@ -15,7 +15,10 @@
 // Three kernels after the preparation: the forward's chain once more, which
 // leaves each chunk's S and W; the chain backwards, warps as there, dS^T in
 // registers (reverse_kernel); then all chunks at once for what meets over the
-// value channels (intra_kernel).
+// value channels (intra_kernel).  4 x 8192 tokens of 32 heads on 16 key heads, d = 128,
+// bf16: preparation 300 us, chain 622 to 780, reverse 1,115 (484 products a warp and
+// chunk, 7.7 k of its 17 k cycles; beside them 250 KB of a chunk in and out),
+// intra 2,485.
 #include "kda_gdn.cuh"
 
 namespace kda {
@@ -419,7 +422,10 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
 // Sixteen warps: warp w has rows 16 (w % 4) .. of every product and quarter
 // w / 4 of its columns; of the two pairs of [64, 64] products, half of q k^T
 // with dO W^T or of k k^T with dY W^T.  The value heads of a key head take turns, dQ and dK stay
-// in registers meanwhile.
+// in registers meanwhile.  A head takes 43 k cycles of an SM: loads and their
+// conversion to pieces 12 k, products 16 k, elementwise work 6 k, the coefficients'
+// tiles 4 k, the rest barriers; its 208 KB of shared memory leave no room for a
+// second CTA or a second buffer.  With eight warps 3.20 ms.
 constexpr int NT = 512;  // of the intra kernel
 
 template <typename T, int DK, int DV> struct IntraShape {

@@ -5,11 +5,16 @@
 // takes 16 of them and walks the chunks alone: it holds S^T [16, dk] in the
 // accumulator layout of the tensor-core instruction, which is at once (rounded
 // to pieces) the layout of a left operand, and so do Y^T and W^T, its
-// intermediates.  Nothing of the recurrence passes through shared memory;
-// that holds only what the warps of a CTA read in common (k, q, A, P of the
-// chunk, double-buffered where that fits, by warps of their own: with the
-// computing warps copying and a barrier for all after every chunk, 4 x 8192 tokens
-// of 32 heads took 774 us (12 k cycles a chunk), now 670.
+// intermediates.  Nothing of the recurrence passes through shared memory; that
+// holds only what the warps of a CTA read in common (k, q, A, P of the chunk),
+// twice where it fits, filled by warps of their own.
+//
+// 4 x 8192 tokens of 32 heads on 16 key heads, d = 128, bf16: 670 us, 10.2 k cycles a
+// chunk.  What bounds it: 400 tensor-core products a warp and chunk, two warps
+// a scheduler at 8 cycles each, 6.4 k cycles, covered only in part by the other
+// warp's elementwise work.  With the computing warps copying and a barrier for
+// all after every chunk 774 us.  Half the value channels a CTA shorten a chunk
+// where chains are few (130 tokens of 2 heads: 21.9 -> 13.9 us).
 #include "kda_gdn.cuh"
 
 namespace kda {

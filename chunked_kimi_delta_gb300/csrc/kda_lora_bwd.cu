@@ -2,7 +2,9 @@
 //   du = scale dY B,  dX += du A,  dA = sum over rows of du^T x,  dB = sum over rows of scale dY^T (x A^T)
 // du and dX are the forward's kernel with the matrices' roles changed (both
 // transposed once), u = x A^T is it again in the same launch.  dA and dB share a
-// launch too: tiles of 64 rows of one adapter, [columns, ranks] in registers.
+// launch too: tiles of 64 rows of one adapter, [columns, ranks] in registers,
+// narrow operands in three pieces (24 bits).  32,768 rows, 4,096 and 4,096 wide, rank 64:
+// du, dX and u 305 us, dA and dB 276 (their tensor-core products alone 170).
 #include "kda_fill.cuh"
 #include "kda_lora_kernel.cuh"
 
