@@ -172,6 +172,30 @@ def test_step(cuda_lib, dtype, cache, dk, dv, T, gap, v_first):
     assert torch.equal(base[:, h * dk * dv:], before[:, h * dk * dv:])
 
 
+def test_offsets_beyond_32_bits(cuda_lib):
+    """2.2 G elements of v and out, and a pool of as many: a run cut at a chunk's end gives the same bits, and the step
+    finds the last row."""
+    T, cut, H, D = 262_208 + 77, 262_144, 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    q, k = (torch.randn(1, T, 1, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    v = torch.empty(1, T, H, D, dtype=BF16, device="cuda").normal_(generator=gen)
+    g, beta = (torch.randn(1, T, H, generator=gen, device="cuda") for _ in range(2))
+    kw = dict(a_log=torch.zeros(H, device="cuda"), gate_in_kernel=True, beta_sigmoid=True)
+    out, fin = cuda_lib.kda_gdn_chunk_fwd(q, k, v, g, beta, **kw)
+    _, mid = cuda_lib.kda_gdn_chunk_fwd(*(x[:, :cut].contiguous() for x in (q, k, v, g, beta)), **kw)
+    end = [x[:, cut:].contiguous() for x in (q, k, v, g, beta)]
+    late, last = cuda_lib.kda_gdn_chunk_fwd(*end, initial_state=mid, **kw)
+    assert torch.equal(out[:, cut:], late) and torch.equal(fin, last)
+    del v, out, late
+    pool = torch.zeros(2100, H, D, D, device="cuda")  # 2.2 G elements
+    pool[2099] = mid[0]
+    idx = torch.tensor([2099], device="cuda")
+    one = cuda_lib.kda_gdn_recurrent_step(*(x[:, :1].contiguous() for x in end), pool, idx, **kw)
+    want, state = cuda_lib.kda_gdn_chunk_fwd(*(x[:, :1].contiguous() for x in end), initial_state=mid, **kw)
+    assert off(one, want.double().cpu().numpy()) <= 2 * TOL[BF16] and off(pool[2099], state[0].double().cpu().numpy()) <= 2 * TOL[F32]
+    assert float(pool[:2099].abs().max()) == 0
+
+
 def test_prefill_then_decode_is_one_run(cuda_lib):
     """The chunked call on a prefix and the step on what follows, against the oracle on all of it."""
     p = problem([140], hk=2, h=4, seed=4)

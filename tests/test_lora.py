@@ -93,6 +93,31 @@ def test_equal_requests(cuda_lib, dtype, rows, requests):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rank", [30, 50, 128])
+def test_ranks_of_few_rows_each(cuda_lib, dtype, rank):
+    run(cuda_lib, problem([1] * 20, 520, 300, rank, dtype=dtype, packed=False, seed=rank))
+    run(cuda_lib, problem([3, 40, 0, 1, 1, 2, 1, 1], 260, 130, rank, dtype=dtype, seed=rank))
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """2.3 G elements of y: the last request's rows against a call on them alone."""
+    rows, n_out = 70_001, 32_768
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(rows, 64, generator=gen, device="cuda").bfloat16()
+    a, b = (torch.randn(*s, generator=gen, device="cuda").bfloat16() for s in ((2, 8, 64), (2, n_out, 8)))
+    y = torch.zeros(rows, n_out, dtype=BF16, device="cuda")
+    y[-3:] = torch.randn(3, n_out, generator=gen, device="cuda").bfloat16()
+    tail = y[-3:].clone()
+    idx, cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([0, rows - 3, rows], dtype=torch.int32, device="cuda")
+    cuda_lib.kda_lora(x, a, b, idx, y, cu_seqlens=cu, out=y)
+    alone = cuda_lib.kda_lora(x[-3:].contiguous(), a, b, idx[1:], tail, cu_seqlens=torch.tensor([0, 3], dtype=torch.int32, device="cuda"))
+    # the sums over 64 columns run in another order of parts: half a step of bf16
+    assert off(y[-3:], alone.double().cpu().numpy()) <= 2.0 ** -8
+    first = cuda_lib.kda_lora(x[:3].contiguous(), a, b, idx[:1], torch.zeros_like(tail), cu_seqlens=torch.tensor([0, 3], dtype=torch.int32, device="cuda"))
+    assert off(y[:3], first.double().cpu().numpy()) <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_many_requests(cuda_lib, dtype):
     """More requests than a warp looks at in one turn, empty ones among them, one adapter for several."""
     gen = torch.Generator().manual_seed(3)
