@@ -97,9 +97,9 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
   const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;  // right operand, rows are its columns
   const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;  // right operand, transposed on the way
   // Started together the groups stay in step, and then wait for the same unit at a time: 712 us for 4 x 8192 tokens of
-  // 32 heads, 670 to 680 with the second one a chunk and a half later (storing: 770 and 622).  The reverse chain is
-  // better off without (1115 and 1180 us).
-  if (Sh::STAGES == 2 && group == 1 && nc >= 16) __nanosleep(8000);
+  // 32 heads, 670 to 680 with the second one a chunk and a half later.  Storing, a chunk and a half gives 622 or 780 us
+  // from run to run, two chunks 622 to 635.  The reverse chain is better off without (1115 and 1180 us).
+  if (Sh::STAGES == 2 && group == 1 && nc >= 16) __nanosleep(STORE ? 11000 : 8000);
   for (int c = 0; c < nc; ++c) {
     const uint32_t st = base + (Sh::STAGES == 2 ? (c & 1) * Sh::STAGE : 0);
     if constexpr (Sh::STAGES == 2) {
