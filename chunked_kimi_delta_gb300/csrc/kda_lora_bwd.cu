@@ -23,13 +23,22 @@ struct Transpose {  // dst[l][c][r] = src[l][r][c], rows of src R; dst's row pit
   __host__ __device__ int64_t blocks(int L) const { return src ? (int64_t)L * ((C + 31) / 32) * ((ld + 31) / 32) : 0; }
 };
 
+// A block does one of the two.
+template <typename T> union BeforeShared {
+  struct {
+    int l[1024], r0[1024], r1[1024];  // adapter and rows of the requests looked at
+  } requests;
+  T tile[32][33];
+};
+
 template <typename T>
 __global__ void __launch_bounds__(256)
 before_kernel(Args a, int32_t *count, int2 *list, int64_t cap, int64_t list_blocks, Transpose t0, Transpose t1) {
-  __shared__ int s_l[1024], s_r0[1024], s_r1[1024];
+  __shared__ BeforeShared<T> sh;
+  auto &s_l = sh.requests.l, &s_r0 = sh.requests.r0, &s_r1 = sh.requests.r1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x >= list_blocks) {
-    T(*tile)[33] = reinterpret_cast<T(*)[33]>(s_l);
+    auto &tile = sh.tile;
     int64_t b = blockIdx.x - list_blocks;
     const bool second = b >= t0.blocks(a.adapters);
     if (second) b -= t0.blocks(a.adapters);
