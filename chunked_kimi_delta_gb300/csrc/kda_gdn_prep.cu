@@ -191,7 +191,7 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
     const int which = tid / C, r = tid % C;
     const float ss = s_r[which][r];
     const bool l2 = (p.gp.flags & KDA_L2NORM_QK) != 0;
-    const float f = l2 ? 1.f / sqrtf(ss + p.gp.eps) : 1.f;
+    const float f = r >= len ? 0.f : l2 ? 1.f / sqrtf(ss + p.gp.eps) : 1.f;  // eps may be zero
     s_r[which][r] = f;
     s_num[which][r] *= f;
     float top = l2 ? ss * (f * f) : ss;
