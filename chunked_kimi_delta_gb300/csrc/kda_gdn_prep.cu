@@ -17,6 +17,8 @@
 // instructions of a CTA at 46% of the issue slots, in dependent steps between
 // barriers.  With the products in registers, and so three CTAs an SM and block
 // column c of the inverse by warp c alone, 722 us.
+#include <float.h>
+
 #include "kda_gdn.cuh"
 
 namespace kda {
@@ -192,9 +194,11 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
     const float ss = s_r[which][r];
     const bool l2 = (p.gp.flags & KDA_L2NORM_QK) != 0;
     const float f = r >= len ? 0.f : l2 ? 1.f / sqrtf(ss + p.gp.eps) : 1.f;  // eps may be zero
+    const float unit = s_num[which][r] * f;
     s_r[which][r] = f;
-    s_num[which][r] *= f;
-    float top = l2 ? ss * (f * f) : ss;
+    s_num[which][r] = unit;
+    // the row's norm, from above; where its squares leave fp32's range by its largest value, below 2^14 units
+    float top = ss > 1e-30f && ss < 1e30f ? sqrtf(ss) * f : fminf(sqrtf((float)DK) * 16384.f * unit, FLT_MAX);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     if (lane == 0) s_top[which][warp & 1] = top;
@@ -254,8 +258,8 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
     }
   }
   // |P| is at most the scale times the largest norms: a unit for its pieces
-  // without looking at P itself (28 binades below it keep their bits)
-  const float bound = fabsf(p.gp.scale) * sqrtf(fmaxf(s_top[0][0], s_top[0][1])) * sqrtf(fmaxf(s_top[1][0], s_top[1][1]));
+  // without looking at P itself
+  const float bound = fminf(fabsf(p.gp.scale) * fmaxf(s_top[1][0], s_top[1][1]), FLT_MAX) * fmaxf(s_top[0][0], s_top[0][1]);
   const float2 sP = piece_scale(bound);
 
   const int group = p.H / p.Hk;
