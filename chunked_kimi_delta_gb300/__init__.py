@@ -30,6 +30,7 @@ KDA_SAFE_GATE = 1 << 8
 KDA_ALLOW_NEG_EIGVAL = 1 << 9
 KDA_STATE_V_FIRST = 1 << 10
 KDA_LAYOUT_HEAD_MAJOR = 1 << 11
+KDA_ZERO_BEHIND = 1 << 12
 KDA_TEST_WAIT_TIMEOUT = 1 << 30   # test only: see include/kda.h
 KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGNMENT = 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_DEVICE_TIMEOUT = 4, 5, 6
@@ -1233,8 +1234,9 @@ def kda_gdn_chunk_fwd(q, k, v, g, beta, *, scale=None, eps=1e-6, a_log=None, dt_
     """Chunked forward of the gated delta rule with one gate per head:
     arguments as :func:`kda_chunk_fwd`, but ``g`` has beta's shape ([B, T, H]
     or [T, H]; head-major [B, H, T] or [H, T]) and ``dt_bias`` is [H].
-    Returns ``(out, final_state)``.  See ``kda_gdn_chunk_fwd`` in
-    include/kda.h."""
+    Tokens behind the last packed sequence are zero in an ``out`` that the
+    call allocates and left alone in a given one.  Returns ``(out,
+    final_state)``.  See ``kda_gdn_chunk_fwd`` in include/kda.h."""
     if stream is not None:
         with _under(stream):
             return kda_gdn_chunk_fwd(q, k, v, g, beta, scale=scale, eps=eps, a_log=a_log, dt_bias=dt_bias,
@@ -1251,6 +1253,7 @@ def kda_gdn_chunk_fwd(q, k, v, g, beta, *, scale=None, eps=1e-6, a_log=None, dt_
     dev = _launch_device(q, k, v, g, beta, a_log, dt_bias, initial_state, cu_seqlens, out, final_state, workspace)
     if out is None:
         out = _alloc(tuple(v.shape), v.stride(), v.dtype)
+        extra_flags |= KDA_ZERO_BEHIND
     if output_final_state and final_state is None:
         shape = _state_shape(dims[0], q, v, state_v_first, head_major)
         final_state = _alloc(shape, (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1), _F32)
@@ -1273,7 +1276,8 @@ def kda_gdn_chunk_bwd(q, k, v, g, beta, d_out, *, d_final_state=None, scale=None
     <d_final_state, final_state> (either may be None) with respect to the
     inputs as given.  Returns a dict of dq, dk, dv (q's dtype), dg, dbeta
     ([.., H] fp32), da_log, ddt_bias ([H]; None without ``gate_in_kernel``)
-    and d_initial_state (by default where there is an initial state).  See
+    and d_initial_state (by default where there is an initial state); tokens
+    behind the last packed sequence have gradients of zero.  See
     ``kda_gdn_chunk_bwd`` in include/kda.h."""
     if stream is not None:
         with _under(stream):
@@ -1300,7 +1304,7 @@ def kda_gdn_chunk_bwd(q, k, v, g, beta, d_out, *, d_final_state=None, scale=None
     grads["d_initial_state"] = (_alloc(shape, (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1), _F32)
                                 if want_d_initial_state else None)
     b = kda_bwd_args(_gdn_args(q, k, v, g, beta, dims, scale, eps, a_log, dt_bias, initial_state, cu_seqlens, l2norm_qk,
-                               beta_sigmoid, gate_in_kernel, state_v_first, head_major, extra_flags, None, None),
+                               beta_sigmoid, gate_in_kernel, state_v_first, head_major, extra_flags | KDA_ZERO_BEHIND, None, None),
                      _ptr(d_out), _ptr(d_final_state), *[_ptr(grads[n]) for n in (
                          "dq", "dk", "dv", "dg", "dbeta", "da_log", "ddt_bias", "d_initial_state")])
     need = lib.kda_gdn_chunk_bwd_workspace_size(ctypes.byref(b))

@@ -11,6 +11,7 @@ inline kda_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK 
 
 constexpr uint32_t kFlags = KDA_L2NORM_QK | KDA_BETA_SIGMOID | KDA_GATE_IN_KERNEL | KDA_USE_EXP2 | KDA_STATE_V_FIRST |
                             KDA_LAYOUT_HEAD_MAJOR;
+constexpr uint32_t kChunkFlags = kFlags | KDA_ZERO_BEHIND;
 constexpr uint32_t kRefused = KDA_REUSE_PREP | KDA_SAFE_GATE | KDA_ALLOW_NEG_EIGVAL;
 
 inline int key_heads(const kda_fwd_args *a) { return a->Hk > 0 ? a->Hk : a->H; }
@@ -19,7 +20,7 @@ inline int64_t tokens(const kda_fwd_args *a) { return (int64_t)a->B * a->T; }
 kda_status check(const kda_fwd_args *a) {
   if (!a || a->B < 1 || a->T < 0 || a->H < 1) return KDA_ERR_INVALID_ARG;
   if (a->Hk < 0 || (a->Hk > 0 && a->H % a->Hk != 0)) return KDA_ERR_INVALID_ARG;
-  if (a->flags & ~(kFlags | kRefused)) return KDA_ERR_INVALID_ARG;
+  if (a->flags & ~(kChunkFlags | kRefused)) return KDA_ERR_INVALID_ARG;
   if (a->qkv_dtype != KDA_F32 && a->qkv_dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
   if (tokens(a) > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta)) return KDA_ERR_INVALID_ARG;
   if ((a->flags & KDA_GATE_IN_KERNEL) && !a->a_log) return KDA_ERR_INVALID_ARG;
@@ -76,16 +77,36 @@ gdn::Problem problem(const kda_fwd_args *a) {
   return p;
 }
 
+// What is set to zero behind the last packed sequence, if the caller wants it.
+struct Written {
+  void *p;
+  int heads, d;  // d: channels, 0 for fp32 numbers without any
+};
+template <size_t N> gdn::BehindAll behind(const kda_fwd_args *a, const Written (&w)[N]) {
+  static_assert(N <= sizeof(gdn::BehindAll::a) / sizeof(gdn::Behind), "");
+  gdn::BehindAll z{};
+  if (!a->cu_seqlens || !(a->flags & KDA_ZERO_BEHIND)) return z;
+  const bool hm = (a->flags & KDA_LAYOUT_HEAD_MAJOR) != 0;
+  for (const Written &x : w) {
+    if (!x.p) continue;
+    const int64_t one = x.d ? (int64_t)x.d * (a->qkv_dtype == KDA_BF16 ? 2 : 4) : 4;
+    z.a[z.n++] = hm ? gdn::Behind{x.p, x.heads, a->T * one, one} : gdn::Behind{x.p, 1, 0, x.heads * one};
+  }
+  return z;
+}
+
 // Chunk offsets of packed sequences (p.s.chunk_off) and their order, then the preparation.
-cudaError_t prepare(const kda_fwd_args *a, bool bwd, gdn::Problem &p, char *ws, const gdn::Plan &pl, cudaStream_t st) {
+cudaError_t prepare(const kda_fwd_args *a, bool bwd, gdn::Problem &p, char *ws, const gdn::Plan &pl, const gdn::BehindAll &z,
+                    cudaStream_t st) {
   int32_t *co = reinterpret_cast<int32_t *>(ws + pl.off_chunks);
   p.s.chunk_off = co;
   cudaError_t e = cudaSuccess;
   if (p.s.bounds && p.s.N <= gdn::ORDERED) {
     p.order = co + p.s.N + 1;
-    e = gdn::launch_gdn_map(p.s, co, co + p.s.N + 1, st);
+    e = gdn::launch_gdn_map(p.s, co, co + p.s.N + 1, z, st);
   } else if (p.s.bounds) {
     e = launch_chunk_map(p.s, co, st);
+    if (e == cudaSuccess && z.n) e = gdn::launch_gdn_map(p.s, nullptr, nullptr, z, st);
   }
   if (e == cudaSuccess) e = gdn::launch_gdn_prep(a->qkv_dtype, bwd, p, ws, pl, st);
   return e;
@@ -110,7 +131,7 @@ kda_status kda_gdn_chunk_fwd(const kda_fwd_args *a, kda_stream_t stream) {
   if (reinterpret_cast<uintptr_t>(a->workspace) & 255u) return KDA_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(a->workspace);
-  cudaError_t e = prepare(a, false, p, ws, pl, st);
+  cudaError_t e = prepare(a, false, p, ws, pl, behind(a, {Written{a->out, p.H, p.dv}}), st);
   if (e == cudaSuccess)
     e = gdn::launch_gdn_chain(a->qkv_dtype, false, p, ws, pl, gdn::ChainOut{a->out, a->initial_state, a->final_state}, st);
   return cuda_status(e);
@@ -145,7 +166,8 @@ kda_status kda_gdn_chunk_bwd(const kda_bwd_args *b, kda_stream_t stream) {
   if (reinterpret_cast<uintptr_t>(b->workspace) & 255u) return KDA_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(b->workspace);
-  cudaError_t e = prepare(a, true, p, ws, pl, st);
+  cudaError_t e = prepare(a, true, p, ws, pl, behind(a, {Written{b->dq, p.Hk, p.dk}, Written{b->dk, p.Hk, p.dk}, Written{b->dv, p.H, p.dv},
+                                                         Written{b->dg, p.H, 0}, Written{b->dbeta, p.H, 0}}), st);
   if (e == cudaSuccess) e = gdn::launch_gdn_chain(a->qkv_dtype, true, p, ws, pl, gdn::ChainOut{nullptr, a->initial_state, nullptr}, st);
   if (e == cudaSuccess)
     e = gdn::launch_gdn_bwd(a->qkv_dtype, p, ws, pl,

@@ -269,8 +269,19 @@ __device__ __forceinline__ float log_decay(float x, const GateParams &gp, float 
 }
 
 // ---------------------------------------------------------------- launchers
-// Chunk offsets [N + 1] and order [N] of at most ORDERED packed sequences.
-cudaError_t launch_gdn_map(const SeqInfo &s, int32_t *chunk_off, int32_t *order, cudaStream_t st);
+// A tensor whose tokens behind the last packed sequence are set to zero: `heads`
+// runs of all tokens, `pitch` bytes apart, `token` bytes each.
+struct Behind {
+  void *p;
+  int64_t heads, pitch, token;
+};
+struct BehindAll {
+  Behind a[5];
+  int n;
+};
+// Chunk offsets [N + 1] and order [N] of at most ORDERED packed sequences (order
+// null: neither), and zeros behind the last one.
+cudaError_t launch_gdn_map(const SeqInfo &s, int32_t *chunk_off, int32_t *order, const BehindAll &z, cudaStream_t st);
 cudaError_t launch_gdn_prep(kda_dtype dt, bool bwd, const Problem &p, char *ws, const Plan &pl, cudaStream_t st);
 
 // The forward's chain writes out and final_state; the backward's first one (out

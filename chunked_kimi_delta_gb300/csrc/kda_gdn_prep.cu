@@ -440,9 +440,29 @@ gdn_prep_kernel(Problem p, char *kq, char *ap, size_t kq_stride, size_t ap_strid
   }
 }
 
-// A thread a sequence.
-__global__ void __launch_bounds__(ORDERED) gdn_map_kernel(SeqInfo s, int32_t *chunk_off, int32_t *order) {
+// Zeros behind the last sequence, the blocks' share `block` of `blocks`.
+__device__ void zero_behind(const SeqInfo &s, const Behind &z, int64_t block, int64_t blocks) {
+  const int64_t end = s.bounds[s.N], tok = end < 0 ? 0 : end > s.T_tot ? s.T_tot : end, bytes = (s.T_tot - tok) * z.token;
+  if (bytes == 0) return;
+  const int64_t first = (block * ORDERED + threadIdx.x) * 16, step = blocks * ORDERED * 16;
+  for (int64_t h = 0; h < z.heads; ++h) {
+    char *to = static_cast<char *>(z.p) + h * z.pitch + tok * z.token;
+    if (z.token % 16 == 0 && z.pitch % 16 == 0) {
+      for (int64_t x = first; x < bytes; x += step) *reinterpret_cast<uint4 *>(to + x) = make_uint4(0, 0, 0, 0);
+    } else {  // g's and beta's, one word a token and head
+      for (int64_t x = first / 4; x < bytes; x += step / 4) *reinterpret_cast<uint32_t *>(to + x) = 0;
+    }
+  }
+}
+
+// The first block: a thread a sequence.
+__global__ void __launch_bounds__(ORDERED) gdn_map_kernel(SeqInfo s, int32_t *chunk_off, int32_t *order, BehindAll z) {
   __shared__ int s_n[ORDERED], s_w[ORDERED / 32];
+  const int with_map = order != nullptr;
+  if ((int)blockIdx.x >= with_map) {
+    for (int i = 0; i < z.n; ++i) zero_behind(s, z.a[i], blockIdx.x - with_map, gridDim.x - with_map);
+    return;
+  }
   const int n = threadIdx.x, lane = n & 31, warp = n >> 5;
   int chunks = 0;
   if (n < s.N) {
@@ -470,8 +490,8 @@ __global__ void __launch_bounds__(ORDERED) gdn_map_kernel(SeqInfo s, int32_t *ch
 
 }  // namespace
 
-cudaError_t launch_gdn_map(const SeqInfo &s, int32_t *chunk_off, int32_t *order, cudaStream_t st) {
-  gdn_map_kernel<<<1, ORDERED, 0, st>>>(s, chunk_off, order);
+cudaError_t launch_gdn_map(const SeqInfo &s, int32_t *chunk_off, int32_t *order, const BehindAll &z, cudaStream_t st) {
+  gdn_map_kernel<<<(order ? 1 : 0) + (z.n ? 32 : 0), ORDERED, 0, st>>>(s, chunk_off, order, z);
   return cudaGetLastError();
 }
 

@@ -93,6 +93,9 @@ enum {
    * workspace copies (included in the workspace sizes).  Rejected with
    * KDA_ERR_UNSUPPORTED by kda_chunk_fwd_host and kda_recurrent_step. */
   KDA_LAYOUT_HEAD_MAJOR = 1u << 11,
+  /* kda_gdn_chunk_fwd and kda_gdn_chunk_bwd only: tokens behind the last
+   * packed sequence are set to zero in out (in dq, dk, dv, dg, dbeta). */
+  KDA_ZERO_BEHIND = 1u << 12,
   /* Test only (no counterpart on the pages): exercises the device-side
    * failure path without faulting or hanging the GPU.  In a kda_chunk_fwd
    * (or kda_chunk_fwd_static_scratch) that runs the tensor-core chain, the
@@ -501,8 +504,8 @@ size_t kda_gdn_chunk_fwd_workspace_size(const kda_fwd_args *args);
  * (packed sequences, grouped key heads, KDA_LAYOUT_HEAD_MAJOR,
  * KDA_STATE_V_FIRST: no copies are made for either), limits and errors as
  * kda_chunk_fwd; KDA_USE_EXP2 changes nothing; g must not be positive.  Tokens
- * of a packed batch behind the last sequence are neither read nor written.
- * KDA_ERR_UNSUPPORTED also for
+ * of a packed batch behind the last sequence (cu[N] may be below T) are not read,
+ * and not written without KDA_ZERO_BEHIND.  KDA_ERR_UNSUPPORTED also for
  * h_out, v_new_out and KDA_REUSE_PREP, and where (B T / 64 + sequences) * H
  * exceeds 2^31 - 1; KDA_ERR_INVALID_ARG for KDA_TEST_WAIT_TIMEOUT (the kernels
  * wait for nothing).  final_state may be initial_state in place. */
@@ -513,7 +516,8 @@ kda_status kda_gdn_chunk_fwd(const kda_fwd_args *args, kda_stream_t stream);
  * is [.., H] and ddt_bias [H], fp32.  The forward's intermediates are computed
  * anew; the workspace holds the states entering and the state gradients
  * leaving every chunk (fp32).  Where the decay is held at e^-256 (zero in
- * fp32) the gate's gradient is that of a decay of zero.  Errors as the forward,
+ * fp32) the gate's gradient is that of a decay of zero.  Tokens behind the last
+ * sequence as in the forward.  Errors as the forward,
  * and KDA_ERR_INVALID_ARG for null dq, dk, dv, dg or dbeta with tokens, or one
  * of the first three being d_out. */
 size_t kda_gdn_chunk_bwd_workspace_size(const kda_bwd_args *args);

@@ -56,3 +56,29 @@ def test_keys_and_queries_whose_squares_leave_the_range(cuda_lib, dtype, l2, k, 
     got, ref = cuda_lib.kda_gdn_chunk_bwd(*args(d), d["d_out"], d_final_state=d["d_final"], **d["kw"]), _reference(p)
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         check(got[n], ref[n], n)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens", [[70, 33], [0, 0], [3] * 1100])
+@pytest.mark.parametrize("head_major", [False, True])
+def test_padding_behind_the_last_sequence(cuda_lib, dtype, lens, head_major):
+    """What lies there may hold anything: it is not read, and what the call allocates is zero there."""
+    p, pad = problem(lens, hk=1, h=3, dk=64, dv=64, dtype=dtype, packed=True, seed=len(lens)), 77
+    want = cuda_lib.kda_gdn_chunk_fwd(*args(cuda(p)), **cuda(p["kw"]))[0] if sum(lens) else p["v"].cuda()
+    wants = cuda_lib.kda_gdn_chunk_bwd(*args(cuda(p)), p["d_out"].cuda(), d_final_state=p["d_final"].cuda(), **cuda(p["kw"]))
+    for n in ("q", "k", "v", "g", "beta", "d_out"):
+        p[n] = torch.cat([p[n], torch.full((pad, *p[n].shape[1:]), float("nan"), dtype=p[n].dtype)])
+        if head_major:
+            p[n] = p[n].transpose(0, 1).contiguous()
+    d = cuda(p)
+    for _ in range(2):  # what the allocator hands out next held NaN
+        for n in ("q", "k", "v", "g", "beta"):
+            torch.full_like(d[n], float("nan"))
+    out = cuda_lib.kda_gdn_chunk_fwd(*args(d), head_major=head_major, **d["kw"])[0]
+    got = dict(cuda_lib.kda_gdn_chunk_bwd(*args(d), d["d_out"], d_final_state=d["d_final"], head_major=head_major, **d["kw"]), out=out)
+    for n in ("out", "dq", "dk", "dv", "dg", "dbeta"):
+        x = got[n].transpose(0, 1) if head_major else got[n]
+        assert torch.equal(x[:sum(lens)], want if n == "out" else wants[n]), n
+        assert bool((x[sum(lens):] == 0).all()), n
+    for n in ("da_log", "ddt_bias", "d_initial_state"):
+        assert torch.equal(got[n], wants[n]), n
