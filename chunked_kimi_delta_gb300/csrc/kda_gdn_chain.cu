@@ -96,10 +96,19 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
 
   const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;  // right operand, rows are its columns
   const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;  // right operand, transposed on the way
-  // Started together the groups stay in step, and then wait for the same unit at a time: 712 us for 4 x 8192 tokens of
-  // 32 heads, 670 to 680 with the second one a chunk and a half later.  Storing, a chunk and a half gives 622 or 780 us
-  // from run to run, two chunks 622 to 635.  The reverse chain is better off without (1115 and 1180 us).
-  if (Sh::STAGES == 2 && group == 1 && nc >= 16) __nanosleep(STORE ? 11000 : 8000);
+  // Started together the groups stay in step and then wait for the same unit at a time, so the second one starts when
+  // the first has W of its first chunk (storing: Y), half (a quarter) of a chunk later.  Together / so / with the first
+  // chunk done, whole calls on 4 sequences of 32 heads, us:
+  //   forward,   128 chunks  bf16 128 x 128 1006 / 966 / 973   bf16 64 x 128 726 / 715 / 717   fp32 64 x 128 955 / 983 / 998
+  //               16 chunks                  140 / 135 / 135                 103 / 99 / 101                  137 / 135 / 137
+  //   gradients, 128 chunks                 4666 / 4541 / 4662              3296 / 3275 / 3307              4410 / 4329 / 4437
+  //               16 chunks                  632 / 615 / 619                 448 / 442 / 451                 590 / 581 / 592
+  // One chunk alone gains nothing from it.  The reverse chain is better off without (1115 and 1180 us).
+  const bool apart = Sh::STAGES == 2 && WARPS == 8 && nc > 1;
+  if (apart && group == 1) bar_sync(BAR_START, 2 * GROUP);
+  auto start_second = [&](int c) {
+    if (apart && group == 0 && c == 0) bar_arrive(BAR_START, 2 * GROUP);
+  };
   for (int c = 0; c < nc; ++c) {
     const uint32_t st = base + (Sh::STAGES == 2 ? (c & 1) * Sh::STAGE : 0);
     if constexpr (Sh::STAGES == 2) {
@@ -208,6 +217,7 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       }
     }
 
+    if constexpr (STORE) start_second(c);
     // ---- W^T = Y^T A^T
     float W[8][4];
     row_scales(Y, z0, z1);
@@ -242,6 +252,7 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     if constexpr (STORE) {
       keep(pl.off_w, W, 8, warp_max(W), MAX_W);
     } else {
+    start_second(c);
     // ---- o += P W
     row_scales(W, z0, z1);
 #pragma unroll

@@ -82,3 +82,25 @@ def test_padding_behind_the_last_sequence(cuda_lib, dtype, lens, head_major):
         assert bool((x[sum(lens):] == 0).all()), n
     for n in ("da_log", "ddt_bias", "d_initial_state"):
         assert torch.equal(got[n], wants[n]), n
+
+
+@pytest.mark.parametrize("dtype,dk", [(BF16, 128), (BF16, 64), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("T", [64, 65, 130, 1093])
+def test_results_do_not_depend_on_what_else_is_computed(cuda_lib, dtype, dk, T):
+    """Many chains (a CTA has all 128 value channels, in two groups of warps) and a few of the same ones (a CTA has half
+    of them): a warp's arithmetic is its own, so the bits are the same."""
+    h = 80
+    p = problem([T, T], hk=h, h=h, dk=dk, dtype=dtype, seed=T)
+    few = dict(p, **{n: p[n][:1, :, 3:5].contiguous() for n in ("q", "k", "v", "g", "beta", "d_out")}, d_final=p["d_final"][:1, 3:5].contiguous())
+    few["kw"] = dict(p["kw"], a_log=p["kw"]["a_log"][3:5].contiguous(), dt_bias=p["kw"]["dt_bias"][3:5].contiguous(),
+                     initial_state=p["kw"]["initial_state"][:1, 3:5].contiguous())
+    res = []
+    for x in (p, few):
+        d = cuda(x)
+        res.append((*cuda_lib.kda_gdn_chunk_fwd(*args(d), **d["kw"]),
+                    cuda_lib.kda_gdn_chunk_bwd(*args(d), d["d_out"], d_final_state=d["d_final"], **d["kw"])))
+    (out, fin, g), (out1, fin1, g1) = res
+    assert torch.equal(out[:1, :, 3:5], out1) and torch.equal(fin[:1, 3:5], fin1)
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(g[n][:1, :, 3:5], g1[n]), n
+    assert torch.equal(g["d_initial_state"][:1, 3:5], g1["d_initial_state"])
