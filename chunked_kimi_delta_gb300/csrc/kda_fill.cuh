@@ -18,7 +18,7 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("
 // Two buffers in shared memory: four warps fill them, groups of four warps, one
 // on each of the SM's schedulers, empty them.  The groups never meet each other,
 // so that one can be at its products while the other is at its elementwise work
-// (BAR_START, where a kernel has the first of them tell the second to begin).
+// (BAR_START and the next: where a kernel has the first of them tell the second to begin).
 constexpr int GROUP = 128, FILL = 128, BAR_FULL = 1, BAR_EMPTY = 5, BAR_GROUP = 9, BAR_START = 11;
 __device__ __forceinline__ int bar_full(int stage, int group) { return BAR_FULL + 2 * stage + group; }
 __device__ __forceinline__ int bar_empty(int stage, int group) { return BAR_EMPTY + 2 * stage + group; }

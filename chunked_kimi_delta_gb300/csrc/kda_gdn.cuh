@@ -14,9 +14,16 @@
 // the scale are numbers per token, applied to sums.
 //
 // Arithmetic.  Products run on the tensor cores as fp16 pieces with fp32
-// sums: a value x is s x = hi + lo + (at most 2^-23 |s x|), s a power of two that takes
-// the largest of its row to [2^13, 2^14) (28 binades below it keep their
-// bits), and a product of two such values is hi hi + hi lo + lo hi.  bf16
+// sums: a value x is s x = hi + lo, s a power of two that takes the largest that
+// shares it to [2^13, 2^14), and a product of two such values is hi hi + hi lo +
+// lo hi.  fp16's numbers end at 2^-24: x is off by at most 2^-23 of itself (22
+// bits and more) down to 2^-15 of that largest one, below that by 2^-38 of it
+// (hi alone: 2^-12 of itself, and from 2^-27 on 2^-38 of the largest).  What shares a unit: a
+// token's k, q and, in the last kernel, d_out; a value channel's row of S, Y, W and
+// their gradients over a chunk's 64 tokens; A and P of a chunk; in the last
+// kernel S, dS', W, dY and the tiles of coefficients, each as a whole.  So
+// tokens of very different size in a chunk cost the small ones bits, but not
+// dq, which is a token's d_out's own (and out, with norms).  bf16
 // inputs are one piece (8 bits fit fp16's 11), so the state, held in fp32,
 // costs two products with them and keeps fp32's accuracy; bf16 pieces would
 // lose 2^-17 of it at the same cost.  What only leads to a bf16 result (o, dq,
@@ -92,12 +99,12 @@ inline size_t ap_bytes(kda_dtype d, bool bwd) { return NUM_BYTES + (size_t)MAT_B
 // the order in which a warp's lanes hold it ([16 value channels][8 columns]
 // tiles, four values a lane): the state entering the chunk and the gradient of
 // the one leaving it ([dv, dk]), W, e^G k S and dY ([dv, 64]); the largest of
-// each of S, dS, W, dY, dO in each warp's 16 channels; sums over each 64
+// each of S, dS, W, dY in each warp's 16 channels; sums over each 64
 // channels for each token; the sums of a_log's and dt_bias's gradients.
 struct Plan {
   size_t off_chunks, off_kq, off_ap, off_s, off_ds, off_w, off_e, off_dy, off_max, off_dots, off_part, total;
 };
-constexpr int MAX_S = 0, MAX_DS = 8, MAX_W = 16, MAX_DY = 24, MAX_DO = 32, MAX_FLOATS = 64;
+constexpr int MAX_S = 0, MAX_DS = 8, MAX_W = 16, MAX_DY = 24, MAX_FLOATS = 32;
 constexpr int DOT_BETA = 0, DOT_K = 64, DOT_Y = 128, DOT_FLOATS = 192;
 inline Plan make_gdn_plan(kda_dtype d, int64_t nchunks, int N, int H, int Hk, int dk, int dv, bool bwd) {
   Plan p{};

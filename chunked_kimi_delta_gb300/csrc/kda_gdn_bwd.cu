@@ -149,11 +149,17 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
 
   const int rb = ((lane >> 4) << 3) + (lane & 7), ub = (lane >> 3) & 1;
   const int rt = (((lane >> 3) & 1) << 3) + (lane & 7), ut = lane >> 4;
+  // The second group begins a chunk when the first has dW of it: left alone they fall in step or out of it as the code
+  // around happens to be (1110 to 1180 us for 4 x 8192 tokens of 32 heads, bf16 128 x 128; so 1089, at the first chunk
+  // alone 1079 to 1170; 64 x 128 800, so 793; 16 chunks 152, so 145).  Two barriers in turn: the first group comes to
+  // the second chunk after this one only when the second has emptied this one's buffer.
+  constexpr bool APART = Sh::STAGES == 2 && WARPS == 8;
   for (int c = nc - 1; c >= 0; --c) {
     const int stage = (nc - 1 - c) & 1;
     const uint32_t so = Sh::STAGES == 2 ? stage * Sh::STAGE : 0, st = base + so;
     if constexpr (Sh::STAGES == 2) {
       bar_sync(bar_full(stage, group), GROUP + FILL);
+      if (APART && group == 1) bar_sync(BAR_START + stage, 2 * GROUP);
     } else {
       load(c, st, tid * 16, WARPS * 512);
 #pragma unroll
@@ -225,10 +231,6 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
     // ---- dW = X + P^T dO
     float O[8][4], Y[8][4];
     load_strip<T>(smem + so + Sh::S_DO + warp * Sh::STRIP, lane, O);
-    {
-      const float m = warp_max(O);
-      if (lane == 0) maxes[MAX_DO] = m;
-    }
     row_scales(O, z0, z1);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -263,6 +265,8 @@ gdn_reverse_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_str
 #pragma unroll
       for (int i = 0; i < 8; ++i) ev[i] = from[i * 32];
     }
+
+    if (APART && group == 0) bar_arrive(BAR_START + stage, 2 * GROUP);
 
     // ---- dY = A^T dW
     row_scales(X, z0, z1);
@@ -436,7 +440,7 @@ template <typename T, int DK, int DV> struct IntraShape {
                             S_S = S_DO + NI * VT, S_DS = S_S + 2 * ST, END = S_DS + NI * ST;
   // over S and dS' once these are used: the coefficients of k and q, then the pairs of dg
   static constexpr uint32_t S_T = S_S, S_X = S_T + 3 * NI * MAT_BYTES, END2 = S_X + C * C * 4;
-  static constexpr uint32_t S_NUM = END > END2 ? END : END2, BYTES = S_NUM + 11 * C * 4 + 128;
+  static constexpr uint32_t S_NUM = END > END2 ? END : END2, BYTES = S_NUM + 11 * C * 4 + 192;
 };
 
 template <int N> __device__ __forceinline__ void zero(float (&x)[N][4]) {
@@ -476,6 +480,8 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         *s_db = s_e;  // [2][C], once e^G is used
   int *s_max = reinterpret_cast<int *>(s_iq + 4 * C);  // [3]
   float *s_z = s_iq + 4 * C + 4;                       // [16]
+  uint8_t *s_do = reinterpret_cast<uint8_t *>(s_z + 16);  // [C]: exponents of d_out's units, a token's each
+  auto unit_of = [&](int i) { return __uint_as_float((uint32_t)s_do[i] << 23); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quarter = warp >> 2, half = quarter >> 1, side = quarter & 1;
   const int mt = side ? 3 - (warp & 3) : warp & 3;  // later rows have more to do: each scheduler gets early and late ones
   const int g = lane >> 2, t = (lane & 3) * 2;
@@ -523,19 +529,14 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       s_f[tid] = exp2f((num[NUM_GH + C - 1] - gh) + (num[NUM_GL + C - 1] - gl));
     }
     if (tid < 3) s_max[tid] = 0;
-    float2 sc[5];  // S, dS', W, dY, dO: one unit of pieces for the whole of each, eight lanes to find its largest
+    float2 sc[4];  // S, dS', W, dY: one unit of pieces for the whole of each, eight lanes to find its largest
     {
       const float *m = reinterpret_cast<const float *>(ws + pl.off_max) + unit * MAX_FLOATS;
-      const bool mine = (lane & 7) < DV / 16;
-      float a = mine ? m[lane] : 0.f, b = mine && lane < 8 ? m[MAX_DO + lane] : 0.f;
+      float a = (lane & 7) < DV / 16 ? m[lane] : 0.f;
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
-        b = fmaxf(b, __shfl_xor_sync(~0u, b, o));
-      }
+      for (int o = 1; o < 8; o <<= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, o));
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[i] = piece_scale(__shfl_sync(~0u, a, 8 * i));
-      sc[4] = piece_scale(__shfl_sync(~0u, b, 0));
     }
     // the states' first share on its way before the rest is worked on
     constexpr int ROUNDS = DV / 16 * US * 32 / NT, EARLY = ROUNDS < 4 ? ROUNDS : 4;
@@ -574,11 +575,19 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         const int r = x / UV, u = x % UV;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (r < len && io.d_out) load8(o + r * p.v.t + u * 8, v);
+        // a token's row in a unit of its own: what is its own alone, dq, keeps its bits beside larger ones
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+        for (int o = 1; o < UV; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        const float2 so = piece_scale(m);
+        if (u == 0) s_do[r] = (uint8_t)(__float_as_uint(so.y) >> 23);
         uint4 hi, lo;
-        split2(v[0] * sc[4].x, v[1] * sc[4].x, hi.x, lo.x);
-        split2(v[2] * sc[4].x, v[3] * sc[4].x, hi.y, lo.y);
-        split2(v[4] * sc[4].x, v[5] * sc[4].x, hi.z, lo.z);
-        split2(v[6] * sc[4].x, v[7] * sc[4].x, hi.w, lo.w);
+        split2(v[0] * so.x, v[1] * so.x, hi.x, lo.x);
+        split2(v[2] * so.x, v[3] * so.x, hi.y, lo.y);
+        split2(v[4] * so.x, v[5] * so.x, hi.z, lo.z);
+        split2(v[6] * so.x, v[7] * so.x, hi.w, lo.w);
         *reinterpret_cast<uint4 *>(smem + Sh::S_DO + unit_at<UV>(r, u)) = hi;
         if constexpr (NI == 2) *reinterpret_cast<uint4 *>(smem + Sh::S_DO + Sh::VT + unit_at<UV>(r, u)) = lo;
       }
@@ -671,7 +680,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int i = row0 + 8 * rr;
-        const float eq = s_e[i] * scale, ek = s_e[i] * s_beta[i];
+        const float eq = s_e[i] * scale, ek = s_e[i] * s_beta[i], un = unit_of(i);
 #pragma unroll
         for (int nt = 0; nt < NW; ++nt) {
           const uint32_t at = unit_at<UK>(i, pass * US + quarter * NW + nt) + t * 2;
@@ -681,7 +690,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
             q.x += ql.x;
             q.y += ql.y;
           }
-          const float a = x[nt][2 * rr] * sc[4].y * sc[0].y, b = x[nt][2 * rr + 1] * sc[4].y * sc[0].y;
+          const float a = x[nt][2 * rr] * un * sc[0].y, b = x[nt][2 * rr + 1] * un * sc[0].y;
           iq[rr] = fmaf(a, q.x, fmaf(b, q.y, iq[rr]));
           dq[pass][nt][2 * rr] = fmaf(eq, a, dq[pass][nt][2 * rr]);
           dq[pass][nt][2 * rr + 1] = fmaf(eq, b, dq[pass][nt][2 * rr + 1]);
@@ -765,7 +774,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
     }
     auto col_of = [&](int nt) { return 16 * (side + (nt & 2)) + 8 * (nt & 1) + t; };
     float db[2] = {0.f, 0.f}, top0 = 0.f, top1 = 0.f;
-    const float un = half ? -sc[3].y : sc[4].y;
+    const float un[2] = {half ? -sc[3].y : unit_of(row0), half ? -sc[3].y : unit_of(row0 + 8)};
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
@@ -774,17 +783,18 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         float mv = 0.f, xv = 0.f;
         if (half ? j < i : j <= i) {
           const float gam = exp2_neg((s_gh[i] - s_gh[j]) + (s_gl[i] - s_gl[j]));
-          mv = m[nt][e] * un * sc[2].y * gam;
+          mv = m[nt][e] * sc[2].y * gam;  // dP in d_out's units
           if (half) {
+            mv *= un[e >> 1];
             const float kk = x[nt][e] * s_kn[i] * s_kn[j];
             db[e >> 1] = fmaf(mv, kk, db[e >> 1]);
             mv *= s_beta[i];
             xv = mv * kk;
             top0 = fmaxf(top0, fmaxf(fabsf(mv * s_kn[j]), fabsf(mv * s_kn[i])));
           } else {
-            xv = mv * (x[nt][e] * s_qn[i] * s_kn[j] * scale);
+            xv = mv * un[e >> 1] * (x[nt][e] * s_qn[i] * s_kn[j] * scale);
             top0 = fmaxf(top0, fabsf(mv * s_kn[j]));
-            top1 = fmaxf(top1, fabsf(mv * s_qn[i]));
+            top1 = fmaxf(top1, fabsf(mv * un[e >> 1] * s_qn[i]));
           }
         }
         m[nt][e] = mv;
@@ -844,9 +854,9 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
           if (j < i) put(2, j, i, mv * ki);
           if (j + 1 < i) put(2, j + 1, i, mw * ki);
         } else {
-          const float qi = s_qn[i] * s2.x;
+          const float qi = s_qn[i] * s2.x, ui = un[e >> 1];
           put2(0, i, j, mv * (s_kn[j] * s1.x), mw * (s_kn[j + 1] * s1.x));
-          put2(1, i, j, mv * qi, mw * qi);
+          put2(1, i, j, mv * ui * qi, mw * ui * qi);
           x_at(i, j) = x[nt][e];
           x_at(i, j + 1) = x[nt][e + 1];
         }
@@ -862,6 +872,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       }
     }
     // dQ += dP.. k, dK += (dP..)^T q + (M + M^T) k
+    const float ud[2] = {unit_of(row0), unit_of(row0 + 8)};
 #pragma unroll
     for (int pass = 0; pass < PASSES; ++pass) {
       float a[NW][4], b[NW][4], d[NW][4];
@@ -898,7 +909,7 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       for (int nt = 0; nt < NW; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          dq[pass][nt][e] = fmaf(scale, a[nt][e] * s1.y, dq[pass][nt][e]);
+          dq[pass][nt][e] = fmaf(scale, a[nt][e] * s1.y * ud[e >> 1], dq[pass][nt][e]);
           dk[pass][nt][e] += scale * (b[nt][e] * s2.y) + d[nt][e] * s3.y;
         }
     }

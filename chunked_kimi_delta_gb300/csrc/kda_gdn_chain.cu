@@ -103,7 +103,7 @@ gdn_chain_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
   //               16 chunks                  140 / 135 / 135                 103 / 99 / 101                  137 / 135 / 137
   //   gradients, 128 chunks                 4666 / 4541 / 4662              3296 / 3275 / 3307              4410 / 4329 / 4437
   //               16 chunks                  632 / 615 / 619                 448 / 442 / 451                 590 / 581 / 592
-  // One chunk alone gains nothing from it.  The reverse chain is better off without (1115 and 1180 us).
+  // One chunk alone gains nothing from it.
   const bool apart = Sh::STAGES == 2 && WARPS == 8 && nc > 1;
   if (apart && group == 1) bar_sync(BAR_START, 2 * GROUP);
   auto start_second = [&](int c) {

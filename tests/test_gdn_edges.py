@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from gdn_testutil import args, check, cuda, oracle_of, problem
+from gdn_testutil import TOL, args, check, cuda, oracle_of, problem
 from test_gdn_bwd import _reference
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +104,72 @@ def test_results_do_not_depend_on_what_else_is_computed(cuda_lib, dtype, dk, T):
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         assert torch.equal(g[n][:1, :, 3:5], g1[n]), n
     assert torch.equal(g["d_initial_state"][:1, 3:5], g1["d_initial_state"])
+
+
+def _per_token(got, ref, T, h):
+    """2-norms over the channels of the error and of the result, for each token and head."""
+    ref = np.asarray(ref).reshape(T, h, -1)
+    x = got.double().cpu().numpy().reshape(ref.shape)
+    return np.linalg.norm(x - ref, axis=-1), np.linalg.norm(ref, axis=-1)
+
+
+# As gdn_testutil's, but fp32's four products in a row with errors that are independent, so that their squares add:
+# sqrt(4) / 4 of their sum
+TOKEN_TOL = {BF16: TOL[BF16], F32: TOL[F32] / 2}
+
+
+def _all(kda, p):
+    d = cuda(p)
+    out, fin = kda.kda_gdn_chunk_fwd(*args(d), **d["kw"])
+    got = kda.kda_gdn_chunk_bwd(*args(d), d["d_out"], d_final_state=d["d_final"], want_d_initial_state=True, **d["kw"])
+    o, f = oracle.chunk_fwd(oracle_of(p), p["kw"]["initial_state"])
+    return dict(got, out=out, final=fin), dict(_reference(p), out=o, final=f)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("gate", ["slow", "strong"])
+@pytest.mark.parametrize("lens", [[300], [1, 130, 0, 70, 2]])
+def test_every_token_and_head_by_itself(cuda_lib, dtype, gate, lens):
+    """No token, head or sequence hides behind the others' size.  A token's sum may cancel (dq of two value heads whose
+    states have decayed is (c1 + c2) k with numbers c of either sign), its terms are then of the size of its neighbours'
+    results: errors of 2^-12 of terms a hundred times the sum are 2^-5 of the sum.  So a token is held to its own size and
+    the root mean square of its head's tokens, which no sum over tokens dilutes.  dg and dbeta are one number: a dot
+    product of 128 channels, which d_final makes larger at the sequences' last tokens than elsewhere (its k dS is 0.1
+    sqrt(128) beside P dO's 0.09 k.q / |k||q| sqrt(128): ten times).  Where such a one cancels its terms are still of that
+    size, so these are held to the largest of their head in the mean square's place."""
+    p = problem(lens, hk=2, h=4, dtype=dtype, gate=gate, seed=21)
+    got, ref = _all(cuda_lib, p)
+    T = sum(lens)
+    for n, h in (("out", 4), ("dq", 2), ("dk", 2), ("dv", 4), ("dg", 4), ("dbeta", 4)):
+        e, size = _per_token(got[n], ref[n], T, h)
+        number = n in ("dg", "dbeta")
+        bound = TOKEN_TOL[F32 if number else dtype] * (size + (size.max(0) if number else np.sqrt((size ** 2).mean(0))))
+        assert np.all(e <= bound), (n, np.max(e / bound))
+    for n in ("final", "d_initial_state"):
+        r = np.asarray(ref[n]).reshape(len(lens), 4, -1)
+        e = np.linalg.norm(got[n].double().cpu().numpy().reshape(r.shape) - r, axis=-1)
+        assert np.all(e <= TOKEN_TOL[F32] * np.linalg.norm(r, axis=-1)), n
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("what", ["q", "d_out", "v"])
+def test_tokens_of_very_different_size_in_one_chunk(cuda_lib, dtype, what):
+    """Tokens of 1, 2^-20 and 2^-30 beside each other.  dq where d_out differs is a token's own and keeps its own
+    accuracy.  P (out where q differs, here without norms) is held against its chunk's largest: its pieces end 2^-15
+    below an ordinary error of that, and that largest is a bound from norms, by Gaussian rows' sqrt(128) = 2^3.5 too high:
+    2^-11 with sums of two terms.  What sums over a chunk's tokens is as good as its largest."""
+    T = 192
+    p = problem([T], hk=1, h=2, dtype=dtype, raw=what == "q", seed=5)
+    e = torch.tensor([0, -20, -30])[torch.randint(0, 3, (T,), generator=torch.Generator().manual_seed(9))]
+    p[what] = (p[what].float() * (2.0 ** e).view(1, T, 1, 1)).to(dtype)
+    p["d_final"] *= 0  # a gradient of the last state would reach every token
+    if what == "v":
+        p["kw"]["initial_state"] *= 0
+    got, ref = _all(cuda_lib, p)
+    share = {("out", "q"): 2.0 ** -11, ("dq", "d_out"): 0.0}
+    for n, h in (("out", 2), ("dq", 1), ("dk", 1), ("dv", 2), ("dg", 2), ("dbeta", 2)):
+        err, size = _per_token(got[n], ref[n], T, h)
+        most = np.repeat(size.reshape(T // 64, 64, h).max(1), 64, 0)
+        tol = TOKEN_TOL[dtype if n not in ("dg", "dbeta") else F32]
+        bound = tol * (size + share.get((n, what), 1.0) * most)
+        assert np.all(err <= bound), (n, np.max(err / bound))
