@@ -547,6 +547,17 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
       sv[e] = reinterpret_cast<const float4 *>(ws + pl.off_s)[unit * (DV / 16) * UK * 32 + from];
       dv_[e] = reinterpret_cast<const float4 *>(ws + pl.off_ds)[unit * (DV / 16) * UK * 32 + from];
     }
+    const T *o = static_cast<const T *>(io.d_out) + batch * p.v.b + tok * p.v.t + h * p.v.h;
+    // bf16 rows of d_out as well; fp32 ones would take too many registers
+    constexpr int OR = C * UV / NT;
+    uint4 raw[OR];
+    if constexpr (NI == 1) {
+#pragma unroll
+      for (int k = 0; k < OR; ++k) {
+        const int x = tid + k * NT, r = x / UV, u = x % UV;
+        raw[k] = r < len && io.d_out ? *reinterpret_cast<const uint4 *>(o + r * p.v.t + u * 8) : make_uint4(0, 0, 0, 0);
+      }
+    }
     {
       const float4 *w = reinterpret_cast<const float4 *>(ws + pl.off_w) + unit * (DV / 16) * 8 * 32;
       const float4 *y = reinterpret_cast<const float4 *>(ws + pl.off_dy) + unit * (DV / 16) * 8 * 32;
@@ -569,12 +580,20 @@ gdn_intra_kernel(Problem p, char *ws, Plan pl, size_t kq_stride, size_t ap_strid
         *reinterpret_cast<uint32_t *>(smem + Sh::S_DY + at8) = hi;
         *reinterpret_cast<uint32_t *>(smem + Sh::S_DY + Sh::VT + at8) = lo;
       }
-      const T *o = static_cast<const T *>(io.d_out) + batch * p.v.b + tok * p.v.t + h * p.v.h;
-#pragma unroll 4
-      for (int x = tid; x < C * UV; x += NT) {
-        const int r = x / UV, u = x % UV;
+#pragma unroll
+      for (int k = 0; k < OR; ++k) {
+        const int x = tid + k * NT, r = x / UV, u = x % UV;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r < len && io.d_out) load8(o + r * p.v.t + u * 8, v);
+        if constexpr (NI == 1) {
+          const uint32_t w8[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w8[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w8[i] & 0xffff0000u);
+          }
+        } else if (r < len && io.d_out) {
+          load8(o + r * p.v.t + u * 8, v);
+        }
         // a token's row in a unit of its own: what is its own alone, dq, keeps its bits beside larger ones
         float m = 0.f;
 #pragma unroll
