@@ -189,6 +189,7 @@ kda_status kda_gdn_recurrent_step(const kda_decode_args *a, kda_stream_t stream)
   if ((a->flags & KDA_GATE_IN_KERNEL) && !a->a_log) return KDA_ERR_INVALID_ARG;
   if (a->N == 0) return KDA_OK;
   if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->out || !a->cache || !a->idx) return KDA_ERR_INVALID_ARG;
+  if (a->out == a->q || a->out == a->k) return KDA_ERR_INVALID_ARG;  // read by the other CTAs of a head, and of a group
   if ((int64_t)a->N * a->H > INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;  // two CTAs a state
   return cuda_status(gdn::launch_gdn_step(*a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -524,7 +524,8 @@ size_t kda_gdn_chunk_bwd_workspace_size(const kda_bwd_args *args);
 kda_status kda_gdn_chunk_bwd(const kda_bwd_args *args, kda_stream_t stream);
 
 /* The recurrent step on pool states, in fp32, as kda_recurrent_step (any
- * pool alignment; KDA_STATE_V_FIRST pools are [H, dv, dk]). */
+ * pool alignment; KDA_STATE_V_FIRST pools are [H, dv, dk]).  out may be v, not q
+ * or k (KDA_ERR_INVALID_ARG). */
 kda_status kda_gdn_recurrent_step(const kda_decode_args *args, kda_stream_t stream);
 
 /* ------------------------------------------------------------------------

@@ -173,3 +173,15 @@ def test_tokens_of_very_different_size_in_one_chunk(cuda_lib, dtype, what):
         tol = TOKEN_TOL[dtype if n not in ("dg", "dbeta") else F32]
         bound = tol * (size + share.get((n, what), 1.0) * most)
         assert np.all(err <= bound), (n, np.max(err / bound))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_step_result_in_the_values_place(cuda_lib, dtype, dv):
+    d = cuda(problem([3] * 40, hk=2, h=4, dv=dv, dtype=dtype, packed=False, seed=8))
+    kw = {n: v for n, v in d["kw"].items() if n not in ("initial_state", "cu_seqlens")}
+    pool, idx = 0.1 * torch.randn(40, 4, 128, dv, device="cuda"), torch.arange(40, device="cuda").flip(0).contiguous()
+    mine = pool.clone()
+    want = cuda_lib.kda_gdn_recurrent_step(*args(d), pool, idx, **kw)
+    got = cuda_lib.kda_gdn_recurrent_step(*args(d), mine, idx, out=d["v"], **kw)
+    assert got is d["v"] and torch.equal(got, want) and torch.equal(mine, pool)
