@@ -580,8 +580,16 @@ template <bool TWO> cudaError_t run(kda_dtype dt, const Pair &both, int n, cudaS
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t per = a.rows / a.requests;
-  const int m = per <= 16 ? 16 : 64;
-  const int64_t tiles = a.cu ? a.rows / m + a.requests + 1 : a.requests * ((per + m - 1) / m);
+  auto tiles_of = [&](int m) { return a.cu ? a.rows / m + a.requests + 1 : a.requests * ((per + m - 1) / m); };
+  // Rows a tile.  Where requests have up to 16 rows in the mean, and where all tiles of 16 run at once, 16: two a SM,
+  // one for fp32 above rank 16.  64 x n rows, 4,096 -> 4,096, tiles of 16 / of 64, us: bf16 rank 16 n = 32 16 / 30,
+  // n = 64 33 / 37, n = 96 (384 tiles) 62 / 47; rank 128 n = 64 107 / 177, n = 96 157 / 156; fp32 rank 16 n = 64 92 / 150,
+  // rank 64 n = 32 158 / 214, n = 48 (192 tiles) 306 / 241.  Rows in all, not the mean, decide above 16: 64 single rows
+  // beside 2,048 22.6 / 32.3, beside 4,096 51.5 / 40.7; 512 x 32 124 / 113.  Eight times 64 at rank 128 would want 64
+  // (47 / 37).
+  const int64_t at_once = (dt == KDA_BF16 || a.rank <= 16 ? 2 : 1) * (int64_t)sms;
+  const int m = per <= 16 || n * tiles_of(16) <= at_once ? 16 : 64;
+  const int64_t tiles = tiles_of(m);
   // CTAs a tile.  Tiles of 64 rows: until every SM has its two (115 tiles of 2,048 -> 4,196: 48.5 us with 4 of
   // them, 51.4 with 2; 512 tiles of 4,096 -> 4,096, enough by themselves: 230 us with 1, 277 with 4, which fill the
   // last round better but add their parts).  Tiles of 16, a few rows each, are the start and end of a CTA more

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_lora import F32, problem
+from test_lora import BF16, F32, problem, run
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +24,17 @@ def test_fp32_gradients_through_every_element_of_the_transposed_tiles(cuda_lib, 
         want = torch.zeros_like(dx)
         want[:, c] = 0.5 * (2.0 + l)
         assert torch.equal(dx, want), (r, c)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n_in,n_out,rank", [(256, 320, 1), (256, 320, 16), (100, 200, 24), (33, 31, 60), (1000, 36, 64), (64, 136, 128)])
+def test_more_rows_than_small_tiles_take_at_once(cuda_lib, dtype, n_in, n_out, rank):
+    """Tiles have 16 rows up to two of them an SM (4,864 rows at 152 SMs) and 64 above: both in one ragged batch's sizes."""
+    for lens in ([5, 0, 4000, 64, 1, 900, 300], [17, 64, 65, 130]):
+        run(cuda_lib, problem(lens, n_in, n_out, rank, dtype=dtype, idx=([2, 1, 0, 2, 3, 1, 0])[:len(lens)], seed=rank))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [17, 64, 100])
+def test_more_equal_requests_than_small_tiles_take_at_once(cuda_lib, dtype, rows):
+    run(cuda_lib, problem([rows] * 320, 136, 72, 16, dtype=dtype, packed=False, seed=rows))
