@@ -16,9 +16,9 @@
 // leaves each chunk's S and W; the chain backwards, warps as there, dS^T in
 // registers (reverse_kernel); then all chunks at once for what meets over the
 // value channels (intra_kernel).  4 x 8192 tokens of 32 heads on 16 key heads, d = 128,
-// bf16: preparation 298 us, chain 627, reverse 1,115 (484 products a warp and
+// bf16: preparation 298 us, chain 641, reverse 1,089 (484 products a warp and
 // chunk, 7.7 k of its 17 k cycles; beside them 250 KB of a chunk in and out),
-// intra 2,485.
+// intra 2,513.  With one unit for a chunk's d_out instead of a token's 2,476.
 #include "kda_gdn.cuh"
 
 namespace kda {

@@ -9,7 +9,7 @@
 // holds only what the warps of a CTA read in common (k, q, A, P of the chunk),
 // twice where it fits, filled by warps of their own.
 //
-// 4 x 8192 tokens of 32 heads on 16 key heads, d = 128, bf16: 670 us, 10.2 k cycles a
+// 4 x 8192 tokens of 32 heads on 16 key heads, d = 128, bf16: 668 us, 10.2 k cycles a
 // chunk.  What bounds it: 400 tensor-core products a warp and chunk, two warps
 // a scheduler at 8 cycles each, 6.4 k cycles, covered only in part by the other
 // warp's elementwise work.  With the computing warps copying and a barrier for

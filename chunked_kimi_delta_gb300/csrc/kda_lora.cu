@@ -19,8 +19,8 @@
 // steps: the tensor core cuts what does not fit off its running sum, always
 // towards zero.
 //
-// 6,731 packed rows of 2,048 -> 4,196, rank 24: 49 us (floor 21: bytes at the copy rate);
-// 64 single rows of 4,096 -> 4,096, rank 16: 12 us alone; du with dX of 32,768 rows of
+// 6,731 packed rows of 2,048 -> 4,196, rank 24: 51 us (floor 21: bytes at the copy rate);
+// 64 single rows of 4,096 -> 4,096, rank 16: 10.3 us, rank 128 43 (floors 2.1 and 15); du with dX of 32,768 rows of
 // 4,096 -> 4,096, rank 64: 230 us (floor 119).  What bounds it is the latency of loads
 // that its phases do not cover: about half the copy rate in both of them.
 #include "kda_lora_kernel.cuh"

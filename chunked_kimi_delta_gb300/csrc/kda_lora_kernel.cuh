@@ -217,6 +217,8 @@ __device__ __forceinline__ void rows_of(const Args &a, int n, int64_t &r0, int64
 }
 
 // Tile -> first row, rows and adapter; a warp's 32 lanes look at 32 requests at once.
+// With offsets every CTA walks them: nothing for hundreds of requests, but 4,096 single rows of
+// 1,024 -> 1,024 take 383 us so and 88 as rows / requests rows each.
 template <int M> __device__ __forceinline__ void find_tile(const Args &a, int64_t tile, int lane, int64_t &row0, int &len, int &l) {
   len = 0;
   if (!a.cu) {

@@ -491,11 +491,16 @@ kda_status kda_state_grad_scan(const float *M, const float *E, const float *dS_f
  *   g       [.., H] fp32 (head-major: [B, H, T]), no channel axis
  *   dt_bias [H] fp32 or NULL;  a_log [H] as before:
  *           with KDA_GATE_IN_KERNEL  g = -exp(a_log[h]) softplus(x + dt_bias[h])
- * Arithmetic: q, k, v (and d_out) of either type enter the products exactly
- * (fp32 ones to 2^-23 of a row's largest) and everything derived from them, the
- * state above all, keeps at least 22 bits, so fp32 results are good to a few
- * 1e-7 of their size whatever the inputs' type, under any decay.  Results of
- * the inputs' type are rounded once (bf16: from values good to 2^-12).
+ * Arithmetic: fp32 sums of products of fp16 pieces.  bf16 inputs are one piece,
+ * fp32 ones and everything derived from inputs, the state above all, two: 22 bits
+ * for values down to 2^-15 of the largest that shares their unit, and 2^-38 of
+ * that largest below.  q, k and, for dq, d_out have a unit per token; the rest
+ * one per value channel or matrix, over a chunk of 64 tokens.  So fp32 results are
+ * off by up to about 1e-6 of their head's size in the chunk, whatever the inputs'
+ * type and under any decay (4e-7 to 9e-7 in the 2-norm as measured), and tokens far
+ * smaller than others of their chunk by more of their own size, except out where q
+ * and k are normalised and dq, which are a token's own.  Results of the inputs' type
+ * are rounded once (bf16: from values good to 2^-12).
  * Every sum runs in a fixed order: results do not change from call to call.
  * ------------------------------------------------------------------------ */
 size_t kda_gdn_chunk_fwd_workspace_size(const kda_fwd_args *args);
@@ -515,7 +520,9 @@ kda_status kda_gdn_chunk_fwd(const kda_fwd_args *args, kda_stream_t stream);
  * with respect to the inputs as given; fields as kda_chunk_bwd, except that dg
  * is [.., H] and ddt_bias [H], fp32.  The forward's intermediates are computed
  * anew; the workspace holds the states entering and the state gradients
- * leaving every chunk (fp32).  Where the decay is held at e^-256 (zero in
+ * leaving every chunk, and three [64, dv] matrices (fp32): 0.26 MB a chunk and
+ * value head of 128 x 128, 4.6 GB for 4 x 8192 tokens of 32 heads (the forward's
+ * 0.7).  Where the decay is held at e^-256 (zero in
  * fp32) the gate's gradient is that of a decay of zero.  Tokens behind the last
  * sequence as in the forward.  Errors as the forward,
  * and KDA_ERR_INVALID_ARG for null dq, dk, dv, dg or dbeta with tokens, or one
@@ -524,8 +531,8 @@ size_t kda_gdn_chunk_bwd_workspace_size(const kda_bwd_args *args);
 kda_status kda_gdn_chunk_bwd(const kda_bwd_args *args, kda_stream_t stream);
 
 /* The recurrent step on pool states, in fp32, as kda_recurrent_step (any
- * pool alignment; KDA_STATE_V_FIRST pools are [H, dv, dk]).  out may be v, not q
- * or k (KDA_ERR_INVALID_ARG). */
+ * pool alignment; KDA_STATE_V_FIRST pools are [H, dv, dk], and slower: 64 x 32
+ * states 250 us for 55).  out may be v, not q or k (KDA_ERR_INVALID_ARG). */
 kda_status kda_gdn_recurrent_step(const kda_decode_args *args, kda_stream_t stream);
 
 /* ------------------------------------------------------------------------
@@ -697,8 +704,8 @@ kda_status kda_fp8_matmul_shared_workspace(void **workspace);
  * Requests are packed rows [cu_seqlens[i], cu_seqlens[i+1]) (rows behind the
  * last request have no adapter), or, without cu_seqlens, rows / num_requests
  * rows each (a decode batch: one).  The sum is held in fp32 and rounded once;
- * u = x A^T keeps 16 bits for bf16 results, 24 for fp32 ones.  out may be y,
- * not x.
+ * u = x A^T keeps 16 bits for bf16 results, 24 for fp32 ones; a row of x with an
+ * infinity or NaN gives infinities and NaN, in that row alone.  out may be y, not x.
  * Any n_in, n_out and rank up to KDA_LORA_MAX_RANK; widths that are multiples
  * of 8 (then of 4) elements are read fastest.  Deterministic.
  * Errors: KDA_ERR_INVALID_ARG (sizes below 1, rows < 0, null pointers, rows
@@ -732,6 +739,9 @@ kda_status kda_lora(const kda_lora_args *args, kda_stream_t stream);
  *   d_a[l] = sum over l's rows of scale[l] (d_out B[l])^T x     [adapters, rank, n_in]
  *   d_b[l] = sum over l's rows of scale[l] d_out^T (x A[l]^T)   [adapters, n_out, rank]
  * (zeros for adapters without rows).  Any of d_x, d_a, d_b may be NULL, not all.
+ * The workspace holds 12 bytes for each row and rank (rounded up to 16, 32, 64 or
+ * 128), the matrices transposed, 8 bytes for each adapter and row tile (rows / 64 +
+ * requests), and up to eight times d_a and d_b.
  * Sums run in a fixed order.  Errors as kda_lora, plus KDA_ERR_WORKSPACE.
  */
 typedef struct {
